@@ -505,6 +505,185 @@ gdn_status gdn_prefill_packed_split(gdn_handle* handle, const gdn_config* cfg,
 gdn_status gdn_split_segment_auto(int32_t num_seqs, const int32_t* cu_seqlens_host,
                                   int32_t num_v_heads, int32_t num_sms, int32_t* segment_len);
 
+/* ---- full-attention layers: paged 8-bit key/value cache ------------------------------ */
+
+/* The hybrid models whose linear layers the calls above serve interleave them with full
+ * attention layers. These calls are the serving side of such a layer: one plan per step
+ * (pages and slots of the step's tokens, built on the GPU so that a step needs no host
+ * lengths and can be captured in a CUDA graph), then per layer a rotary embedding, an append
+ * that quantises keys and values into a paged cache, and the attention that reads it.
+ *
+ * Conventions: a request's tokens are numbered from 0; page p of a request holds its tokens
+ * [p * page_size, (p + 1) * page_size); block_table [num_seqs][max_blocks] int32 (device)
+ * gives each request's pages in order. A token's slot is page * page_size + its place in the
+ * page. Lengths, tables and slots live on the device and are checked there: a value out of
+ * range is never used as an address. Where `status` is a non-NULL device int32, the kernels
+ * raise it (atomic maximum) to GDN_ERR_INVALID_ARGUMENT when they met such a value; they
+ * never clear it, so a caller zeroes it once and reads it when it likes. A bounded device
+ * wait that gave up raises it to GDN_ERR_DEVICE_TIMEOUT. */
+
+/* A paged cache of e4m3 values with one fp32 scale for each page and head. A cached value is
+ * its e4m3 code times its page's and head's scale. All arrays are device memory, k and v
+ * 16-byte aligned. Supported: page_size 16, 32, 64 or 128, head_dim 64, 128 or 256,
+ * num_pages * num_kv_heads * page_size <= INT32_MAX. */
+typedef struct gdn_kv_cache {
+  int32_t num_pages;
+  int32_t page_size;     /* tokens of a page */
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  void* k;               /* [num_pages][num_kv_heads][page_size][head_dim] e4m3 */
+  void* v;               /* the same layout */
+  float* k_scale;        /* [num_pages][num_kv_heads], each finite and >= 0 */
+  float* v_scale;
+} gdn_kv_cache;
+
+/* Pages and slots of one step, built on the GPU (one kernel). Request b has ctx_len[b]
+ * tokens in the cache, in the first ceil(ctx_len[b] / page_size) entries of its table row,
+ * and appends new_len[b] tokens, whose rows follow one another in request order. Requests are
+ * served in order: each takes the pages that its new tokens need beyond the ones it has from
+ * the top of the free stack free_pages[0 .. *free_count) (the top is the last entry), and
+ * they are written behind its present ones in its table row.
+ *  num_tokens       rows of the step's arrays (at least the sum of new_len).
+ *  free_count       [1] pages on the stack. free_count_out [1] receives what is left; it may
+ *                   be free_count itself.
+ *  cu_new           [num_seqs + 1] out: first row of every request, then the number of rows.
+ *  kv_len           [num_seqs] out: ctx_len + new_len, the lengths the attention takes.
+ *  positions        [num_tokens] out (or NULL): the rows' positions, ctx_len[b] + i; 0 past
+ *                   the last row.
+ *  slots            [num_tokens] int64 out: the rows' slots; -1 past the last row.
+ * A request that cannot be served takes no page: its kv_len is 0 and its slots are -1 (the
+ * append then stores nothing for it, and the attention gives it zeros), and status is raised
+ * to GDN_ERR_POOL_EXHAUSTED when the stack ran out (no later request that needs a page is
+ * served then), or to GDN_ERR_INVALID_ARGUMENT for lengths below 0, more pages than
+ * max_blocks, rows past num_tokens, or a page out of range. At most 4,096 requests.
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED, CUDA. */
+gdn_status gdn_kv_plan(gdn_handle* handle, int32_t page_size, int32_t num_seqs,
+                       int32_t num_tokens, const int32_t* ctx_len, const int32_t* new_len,
+                       int32_t* block_table, int32_t max_blocks, int32_t num_pages,
+                       const int32_t* free_pages, const int32_t* free_count,
+                       int32_t* free_count_out, int32_t* cu_new, int32_t* kv_len,
+                       int32_t* positions, int64_t* slots, int32_t* status, void* stream);
+
+/* Give back the pages of requests that ended (one kernel): for every b with release[b] != 0,
+ * in order, the ceil(kv_len[b] / page_size) pages of its table row are pushed on the free
+ * stack and its table entries become -1. A row with a page out of range, or whose pages would
+ * overfill the stack (num_pages entries), is left as it is and raises the status.
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED (more than 4,096 requests), CUDA. */
+gdn_status gdn_kv_release(gdn_handle* handle, int32_t page_size, int32_t num_seqs,
+                          const int32_t* kv_len, const int32_t* release, int32_t* block_table,
+                          int32_t max_blocks, int32_t num_pages, int32_t* free_pages,
+                          int32_t* free_count, int32_t* status, void* stream);
+
+#define GDN_ROPE_MAX_PAIRS 128
+#define GDN_ROPE_MAX_AXES 4
+
+/* How the rotated pairs are shared out among the axes: whole sections one after another, or
+ * in turns (pair i belongs to axis i mod num_axes while that axis has pairs left, the rest
+ * and the turns of exhausted axes to axis 0). */
+typedef enum gdn_rope_axes { GDN_ROPE_SECTIONS = 0, GDN_ROPE_INTERLEAVED = 1 } gdn_rope_axes;
+/* Which elements form pair i of a rotary part of R elements: (i, i + R/2) or (2i, 2i + 1). */
+typedef enum gdn_rope_pairs { GDN_ROPE_HALVES = 0, GDN_ROPE_ADJACENT = 1 } gdn_rope_pairs;
+
+/* A rotary embedding, filled once by gdn_rope_init. A frequency is kept as the 64-bit
+ * fraction of a turn per position, so that position * frequency modulo a turn is one integer
+ * product, exact to 2^-33 of a turn for every int32 position. */
+typedef struct gdn_rope {
+  int32_t head_dim;
+  int32_t rotary_dim;   /* R: the first R elements of a head are rotated, the rest pass */
+  int32_t num_axes;
+  int32_t pair_layout;  /* gdn_rope_pairs */
+  uint64_t turns[GDN_ROPE_MAX_PAIRS];  /* pair i: frequency / (2 pi), times 2^64 */
+  uint8_t axis[GDN_ROPE_MAX_PAIRS];    /* pair i: the axis whose position it follows */
+} gdn_rope;
+
+/* Fill a gdn_rope. sections[num_axes]: pairs of each axis (time, height, width, ...), their
+ * sum R/2. inv_freq: R/2 angular frequencies (radians per position, each in [0, 2 pi)), or
+ * NULL for theta^(-2i/R). Supported: head_dim 64, 128 or 256, rotary_dim a multiple of 16
+ * up to head_dim, 1 to 4 axes. Host arithmetic, no CUDA call. Errors: INVALID_ARGUMENT,
+ * UNSUPPORTED. */
+gdn_status gdn_rope_init(gdn_rope* rope, int32_t head_dim, int32_t rotary_dim,
+                         int32_t num_axes, const int32_t* sections, int32_t axis_layout,
+                         int32_t pair_layout, double theta, const double* inv_freq);
+
+/* Rotate the heads of q and k (one kernel): pair (x, y) with angle w = position[axis] *
+ * frequency becomes (x cos w - y sin w, y cos w + x sin w), in fp32, rounded once.
+ *  positions  [num_axes][pos_stride] int32 (device): row `a` holds the tokens' positions on
+ *             axis a; any int32 value.
+ *  q, q_out   token t's heads at q + t * q_stride (elements), [num_q_heads][head_dim]
+ *             contiguous; q_out the same with its own stride. q_out may be q with the same
+ *             stride (in place); no other overlap. num_q_heads 0: no q. The same for k.
+ * Pointers 16-byte aligned, strides multiples of 16 bytes and at least heads * head_dim (so
+ * q and k may be column ranges of one projection's output). Errors: INVALID_ARGUMENT, CUDA. */
+gdn_status gdn_rope_apply(gdn_handle* handle, const gdn_rope* rope, int32_t io_dtype,
+                          int32_t num_tokens, const int32_t* positions, int64_t pos_stride,
+                          const void* q, int64_t q_stride, int32_t num_q_heads, void* q_out,
+                          int64_t q_out_stride, const void* k, int64_t k_stride,
+                          int32_t num_k_heads, void* k_out, int64_t k_out_stride, void* stream);
+
+/* Quantise the step's keys and values into the cache (one kernel). Row t goes to slots[t]
+ * ([num_tokens] int64, device; a negative slot is skipped). Rows of one page must follow one
+ * another with rising slots, as gdn_kv_plan numbers them, and what the page holds in front of
+ * the first of them must be the request's earlier tokens; the call's rows name each page in
+ * one such run only.
+ * A page's and head's scale is the least power of two s with |x| <= 448 s for every finite
+ * value it has held since its first token (2^-100 at least): it never shrinks while the page
+ * fills, and when it grows the codes in front are rounded to it (exact but for the smallest,
+ * since only their exponent moves). A run that begins at the page's first token starts the
+ * scale anew. Values are rounded to the nearest e4m3, ties to even; infinities are held as
+ * the largest finite value; a NaN in k stays NaN, and a token with a NaN in v gets a NaN key
+ * and zeros for its NaN values: such a token makes NaN every output that attends to it and
+ * no other.
+ *  k, v       token t's heads at k + t * k_stride (elements), [num_kv_heads][head_dim].
+ *  rope       NULL: k is stored as given. Otherwise k is rotated on the way (in fp32, one
+ *             rounding), and when num_q_heads > 0 so is q into q_out, as gdn_rope_apply.
+ * Alignment and strides as gdn_rope_apply. Errors: INVALID_ARGUMENT, UNSUPPORTED, CUDA. */
+gdn_status gdn_kv_append(gdn_handle* handle, const gdn_kv_cache* cache, int32_t io_dtype,
+                         int32_t num_tokens, const int64_t* slots, const void* k,
+                         int64_t k_stride, const void* v, int64_t v_stride,
+                         const gdn_rope* rope, const int32_t* positions, int64_t pos_stride,
+                         const void* q, int64_t q_stride, int32_t num_q_heads, void* q_out,
+                         int64_t q_out_stride, int32_t* status, void* stream);
+
+/* Attention over the paged cache. */
+typedef struct gdn_attn_config {
+  int32_t num_q_heads;  /* a multiple of the cache's num_kv_heads; query head h reads
+                           key/value head h / (num_q_heads / num_kv_heads) */
+  int32_t causal;       /* nonzero: query i of a request with q_len queries and kv_len cached
+                           tokens sees tokens 0 .. kv_len - q_len + i; zero: all of them */
+  int32_t io_dtype;     /* gdn_dtype of q and o */
+  float scale;          /* of the scores, usually 1/sqrt(head_dim) */
+} gdn_attn_config;
+
+/* Device workspace of gdn_attn_paged for calls of at most these sizes (multiple of 256). */
+gdn_status gdn_attn_workspace_size(const gdn_attn_config* cfg, const gdn_kv_cache* cache,
+                                   int32_t num_seqs, int32_t num_tokens, int32_t max_q_len,
+                                   int32_t max_kv_len, size_t* bytes);
+
+/* o = softmax(scale q K^T) V for a pack of requests of any mix of lengths: decoding requests
+ * (one query), drafts (a few) and prompts, behind any cached prefix. K and V are the cached
+ * tokens, the call's own among them (append first).
+ *  num_tokens   rows of q, o and lse.
+ *  max_q_len, max_kv_len  host bounds of the requests' lengths: they choose the kernels and
+ *               the split of the work; a longer request is cut to them (status raised).
+ *  cu_q         [num_seqs + 1] device: request b's queries are rows [cu_q[b], cu_q[b+1]).
+ *  kv_len       [num_seqs] device: its cached tokens (0 is allowed).
+ *  q, o         token t's heads at q + t * q_stride (elements), [num_q_heads][head_dim].
+ *  lse          [num_tokens][num_q_heads] fp32 out, or NULL: log of the sum of exponentials.
+ * A query that sees no token gives o = 0 and lse = -inf. Pages out of range count as absent
+ * (status raised). Rows outside every request are not written. Scores, softmax sums and
+ * outputs are accumulated in fp32; products take fp16 operands: the cache's codes and the
+ * powers-of-two-normalised bf16 queries exactly, probabilities rounded to 11 bits (fp32 io:
+ * queries and probabilities as two fp16 terms, 22 bits). Results do not depend on atomics:
+ * the same call gives the same bits. At most 4,096 requests.
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED, WORKSPACE_TOO_SMALL, CUDA. */
+gdn_status gdn_attn_paged(gdn_handle* handle, const gdn_attn_config* cfg,
+                          const gdn_kv_cache* cache, int32_t num_seqs, int32_t num_tokens,
+                          int32_t max_q_len, int32_t max_kv_len, const int32_t* cu_q,
+                          const int32_t* kv_len, const int32_t* block_table,
+                          int32_t max_blocks, const void* q, int64_t q_stride, void* o,
+                          int64_t o_stride, float* lse, void* workspace,
+                          size_t workspace_bytes, int32_t* status, void* stream);
+
 /* ---- host-side scheduling policy (no device work) ---------------------------------- */
 
 /* Prefix-cache checkpoint position of a prompt of `len` tokens on a grid of `block`

@@ -1371,6 +1371,8 @@ int32_t gdn_mixed_budget(int32_t num_waiting, const int32_t* remaining, int32_t 
 
 namespace gdn {
 
+int handle_device(const gdn_handle* h) { return h->device; }
+
 gdn_status plan_prefill(const gdn_handle* h, const gdn_config* cfg, int32_t num_seqs,
                         const int32_t* cu, const int32_t* ckpt_cu, const int32_t* ckpt_pos,
                         PrefillPlan* out) {

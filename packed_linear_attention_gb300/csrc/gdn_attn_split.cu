@@ -1,0 +1,771 @@
+// gdn_attn_split.cu — attention of few queries over the paged e4m3 cache, the work split over
+// the cached tokens.
+//
+// A unit is (request, key/value head, up to 8 NT query rows); its work items are the 64-token
+// tiles of the request's cache. All units' items form one line that is cut into equal pieces,
+// one for each resident block, whatever the requests' lengths: one user's 32K context and a
+// ragged batch both fill every SM, and no host lengths are needed (each block finds its piece
+// from a prefix sum over the requests). A block that covers a unit's whole range writes the
+// output; pieces of a unit that was cut leave (max, sum, accumulator) in the workspace and a
+// second kernel joins them in order, so the result does not depend on timing.
+//
+// Bound: HBM. A cached token is read once for all query rows of its head. One producer warp
+// keeps the stages' TMA copies in flight (page ids and scales are fetched 512 tokens ahead);
+// four consumer warps take 16 tokens of every tile each, with running maximum, sum and
+// accumulator of their own, merged when the piece ends.
+//
+// Products run transposed on m16n8k16 f16 warp MMAs (the tensor rate is not the bound here,
+// and 8 query rows fill n = 8 exactly):
+//   S^T (16 tokens x 8 rows) = K (16 x D) Q^T      O^T (D x 8 rows) += V^T P^T
+// e4m3 values are f16 values, so K and V enter exactly. The contraction index of S may be
+// permuted alike in K and Q, so a thread takes its K operand as whole 16-byte chunks of a
+// token's row; V^T is read with transposing 16-bit ldmatrix (two channels to an element) and
+// one byte permutation. The queries are scaled by a power of two per row into the f16 range
+// (bf16 fits exactly); fp32 queries and probabilities are two f16 terms.
+// The running maximum is only raised when a score passes it by 2^8 (in log2 units, 8): until
+// then probabilities stay below 2^8 and no cross-lane reduction is needed. Value scales enter
+// as ratios to the largest met so far, so that probabilities fill the f16 range.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <type_traits>
+
+#include "gdn_attn_internal.h"
+#include "gdn_internal.h"
+#include "ptx_sm103.cuh"
+
+namespace gdn {
+namespace {
+
+using namespace ptx;
+
+constexpr int kWarps = 4;                       // consumer warps
+constexpr int kThreads = 32 * (kWarps + 1);     // and the producer warp
+constexpr int kTile = kSplitTile;
+constexpr int kGroups = kTile / 16;             // 16-token groups of a tile, one per warp
+constexpr int kCtasPerSm = 2;
+constexpr int kMaxStages = 8;
+constexpr uint32_t kWaitLimit = 1u << 24;
+constexpr float kLazyMax = 8.f;                 // log2 units
+constexpr float kProbScale = 128.f;             // probabilities times this, at most 2^15 in f16
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kStatusTimeout = GDN_ERR_DEVICE_TIMEOUT;
+constexpr size_t kSmemPerCta = 112 * 1024;      // two blocks share an SM's 227 KB
+
+#define GDN_INF __int_as_float(0x7f800000)
+
+struct SplitDesc {  // what a worker's last, unfinished unit is; count 0: none
+  int32_t seq, head, row_tile, count;
+};
+
+struct SplitParams {
+  AttnArgs a;
+  CUtensorMap tk, tv;
+  SplitDesc* desc;    // [workers]
+  float* part;        // [2 workers][RB (D + 2)]
+  int32_t stages;
+  uint32_t off_q, off_red, off_pre;  // shared-memory map after the stages
+};
+
+__device__ __forceinline__ uint32_t e4m3_to_half2(uint16_t x) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t lo_half2(uint32_t w) { return e4m3_to_half2((uint16_t)w); }
+__device__ __forceinline__ uint32_t hi_half2(uint32_t w) { return e4m3_to_half2((uint16_t)(w >> 16)); }
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ float2 half2_floats(uint32_t h) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// Byte offset of 16-byte chunk `chunk` of row `row` in a tile of 64 rows as TMA wrote it:
+// regions of 128 bytes a row under the 128-byte swizzle, or rows of 64 bytes under the 64-byte
+// one.
+template <int D>
+__device__ __forceinline__ uint32_t tile_offset(int row, int chunk) {
+  if constexpr (D == 64) return row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
+  else return (chunk >> 3) * (kTile * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+}
+
+struct GroupMeta {
+  float ks, vs;   // ks < 0: the group's page is absent
+};
+
+template <int NT>
+struct SmemHead {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  GroupMeta meta[kMaxStages][kGroups];
+  float row_scale[8 * NT];
+  int32_t row_limit[8 * NT];
+  float m[kWarps][8 * NT], l[kWarps][8 * NT], vref[kWarps];
+  int64_t scan[8];
+  int32_t dead;
+};
+
+// Waits for a phase with a bound; after any wait of the block gave up, none waits again, so
+// that every loop still runs its course and no thread is left at a barrier.
+__device__ __forceinline__ void wait_or_die(uint64_t* bar, uint32_t parity, volatile int32_t* dead,
+                                            int32_t* status) {
+  if (mbar_try_wait(bar, parity)) return;
+  if (*dead) return;
+  if (!mbar_wait_bounded(bar, parity, kWaitLimit)) {
+    *dead = 1;
+    raise_status(status, kStatusTimeout);
+  }
+}
+
+// One piece of a unit.
+struct Segment {
+  int32_t seq, head, row_tile;
+  int32_t t0, t1, tiles;  // tiles [t0, t1) of `tiles`
+};
+
+template <int RB>
+__device__ __forceinline__ int32_t seq_items(const AttnArgs& a, const AttnSeq& s) {
+  if (s.q_len == 0 || s.q_len > a.split_q) return 0;
+  return a.hkv * ((s.q_len * a.group + RB - 1) / RB) * max(1, (s.kv_len + kTile - 1) / kTile);
+}
+
+// The segment that begins at item `w` and ends at or before item `w1`.
+template <int RB>
+__device__ __forceinline__ Segment find_segment(const AttnArgs& a, const int32_t* pre, int32_t w,
+                                                int32_t w1, AttnSeq& s) {
+  int32_t lo = 0, hi = a.num_seqs - 1;
+  while (lo < hi) {  // the last request whose items begin at or before w
+    const int32_t mid = (lo + hi + 1) >> 1;
+    if (pre[mid] <= w) lo = mid;
+    else hi = mid - 1;
+  }
+  bool bad = false;
+  s = attn_seq(a, lo, bad);
+  const int32_t row_tiles = (s.q_len * a.group + RB - 1) / RB;
+  Segment g;
+  g.seq = lo;
+  g.tiles = max(1, (s.kv_len + kTile - 1) / kTile);
+  const int32_t x = w - pre[lo], unit = x / g.tiles;
+  g.head = unit / row_tiles;
+  g.row_tile = unit % row_tiles;
+  g.t0 = x % g.tiles;
+  g.t1 = min(g.tiles, g.t0 + (w1 - w));
+  return g;
+}
+
+template <typename T>
+__device__ __forceinline__ void load4(const T* p, float (&x)[4]);
+template <>
+__device__ __forceinline__ void load4<float>(const float* p, float (&x)[4]) {
+  const float4 v = *reinterpret_cast<const float4*>(p);
+  x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+}
+template <>
+__device__ __forceinline__ void load4<__nv_bfloat16>(const __nv_bfloat16* p, float (&x)[4]) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  x[0] = __uint_as_float(v.x << 16); x[1] = __uint_as_float(v.x & 0xFFFF0000u);
+  x[2] = __uint_as_float(v.y << 16); x[3] = __uint_as_float(v.y & 0xFFFF0000u);
+}
+__device__ __forceinline__ void store4(float* p, const float (&x)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&x)[4]) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
+                                            *reinterpret_cast<const uint32_t*>(&b));
+}
+
+// T: type of q and o. NT: tiles of 8 query rows.
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+split_kernel(const __grid_constant__ SplitParams p) {
+  constexpr int RB = 8 * NT;
+  constexpr int kTerms = std::is_same<T, float>::value ? 2 : 1;
+  constexpr int kSteps = D / 16;          // k steps of S, and 16-channel chunks of O
+  constexpr int kRed = D + 8;             // row stride of the merge buffer
+  constexpr uint32_t kTileBytes = kTile * D;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ SmemHead<NT> sm;
+  const AttnArgs& a = p.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint2* qfrag = reinterpret_cast<uint2*>(smem + p.off_q);  // [terms][NT][kSteps][32]
+  float* red = reinterpret_cast<float*>(smem + p.off_red);  // [RB][kRed]
+  int32_t* pre = reinterpret_cast<int32_t*>(smem + p.off_pre);  // [num_seqs + 1]
+
+  // ---- prefix sums of the requests' items (every block for itself)
+  {
+    const int per = (a.num_seqs + kThreads - 1) / kThreads, b0 = tid * per;
+    const int b1 = min(a.num_seqs, b0 + per);
+    int32_t sum = 0;
+    bool bad = false;
+    for (int b = b0; b < b1; ++b) {
+      const AttnSeq s = attn_seq(a, b, bad);
+      sum += seq_items<RB>(a, s);
+    }
+    if (bad && blockIdx.x == 0) raise_status(a.status, GDN_ERR_INVALID_ARGUMENT);
+    int32_t inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) sm.scan[warp] = inc;
+    if (tid == 0) {
+      sm.dead = 0;
+      for (int s = 0; s < p.stages; ++s) {
+        mbar_init(&sm.full[s], 1);
+        mbar_init(&sm.empty[s], kWarps);
+      }
+      fence_mbar_init();
+    }
+    __syncthreads();
+    int32_t at = inc - sum;
+    for (int w = 0; w < warp; ++w) at += (int32_t)sm.scan[w];
+    for (int b = b0; b < b1; ++b) {
+      pre[b] = at;
+      at += seq_items<RB>(a, attn_seq(a, b, bad));
+    }
+    if (b1 == a.num_seqs && b0 < b1) pre[a.num_seqs] = at;
+    __syncthreads();
+  }
+  // G workers share W items, every one at least one
+  const int64_t W = pre[a.num_seqs], G = min((int64_t)gridDim.x, W);
+  if (blockIdx.x >= G) {
+    if (tid == 0) p.desc[blockIdx.x].count = 0;
+    return;
+  }
+  const int32_t w0 = (int32_t)(W * blockIdx.x / G), w1 = (int32_t)(W * (blockIdx.x + 1) / G);
+  uint32_t it = 0;  // tiles since the start: stage and phase
+  const int S = p.stages;
+
+  if (warp == kWarps) {
+    // ---- producer
+    const int box_rows = min(a.page_size, kTile), per_box = box_rows / 16;
+    const uint32_t box_bytes = (uint32_t)box_rows * D;
+    for (int32_t w = w0; w < w1;) {
+      AttnSeq s;
+      const Segment g = find_segment<RB>(a, pre, w, w1, s);
+      w += g.t1 - g.t0;
+      const int32_t* table = a.block_table + (int64_t)g.seq * a.max_blocks;
+      for (int32_t tb = g.t0; tb < g.t1; tb += 8) {  // 8 tiles' pages and scales, one group a lane
+        const int32_t tok = tb * kTile + lane * 16;
+        int32_t id = -1;
+        float ks = -1.f, vs = 0.f;
+        if (tok < s.kv_len && tok < g.t1 * kTile) {
+          id = table[tok / a.page_size];
+          if (id >= 0 && id < a.num_pages) {
+            ks = a.k_scale[(int64_t)id * a.hkv + g.head];
+            vs = a.v_scale[(int64_t)id * a.hkv + g.head];
+            if (!(ks >= 0.f)) ks = 0.f;  // not a scale: the group counts as zeros
+          } else {
+            id = -1;
+            raise_status(a.status, GDN_ERR_INVALID_ARGUMENT);
+          }
+        }
+        for (int j = 0; j < 8 && tb + j < g.t1; ++j, ++it) {
+          const int st = it % S;
+          wait_or_die(&sm.empty[st], ((it / S) & 1u) ^ 1u, &sm.dead, a.status);
+          const int first = j * kGroups;
+          if (lane >= first && lane < first + kGroups) sm.meta[st][lane - first] = {ks, vs};
+          // one lane per box: the lanes that hold its first group
+          const bool box = lane >= first && lane < first + kGroups &&
+                           (lane - first) % per_box == 0 && id >= 0;
+          const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, box));
+          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(&sm.full[st], 2 * boxes * box_bytes);
+          __syncwarp();
+          if (box) {
+            uint8_t* dk = smem + (uint32_t)st * 2 * kTileBytes;
+            const int32_t y = (int32_t)(((int64_t)id * a.hkv + g.head) * a.page_size +
+                                        tok % a.page_size);
+            const uint32_t row = (uint32_t)(lane - first) * 16;
+#pragma unroll
+            for (int r = 0; r < (D + 127) / 128; ++r) {
+              const uint32_t at = r * (kTile * 128) + row * (D == 64 ? 64 : 128);
+              tma_load_2d(dk + at, &p.tk, 128 * r, y, &sm.full[st]);
+              tma_load_2d(dk + kTileBytes + at, &p.tv, 128 * r, y, &sm.full[st]);
+            }
+          }
+        }
+      }
+    }
+    // after a wait gave up, copies may still be in flight: let them land
+    if (sm.dead)
+      for (int k = 0; k < S && k < (int)it; ++k) {
+        const uint32_t i = it - 1 - k;
+        mbar_wait_bounded(&sm.full[i % S], (i / S) & 1u, kWaitLimit);
+      }
+    return;
+  }
+
+  // ---- consumers
+  const int c = lane & 3, n8 = lane >> 2;
+  SplitDesc desc = {0, 0, 0, 0};
+  for (int32_t w = w0; w < w1;) {
+    AttnSeq s;
+    const Segment g = find_segment<RB>(a, pre, w, w1, s);
+    const int32_t wbeg = w;
+    w += g.t1 - g.t0;
+    const int32_t rows = s.q_len * a.group, r0 = g.row_tile * RB;
+    // queries of the unit as f16 operands, a row per warp and round
+    for (int r = warp; r < RB; r += kWarps) {
+      const int32_t row = r0 + r;
+      const bool live = row < rows;
+      const int32_t i = live ? row / a.group : 0;
+      const T* src = static_cast<const T*>(a.q) + (int64_t)(s.row0 + i) * a.q_stride +
+                     (int64_t)(g.head * a.group + (live ? row % a.group : 0)) * D;
+      constexpr int kQuads = (D / 4 + 31) / 32;
+      float x[kQuads][4];
+      float amax = 0.f;
+#pragma unroll
+      for (int k = 0; k < kQuads; ++k) {
+        const int quad = lane + 32 * k;
+        x[k][0] = x[k][1] = x[k][2] = x[k][3] = 0.f;
+        if (live && quad < D / 4) load4(src + 4 * quad, x[k]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fabsf(x[k][e]));
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      // power of two that brings the row's largest magnitude to [2^13, 2^14)
+      int ex = (int)(__float_as_uint(amax) >> 23) - 127;
+      ex = ex == 128 ? 13 : max(ex, -100);  // a row with an infinity keeps its values
+      const float up = __uint_as_float((uint32_t)(13 - ex + 127) << 23);
+#pragma unroll
+      for (int k = 0; k < kQuads; ++k) {
+        const int quad = lane + 32 * k;
+        if (quad < D / 4) {
+          // element 4 quad + 2 f + e sits in chunk quad / 4, word i = quad % 4 of the chunk
+          const int chunk = quad >> 2, word = quad & 3;
+          const int step = D == 64 ? word : (chunk >> 3) * 8 + (chunk & 1) * 4 + word;
+          const int ln = (r & 7) * 4 + (D == 64 ? chunk : (chunk & 7) >> 1);
+          float y[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] = x[k][e] * up;
+          uint2 h = make_uint2(f16x2(y[0], y[1]), f16x2(y[2], y[3]));
+          qfrag[((r >> 3) * kSteps + step) * 32 + ln] = h;
+          if constexpr (kTerms == 2) {
+            const float2 h0 = half2_floats(h.x), h1 = half2_floats(h.y);
+            qfrag[((NT + (r >> 3)) * kSteps + step) * 32 + ln] =
+                make_uint2(f16x2(y[0] - h0.x, y[1] - h0.y), f16x2(y[2] - h1.x, y[3] - h1.y));
+          }
+        }
+      }
+      if (lane == 0) {
+        sm.row_scale[r] = a.scale_log2 * __uint_as_float((uint32_t)(ex - 13 + 127) << 23);
+        sm.row_limit[r] = live ? attn_limit(a, s, i) : s.kv_len;
+      }
+    }
+    named_sync(1, 32 * kWarps);
+    float rs[NT][2];
+    int32_t lim[NT][2];
+    const int32_t min_limit = sm.row_limit[0];  // limits rise with the row
+    const int32_t max_limit = attn_limit(a, s, (min(rows, r0 + RB) - 1) / a.group);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        rs[t][e] = sm.row_scale[8 * t + 2 * c + e];
+        lim[t][e] = sm.row_limit[8 * t + 2 * c + e];
+      }
+
+    float O[kSteps][NT][4];
+    float m[NT][2], l[NT][2], vref = 0.f;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      m[t][0] = m[t][1] = -GDN_INF;
+      l[t][0] = l[t][1] = 0.f;
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) O[k][t][e] = 0.f;
+    }
+
+    for (int32_t t = g.t0; t < g.t1; ++t, ++it) {
+      const int st = it % S;
+      wait_or_die(&sm.full[st], (it / S) & 1u, &sm.dead, a.status);
+      const int32_t j0 = t * kTile + 16 * warp;
+      const GroupMeta meta = sm.meta[st][warp];
+      if (j0 < max_limit && meta.ks >= 0.f) {
+        const uint32_t sk = smem_u32(smem) + (uint32_t)st * 2 * kTileBytes, sv = sk + kTileBytes;
+        // ---- S^T = K Q^T, two accumulator chains
+        float acc[2][NT][4];
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[x][n][e] = 0.f;
+#pragma unroll
+        for (int q = 0; q < kSteps / 4; ++q) {  // chunks of 16 channels: 4 k steps each
+          const int chunk = D == 64 ? c : (q >> 1) * 8 + 2 * c + (q & 1);
+          uint32_t ka[4], kb[4];
+          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(ka[0]), "=r"(ka[1]), "=r"(ka[2]), "=r"(ka[3])
+                       : "r"(sk + tile_offset<D>(16 * warp + n8, chunk)));
+          asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                       : "=r"(kb[0]), "=r"(kb[1]), "=r"(kb[2]), "=r"(kb[3])
+                       : "r"(sk + tile_offset<D>(16 * warp + n8 + 8, chunk)));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int step = 4 * q + i;
+            const uint32_t A[4] = {lo_half2(ka[i]), lo_half2(kb[i]), hi_half2(ka[i]),
+                                   hi_half2(kb[i])};
+#pragma unroll
+            for (int x = 0; x < kTerms; ++x)
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                const uint2 b = qfrag[((x * NT + n) * kSteps + step) * 32 + lane];
+                const uint32_t B[2] = {b.x, b.y};
+                mma_f16_16816(acc[step & 1][n], A, B);
+              }
+          }
+        }
+        // ---- scores, running maximum, probabilities
+        float s4[NT][4];
+        bool over = false;
+        const bool masked = j0 + 16 > min_limit;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float x = (acc[0][n][e] + acc[1][n][e]) * (meta.ks * rs[n][e & 1]);
+            if (masked && j0 + n8 + (e >= 2 ? 8 : 0) >= lim[n][e & 1]) x = -GDN_INF;
+            s4[n][e] = x;
+            over = over || x > m[n][e & 1] + kLazyMax;
+          }
+        if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float x = fmaxf(s4[n][e], s4[n][e + 2]);
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+              x = fmaxf(x, m[n][e]);
+              const float f = x == -GDN_INF ? 1.f : ex2(m[n][e] - x);
+              m[n][e] = x;
+              l[n][e] *= f;
+#pragma unroll
+              for (int k = 0; k < kSteps; ++k) {
+                O[k][n][e] *= f;
+                O[k][n][e + 2] *= f;
+              }
+            }
+        }
+        if (meta.vs > vref) {
+          const float f = vref / meta.vs;
+          vref = meta.vs;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) O[k][n][e] *= f;
+        }
+        const float pv = vref > 0.f ? meta.vs / vref * kProbScale : 0.f;
+        uint32_t B[kTerms][NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float y[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float mu = m[n][e & 1] == -GDN_INF ? 0.f : m[n][e & 1];
+            const float pr = ex2(s4[n][e] - mu);
+            l[n][e & 1] += pr;
+            y[e] = pr * pv;
+          }
+          const uint32_t h0 = f16x2(y[0], y[1]), h1 = f16x2(y[2], y[3]);
+          B[0][n][0] = movmatrix_trans(h0);
+          B[0][n][1] = movmatrix_trans(h1);
+          if constexpr (kTerms == 2) {
+            const float2 z0 = half2_floats(h0), z1 = half2_floats(h1);
+            B[kTerms - 1][n][0] = movmatrix_trans(f16x2(y[0] - z0.x, y[1] - z0.y));
+            B[kTerms - 1][n][1] = movmatrix_trans(f16x2(y[2] - z1.x, y[3] - z1.y));
+          }
+        }
+        // ---- O^T += V^T P^T
+        // rows past the cached tokens hold anything: they are taken as zeros
+        const int32_t left = s.kv_len - j0;
+        uint32_t mlo = 0xffffffffu, mhi = 0xffffffffu;
+        if (left < 16) {
+          mlo = (2 * c < left ? 0x0000ffffu : 0u) | (2 * c + 1 < left ? 0xffff0000u : 0u);
+          mhi = (2 * c + 8 < left ? 0x0000ffffu : 0u) | (2 * c + 9 < left ? 0xffff0000u : 0u);
+        }
+        const int vrow = 16 * warp + ((lane >> 3) & 1) * 8 + (lane & 7), vch = lane >> 4;
+#pragma unroll
+        for (int k = 0; k < kSteps; k += 2) {
+          uint32_t r4[4];
+          ldmatrix_x4_trans(r4, sv + tile_offset<D>(vrow, k + vch));
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t x = __byte_perm(r4[2 * h] & mlo, 0, 0x3120);
+            const uint32_t z = __byte_perm(r4[2 * h + 1] & mhi, 0, 0x3120);
+            const uint32_t A[4] = {lo_half2(x), hi_half2(x), lo_half2(z), hi_half2(z)};
+#pragma unroll
+            for (int xx = 0; xx < kTerms; ++xx)
+#pragma unroll
+              for (int n = 0; n < NT; ++n) mma_f16_16816(O[k + h][n], A, B[xx][n]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.empty[st]);
+    }
+
+    // ---- merge the four warps
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float x = l[n][e];
+        x += __shfl_xor_sync(0xffffffffu, x, 4);
+        x += __shfl_xor_sync(0xffffffffu, x, 8);
+        x += __shfl_xor_sync(0xffffffffu, x, 16);
+        if (n8 == 0) {
+          sm.m[warp][8 * n + 2 * c + e] = m[n][e];
+          sm.l[warp][8 * n + 2 * c + e] = x;
+        }
+      }
+    named_sync(1, 32 * kWarps);
+    float f[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float M = sm.m[0][8 * n + 2 * c + e];
+#pragma unroll
+        for (int x = 1; x < kWarps; ++x) M = fmaxf(M, sm.m[x][8 * n + 2 * c + e]);
+        f[n][e] = m[n][e] == -GDN_INF ? 0.f : ex2(m[n][e] - M) * (vref / kProbScale);
+      }
+    for (int x = 0; x < kWarps; ++x) {
+      if (warp == x) {
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float2* at = reinterpret_cast<float2*>(red + (8 * n + 2 * c + e) * kRed + 16 * k +
+                                                     2 * n8);
+              float2 y = make_float2(O[k][n][e] * f[n][e], O[k][n][e + 2] * f[n][e]);
+              if (x > 0) {
+                const float2 z = *at;
+                y.x += z.x;
+                y.y += z.y;
+              }
+              *at = y;
+            }
+      }
+      named_sync(1, 32 * kWarps);
+    }
+    // ---- write the output, or the piece
+    const bool whole = g.t0 == 0 && g.t1 == g.tiles;
+    float* part = p.part + ((int64_t)2 * blockIdx.x + (g.t0 > 0 ? 0 : 1)) * (RB * (D + 2));
+    for (int r = warp; r < RB; r += kWarps) {
+      const int32_t row = r0 + r;
+      if (row >= rows) break;
+      float M = sm.m[0][r];
+#pragma unroll
+      for (int x = 1; x < kWarps; ++x) M = fmaxf(M, sm.m[x][r]);
+      float L = 0.f;  // a warp without a maximum has a sum of 0, or NaN where a key was
+#pragma unroll
+      for (int x = 0; x < kWarps; ++x)
+        L += sm.m[x][r] == -GDN_INF ? sm.l[x][r] : sm.l[x][r] * ex2(sm.m[x][r] - M);
+      const float inv = !whole ? 1.f : L == 0.f ? 0.f : 1.f / L;
+      const int64_t tok = s.row0 + row / a.group;
+      const int head = g.head * a.group + row % a.group;
+      for (int quad = lane; quad < D / 4; quad += 32) {
+        const float4 v = *reinterpret_cast<const float4*>(red + r * kRed + 4 * quad);
+        const float y[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
+        if (whole) store4(static_cast<T*>(a.o) + tok * a.o_stride + (int64_t)head * D + 4 * quad, y);
+        else store4(part + r * D + 4 * quad, y);
+      }
+      if (lane == 0) {
+        if (!whole) {
+          part[RB * D + 2 * r] = M;
+          part[RB * D + 2 * r + 1] = L;
+        } else if (a.lse) {
+          a.lse[tok * (a.hkv * a.group) + head] = L == 0.f ? -GDN_INF : (M + log2f(L)) * kLn2;
+        }
+      }
+    }
+    if (g.t0 == 0 && g.t1 < g.tiles) {  // the unit goes on in later blocks: up to which?
+      const int64_t last = (int64_t)wbeg + g.tiles - 1;
+      int64_t k = last * G / W;
+      while (W * (k + 1) / G <= last) ++k;
+      while (W * k / G > last) --k;
+      desc = {g.seq, g.head, g.row_tile, (int32_t)(k - blockIdx.x + 1)};
+    }
+    named_sync(1, 32 * kWarps);  // the next unit writes the shared arrays again
+  }
+  if (tid == 0) p.desc[blockIdx.x] = desc;
+}
+
+constexpr int kJoinThreads = 256;
+constexpr int kMaxWorkers = kCtasPerSm * kMaxSms;
+
+// Joins the pieces of the unit that worker blockIdx.x began and did not finish, row
+// blockIdx.y of it.
+template <typename T, int D, int RB>
+__global__ void __launch_bounds__(kJoinThreads)
+join_kernel(AttnArgs a, const SplitDesc* desc, const float* part) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces are written
+  __shared__ float weight[kMaxWorkers];
+  __shared__ float red[kJoinThreads / 32];
+  __shared__ float4 sum[kJoinThreads];
+  const SplitDesc d = desc[blockIdx.x];
+  if (d.count == 0) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  bool bad = false;
+  const AttnSeq s = attn_seq(a, d.seq, bad);
+  const int r = blockIdx.y;
+  const int32_t row = d.row_tile * RB + r;
+  if (row >= s.q_len * a.group) return;
+  // piece i: the second slot of the first worker, then the first slots of the next ones
+  auto piece = [&](int i) {
+    return part + ((int64_t)2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * (RB * (D + 2));
+  };
+  auto block_reduce = [&](float x, bool take_max) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float y = __shfl_xor_sync(0xffffffffu, x, o);
+      x = take_max ? fmaxf(x, y) : x + y;
+    }
+    __syncthreads();
+    if (lane == 0) red[warp] = x;
+    __syncthreads();
+    x = red[0];
+#pragma unroll
+    for (int w = 1; w < kJoinThreads / 32; ++w) x = take_max ? fmaxf(x, red[w]) : x + red[w];
+    return x;
+  };
+  float M = -GDN_INF;
+  for (int i = tid; i < d.count; i += kJoinThreads) M = fmaxf(M, piece(i)[RB * D + 2 * r]);
+  M = block_reduce(M, true);
+  float L = 0.f;
+  for (int i = tid; i < d.count; i += kJoinThreads) {
+    const float mi = piece(i)[RB * D + 2 * r];
+    const float f = mi == -GDN_INF ? 0.f : ex2(mi - M);
+    weight[i] = f;
+    L += piece(i)[RB * D + 2 * r + 1] * (mi == -GDN_INF ? 1.f : f);
+  }
+  L = block_reduce(L, false);
+  constexpr int kQuads = D / 4, kSets = kJoinThreads / kQuads;
+  const int quad = tid % kQuads, set = tid / kQuads;
+  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = set; i < d.count; i += kSets) {
+    const float4 v = *reinterpret_cast<const float4*>(piece(i) + r * D + 4 * quad);
+    const float f = weight[i];
+    y.x += v.x * f; y.y += v.y * f; y.z += v.z * f; y.w += v.w * f;
+  }
+  sum[tid] = y;
+  __syncthreads();
+  if (set == 0) {
+#pragma unroll
+    for (int k = 1; k < kSets; ++k) {
+      const float4 v = sum[k * kQuads + quad];
+      y.x += v.x; y.y += v.y; y.z += v.z; y.w += v.w;
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const int64_t tok = s.row0 + row / a.group;
+    const int head = d.head * a.group + row % a.group;
+    const float z[4] = {y.x * inv, y.y * inv, y.z * inv, y.w * inv};
+    store4(static_cast<T*>(a.o) + tok * a.o_stride + (int64_t)head * D + 4 * quad, z);
+    if (tid == 0 && a.lse)
+      a.lse[tok * (a.hkv * a.group) + head] = L == 0.f ? -GDN_INF : (M + log2f(L)) * kLn2;
+  }
+}
+
+size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+constexpr int max_tiles(int d) { return d == 256 ? 2 : 4; }  // row tiles of 8, by registers
+
+template <typename T, int D, int NT>
+int launch(const AttnArgs& a, const gdn_kv_cache& c, int num_sms, cudaStream_t stream) {
+  constexpr int RB = 8 * NT;
+  constexpr int kTerms = std::is_same<T, float>::value ? 2 : 1;
+  SplitParams p;
+  p.a = a;
+  const int box = std::min(c.page_size, kTile);
+  if (!make_cache_map(&p.tk, c.k, c, box) || !make_cache_map(&p.tv, c.v, c, box))
+    return (int)cudaErrorInvalidValue;
+  // one block per SM slot, no more than there can be items
+  const int64_t units = ((int64_t)a.num_tokens * a.group + RB - 1) / RB + a.num_seqs;
+  const int64_t items = units * a.hkv * std::max(1, (a.max_kv_len + kTile - 1) / kTile);
+  const int workers = (int)std::min<int64_t>((int64_t)kCtasPerSm * num_sms, items);
+  p.desc = reinterpret_cast<SplitDesc*>(a.partials);
+  p.part = a.partials + align_up(sizeof(SplitDesc) * kCtasPerSm * kMaxSms, 256) / sizeof(float);
+  const size_t q = (size_t)kTerms * NT * D * 16, red = sizeof(float) * RB * (D + 8);
+  const size_t fixed = q + red + align_up(sizeof(int32_t) * (a.num_seqs + 1), 16) + 1024 +
+                       sizeof(SmemHead<NT>);
+  const size_t stage = 2 * (size_t)kTile * D;
+  p.stages = (int)std::min<size_t>(kMaxStages, std::max<size_t>(2, (kSmemPerCta - fixed) / stage));
+  p.off_q = (uint32_t)(p.stages * stage);
+  p.off_red = p.off_q + (uint32_t)q;
+  p.off_pre = p.off_red + (uint32_t)red;
+  const size_t smem = p.off_pre + sizeof(int32_t) * (a.num_seqs + 1) + 1024;
+  static std::atomic<int> ready[kMaxDevices];
+  int e = configure_once(ready, [] {
+    return (int)cudaFuncSetAttribute(split_kernel<T, D, NT>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+  });
+  if (e != 0) return e;
+  split_kernel<T, D, NT><<<workers, kThreads, smem, stream>>>(p);
+  if ((e = (int)cudaGetLastError()) != 0 || workers == 1) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(workers, RB);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];  // its launch overlaps the first kernel's end
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return (int)cudaLaunchKernelEx(&cfg, join_kernel<T, D, RB>, a, (const SplitDesc*)p.desc,
+                                 (const float*)p.part);
+}
+
+}  // namespace
+
+size_t split_workspace(const gdn_attn_config& cfg, const gdn_kv_cache& c) {
+  const size_t workers = (size_t)kCtasPerSm * kMaxSms;
+  return align_up(sizeof(SplitDesc) * workers, 256) +
+         2 * workers * 8 * max_tiles(c.head_dim) * (c.head_dim + 2) * sizeof(float);
+}
+
+int launch_attn_split(const AttnArgs& a, const gdn_kv_cache& c, bool bf16, int num_sms,
+                      void* stream) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int64_t rows = (int64_t)std::min(a.max_q_len, a.split_q) * a.group;
+  auto tiles = [&](auto type, auto dim) {
+    using T = decltype(type);
+    constexpr int D = decltype(dim)::value;
+    if (rows <= 8) return launch<T, D, 1>(a, c, num_sms, s);
+    if constexpr (D == 256) return launch<T, D, 2>(a, c, num_sms, s);
+    else return rows <= 16 ? launch<T, D, 2>(a, c, num_sms, s) : launch<T, D, 4>(a, c, num_sms, s);
+  };
+  auto dims = [&](auto type) {
+    if (c.head_dim == 64) return tiles(type, std::integral_constant<int, 64>());
+    if (c.head_dim == 128) return tiles(type, std::integral_constant<int, 128>());
+    return tiles(type, std::integral_constant<int, 256>());
+  };
+  return bf16 ? dims(__nv_bfloat16()) : dims(float());
+}
+
+}  // namespace gdn

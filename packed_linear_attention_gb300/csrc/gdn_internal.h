@@ -213,6 +213,9 @@ gdn_status plan_prefill(const gdn_handle* h, const gdn_config* cfg, int32_t num_
 void write_worklist(void* dst, const PrefillPlan& plan, const gdn_config* cfg, int32_t num_seqs,
                     const int32_t* cu, const int32_t* ckpt_cu, const int32_t* ckpt_pos);
 
+// The CUDA device a handle is bound to (gdn_api.cu).
+int handle_device(const gdn_handle* h);
+
 // Row block of a unit for each kernel family.
 constexpr int kRecurrentRows = 32;
 constexpr bool kChunkedReady = true;

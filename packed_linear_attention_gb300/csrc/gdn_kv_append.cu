@@ -1,0 +1,438 @@
+// gdn_kv_append.cu — rotary embedding with several position axes, and the append that
+// quantises keys and values into the paged e4m3 cache.
+//
+// Rotation. Pair i turns by position * f_i, f_i in turns per position held as a 64-bit binary
+// fraction: the low 64 bits of the integer product position * F_i are the angle modulo a turn,
+// with no range reduction and no rounding that grows with the position; its top 32 bits give
+// the angle to 2^-32 of a turn, and sincospif does the rest. Both kernels are bound by HBM
+// (every element is read and written once); a thread of the rotation takes the same pairs of
+// several heads of a token, so that the sine and cosine are formed once for them.
+//
+// Append. A unit is a run of rows that land in one page, for one head: keys by one half of a
+// block's 512 threads and values by the other, eight elements a thread, so the run is read
+// once, held in registers (rotated, fp32) while its largest magnitude is found, and stored as
+// codes. With power-of-two scales the division is exact, and a later, larger scale only moves
+// the exponents of the codes that are already there. No unit list is needed: a row begins a
+// run when its slot opens a page or does not follow the previous row's slot.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "gdn_attn_internal.h"
+
+namespace gdn {
+namespace {
+
+constexpr int kRopeThreads = 256;
+constexpr int kHalf = 256;               // threads for the keys, and as many for the values
+constexpr int kAppendThreads = 2 * kHalf;
+constexpr int kBatch = 8;                // rows of a thread held in registers
+constexpr int kMinExp = -100;            // exponent of the smallest scale
+
+struct RopeDev {  // gdn_rope without what the kernels do not need
+  uint64_t turns[GDN_ROPE_MAX_PAIRS];
+  uint8_t axis[GDN_ROPE_MAX_PAIRS];
+  int32_t head_dim, rotary_dim, adjacent;
+};
+
+// Eight consecutive elements of a tensor, as loaded.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 w;
+  __device__ void load(const __nv_bfloat16* p) { w = *reinterpret_cast<const uint4*>(p); }
+  __device__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = w; }
+  __device__ void get(float (&x)[8]) const {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(u[i] << 16);
+      x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    }
+  }
+  __device__ void set(const float (&x)[8]) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      u[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    w = make_uint4(u[0], u[1], u[2], u[3]);
+  }
+};
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ void store(float* p) const {
+    reinterpret_cast<float4*>(p)[0] = a;
+    reinterpret_cast<float4*>(p)[1] = b;
+  }
+  __device__ void get(float (&x)[8]) const {
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  }
+  __device__ void set(const float (&x)[8]) {
+    a = make_float4(x[0], x[1], x[2], x[3]);
+    b = make_float4(x[4], x[5], x[6], x[7]);
+  }
+};
+
+// cos and sin of pair i at a token whose positions start at `pos` (one row per axis).
+__device__ __forceinline__ void pair_angle(const RopeDev& r, int i, const int32_t* pos,
+                                           int64_t pos_stride, float& c, float& s) {
+  const int64_t at = __ldg(pos + r.axis[i] * pos_stride);
+  const uint64_t turn = (uint64_t)at * r.turns[i];
+  // half turns in [-1, 1)
+  sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &s, &c);
+}
+
+// One thread: 16 elements of every head of a token in [head0, head1), the heads of x[0]
+// followed by those of x[1]. Item i < R/16 are the pairs 8i..8i+7 (elements 8i.. and
+// R/2 + 8i.. in the halves layout, 16i.. in the adjacent one), the later items copy.
+template <typename T>
+__device__ __forceinline__ void rope_heads(const RopeDev& r, const RopeArgs& a, int64_t token,
+                                           int item, int head0, int head1) {
+  const int D = r.head_dim, R = r.rotary_dim;
+  const bool turn = 16 * item < R;
+  const int lo = turn && !r.adjacent ? 8 * item : 16 * item;
+  const int hi = turn && !r.adjacent ? lo + R / 2 : lo + 8;
+  float c[8], s[8];
+  if (turn) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      pair_angle(r, 8 * item + e, a.positions + token, a.pos_stride, c[e], s[e]);
+  }
+#pragma unroll 4
+  for (int h = head0; h < head1; ++h) {
+    const bool second = h >= a.x[0].heads;
+    const RopeHeads& x = second ? a.x[1] : a.x[0];
+    const int hh = second ? h - a.x[0].heads : h;
+    const T* in = static_cast<const T*>(x.in) + token * x.in_stride + (int64_t)hh * D;
+    T* out = static_cast<T*>(x.out) + token * x.out_stride + (int64_t)hh * D;
+    if (!turn && in == out) continue;  // in place: nothing to copy
+    Raw8<T> u, v;
+    // plain loads: in place, another item's store may follow, but never to these elements
+    u.load(in + lo);
+    v.load(in + hi);
+    if (turn) {
+      float p[8], q[8];
+      u.get(p);
+      v.get(q);
+      if (r.adjacent) {  // (p0 p1) (p2 p3) ... then q's pairs
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x0 = p[2 * e], y0 = p[2 * e + 1], x1 = q[2 * e], y1 = q[2 * e + 1];
+          p[2 * e] = x0 * c[e] - y0 * s[e];
+          p[2 * e + 1] = y0 * c[e] + x0 * s[e];
+          q[2 * e] = x1 * c[4 + e] - y1 * s[4 + e];
+          q[2 * e + 1] = y1 * c[4 + e] + x1 * s[4 + e];
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float x0 = p[e], y0 = q[e];
+          p[e] = x0 * c[e] - y0 * s[e];
+          q[e] = y0 * c[e] + x0 * s[e];
+        }
+      }
+      u.set(p);
+      v.set(q);
+    }
+    u.store(out + lo);
+    v.store(out + hi);
+  }
+}
+
+// Block `block` of a rotation over num_tokens tokens, `slices` slices of the heads.
+template <typename T>
+__device__ __forceinline__ void rope_block(const RopeDev& r, const RopeArgs& a, int64_t block,
+                                           int slices, int threads, int tid) {
+  const int items = r.head_dim / 16, heads = a.x[0].heads + a.x[1].heads;
+  const int64_t g = block / slices * threads + tid;
+  const int64_t token = g / items;
+  if (token >= a.num_tokens) return;
+  const int slice = (int)(block % slices), per = (heads + slices - 1) / slices;
+  rope_heads<T>(r, a, token, (int)(g % items), slice * per, min(heads, (slice + 1) * per));
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kRopeThreads)
+rope_kernel(const __grid_constant__ RopeDev r, const __grid_constant__ RopeArgs a, int slices) {
+  rope_block<T>(r, a, blockIdx.x, slices, kRopeThreads, threadIdx.x);
+}
+
+// Two fp32 values as e4m3 codes (nearest even, NaN kept, larger magnitudes to 448).
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t code) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)code));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// Exponent of the least power of two s with amax <= 448 s = 1.75 * 2^8 s, amax finite >= 0.
+__device__ __forceinline__ int scale_exp(float amax) {
+  const uint32_t b = __float_as_uint(amax);
+  const int e = (int)(b >> 23) - 127 - 8 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return max(e, kMinExp);  // zeros and subnormals among them
+}
+__device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+struct AppendDev {
+  AppendArgs a;
+  int32_t rows_per_block;  // rows whose runs a block handles
+  int32_t append_blocks;   // the blocks after them rotate q
+  int32_t rope_slices;
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kAppendThreads)
+append_kernel(const __grid_constant__ AppendDev p, const __grid_constant__ RopeDev r) {
+  const AppendArgs& a = p.a;
+  const int tid = threadIdx.x;
+  if ((int)blockIdx.x >= p.append_blocks) {
+    rope_block<T>(r, a.rope_args, blockIdx.x - p.append_blocks, p.rope_slices, kAppendThreads, tid);
+    return;
+  }
+  constexpr int kVec = D / 8;              // threads of a row
+  constexpr int kRows = kHalf / kVec;      // rows of a pass
+  __shared__ int s_start[128];
+  __shared__ int s_nstart, s_n;
+  __shared__ uint32_t s_amax[2];
+  __shared__ uint32_t s_nan[4];            // rows of v that hold a NaN
+  const int P = a.cache.page_size, H = a.cache.num_kv_heads;
+  const int head = (int)(blockIdx.x % H);
+  const int64_t row0 = (int64_t)(blockIdx.x / H) * p.rows_per_block;
+  const int64_t nslots = (int64_t)a.cache.num_pages * P;
+  const bool is_v = tid >= kHalf;
+  const int lt = tid & (kHalf - 1), vec = lt % kVec, sub = lt / kVec;
+  const T* src = static_cast<const T*>(is_v ? a.v : a.k) + (int64_t)head * D;
+  const int64_t stride = is_v ? a.v_stride : a.k_stride;
+  const int R = a.rotate && !is_v ? r.rotary_dim : 0;
+  const bool rot = 8 * vec < R;
+  // the chunk's pairs and, in the halves layout, the chunk that holds their other elements
+  const int half = R / 2, pair0 = r.adjacent ? 4 * vec : (8 * vec < half ? 8 * vec : 8 * vec - half);
+  const int other = 8 * vec < half ? 8 * vec + half : 8 * vec - half;
+
+  if (tid == 0) s_nstart = 0;
+  __syncthreads();
+  if (tid < p.rows_per_block && row0 + tid < a.num_tokens) {
+    const int64_t row = row0 + tid, slot = a.slots[row];
+    if (slot >= nslots) {
+      raise_status(a.status, GDN_ERR_INVALID_ARGUMENT);
+    } else if (slot >= 0 && (row == 0 || slot % P == 0 || a.slots[row - 1] != slot - 1)) {
+      s_start[atomicAdd(&s_nstart, 1)] = tid;
+    }
+  }
+  __syncthreads();
+  const int nstart = s_nstart;
+  for (int u = 0; u < nstart; ++u) {  // in any order: the runs are independent
+    const int64_t row = row0 + s_start[u], slot = a.slots[row];
+    const int64_t page = slot / P;
+    const int off = (int)(slot % P);
+    if (tid == 0) s_n = P - off;
+    if (tid < 2) s_amax[tid] = 0;
+    if (tid < 4) s_nan[tid] = 0;
+    __syncthreads();
+    if (tid > 0 && tid < P - off &&
+        (row + tid >= a.num_tokens || a.slots[row + tid] != slot + tid))
+      atomicMin(&s_n, tid);
+    __syncthreads();
+    const int n = s_n;
+
+    // rows sub, sub + kRows, ...: the last kBatch passes stay in registers
+    auto fetch = [&](int i, float (&x)[8]) {
+      const T* at = src + (row + i) * stride;
+      Raw8<T> w;
+      w.load(at + 8 * vec);
+      w.get(x);
+      if (rot) {
+        const int32_t* pos = a.rope_args.positions + row + i;
+        float c, s;
+        if (r.adjacent) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            pair_angle(r, pair0 + e, pos, a.rope_args.pos_stride, c, s);
+            const float x0 = x[2 * e], y0 = x[2 * e + 1];
+            x[2 * e] = x0 * c - y0 * s;
+            x[2 * e + 1] = y0 * c + x0 * s;
+          }
+        } else {
+          Raw8<T> w2;
+          float y[8];
+          w2.load(at + other);
+          w2.get(y);
+          const bool low = 8 * vec < half;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            pair_angle(r, pair0 + e, pos, a.rope_args.pos_stride, c, s);
+            x[e] = low ? x[e] * c - y[e] * s : x[e] * c + y[e] * s;
+          }
+        }
+      }
+    };
+    const int passes = (n + kRows - 1) / kRows, batches = (passes + kBatch - 1) / kBatch;
+    float x[kBatch][8];
+    float amax = 0.f;
+    for (int b = 0; b < batches; ++b) {
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int i = (b * kBatch + j) * kRows + sub;
+        if (i < n) fetch(i, x[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int i = (b * kBatch + j) * kRows + sub;
+        if (i < n) {
+          bool nan = false;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float m = fabsf(x[j][e]);
+            nan = nan || m != m;
+            if (m < __int_as_float(0x7f800000)) amax = fmaxf(amax, m);
+          }
+          if (is_v && nan) atomicOr(&s_nan[i >> 5], 1u << (i & 31));
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    if ((tid & 31) == 0) atomicMax(&s_amax[is_v], __float_as_uint(amax));
+    __syncthreads();
+    float* sp = (is_v ? a.cache.v_scale : a.cache.k_scale) + page * H + head;
+    uint8_t* codes = static_cast<uint8_t*>(is_v ? a.cache.v : a.cache.k) +
+                     ((page * H + head) * P) * (int64_t)D;
+    const float need = exp2_int(scale_exp(__uint_as_float(s_amax[is_v])));
+    float scale = need;
+    if (off > 0) {
+      const float old = *sp;
+      scale = fmaxf(old, need);
+      if (scale > old) {  // the rows in front move to the larger scale
+        const float f = old / scale;
+        for (int i = sub; i < off; i += kRows) {
+          uint2* c = reinterpret_cast<uint2*>(codes + (int64_t)i * D + 8 * vec);
+          uint2 w = *c;
+          uint32_t z[4] = {w.x & 0xFFFFu, w.x >> 16, w.y & 0xFFFFu, w.y >> 16};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 y = from_e4m3x2(z[e]);
+            z[e] = e4m3x2(y.x * f, y.y * f);
+          }
+          *c = make_uint2(z[0] | z[1] << 16, z[2] | z[3] << 16);
+        }
+      }
+    }
+    const float inv = 1.f / scale;  // exact: a power of two (or the caller's own old scale)
+    auto put = [&](int i, const float (&x)[8]) {
+      float y[8];
+      const bool bad = (s_nan[i >> 5] >> (i & 31)) & 1u;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        y[e] = x[e] * inv;
+        if (is_v) y[e] = y[e] == y[e] ? y[e] : 0.f;
+        else if (bad) y[e] = __int_as_float(0x7fffffff);
+      }
+      *reinterpret_cast<uint2*>(codes + (int64_t)(off + i) * D + 8 * vec) =
+          make_uint2(e4m3x2(y[0], y[1]) | e4m3x2(y[2], y[3]) << 16,
+                     e4m3x2(y[4], y[5]) | e4m3x2(y[6], y[7]) << 16);
+    };
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = ((batches - 1) * kBatch + j) * kRows + sub;
+      if (i < n) put(i, x[j]);
+    }
+    for (int i = sub; i < (batches - 1) * kBatch * kRows; i += kRows) {
+      float y[8];
+      fetch(i, y);
+      put(i, y);
+    }
+    __syncthreads();  // every thread has read the old scale and the flags
+    if (lt == 0) *sp = scale;
+  }
+}
+
+RopeDev device_rope(const gdn_rope& rope) {
+  RopeDev r;
+  for (int i = 0; i < GDN_ROPE_MAX_PAIRS; ++i) {
+    r.turns[i] = rope.turns[i];
+    r.axis[i] = rope.axis[i];
+  }
+  r.head_dim = rope.head_dim;
+  r.rotary_dim = rope.rotary_dim;
+  r.adjacent = rope.pair_layout == GDN_ROPE_ADJACENT;
+  return r;
+}
+
+// Slices of the heads: one while the tokens alone fill the SMs, else up to one per head, so
+// that a decode step's few tokens still spread over the GPU.
+int rope_slices(int64_t threads, int heads) {
+  constexpr int64_t kFill = 152 * 1024;
+  int s = 1;
+  while (s < heads && threads * s < kFill) s *= 2;
+  return std::min(s, heads);
+}
+
+}  // namespace
+
+int launch_rope(const gdn_rope& rope, const RopeArgs& a, bool bf16, void* stream) {
+  const int heads = a.x[0].heads + a.x[1].heads;
+  if (a.num_tokens == 0 || heads == 0) return 0;
+  const int64_t threads = (int64_t)a.num_tokens * (rope.head_dim / 16);
+  const int slices = rope_slices(threads, heads);
+  const int64_t blocks = (threads + kRopeThreads - 1) / kRopeThreads * slices;
+  if (blocks > INT32_MAX) return (int)cudaErrorInvalidValue;
+  const RopeDev r = device_rope(rope);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (bf16) rope_kernel<__nv_bfloat16><<<(unsigned)blocks, kRopeThreads, 0, s>>>(r, a, slices);
+  else rope_kernel<float><<<(unsigned)blocks, kRopeThreads, 0, s>>>(r, a, slices);
+  return (int)cudaGetLastError();
+}
+
+int launch_kv_append(const gdn_rope* rope, const AppendArgs& a, bool bf16, void* stream) {
+  if (a.num_tokens == 0) return 0;
+  AppendDev p;
+  p.a = a;
+  const int H = a.cache.num_kv_heads;
+  // rows per block: a page's worth when that still fills the SMs, else fewer
+  int rows = a.cache.page_size;
+  while (rows > 1 && ((int64_t)a.num_tokens + rows - 1) / rows * H < 2 * 152) rows /= 2;
+  p.rows_per_block = rows;
+  const int64_t append = ((int64_t)a.num_tokens + rows - 1) / rows * H;
+  int64_t turn = 0;
+  p.rope_slices = 1;
+  RopeDev r = {};
+  if (rope) r = device_rope(*rope);
+  if (a.rotate && a.rope_args.x[0].heads > 0) {
+    const int64_t threads = (int64_t)a.num_tokens * (rope->head_dim / 16);
+    p.rope_slices = rope_slices(threads, a.rope_args.x[0].heads);
+    turn = (threads + kAppendThreads - 1) / kAppendThreads * p.rope_slices;
+  }
+  if (append + turn > INT32_MAX) return (int)cudaErrorInvalidValue;
+  p.append_blocks = (int32_t)append;
+  const unsigned blocks = (unsigned)(append + turn);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  auto run = [&](auto type, auto dim) {
+    using T = decltype(type);
+    append_kernel<T, decltype(dim)::value><<<blocks, kAppendThreads, 0, s>>>(p, r);
+  };
+  auto pick = [&](auto type) {
+    if (a.cache.head_dim == 64) run(type, std::integral_constant<int, 64>());
+    else if (a.cache.head_dim == 128) run(type, std::integral_constant<int, 128>());
+    else run(type, std::integral_constant<int, 256>());
+  };
+  if (bf16) pick(__nv_bfloat16());
+  else pick(float());
+  return (int)cudaGetLastError();
+}
+
+}  // namespace gdn

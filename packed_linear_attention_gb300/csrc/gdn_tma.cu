@@ -12,6 +12,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "gdn_attn_internal.h"
 #include "gdn_internal.h"
 
 namespace gdn {
@@ -47,6 +48,21 @@ bool make_bf16_map(CUtensorMap* m, const void* base, uint64_t cols, uint64_t row
   const cuuint32_t estr[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
+bool make_cache_map(CUtensorMap* m, const void* base, const gdn_kv_cache& c, int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)c.head_dim,
+                              (cuuint64_t)c.num_pages * c.num_kv_heads * c.page_size};
+  const cuuint64_t strides[1] = {(cuuint64_t)c.head_dim};
+  const cuuint32_t box[2] = {(cuuint32_t)std::min(c.head_dim, 128), (cuuint32_t)box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            c.head_dim == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
          CUDA_SUCCESS;
 }
@@ -181,6 +197,8 @@ namespace {
 // store the same value.
 std::atomic<int> g_sms[64];
 
+}  // namespace
+
 int device_sms(int* out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -194,8 +212,6 @@ int device_sms(int* out) {
   *out = n;
   return 0;
 }
-
-}  // namespace
 
 int launch_chunked_prefill(const PrefillArgs& a, int64_t total_tokens, int schedule,
                            const ChunkLoad& load, void* stream) {

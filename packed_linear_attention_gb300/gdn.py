@@ -34,6 +34,11 @@ KERNEL_AUTO = 0
 KERNEL_RECURRENT = 1
 KERNEL_CHUNKED_PIPELINED = 2
 KERNEL_CHUNKED_THROUGHPUT = 3
+GDN_ROPE_SECTIONS = 0
+GDN_ROPE_INTERLEAVED = 1
+GDN_ROPE_HALVES = 0
+GDN_ROPE_ADJACENT = 1
+GDN_ROPE_MAX_PAIRS = 128
 
 # every symbol include/gdn.h declares
 EXPORTS = (
@@ -48,7 +53,8 @@ EXPORTS = (
     "gdn_chunked_schedule", "gdn_set_test_hook", "gdn_prefill_packed_pool",
     "gdn_prefill_launch_count", "gdn_prefill_packed_snapshot", "gdn_checkpoint_copy_event",
     "gdn_checkpoint_copy_join", "gdn_noalloc_read_status", "gdn_noalloc_set_test_hook",
-    "gdn_split_segment_auto",
+    "gdn_split_segment_auto", "gdn_kv_plan", "gdn_kv_release", "gdn_rope_init",
+    "gdn_rope_apply", "gdn_kv_append", "gdn_attn_workspace_size", "gdn_attn_paged",
 )
 
 
@@ -73,6 +79,25 @@ class gdn_config(ctypes.Structure):
                 ("dt_bias", ctypes.c_void_p)]
 
 
+class gdn_kv_cache(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class gdn_rope(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+                ("num_axes", ctypes.c_int32), ("pair_layout", ctypes.c_int32),
+                ("turns", ctypes.c_uint64 * GDN_ROPE_MAX_PAIRS),
+                ("axis", ctypes.c_uint8 * GDN_ROPE_MAX_PAIRS)]
+
+
+class gdn_attn_config(ctypes.Structure):
+    _fields_ = [("num_q_heads", ctypes.c_int32), ("causal", ctypes.c_int32),
+                ("io_dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -90,6 +115,9 @@ def load(path: str = LIB_PATH):
         P, I32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
         CFG = ctypes.POINTER(gdn_config)
         IP = ctypes.POINTER(ctypes.c_int32)
+        I64 = ctypes.c_int64
+        CACHE, ROPE = ctypes.POINTER(gdn_kv_cache), ctypes.POINTER(gdn_rope)
+        ACFG = ctypes.POINTER(gdn_attn_config)
         sig = {
             "gdn_abi_version": (I32, []),
             "gdn_status_string": (ctypes.c_char_p, [I32]),
@@ -138,6 +166,19 @@ def load(path: str = LIB_PATH):
             "gdn_decode_step": (I32, [P, CFG, I32, P, P, P, P, P, P, I32, P, P, P]),
             "gdn_ckpt_position": (I32, [I32, I32, I32]),
             "gdn_mixed_budget": (I32, [I32, IP, I32, I32, IP]),
+            "gdn_kv_plan": (I32, [P, I32, I32, I32, P, P, P, I32, I32, P, P, P, P, P, P, P, P,
+                                  P]),
+            "gdn_kv_release": (I32, [P, I32, I32, P, P, P, I32, I32, P, P, P, P]),
+            "gdn_rope_init": (I32, [ctypes.POINTER(gdn_rope), I32, I32, I32, IP, I32, I32,
+                                    ctypes.c_double, ctypes.POINTER(ctypes.c_double)]),
+            "gdn_rope_apply": (I32, [P, ROPE, I32, I32, P, I64, P, I64, I32, P, I64, P, I64, I32,
+                                     P, I64, P]),
+            "gdn_kv_append": (I32, [P, CACHE, I32, I32, P, P, I64, P, I64, ROPE, P, I64, P, I64,
+                                    I32, P, I64, P, P]),
+            "gdn_attn_workspace_size": (I32, [ACFG, CACHE, I32, I32, I32, I32,
+                                              ctypes.POINTER(SZ)]),
+            "gdn_attn_paged": (I32, [P, ACFG, CACHE, I32, I32, I32, I32, P, P, P, I32, P, I64, P,
+                                     I64, P, P, SZ, P, P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -537,6 +578,126 @@ def gdn_mixed_budget(remaining, budget: int, max_prompts: int) -> tuple[int, lis
     if served < 0:
         raise GdnError(GDN_ERR_INVALID_ARGUMENT, "gdn_mixed_budget")
     return int(served), [int(take[i]) for i in range(rem.size)]
+
+
+# ---- full-attention layers: paged 8-bit key/value cache -----------------------------------
+
+def make_kv_cache(k, v, k_scale, v_scale) -> gdn_kv_cache:
+    """The record of a cache held in tensors: k and v [pages][kv heads][page size][head dim]
+    (float8_e4m3fn or uint8), scales [pages][kv heads] fp32. The tensors must be contiguous
+    and outlive every call using the record."""
+    pages, heads, page, dim = k.shape
+    if v.shape != k.shape or tuple(k_scale.shape) != (pages, heads) or \
+            tuple(v_scale.shape) != (pages, heads):
+        raise GdnError(GDN_ERR_INVALID_ARGUMENT, "make_kv_cache: shapes")
+    if not all(x.is_contiguous() for x in (k, v, k_scale, v_scale)) or \
+            k.element_size() != 1 or v.element_size() != 1 or \
+            k_scale.element_size() != 4 or v_scale.element_size() != 4:
+        raise GdnError(GDN_ERR_INVALID_ARGUMENT, "make_kv_cache: layout")
+    return gdn_kv_cache(pages, page, heads, dim, _addr(k), _addr(v), _addr(k_scale),
+                        _addr(v_scale))
+
+
+def make_attn_config(num_q_heads, *, scale, causal=True, io_dtype=GDN_BF16) -> gdn_attn_config:
+    return gdn_attn_config(int(num_q_heads), 1 if causal else 0, int(io_dtype), float(scale))
+
+
+def _ref(record):
+    return None if record is None else ctypes.byref(record)
+
+
+def gdn_kv_plan(handle, page_size, num_seqs, num_tokens, ctx_len, new_len, block_table,
+                max_blocks, num_pages, free_pages, free_count, free_count_out, cu_new, kv_len,
+                positions, slots, status=None, stream=None, *, raise_on_error=True) -> int:
+    """Pages, slots and positions of one step's tokens from the requests' lengths, on the GPU."""
+    st = load().gdn_kv_plan(
+        handle, page_size, num_seqs, num_tokens, _addr(ctx_len), _addr(new_len),
+        _addr(block_table), max_blocks, num_pages, _addr(free_pages), _addr(free_count),
+        _addr(free_count_out), _addr(cu_new), _addr(kv_len), _addr(positions), _addr(slots),
+        _addr(status), _stream(stream))
+    if raise_on_error:
+        _check(st, "gdn_kv_plan")
+    return st
+
+
+def gdn_kv_release(handle, page_size, num_seqs, kv_len, release, block_table, max_blocks,
+                   num_pages, free_pages, free_count, status=None, stream=None, *,
+                   raise_on_error=True) -> int:
+    """Give the pages of the requests with release[b] != 0 back to the free stack."""
+    st = load().gdn_kv_release(
+        handle, page_size, num_seqs, _addr(kv_len), _addr(release), _addr(block_table),
+        max_blocks, num_pages, _addr(free_pages), _addr(free_count), _addr(status),
+        _stream(stream))
+    if raise_on_error:
+        _check(st, "gdn_kv_release")
+    return st
+
+
+def gdn_rope_init(head_dim, rotary_dim, sections, axis_layout=GDN_ROPE_SECTIONS,
+                  pair_layout=GDN_ROPE_HALVES, theta=10000.0, inv_freq=None) -> gdn_rope:
+    """A rotary embedding; `sections` are the pairs of each axis, `inv_freq` (host, rotary_dim/2
+    doubles) replaces theta^(-2i/rotary_dim)."""
+    rope = gdn_rope()
+    freq = None
+    if inv_freq is not None:
+        f = np.ascontiguousarray(inv_freq, dtype=np.float64)
+        if f.size != rotary_dim // 2:
+            raise GdnError(GDN_ERR_INVALID_ARGUMENT, "gdn_rope_init")
+        freq = (ctypes.c_double * f.size)(*f.tolist())
+    _check(load().gdn_rope_init(ctypes.byref(rope), int(head_dim), int(rotary_dim),
+                                len(sections), _i32(sections), int(axis_layout),
+                                int(pair_layout), float(theta), freq), "gdn_rope_init")
+    return rope
+
+
+def gdn_rope_apply(handle, rope, io_dtype, num_tokens, positions, pos_stride, q, q_stride,
+                   num_q_heads, q_out, q_out_stride, k, k_stride, num_k_heads, k_out,
+                   k_out_stride, stream=None, *, raise_on_error=True) -> int:
+    """Rotate the heads of q and k; strides in elements from token to token."""
+    st = load().gdn_rope_apply(
+        handle, _ref(rope), io_dtype, num_tokens, _addr(positions), pos_stride, _addr(q),
+        q_stride, num_q_heads, _addr(q_out), q_out_stride, _addr(k), k_stride, num_k_heads,
+        _addr(k_out), k_out_stride, _stream(stream))
+    if raise_on_error:
+        _check(st, "gdn_rope_apply")
+    return st
+
+
+def gdn_kv_append(handle, cache, io_dtype, num_tokens, slots, k, k_stride, v, v_stride,
+                  rope=None, positions=None, pos_stride=0, q=None, q_stride=0, num_q_heads=0,
+                  q_out=None, q_out_stride=0, status=None, stream=None, *,
+                  raise_on_error=True) -> int:
+    """Quantise a step's keys and values into the cache; with `rope`, k (and q into q_out) are
+    rotated on the way."""
+    st = load().gdn_kv_append(
+        handle, _ref(cache), io_dtype, num_tokens, _addr(slots), _addr(k), k_stride, _addr(v),
+        v_stride, _ref(rope), _addr(positions), pos_stride, _addr(q), q_stride, num_q_heads,
+        _addr(q_out), q_out_stride, _addr(status), _stream(stream))
+    if raise_on_error:
+        _check(st, "gdn_kv_append")
+    return st
+
+
+def gdn_attn_workspace_size(cfg: gdn_attn_config, cache: gdn_kv_cache, num_seqs, num_tokens,
+                            max_q_len, max_kv_len) -> int:
+    n = ctypes.c_size_t()
+    _check(load().gdn_attn_workspace_size(ctypes.byref(cfg), ctypes.byref(cache), int(num_seqs),
+                                          int(num_tokens), int(max_q_len), int(max_kv_len),
+                                          ctypes.byref(n)), "gdn_attn_workspace_size")
+    return n.value
+
+
+def gdn_attn_paged(handle, cfg, cache, num_seqs, num_tokens, max_q_len, max_kv_len, cu_q,
+                   kv_len, block_table, max_blocks, q, q_stride, o, o_stride, lse, workspace,
+                   workspace_bytes, status=None, stream=None, *, raise_on_error=True) -> int:
+    """Attention of a pack of requests over the paged cache (decode, drafts and prompts)."""
+    st = load().gdn_attn_paged(
+        handle, _ref(cfg), _ref(cache), num_seqs, num_tokens, max_q_len, max_kv_len,
+        _addr(cu_q), _addr(kv_len), _addr(block_table), max_blocks, _addr(q), q_stride, _addr(o),
+        o_stride, _addr(lse), _addr(workspace), workspace_bytes, _addr(status), _stream(stream))
+    if raise_on_error:
+        _check(st, "gdn_attn_paged")
+    return st
 
 
 # ---- convenience: one prefill call on device tensors ---------------------------------------
