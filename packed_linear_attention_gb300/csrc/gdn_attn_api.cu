@@ -155,9 +155,10 @@ gdn_status gdn_kv_plan(gdn_handle* h, int32_t page_size, int32_t num_seqs, int32
                         (const void*)positions, (const void*)status})
     if (!aligned(p, 4)) return GDN_ERR_INVALID_ARGUMENT;
   if (!aligned(slots, 8)) return GDN_ERR_INVALID_ARGUMENT;
-  // outputs are written while other blocks still read the inputs
+  // outputs are written while other blocks still read the inputs (how many entries the free
+  // stack has is known on the device alone: its first one is looked at)
   const Span in[] = {span_of(ctx_len, 1, 0, num_seqs, 4), span_of(new_len, 1, 0, num_seqs, 4),
-                     span_of(free_pages, 1, 0, num_pages, 4), span_of(free_count, 1, 0, 1, 4)};
+                     span_of(free_pages, 1, 0, 1, 4), span_of(free_count, 1, 0, 1, 4)};
   const Span table = span_of(block_table, 1, 0, (int64_t)num_seqs * max_blocks, 4);
   const Span out[] = {table, span_of(cu_new, 1, 0, num_seqs + 1, 4),
                       span_of(kv_len, 1, 0, num_seqs, 4),
@@ -410,6 +411,8 @@ gdn_status gdn_attn_paged(gdn_handle* h, const gdn_attn_config* cfg, const gdn_k
   a.scale_log2 = cfg->scale * 1.4426950408889634f;
   a.status = status;
   a.partials = static_cast<float*>(workspace);
+  a.counter = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) +
+                                         gdn::attn_workspace(*cfg, *cache) - 256);
   return on_device(h, [&] { return gdn::launch_attn(a, *cache, cfg->io_dtype == GDN_BF16, stream); });
 }
 
@@ -419,7 +422,7 @@ namespace gdn {
 
 size_t attn_workspace(const gdn_attn_config& cfg, const gdn_kv_cache& c) {
   const size_t n = split_workspace(cfg, c);
-  return (n + 255) / 256 * 256;
+  return (n + 255) / 256 * 256 + 256;  // and the tile kernel's counter
 }
 
 int launch_attn(const AttnArgs& args, const gdn_kv_cache& c, bool bf16, void* stream) {
@@ -427,8 +430,12 @@ int launch_attn(const AttnArgs& args, const gdn_kv_cache& c, bool bf16, void* st
   int sms = 0;
   const int e = device_sms(&sms);
   if (e != 0) return e;
-  a.split_q = a.max_q_len;
-  return launch_attn_split(a, c, bf16, std::min(sms, kMaxSms), stream);
+  sms = std::min(sms, kMaxSms);
+  // fp32 queries need more than the tile kernel's operands hold
+  a.split_q = bf16 ? std::max(1, 64 / a.group) : a.max_q_len;
+  const int r = launch_attn_split(a, c, bf16, sms, stream);
+  if (r != 0 || a.max_q_len <= a.split_q) return r;
+  return launch_attn_tile(a, c, sms, stream);
 }
 
 }  // namespace gdn

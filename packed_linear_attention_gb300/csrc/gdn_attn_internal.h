@@ -74,9 +74,11 @@ struct AttnArgs {
   // to the tile kernel (gdn_attn_tile.cu).
   int32_t split_q;
   int32_t* status;
-  float* partials;             // workspace
+  float* partials;             // workspace of the split kernel
+  int32_t* counter;            // workspace of the tile kernel: units taken
 };
 constexpr int kSplitTile = 64;     // cached tokens of a work item of the split kernel
+constexpr int kTileRows = 128;     // query rows of a unit of the tile kernel
 
 constexpr int kMaxSms = 160;       // the workspace is sized without asking the device
 
@@ -86,6 +88,7 @@ int launch_attn(const AttnArgs& a, const gdn_kv_cache& c, bool bf16, void* strea
 size_t split_workspace(const gdn_attn_config& cfg, const gdn_kv_cache& c);
 int launch_attn_split(const AttnArgs& a, const gdn_kv_cache& c, bool bf16, int num_sms,
                       void* stream);
+int launch_attn_tile(const AttnArgs& a, const gdn_kv_cache& c, int num_sms, void* stream);
 // uint8 map over the cache's rows ([pages * heads * page_size] x head_dim) with boxes of
 // box_rows rows x 128 bytes (64 for head_dim 64), swizzled by as much (gdn_tma.cu).
 bool make_cache_map(CUtensorMap* m, const void* base, const gdn_kv_cache& c, int box_rows);

@@ -3,8 +3,9 @@
 //
 // Rotation. Pair i turns by position * f_i, f_i in turns per position held as a 64-bit binary
 // fraction: the low 64 bits of the integer product position * F_i are the angle modulo a turn,
-// with no range reduction and no rounding that grows with the position; its top 32 bits give
-// the angle to 2^-32 of a turn, and sincospif does the rest. Both kernels are bound by HBM
+// with no rounding that grows with the position. Its top bits, rounded, name the quarter turn;
+// the rest, at most an eighth of a turn, is one fp32 number, and the Taylor series of sine and
+// cosine to r^9 and r^10 leave less than 2^-28. Both kernels are bound by HBM
 // (every element is read and written once); a thread of the rotation takes the same pairs of
 // several heads of a token, so that the sine and cosine are formed once for them.
 //
@@ -89,8 +90,24 @@ __device__ __forceinline__ void pair_angle(const RopeDev& r, int i, const int32_
                                            int64_t pos_stride, float& c, float& s) {
   const int64_t at = __ldg(pos + r.axis[i] * pos_stride);
   const uint64_t turn = (uint64_t)at * r.turns[i];
-  // half turns in [-1, 1)
-  sincospif((float)(int32_t)(turn >> 32) * 4.656612873077393e-10f, &s, &c);
+  const uint32_t quarter = (uint32_t)((turn + (1ull << 61)) >> 62);
+  // the rest in 2^-34 turns, in [-2^31, 2^31], times 2 pi 2^-34
+  const float x = (float)(int32_t)((int64_t)(turn - ((uint64_t)quarter << 62)) >> 30) *
+                  (6.283185307179586f / 17179869184.f);
+  const float z = x * x;
+  float p = fmaf(z, 1.f / 362880, -1.f / 5040);
+  p = fmaf(z, p, 1.f / 120);
+  p = fmaf(z, p, -1.f / 6);
+  const float sn = fmaf(x * z, p, x);
+  float q = fmaf(z, -1.f / 3628800, 1.f / 40320);
+  q = fmaf(z, q, -1.f / 720);
+  q = fmaf(z, q, 1.f / 24);
+  q = fmaf(z, q, -0.5f);
+  const float cs = fmaf(z, q, 1.f);
+  c = quarter & 1 ? sn : cs;
+  s = quarter & 1 ? cs : sn;
+  if (quarter == 1 || quarter == 2) c = -c;
+  if (quarter & 2) s = -s;
 }
 
 // One thread: 16 elements of every head of a token in [head0, head1), the heads of x[0]

@@ -139,6 +139,22 @@ def test_prompts(hq, hkv, dim, io, page):
     Case(3, q, kv, hq, hkv, dim, page, io, gap=8).check(torch_cuda())
 
 
+@pytest.mark.parametrize("hq,hkv,dim,page", [(8, 1, 256, 64), (8, 1, 256, 16), (4, 2, 128, 128),
+                                             (3, 1, 128, 32), (2, 2, 64, 16), (7, 1, 64, 128)])
+def test_long_prompts(hq, hkv, dim, page):
+    """Prompts of several row and column tiles, behind prefixes that end inside a tile, beside
+    a decoding request and a draft."""
+    Case(20, [530, 1, 260, 3], [530, 700, 1413, 90], hq, hkv, dim, page, gap=8).check(torch_cuda())
+
+
+def test_many_prompts_of_one_pass():
+    """More units than blocks, of very different sizes."""
+    rng = np.random.default_rng(21)
+    q = rng.integers(1, 120, 90).tolist()
+    kv = [n + int(rng.integers(0, 400)) for n in q]
+    Case(21, q, kv, 8, 2, 64, 32).check(torch_cuda())
+
+
 @pytest.mark.parametrize("io", ["bf16", "f32"])
 def test_prompts_without_causal_mask(io):
     Case(4, [130, 40], [70, 333], 16, 2, 128, 32, io, causal=False).check(torch_cuda())
@@ -186,6 +202,18 @@ def test_result_does_not_depend_on_the_pack_or_the_stream():
     np.testing.assert_array_equal(lse, lse2)
     o3, _, _ = c.run(torch, lse=False)
     np.testing.assert_array_equal(o, o3)
+
+
+def test_a_query_with_an_infinity_or_nan_spoils_its_own_rows_only():
+    torch = torch_cuda()
+    for q, kv in (([3], [50]), ([200], [200])):
+        for bad in (np.inf, np.nan):
+            c = Case(16, q, kv, 8, 2, 128, 16)
+            c.q[1, 2, 5] = bad
+            o, lse, _ = c.run(torch)
+            assert np.isnan(o[1, 2]).all()
+            o[1, 2] = 0
+            assert np.isfinite(o).all()
 
 
 def test_a_nan_key_reaches_only_those_who_see_it():
