@@ -369,7 +369,9 @@ tile_kernel(const __grid_constant__ TileParams p) {
   } else if (warp == kIssuer) {
     // ---- MMA issue
     constexpr uint32_t id_s = idesc_f16(kRows, BN, 0, 0), id_o = idesc_f16(kRows, D, 0, 1);
-    const uint32_t s0 = smem_u32(smem);
+    const uint64_t q_desc = f8_desc<D>(smem_u32(smem) + Sh::OFF_Q);
+    const uint64_t h_desc = smem_desc_sw128(smem_u32(smem) + Sh::OFF_H, BN * 128, 1024);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tbase, 0), el = elect_lane();
     uint32_t g = 0, units = 0, nq = 0;
     Unit u;
     while (next_unit(u)) {
@@ -380,49 +382,51 @@ tile_kernel(const __grid_constant__ TileParams p) {
         const int st = j % Sh::SK;
         ok = ok && wait_or_die(&sm.kfull[st], (j / Sh::SK) & 1u, sm, a.status);
         tc_fence_after();
-        if (ok && lane == 0) {
-          const uint32_t q0 = s0 + Sh::OFF_Q, k0 = s0 + Sh::OFF_K + st * Sh::kTileBytes;
-          const uint32_t d = tbase + Sh::TM_S + (j & 1u) * BN;
+        if (ok) {
+          const uint64_t kd = q_desc + (Sh::OFF_K + st * Sh::kTileBytes) / 16;
+          const uint32_t d = tm + Sh::TM_S + (j & 1u) * BN;
 #pragma unroll
           for (int term = 0; term < 2; ++term)
 #pragma unroll
             for (int k = 0; k < D / 32; ++k)
-              mma_f8_ss(d, f8_desc<D>(q0 + term * Sh::kQBytes + (k >> 2) * (kRows * 128) + (k & 3) * 32),
-                        f8_desc<D>(k0 + (k >> 2) * (BN * 128) + (k & 3) * 32), id_s, term + k > 0);
-          mma_commit(&sm.kempty[st]);
-          mma_commit(&sm.sfull[j & 1u]);
-          if (last) mma_commit(&sm.qempty);
+              warp_mma_f8_ss(
+                  el, d, q_desc + (term * Sh::kQBytes + (k >> 2) * (kRows * 128) + (k & 3) * 32) / 16,
+                  kd + ((k >> 2) * (BN * 128) + (k & 3) * 32) / 16, id_s, term + k > 0);
+          if (el) {
+            mma_commit(&sm.kempty[st]);
+            mma_commit(&sm.sfull[j & 1u]);
+            if (last) mma_commit(&sm.qempty);
+          }
         }
         __syncwarp();
       };
-      issue_s(g, u.tiles == 1);
-      if (u.tiles > 1) issue_s(g + 1, u.tiles == 2);
-      for (int32_t i = 0; i < u.tiles && ok; ++i, ++g) {
+      const int32_t tiles = __shfl_sync(0xffffffffu, u.tiles, 0);
+      issue_s(g, tiles == 1);
+      if (tiles > 1) issue_s(g + 1, tiles == 2);
+      for (int32_t i = 0; i < tiles && ok; ++i, ++g) {
         const uint32_t b = g & 1u, ph = (g >> 1) & 1u;
         ok = wait_or_die(&sm.hfull[b], ph, sm, a.status) &&
              wait_or_die(&sm.pfull[b], ph, sm, a.status) &&
              (i > 0 || wait_or_die(&sm.ofree, (units & 1u) ^ 1u, sm, a.status));
         tc_fence_after();
-        if (ok && lane == 0) {
-          const uint32_t h0 = s0 + Sh::OFF_H + b * Sh::kHBytes;
-          const uint32_t pa = tbase + Sh::TM_P + b * (BN / 2);
+        if (ok) {
+          const uint64_t hd = h_desc + b * (Sh::kHBytes / 16);
+          const uint32_t pa = tm + Sh::TM_P + b * (BN / 2);
 #pragma unroll
           for (int k = 0; k < BN / 16; ++k)
-            mma_f16_ts(tbase + Sh::TM_O, pa + 8 * k,
-                       smem_desc_sw128(h0 + k * 2048, BN * 128, 1024), id_o, i > 0 || k > 0);
-          mma_commit(&sm.odone[b]);
+            warp_mma_f16_ts(el, tm + Sh::TM_O, pa + 8 * k, hd + k * (2048 / 16), id_o,
+                            i > 0 || k > 0);
+          if (el) mma_commit(&sm.odone[b]);
         }
         __syncwarp();
-        if (i + 2 < u.tiles) issue_s(g + 2, i + 3 == u.tiles);
+        if (i + 2 < tiles) issue_s(g + 2, i + 3 == tiles);
       }
       ++units;
       if (!ok) break;
     }
     // what was issued has completed before the block's memory goes
-    if (lane == 0) {
-      mma_commit(&sm.drain);
-      mbar_wait_bounded(&sm.drain, 0, kWaitLimit);
-    }
+    if (el) mma_commit(&sm.drain);
+    mbar_wait_bounded(&sm.drain, 0, kWaitLimit);
   } else if (warp >= kSoftWarps) {
     // ---- operands: Q of the unit, then its V tiles
     const int aw = warp - kSoftWarps, at = tid - kSoftThreads;

@@ -310,14 +310,41 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
       : "memory");
 }
 
-// 8-bit operands (e4m3 x e4m3, K = 32): the instruction descriptor has idesc_f16's fields,
-// with format 0 = e4m3; a 32-byte step along K is 32 elements.
-__device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                          uint32_t idesc, uint32_t accumulate) {
+// ---- MMA issued by a whole converged warp --------------------------------------------------
+// One lane issues (elect_lane(), asked once), but every lane of the warp executes the wrapper
+// with the same values, so that descriptors stay in uniform registers. Under a branch on one
+// lane the compiler has to move them there one by one: measured 126 to 187 clocks an MMA,
+// against the 32 to 128 that the tensor pipe takes.
+
+// 1 in one lane of the (converged) warp.
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n"
+               : "=r"(r));
+  return r;
+}
+
+// kind::f16 with A in tensor memory.
+__device__ __forceinline__ void warp_mma_f16_ts(uint32_t elected, uint32_t d_tmem,
+                                                uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                                uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected)
+      : "memory");
+}
+
+// 8-bit operands (e4m3 x e4m3, K = 32): the instruction descriptor has idesc_f16's fields,
+// with format 0 = e4m3; a 32-byte step along K is 32 elements, and in tensor memory a column
+// holds four of them.
+__device__ __forceinline__ void warp_mma_f8_ss(uint32_t elected, uint32_t d_tmem, uint64_t a_desc,
+                                               uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected)
       : "memory");
 }
 
