@@ -3,25 +3,33 @@
 //
 // A unit is (request, key/value head, 128 query rows), the rows of a head group's queries one
 // after another (row = query * group + head), so that a key/value tile serves every query head
-// of its group. Per tile of BN cached tokens (64 for heads of 256, else 128):
+// of its group. Per tile of BN = 64 cached tokens:
 //   S (128 x BN)  = Q K^T                        running maximum m and sum l per row
 //   O (128 x D)  += P V,  P = 2^(S - m)
 //
 // Operands. K enters as it lies in the cache: e4m3 tiles come by TMA into the swizzled layout
-// that kind::f8f6f4 reads, and Q is split into two e4m3 terms, q 2^k = hi + lo (hi to four
+// that kind::f8f6f4 reads. Q stays in tensor memory for the whole unit and is split into two e4m3 terms, q 2^k = hi + lo (hi to four
 // significant bits, lo the rest; the row's power of two brings its largest value to [128,
 // 256)): a bf16 value has eight bits, so the two terms are exact down to 2^-10 of the row's
 // largest value and off by at most 2^-18 of it below. Two e4m3 products cost what one f16
 // product costs, and no K tile is converted. Such a split of P would lose the small
 // probabilities of a long context, so P is f16 (from registers to TMEM, as the A operand) and
-// V is widened to f16 in shared memory (exact).
+// V is widened to f16 on its way from the cache to shared memory (exact). Shared memory is what
+// a tile would be bound by otherwise: with Q and a staged e4m3 V read from it, a tile of 64
+// tokens at D = 256 moved 208 KB through 128 bytes a clock against 1,024 clocks of products;
+// this way it moves 112 KB.
 // The maximum is raised only when a score passes it by 2^8 (see gdn_attn_split.cu); value
 // scales enter P as ratios to the largest that the unit has met.
 //
-// Block: 18 warps. 0-7 softmax (a row is shared by two threads, one for each half of the tile's
-// columns) and epilogue; 8-15 Q and V operands; 16 the TMA producer and unit scheduler; 17 the
-// MMA issuer. S is double buffered: S(i + 1) runs under the softmax of tile i, P V(i) under
-// that of tile i + 1. Units come from a counter, heaviest rows of a request first.
+// Block: 20 warps. 0-3 and 4-7 softmax, tile by tile in turns, a row to a thread: the latency
+// of a tile (tensor memory loads, 64 exponentials, the store of P) is then two tiles long. Only
+// the running maximum passes from one group to the other, warp by warp, through shared memory
+// and a pair of named barriers. 8-15 operands: V tiles, and the next unit's Q, whose bf16 rows
+// a bulk copy brings to shared memory while this unit runs and which moves to tensor memory
+// when its last S is done; 16 the producer (units, K tiles, Q rows); 17 the MMA issuer; two
+// idle (register shares move by whole groups of four warps). S is free again as soon as a
+// group holds it in registers, so S is issued two tiles ahead of P V. Units come from a
+// counter, heaviest rows of a request first.
 // Every wait is bounded; after one gave up the block's warps leave at their unit's end.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -43,24 +51,26 @@ using namespace ptx;
 constexpr int kRows = kTileRows;          // query rows of a unit (the MMA's M)
 constexpr int kSoftWarps = 8, kAuxWarps = 8;
 constexpr int kProducer = kSoftWarps + kAuxWarps, kIssuer = kProducer + 1;
-constexpr int kWarps = kIssuer + 1, kThreads = 32 * kWarps;
+constexpr int kWarps = 20, kThreads = 32 * kWarps;
+// Registers of a thread: 640 threads are launched with 96; the softmax warps take what the
+// others give (256 * 120 + 256 * 88 + 128 * 64 = 640 * 96).
+constexpr int kSoftRegs = 120, kAuxRegs = 88, kMiscRegs = 64;
+static_assert(256 * kSoftRegs + 256 * kAuxRegs + 128 * kMiscRegs == kThreads * 96, "registers");
 constexpr int kSoftThreads = 32 * kSoftWarps, kAuxThreads = 32 * kAuxWarps;
-constexpr int kMeta = 8;                  // ring of tile scales
+constexpr int kMeta = 16;                 // ring of tile scales: K stages and three more
 constexpr int kCoarse = kMaxSeqs / 32;    // prefix sums are kept for every 32 requests
 constexpr uint32_t kWaitLimit = 1u << 24;
 constexpr float kLazyMax = 8.f;
 constexpr float kProbScale = 128.f;
+constexpr float kMinRatio = 9.094947e-13f;  // 2^-40: value scales below that of vref count as it
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kSoftBar = 2;               // named barrier of the softmax warps
+constexpr int kSoftBar = 2, kAuxBar = 3;  // named barriers of the softmax and operand warps
+constexpr int kPairBar = 4;               // 4-11: a pair of softmax warps, either direction
+constexpr int BN = 64;                    // cached tokens of a tile
+constexpr int kGroups = BN / 16;
 
 #define GDN_INF __int_as_float(0x7f800000)
 
-// Byte offset of 16-byte chunk `chunk` of row `row` in an e4m3 operand tile of `rows` rows.
-template <int D>
-__device__ __forceinline__ uint32_t f8_offset(int row, int chunk, int rows) {
-  if constexpr (D == 64) return row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
-  else return (chunk >> 3) * (rows * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
-}
 template <int D>
 __device__ __forceinline__ uint64_t f8_desc(uint32_t addr) {
   return D == 64 ? smem_desc_sw64(addr, 16, 512) : smem_desc_sw128(addr, 16, 1024);
@@ -72,24 +82,31 @@ struct Unit {
   int32_t tiles, pad;
 };
 
-template <int G>
 struct TileMeta {
-  float ks[G];    // key scale of each 16-token group; negative: its page is absent
-  float vr[G];    // value scale / vref * kProbScale
-  float vref;     // largest value scale of the unit so far
-  float vfac;     // what the accumulator is multiplied by as vref grew
+  float ks[kGroups];    // key scale of each 16-token group
+  float lv[kGroups];    // log2 of what P is weighted with: value scale / vref * kProbScale
+  int32_t id[kGroups];  // page; negative: absent, or past the cached tokens
+  uint32_t absent;      // bit g: group g is absent
+  float vref;           // largest value scale of the unit so far
+  float vfac;           // what the accumulator is multiplied by as vref grew
 };
 
-template <int G>
+constexpr int kMaxStages = 8;
+// P V products are counted on a ring of four barriers: a softmax group that waits for the
+// product of tile j - 1 knows that of tile j - 4 done, so no phase can be taken for another.
+constexpr int kDone = 4;
 struct Smem {
-  uint64_t kfull[4], kempty[4], vfull[4], vempty[4];
-  uint64_t sfull[2], pfull[2], odone[2], hfull[2];
-  uint64_t qfull, qempty, ofree, drain;
+  uint64_t kfull[kMaxStages], kempty[kMaxStages];
+  uint64_t pfull[2], sfull[2], odone[kDone], hfull[4];
+  uint64_t sfree, qfull, qempty, ofree, drain, rawfull, rawempty;
   uint64_t mfull[kMeta];
   uint64_t ufull[2], uempty[2];
   Unit unit[2];
-  TileMeta<G> meta[kMeta];
-  float exchange[2][kRows];
+  TileMeta meta[kMeta];
+  float m[kRows];            // running maximum on its way between the softmax groups
+  float exchange_v[kRows];
+  float exchange_l[2][kRows];
+  uint16_t exchange_q[2][kRows];
   int8_t row_exp[2][kRows];  // power of two of a row of Q (two units' worth)
   int32_t coarse[kCoarse + 1];
   uint32_t tmem;
@@ -98,56 +115,74 @@ struct Smem {
 
 template <int D>
 struct Shape {
-  static constexpr int BN = D == 256 ? 64 : 128;
-  static constexpr int kGroups = BN / 16;
-  static constexpr int SK = 4;                                  // K stages
-  static constexpr int SV = D == 256 ? 2 : D == 128 ? 3 : 4;    // V stages (e4m3)
+  static constexpr int SK = D == 256 ? 5 : 8;                   // K stages
+  static constexpr int NH = D == 256 ? 2 : 4;                   // V tiles in f16
   static constexpr uint32_t kTileBytes = BN * D;                // one e4m3 tile
-  static constexpr uint32_t kQBytes = kRows * D;                // one term of Q
-  static constexpr uint32_t kHBytes = 2 * BN * D;               // a V tile in f16
-  static constexpr uint32_t OFF_Q = 0;
-  static constexpr uint32_t OFF_K = OFF_Q + 2 * kQBytes;
-  static constexpr uint32_t OFF_V = OFF_K + SK * kTileBytes;
-  static constexpr uint32_t OFF_H = OFF_V + SV * kTileBytes;
-  static constexpr uint32_t OFF_SM = OFF_H + 2 * kHBytes;
-  static constexpr uint32_t kSmem = OFF_SM + sizeof(Smem<kGroups>);
+  static constexpr uint32_t kHBytes = 2 * BN * D;
+  static constexpr uint32_t kRawPitch = 2 * D + 16;             // a bf16 row of Q: odd in 16 bytes
+  static constexpr uint32_t OFF_K = 0;
+  static constexpr uint32_t OFF_H = OFF_K + SK * kTileBytes;
+  static constexpr uint32_t OFF_RAW = OFF_H + NH * kHBytes;
+  static constexpr uint32_t OFF_SM = OFF_RAW + kRows * kRawPitch;
+  static constexpr uint32_t kSmem = OFF_SM + sizeof(Smem);
   static_assert(kSmem <= 227 * 1024, "shared memory of a block");
   static constexpr uint32_t kRowPitch = D == 64 ? 64 : 128;     // bytes of a row in a region
-  // TMEM columns: S twice, P twice (f16, two to a column), O
-  static constexpr uint32_t TM_S = 0, TM_P = 2 * BN, TM_O = D == 256 ? 256 : 384;
+  // TMEM columns: O, the two terms of Q (four elements a column), S, P twice (f16, two a column)
+  static constexpr uint32_t TM_O = 0, TM_Q = D, TM_S = D + D / 2, TM_P = TM_S + BN;
+  static_assert(TM_P + BN <= 512, "tensor memory");
 };
 
 struct TileParams {
   AttnArgs a;
-  CUtensorMap tk, tv;
+  CUtensorMap tk;
+  const void* v;      // the cache's values
   int32_t* counter;   // units taken
 };
 
-// A whole warp waits for a phase; one answer for the warp. After any wait of the block gave up,
-// none waits again.
-template <class S>
-__device__ __forceinline__ bool wait_or_die(uint64_t* bar, uint32_t parity, S& sm,
+// A whole warp waits for a phase; one answer for the warp. After any wait of the block gave up
+// (a second), none waits again. (The slow part is not a function of its own: a call in the
+// softmax loop would leave too few registers.)
+__device__ __forceinline__ bool wait_or_die(uint64_t* bar, uint32_t parity, Smem& sm,
                                             int32_t* status) {
   bool ok = mbar_try_wait(bar, parity);
-  if (!ok) {
+  if (!__all_sync(0xffffffffu, ok)) {
     volatile int32_t* dead = &sm.dead;
-    WaitClock clk;
-    for (uint32_t i = 0; !ok; ++i) {
-      if ((i & 15u) == 0u && *dead) break;
-      if (i >= kWaitLimit || clk.expired(i)) {
-        *dead = 1;
-        raise_status(status, GDN_ERR_DEVICE_TIMEOUT);
-        break;
-      }
+    const uint64_t t0 = global_ns();
+#pragma unroll 1
+    for (uint32_t i = 1; !ok; ++i) {
       ok = mbar_try_wait(bar, parity);
+      if ((i & 63u) == 0u && !ok) {
+        if (*dead) break;
+        if (global_ns() - t0 > kWaitNs) {
+          *dead = 1;
+          raise_status(status, GDN_ERR_DEVICE_TIMEOUT);
+        }
+      }
     }
+    ok = __all_sync(0xffffffffu, ok);
   }
-  return __all_sync(0xffffffffu, ok);
+  return ok;
 }
 
 __device__ __forceinline__ int32_t seq_units(const AttnArgs& a, const AttnSeq& s) {
   if (s.q_len <= a.split_q) return 0;
   return a.hkv * ((s.q_len * a.group + kRows - 1) / kRows);
+}
+
+template <int N>
+__device__ __forceinline__ void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void give_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+// A warp's part in a two-warp barrier: announce, or wait for the other's announcement.
+__device__ __forceinline__ void pair_arrive(int id) {
+  asm volatile("bar.arrive %0, 64;" ::"r"(id) : "memory");
+}
+__device__ __forceinline__ void pair_wait(int id) {
+  asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
 }
 
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
@@ -166,9 +201,8 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 tile_kernel(const __grid_constant__ TileParams p) {
   using Sh = Shape<D>;
-  constexpr int BN = Sh::BN;
   extern __shared__ __align__(1024) uint8_t smem[];  // no static shared memory in front of it
-  Smem<Sh::kGroups>& sm = *reinterpret_cast<Smem<Sh::kGroups>*>(smem + Sh::OFF_SM);
+  Smem& sm = *reinterpret_cast<Smem*>(smem + Sh::OFF_SM);
   const AttnArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (smem_u32(smem) & 1023u) {  // the swizzles need it; the declaration asks for it
@@ -179,24 +213,26 @@ tile_kernel(const __grid_constant__ TileParams p) {
   // ---- set-up: barriers, tensor memory, units before every 32nd request
   if (tid == 0) {
     sm.dead = 0;
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < Sh::SK; ++i) {
       mbar_init(&sm.kfull[i], 1);
       mbar_init(&sm.kempty[i], 1);
-      mbar_init(&sm.vfull[i], 1);
-      mbar_init(&sm.vempty[i], kAuxWarps);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.sfull[i], 1);
-      mbar_init(&sm.pfull[i], kSoftWarps);
-      mbar_init(&sm.odone[i], 1);
-      mbar_init(&sm.hfull[i], kAuxWarps);
+      mbar_init(&sm.pfull[i], kSoftWarps / 2);
       mbar_init(&sm.ufull[i], 1);
       mbar_init(&sm.uempty[i], kSoftWarps + kAuxWarps + 1);
     }
+    for (int i = 0; i < kDone; ++i) mbar_init(&sm.odone[i], 1);
+    for (int i = 0; i < Sh::NH; ++i) mbar_init(&sm.hfull[i], kAuxWarps);
     for (int i = 0; i < kMeta; ++i) mbar_init(&sm.mfull[i], 1);
+    mbar_init(&sm.sfull[0], 1);  // a barrier for each softmax group: it waits for every second S
+    mbar_init(&sm.sfull[1], 1);
+    mbar_init(&sm.sfree, kSoftWarps / 2);
     mbar_init(&sm.qfull, kAuxWarps);
     mbar_init(&sm.qempty, 1);
     mbar_init(&sm.ofree, kSoftWarps);
+    mbar_init(&sm.rawfull, 1);
+    mbar_init(&sm.rawempty, kAuxWarps);
     mbar_init(&sm.drain, 1);
     fence_mbar_init();
   }
@@ -237,330 +273,358 @@ tile_kernel(const __grid_constant__ TileParams p) {
     return u.seq >= 0;
   };
 
-  if (warp == kProducer) {
-    // ---- units, pages and scales, TMA copies
-    const int box_rows = min(a.page_size, BN), per_box = box_rows / 16;
-    const uint32_t box_bytes = (uint32_t)box_rows * D;
-    constexpr int kBatchTiles = 32 / Sh::kGroups;
-    uint32_t it = 0;
-    for (uint32_t n = 0;; ++n) {
-      int32_t x = 0;
-      if (lane == 0) x = atomicAdd(p.counter, 1);
-      x = __shfl_sync(0xffffffffu, x, 0);
-      Unit u = {-1, 0, 0, 0, 0, 0, 0, 0};
-      if (x < total) {
-        int lo = 0, hi = chunks - 1;
-        while (lo < hi) {
-          const int mid = (lo + hi + 1) >> 1;
-          if (sm.coarse[mid] <= x) lo = mid;
-          else hi = mid - 1;
-        }
-        const int b = 32 * lo + lane;
-        bool cut = false;
-        AttnSeq s = {0, 0, 0};
-        int32_t mine = 0;
-        if (b < a.num_seqs) {
-          s = attn_seq(a, b, cut);
-          mine = seq_units(a, s);
-        }
-        int32_t inc = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int32_t y = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += y;
-        }
-        const int32_t y = x - sm.coarse[lo];
-        const int src = __ffs(__ballot_sync(0xffffffffu, inc > y)) - 1;
-        u.seq = 32 * lo + src;
-        u.row0 = __shfl_sync(0xffffffffu, s.row0, src);
-        u.q_len = __shfl_sync(0xffffffffu, s.q_len, src);
-        u.kv_len = __shfl_sync(0xffffffffu, s.kv_len, src);
-        const int32_t k = y - __shfl_sync(0xffffffffu, inc - mine, src);
-        const int32_t row_tiles = (u.q_len * a.group + kRows - 1) / kRows;
-        u.head = k / row_tiles;
-        u.first = (row_tiles - 1 - k % row_tiles) * kRows;  // the rows that see most come first
-        const int32_t last = min(u.q_len * a.group, u.first + kRows) - 1;
-        const AttnSeq q = {u.row0, u.q_len, u.kv_len};
-        u.tiles = (attn_limit(a, q, last / a.group) + BN - 1) / BN;
-        // the queries on their way to L2, before their turn
-        const int32_t t0 = u.first / a.group, t1 = last / a.group;
-        for (int32_t t = t0 + lane; t <= t1; t += 32)
-          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
-                           static_cast<const __nv_bfloat16*>(a.q) +
-                           (int64_t)(u.row0 + t) * a.q_stride + (int64_t)u.head * a.group * D),
-                       "r"(a.group * D * 2)
-                       : "memory");
-      }
-      const int slot = n & 1;
-      if (!wait_or_die(&sm.uempty[slot], ((n >> 1) & 1u) ^ 1u, sm, a.status)) break;
-      if (lane == 0) {
-        sm.unit[slot] = u;
-        mbar_arrive(&sm.ufull[slot]);
-      }
-      if (u.seq < 0) break;
-      const int32_t* table = a.block_table + (int64_t)u.seq * a.max_blocks;
-      float vref = 0.f;
-      for (int32_t tb = 0; tb < u.tiles; tb += kBatchTiles) {
-        const int32_t tok = tb * BN + lane * 16;
-        int32_t id = -1;
-        float ks = -1.f, vs = 0.f;
-        if (tok < u.kv_len && tok < u.tiles * BN) {
-          id = table[tok / a.page_size];
-          if (id >= 0 && id < a.num_pages) {
-            ks = a.k_scale[(int64_t)id * a.hkv + u.head];
-            vs = a.v_scale[(int64_t)id * a.hkv + u.head];
-            if (!(ks >= 0.f)) ks = 0.f;
-            if (!(vs >= 0.f)) vs = 0.f;
-          } else {
-            id = -1;
-            raise_status(a.status, GDN_ERR_INVALID_ARGUMENT);
+  if (warp >= kProducer) {
+    give_registers<kMiscRegs>();
+    if (warp == kProducer) {
+      // ---- units, pages and scales, Q rows, K tiles
+      const int box_rows = min(a.page_size, BN), per_box = box_rows / 16;
+      const uint32_t box_bytes = (uint32_t)box_rows * D;
+      constexpr int kBatchTiles = 32 / kGroups;
+      uint32_t it = 0, raws = 0;
+      for (uint32_t n = 0;; ++n) {
+        int32_t x = 0;
+        if (lane == 0) x = atomicAdd(p.counter, 1);
+        x = __shfl_sync(0xffffffffu, x, 0);
+        Unit u = {-1, 0, 0, 0, 0, 0, 0, 0};
+        int32_t last = 0;
+        if (x < total) {
+          int lo = 0, hi = chunks - 1;
+          while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (sm.coarse[mid] <= x) lo = mid;
+            else hi = mid - 1;
           }
+          const int b = 32 * lo + lane;
+          bool cut = false;
+          AttnSeq s = {0, 0, 0};
+          int32_t mine = 0;
+          if (b < a.num_seqs) {
+            s = attn_seq(a, b, cut);
+            mine = seq_units(a, s);
+          }
+          int32_t inc = mine;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+          }
+          const int32_t y = x - sm.coarse[lo];
+          const int src = __ffs(__ballot_sync(0xffffffffu, inc > y)) - 1;
+          u.seq = 32 * lo + src;
+          u.row0 = __shfl_sync(0xffffffffu, s.row0, src);
+          u.q_len = __shfl_sync(0xffffffffu, s.q_len, src);
+          u.kv_len = __shfl_sync(0xffffffffu, s.kv_len, src);
+          const int32_t k = y - __shfl_sync(0xffffffffu, inc - mine, src);
+          const int32_t row_tiles = (u.q_len * a.group + kRows - 1) / kRows;
+          u.head = k / row_tiles;
+          u.first = (row_tiles - 1 - k % row_tiles) * kRows;  // the rows that see most come first
+          last = min(u.q_len * a.group, u.first + kRows) - 1;
+          const AttnSeq q = {u.row0, u.q_len, u.kv_len};
+          u.tiles = (attn_limit(a, q, last / a.group) + BN - 1) / BN;
         }
-        for (int j = 0; j < kBatchTiles && tb + j < u.tiles; ++j, ++it) {
-          const int first = j * Sh::kGroups;
-          const bool mine = lane >= first && lane < first + Sh::kGroups;
-          const bool box = mine && (lane - first) % per_box == 0 && id >= 0;
-          const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, box));
-          const float top = __uint_as_float(
-              __reduce_max_sync(0xffffffffu, mine ? __float_as_uint(vs) : 0u));
-          const float fac = top > vref ? vref / top : 1.f;
-          vref = fmaxf(vref, top);
-          const int ms = it % kMeta, kst = it % Sh::SK, vst = it % Sh::SV;
-          if (!wait_or_die(&sm.kempty[kst], ((it / Sh::SK) & 1u) ^ 1u, sm, a.status)) break;
-          if (mine) {
-            sm.meta[ms].ks[lane - first] = ks;
-            sm.meta[ms].vr[lane - first] = vref > 0.f ? vs / vref * kProbScale : 0.f;
-          }
-          if (lane == 0) {
-            sm.meta[ms].vref = vref;
-            sm.meta[ms].vfac = fac;
-          }
-          const int32_t y = (int32_t)(((int64_t)id * a.hkv + u.head) * a.page_size +
-                                      tok % a.page_size);
-          const uint32_t at = (uint32_t)(lane - first) * 16 * Sh::kRowPitch;
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&sm.mfull[ms]);
-            mbar_arrive_expect_tx(&sm.kfull[kst], boxes * box_bytes);
-          }
-          __syncwarp();
-          if (box)
-#pragma unroll
-            for (int r = 0; r < (D + 127) / 128; ++r)
-              tma_load_2d(smem + Sh::OFF_K + kst * Sh::kTileBytes + r * (BN * 128) + at, &p.tk,
-                          128 * r, y, &sm.kfull[kst]);
-          const bool go = wait_or_die(&sm.vempty[vst], ((it / Sh::SV) & 1u) ^ 1u, sm, a.status);
-          if (lane == 0) mbar_arrive_expect_tx(&sm.vfull[vst], go ? boxes * box_bytes : 0u);
-          __syncwarp();
-          if (box && go)
-#pragma unroll
-            for (int r = 0; r < (D + 127) / 128; ++r)
-              tma_load_2d(smem + Sh::OFF_V + vst * Sh::kTileBytes + r * (BN * 128) + at, &p.tv,
-                          128 * r, y, &sm.vfull[vst]);
+        const int slot = n & 1;
+        if (!wait_or_die(&sm.uempty[slot], ((n >> 1) & 1u) ^ 1u, sm, a.status)) break;
+        if (lane == 0) {
+          sm.unit[slot] = u;
+          mbar_arrive(&sm.ufull[slot]);
         }
-      }
-    }
-    if (sm.dead) {  // copies may be in flight: let them land
-      for (uint32_t k = 0; k < Sh::SK && k < it; ++k)
-        mbar_wait_bounded(&sm.kfull[(it - 1 - k) % Sh::SK], ((it - 1 - k) / Sh::SK) & 1u, kWaitLimit);
-      for (uint32_t k = 0; k < Sh::SV && k < it; ++k)
-        mbar_wait_bounded(&sm.vfull[(it - 1 - k) % Sh::SV], ((it - 1 - k) / Sh::SV) & 1u, kWaitLimit);
-    }
-  } else if (warp == kIssuer) {
-    // ---- MMA issue
-    constexpr uint32_t id_s = idesc_f16(kRows, BN, 0, 0), id_o = idesc_f16(kRows, D, 0, 1);
-    const uint64_t q_desc = f8_desc<D>(smem_u32(smem) + Sh::OFF_Q);
-    const uint64_t h_desc = smem_desc_sw128(smem_u32(smem) + Sh::OFF_H, BN * 128, 1024);
-    const uint32_t tm = __shfl_sync(0xffffffffu, tbase, 0), el = elect_lane();
-    uint32_t g = 0, units = 0, nq = 0;
-    Unit u;
-    while (next_unit(u)) {
-      if (u.tiles == 0) continue;
-      bool ok = wait_or_die(&sm.qfull, nq & 1u, sm, a.status);
-      ++nq;
-      auto issue_s = [&](uint32_t j, bool last) {  // j: tile number since the start
-        const int st = j % Sh::SK;
-        ok = ok && wait_or_die(&sm.kfull[st], (j / Sh::SK) & 1u, sm, a.status);
-        tc_fence_after();
-        if (ok) {
-          const uint64_t kd = q_desc + (Sh::OFF_K + st * Sh::kTileBytes) / 16;
-          const uint32_t d = tm + Sh::TM_S + (j & 1u) * BN;
-#pragma unroll
-          for (int term = 0; term < 2; ++term)
-#pragma unroll
-            for (int k = 0; k < D / 32; ++k)
-              warp_mma_f8_ss(
-                  el, d, q_desc + (term * Sh::kQBytes + (k >> 2) * (kRows * 128) + (k & 3) * 32) / 16,
-                  kd + ((k >> 2) * (BN * 128) + (k & 3) * 32) / 16, id_s, term + k > 0);
-          if (el) {
-            mma_commit(&sm.kempty[st]);
-            mma_commit(&sm.sfull[j & 1u]);
-            if (last) mma_commit(&sm.qempty);
-          }
-        }
+        if (u.seq < 0) break;
+        if (u.tiles == 0) continue;
+        // the unit's rows of Q, one copy each, when the last unit's have moved on
+        if (!wait_or_die(&sm.rawempty, (raws & 1u) ^ 1u, sm, a.status)) break;
+        ++raws;
+        if (lane == 0)
+          mbar_arrive_expect_tx(&sm.rawfull, (uint32_t)(last - u.first + 1) * 2 * D);
         __syncwarp();
-      };
-      const int32_t tiles = __shfl_sync(0xffffffffu, u.tiles, 0);
-      issue_s(g, tiles == 1);
-      if (tiles > 1) issue_s(g + 1, tiles == 2);
-      for (int32_t i = 0; i < tiles && ok; ++i, ++g) {
-        const uint32_t b = g & 1u, ph = (g >> 1) & 1u;
-        ok = wait_or_die(&sm.hfull[b], ph, sm, a.status) &&
-             wait_or_die(&sm.pfull[b], ph, sm, a.status) &&
-             (i > 0 || wait_or_die(&sm.ofree, (units & 1u) ^ 1u, sm, a.status));
-        tc_fence_after();
-        if (ok) {
-          const uint64_t hd = h_desc + b * (Sh::kHBytes / 16);
-          const uint32_t pa = tm + Sh::TM_P + b * (BN / 2);
-#pragma unroll
-          for (int k = 0; k < BN / 16; ++k)
-            warp_mma_f16_ts(el, tm + Sh::TM_O, pa + 8 * k, hd + k * (2048 / 16), id_o,
-                            i > 0 || k > 0);
-          if (el) mma_commit(&sm.odone[b]);
+        for (int32_t r = u.first + lane; r <= last; r += 32) {
+          const int32_t i = r / a.group, h = r - i * a.group;
+          bulk_load(smem + Sh::OFF_RAW + (r - u.first) * Sh::kRawPitch,
+                    static_cast<const __nv_bfloat16*>(a.q) + (int64_t)(u.row0 + i) * a.q_stride +
+                        (int64_t)(u.head * a.group + h) * D,
+                    2 * D, &sm.rawfull);
         }
-        __syncwarp();
-        if (i + 2 < tiles) issue_s(g + 2, i + 3 == tiles);
+        const int32_t* table = a.block_table + (int64_t)u.seq * a.max_blocks;
+        float vref = 0.f;
+        bool ok = true;
+        for (int32_t tb = 0; tb < u.tiles && ok; tb += kBatchTiles) {
+          const int32_t tok = tb * BN + lane * 16;
+          int32_t id = -1;
+          float ks = 0.f, vs = 0.f;
+          if (tok < u.kv_len && tok < u.tiles * BN) {
+            id = table[tok / a.page_size];
+            if (id >= 0 && id < a.num_pages) {
+              ks = a.k_scale[(int64_t)id * a.hkv + u.head];
+              vs = a.v_scale[(int64_t)id * a.hkv + u.head];
+              if (!(ks >= 0.f)) ks = 0.f;
+              if (!(vs >= 0.f)) vs = 0.f;
+            } else {
+              id = -1;
+              raise_status(a.status, GDN_ERR_INVALID_ARGUMENT);
+            }
+          }
+          for (int j = 0; j < kBatchTiles && tb + j < u.tiles; ++j, ++it) {
+            const int first = j * kGroups;
+            const bool mine = lane >= first && lane < first + kGroups;
+            const bool box = mine && (lane - first) % per_box == 0 && id >= 0;
+            const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, box));
+            const float top = __uint_as_float(
+                __reduce_max_sync(0xffffffffu, mine ? __float_as_uint(vs) : 0u));
+            const float fac = top > vref ? vref / top : 1.f;
+            vref = fmaxf(vref, top);
+            const int ms = it % kMeta, kst = it % Sh::SK;
+            const uint32_t gone = __ballot_sync(0xffffffffu, mine && id < 0) >> first;
+            ok = wait_or_die(&sm.kempty[kst], ((it / Sh::SK) & 1u) ^ 1u, sm, a.status);
+            if (!ok) break;
+            if (mine) {
+              sm.meta[ms].ks[lane - first] = ks;
+              sm.meta[ms].lv[lane - first] =
+                  log2f(fmaxf(vref > 0.f ? vs / vref : 0.f, kMinRatio) * kProbScale);
+              sm.meta[ms].id[lane - first] = id;
+            }
+            if (lane == 0) {
+              sm.meta[ms].absent = gone & ((1u << kGroups) - 1);
+              sm.meta[ms].vref = vref;
+              sm.meta[ms].vfac = fac;
+            }
+            const int32_t y = (int32_t)(((int64_t)id * a.hkv + u.head) * a.page_size +
+                                        tok % a.page_size);
+            const uint32_t at = (uint32_t)(lane - first) * 16 * Sh::kRowPitch;
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&sm.mfull[ms]);
+              mbar_arrive_expect_tx(&sm.kfull[kst], boxes * box_bytes);
+            }
+            __syncwarp();
+            if (box)
+#pragma unroll
+              for (int r = 0; r < (D + 127) / 128; ++r)
+                tma_load_2d(smem + Sh::OFF_K + kst * Sh::kTileBytes + r * (BN * 128) + at, &p.tk,
+                            128 * r, y, &sm.kfull[kst]);
+          }
+        }
+        if (!ok) break;
       }
-      ++units;
-      if (!ok) break;
+      if (sm.dead) {  // copies may be in flight: let them land
+        for (uint32_t k = 0; k < Sh::SK && k < it; ++k)
+          mbar_wait_bounded(&sm.kfull[(it - 1 - k) % Sh::SK], ((it - 1 - k) / Sh::SK) & 1u,
+                            kWaitLimit);
+        if (raws > 0) mbar_wait_bounded(&sm.rawfull, (raws - 1) & 1u, kWaitLimit);
+      }
+    } else if (warp == kIssuer) {
+      // ---- MMA issue
+      constexpr uint32_t id_s = idesc_f16(kRows, BN, 0, 0), id_o = idesc_f16(kRows, D, 0, 1);
+      const uint64_t k_desc = f8_desc<D>(smem_u32(smem) + Sh::OFF_K);
+      const uint64_t h_desc = smem_desc_sw128(smem_u32(smem) + Sh::OFF_H, BN * 128, 1024);
+      const uint32_t tm = __shfl_sync(0xffffffffu, tbase, 0), el = elect_lane();
+      uint32_t g = 0, nq = 0;
+      Unit u;
+      while (next_unit(u)) {
+        const int32_t tiles = __shfl_sync(0xffffffffu, u.tiles, 0);
+        if (tiles == 0) continue;
+        bool ok = wait_or_die(&sm.qfull, nq & 1u, sm, a.status);
+        auto issue_s = [&](uint32_t j, bool last) {  // j: tile number since the start
+          const int st = j % Sh::SK;
+          ok = ok && wait_or_die(&sm.kfull[st], (j / Sh::SK) & 1u, sm, a.status) &&
+               wait_or_die(&sm.sfree, (j & 1u) ^ 1u, sm, a.status);
+          tc_fence_after();
+          if (ok) {
+            const uint64_t kd = k_desc + (uint32_t)(st * (Sh::kTileBytes / 16));
+#pragma unroll
+            for (int term = 0; term < 2; ++term)
+#pragma unroll
+              for (int k = 0; k < D / 32; ++k)
+                warp_mma_f8_ts(el, tm + Sh::TM_S, tm + Sh::TM_Q + term * (D / 4) + 8 * k,
+                               kd + ((k >> 2) * (BN * 128) + (k & 3) * 32) / 16, id_s,
+                               term + k > 0);
+            if (el) {
+              mma_commit(&sm.kempty[st]);
+              mma_commit(&sm.sfull[j & 1u]);
+              if (last) mma_commit(&sm.qempty);
+            }
+          }
+          __syncwarp();
+        };
+        issue_s(g, tiles == 1);
+        if (tiles > 1) issue_s(g + 1, tiles == 2);
+        for (int32_t i = 0; i < tiles && ok; ++i, ++g) {
+          if (i + 2 < tiles) issue_s(g + 2, i + 3 == tiles);
+          const uint32_t b = g & 1u, hb = g % Sh::NH;
+          ok = ok && wait_or_die(&sm.hfull[hb], (g / Sh::NH) & 1u, sm, a.status) &&
+               wait_or_die(&sm.pfull[b], (g >> 1) & 1u, sm, a.status) &&
+               (i > 0 || wait_or_die(&sm.ofree, (nq & 1u) ^ 1u, sm, a.status));
+          tc_fence_after();
+          if (ok) {
+            const uint64_t hd = h_desc + (uint32_t)(hb * (Sh::kHBytes / 16));
+            const uint32_t pa = tm + Sh::TM_P + b * (BN / 2);
+#pragma unroll
+            for (int k = 0; k < BN / 16; ++k)
+              warp_mma_f16_ts(el, tm + Sh::TM_O, pa + 8 * k, hd + k * (2048 / 16), id_o,
+                              i > 0 || k > 0);
+            if (el) mma_commit(&sm.odone[g % kDone]);
+          }
+          __syncwarp();
+        }
+        ++nq;
+        if (!ok) break;
+      }
+      // what was issued has completed before the block's memory goes
+      if (el) mma_commit(&sm.drain);
+      mbar_wait_bounded(&sm.drain, 0, kWaitLimit);
     }
-    // what was issued has completed before the block's memory goes
-    if (el) mma_commit(&sm.drain);
-    mbar_wait_bounded(&sm.drain, 0, kWaitLimit);
   } else if (warp >= kSoftWarps) {
-    // ---- operands: Q of the unit, then its V tiles
+    // ---- operands: Q of a unit, then its V tiles
+    give_registers<kAuxRegs>();
     const int aw = warp - kSoftWarps, at = tid - kSoftThreads;
     uint32_t g = 0, nq = 0;
     Unit u;
-    while (next_unit(u)) {
-      if (u.tiles == 0) continue;
-      const int32_t rows = u.q_len * a.group;
-      constexpr int kPer = D / 32;  // elements of a lane
-      bool ok = wait_or_die(&sm.qempty, (nq & 1u) ^ 1u, sm, a.status);
-      const float sign = a.scale_log2 < 0.f ? -1.f : 1.f;
-      constexpr int kBatch = 8;
-      for (int rb = 0; rb < kRows / kAuxWarps && ok; rb += kBatch) {
-        uint32_t w[kBatch][kPer / 2];
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int32_t row = u.first + aw * (kRows / kAuxWarps) + rb + k;
-          const bool live = row < rows;
-          const int32_t i = live ? row / a.group : 0, hd = live ? row - i * a.group : 0;
-          const uint32_t* src = reinterpret_cast<const uint32_t*>(
-              static_cast<const __nv_bfloat16*>(a.q) + (int64_t)(u.row0 + i) * a.q_stride +
-              (int64_t)(u.head * a.group + hd) * D + lane * kPer);
-#pragma unroll
-          for (int e = 0; e < kPer / 2; ++e) w[k][e] = 0;
-          if (live) {
-            if constexpr (kPer == 8) {
-              const uint4 v = *reinterpret_cast<const uint4*>(src);
-              w[k][0] = v.x; w[k][1] = v.y; w[k][2] = v.z; w[k][3] = v.w;
-            } else if constexpr (kPer == 4) {
-              const uint2 v = *reinterpret_cast<const uint2*>(src);
-              w[k][0] = v.x; w[k][1] = v.y;
-            } else {
-              w[k][0] = *src;
-            }
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int r = aw * (kRows / kAuxWarps) + rb + k;
-          // largest magnitude: bf16 bit patterns without their signs order like integers
+    // a thread's place in V tiles: 16 channels of every (256 * 16 / D)-th token. Eight lanes
+    // take four chunks of two neighbouring tokens, whose f16 chunks fall on distinct banks.
+    constexpr int kChunks = D / 16, kStep = kAuxThreads / kChunks, kV = BN / kStep;
+    const int vc = (at & 3) | ((at >> 3) & (kChunks / 4 - 1)) << 2;
+    const int vt = ((at >> 2) & 1) | (at >> 3) / (kChunks / 4) << 1;
+    const uint32_t h0 = sw128_offset(vt, 16 * vc, BN), h1 = sw128_offset(vt, 16 * vc + 8, BN);
+    static_assert(kStep % 8 == 0, "the swizzle repeats from step to step");
+    const uint8_t* vbase = static_cast<const uint8_t*>(p.v) + 16 * vc;
+    const int page_mask = a.page_size - 1;
+    // and in Q: half of a row
+    const int qr = 32 * (warp & 3) + lane, qhalf = aw >> 2;
+    uint8_t* raw = smem + Sh::OFF_RAW + qr * Sh::kRawPitch + qhalf * D;
+    bool more = next_unit(u);
+    while (true) {
+      if (named_any(kAuxBar, kAuxThreads, !more)) break;  // these warps leave together
+      if (u.tiles > 0) {
+        bool ok = wait_or_die(&sm.rawfull, nq & 1u, sm, a.status);
+        {
+          const bool live = u.first + qr < u.q_len * a.group;
+          // largest magnitude of the row: bf16 bit patterns without their signs order like
+          // integers
           uint32_t top = 0;
-#pragma unroll
-          for (int e = 0; e < kPer / 2; ++e)
-            top = __vmaxu2(top, w[k][e] & 0x7fff7fffu);
-          top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+#pragma unroll 4
+          for (int c = 0; c < D; c += 16) {
+            const uint4 w = *reinterpret_cast<const uint4*>(raw + c);
+            top = __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
+                                         __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
+          }
+          sm.exchange_q[qhalf][qr] = (uint16_t)max(top & 0xffffu, top >> 16);
+          named_sync(kAuxBar, kAuxThreads);
+          top = max(sm.exchange_q[0][qr], sm.exchange_q[1][qr]);
           int ex = (int)(top >> 7) - 127;        // [128, 256) after the scaling
           const bool wild = ex == 128;           // an infinity or NaN: the row is NaN
           ex = wild ? 7 : max(ex, -100);
-          const float up = wild ? __int_as_float(0x7fffffff)
-                                : sign * __uint_as_float((uint32_t)(7 - ex + 127) << 23);
-          uint32_t hi[(kPer + 3) / 4], lo[(kPer + 3) / 4];
+          if (!live) ex = 7;
+          float up = wild ? __int_as_float(0x7fffffff)
+                          : __uint_as_float((uint32_t)(7 - ex + 127) << 23);
+          if (a.scale_log2 < 0.f) up = -up;
+          // in place: eight values become eight e4m3 codes of each term
+#pragma unroll 2
+          for (int c = 0; c < D; c += 16) {
+            uint4* at8 = reinterpret_cast<uint4*>(raw + c);
+            const uint4 v = *at8;
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
-          for (int e = 0; e < (kPer + 3) / 4; ++e) hi[e] = lo[e] = 0;
-#pragma unroll
-          for (int e = 0; e < kPer / 2; ++e) {
-            const uint32_t h = f16x2(__uint_as_float(w[k][e] << 16) * up,
-                                     __uint_as_float(w[k][e] & 0xffff0000u) * up);
-            const uint16_t c = half2_to_e4m3(h);
-            const uint32_t back = e4m3_to_half2(c);
-            const __half2 rest = __hsub2(*reinterpret_cast<const __half2*>(&h),
-                                         *reinterpret_cast<const __half2*>(&back));
-            hi[e >> 1] |= (uint32_t)c << (16 * (e & 1));
-            lo[e >> 1] |= (uint32_t)half2_to_e4m3(h2_bits(rest)) << (16 * (e & 1));
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t h = f16x2(__uint_as_float(w[e] << 16) * up,
+                                       __uint_as_float(w[e] & 0xffff0000u) * up);
+              const uint16_t k = half2_to_e4m3(h);
+              const uint32_t back = e4m3_to_half2(k);
+              const __half2 rest = __hsub2(*reinterpret_cast<const __half2*>(&h),
+                                           *reinterpret_cast<const __half2*>(&back));
+              hi[e >> 1] |= (uint32_t)k << (16 * (e & 1));
+              lo[e >> 1] |= (uint32_t)half2_to_e4m3(h2_bits(rest)) << (16 * (e & 1));
+            }
+            *at8 = live ? make_uint4(hi[0], hi[1], lo[0], lo[1]) : make_uint4(0, 0, 0, 0);
           }
-          const int d0 = lane * kPer;
-          uint8_t* dst = smem + Sh::OFF_Q + f8_offset<D>(r, d0 >> 4, kRows) + (d0 & 15);
-          if constexpr (kPer == 8) {
-            *reinterpret_cast<uint2*>(dst) = make_uint2(hi[0], hi[1]);
-            *reinterpret_cast<uint2*>(dst + Sh::kQBytes) = make_uint2(lo[0], lo[1]);
-          } else if constexpr (kPer == 4) {
-            *reinterpret_cast<uint32_t*>(dst) = hi[0];
-            *reinterpret_cast<uint32_t*>(dst + Sh::kQBytes) = lo[0];
-          } else {
-            *reinterpret_cast<uint16_t*>(dst) = (uint16_t)hi[0];
-            *reinterpret_cast<uint16_t*>(dst + Sh::kQBytes) = (uint16_t)lo[0];
+          if (qhalf == 0) sm.row_exp[nq & 1u][qr] = (int8_t)(ex - 7);
+        }
+        // to tensor memory, when the S products of the unit before have read theirs
+        ok = wait_or_die(&sm.qempty, (nq & 1u) ^ 1u, sm, a.status) && ok;
+        tc_fence_after();
+        {
+          const uint32_t tq = tbase + ((uint32_t)(32 * (warp & 3)) << 16) + Sh::TM_Q +
+                              qhalf * (D / 8);
+#pragma unroll 1
+          for (int c = 0; c < D / 64; ++c) {  // 32 elements: eight columns of each term
+            uint32_t hi[8], lo[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint4 w = *reinterpret_cast<const uint4*>(raw + 64 * c + 16 * e);
+              hi[2 * e] = w.x; hi[2 * e + 1] = w.y; lo[2 * e] = w.z; lo[2 * e + 1] = w.w;
+            }
+            tmem_st8(tq + 8 * c, hi);
+            tmem_st8(tq + D / 4 + 8 * c, lo);
           }
-          if (lane == 0) sm.row_exp[nq & 1u][r] = (int8_t)(ex - 7);
         }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.qfull);
-      ++nq;
-      for (int32_t t = 0; t < u.tiles && ok; ++t, ++g) {
-        const int st = g % Sh::SV;
-        const uint32_t b = g & 1u;
-        ok = wait_or_die(&sm.vfull[st], (g / Sh::SV) & 1u, sm, a.status) &&
-             wait_or_die(&sm.odone[b], ((g >> 1) & 1u) ^ 1u, sm, a.status);  // P V(g - 2) is done
-        const auto& m = sm.meta[g % kMeta];
-        const uint8_t* src = smem + Sh::OFF_V + st * Sh::kTileBytes;
-        uint8_t* dst = smem + Sh::OFF_H + b * Sh::kHBytes;
-        constexpr int kChunks = BN * D / 16 / kAuxThreads;
-        uint4 v[kChunks];
-#pragma unroll
-        for (int k = 0; k < kChunks; ++k) {
-          const int x = k * kAuxThreads + at, tok = x % BN, chunk = x / BN;
-          v[k] = *reinterpret_cast<const uint4*>(src + f8_offset<D>(tok, chunk, BN));
-          // places past the cached tokens, or without a page, hold anything: zeros
-          if (t * BN + tok >= u.kv_len || m.ks[tok >> 4] < 0.f) v[k] = make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int k = 0; k < kChunks; ++k) {
-          const int x = k * kAuxThreads + at, tok = x % BN, chunk = x / BN;
-          const uint32_t s4[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-          uint32_t h[8];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            h[2 * e] = e4m3_to_half2((uint16_t)s4[e]);
-            h[2 * e + 1] = e4m3_to_half2((uint16_t)(s4[e] >> 16));
-          }
-          *reinterpret_cast<uint4*>(dst + sw128_offset(tok, 16 * chunk, BN)) =
-              make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(dst + sw128_offset(tok, 16 * chunk + 8, BN)) =
-              make_uint4(h[4], h[5], h[6], h[7]);
-        }
-        fence_proxy_async_smem();
+        tmem_st_wait();
+        tc_fence_before();
+        fence_proxy_async_smem();  // the next rows come by the async proxy
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&sm.hfull[b]);
-          mbar_arrive(&sm.vempty[st]);
+          mbar_arrive(&sm.qfull);
+          mbar_arrive(&sm.rawempty);
+        }
+        ++nq;
+        // V tiles: the next tile's loads are on their way while this one is stored
+        uint4 v[kV];
+        auto load_v = [&](int32_t t, uint32_t j) {  // j: tile number since the start
+          ok = ok && wait_or_die(&sm.mfull[j % kMeta], (j / kMeta) & 1u, sm, a.status);
+          const TileMeta& m = sm.meta[j % kMeta];
+#pragma unroll
+          for (int k = 0; k < kV; ++k) {
+            const int32_t tok = vt + k * kStep, pos = t * BN + tok, id = m.id[tok >> 4];
+            v[k] = make_uint4(0, 0, 0, 0);  // past the cached tokens, or without a page: zeros
+            if (ok && id >= 0 && pos < u.kv_len)
+              v[k] = *reinterpret_cast<const uint4*>(
+                  vbase + ((int64_t)(id * a.hkv + u.head) * a.page_size + (pos & page_mask)) * D);
+          }
+        };
+        load_v(0, g);
+        for (int32_t t = 0; t < u.tiles && ok; ++t, ++g) {
+          const uint32_t hb = g % Sh::NH;
+          if (g >= Sh::NH) {  // P V(g - NH) has read this buffer
+            const uint32_t o = g - Sh::NH;
+            ok = wait_or_die(&sm.odone[o % kDone], (o / kDone) & 1u, sm, a.status);
+          }
+          uint8_t* dst = smem + Sh::OFF_H + hb * Sh::kHBytes;
+          uint4 cur[kV];
+#pragma unroll
+          for (int k = 0; k < kV; ++k) cur[k] = v[k];
+          if (t + 1 < u.tiles) load_v(t + 1, g + 1);
+#pragma unroll
+          for (int k = 0; k < kV; ++k) {
+            const uint32_t s4[4] = {cur[k].x, cur[k].y, cur[k].z, cur[k].w};
+            uint32_t h[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              h[2 * e] = e4m3_to_half2((uint16_t)s4[e]);
+              h[2 * e + 1] = e4m3_to_half2((uint16_t)(s4[e] >> 16));
+            }
+            *reinterpret_cast<uint4*>(dst + h0 + k * kStep * 128) =
+                make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(dst + h1 + k * kStep * 128) =
+                make_uint4(h[4], h[5], h[6], h[7]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.hfull[hb]);
         }
       }
-      if (!ok) break;
+      more = next_unit(u);
     }
   } else {
-    // ---- softmax and epilogue
-    const int half = warp >> 2, r = 32 * (warp & 3) + lane;
-    const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
-    constexpr int kCols = BN / 2;      // columns of a thread
+    // ---- softmax (tiles of this group's parity) and epilogue
+    take_registers<kSoftRegs>();
+    const uint32_t grp = warp >> 2;
+    const int r = 32 * (warp & 3) + lane;
+    const uint32_t t_row = tbase + ((uint32_t)(32 * (warp & 3)) << 16);
+    const int from_other = kPairBar + 2 * (warp & 3) + (int)grp,
+              to_other = kPairBar + 2 * (warp & 3) + (int)(grp ^ 1u);
+    const float scale = fabsf(a.scale_log2);
     uint32_t g = 0, nq = 0;
     Unit u;
     while (true) {
       const bool more = next_unit(u);
-      // the warps leave together, so that none is left at their barrier
+      // the warps leave together, so that none is left at a barrier
       if (named_any(kSoftBar, kSoftThreads, !more)) break;
       const int32_t rows = u.q_len * a.group, row = u.first + r;
       const bool live = row < rows;
@@ -568,121 +632,135 @@ tile_kernel(const __grid_constant__ TileParams p) {
       const AttnSeq s = {u.row0, u.q_len, u.kv_len};
       const int32_t limit = live ? attn_limit(a, s, query) : u.kv_len;
       const int32_t min_limit = attn_limit(a, s, u.first / a.group);
-      float m = -GDN_INF, l = 0.f, vref = 0.f;
-      float rs = 0.f;
-      for (int32_t i = 0; i < u.tiles; ++i, ++g) {
-        const uint32_t b = g & 1u, ph = (g >> 1) & 1u;
-        wait_or_die(&sm.mfull[g % kMeta], (g / kMeta) & 1u, sm, a.status);
-        wait_or_die(&sm.sfull[b], ph, sm, a.status);
+      float m = -GDN_INF, l = 0.f, vref = 0.f, rs = 0.f;
+      const uint32_t first = (g & 1u) ^ grp;  // this group's first tile of the unit
+      for (int32_t i = (int32_t)first; i < u.tiles; i += 2) {
+        const uint32_t j = g + i, b = grp;  // tile number since the start; its P buffer
+        wait_or_die(&sm.mfull[j % kMeta], (j / kMeta) & 1u, sm, a.status);
+        wait_or_die(&sm.sfull[grp], (j >> 1) & 1u, sm, a.status);
         tc_fence_after();
-        if (i == 0)
-          rs = fabsf(a.scale_log2) *
-               __uint_as_float((uint32_t)(sm.row_exp[nq & 1u][r] + 127) << 23);
-        const auto& meta = sm.meta[g % kMeta];
-        uint32_t x[kCols];
-#pragma unroll
-        for (int c = 0; c < kCols; c += 32)
-          tmem_ld32(tbase + lane_off + Sh::TM_S + b * BN + half * kCols + c,
-                    reinterpret_cast<uint32_t(&)[32]>(x[c]));
+        const TileMeta& meta = sm.meta[j % kMeta];
+        uint32_t x[BN];
+        tmem_ld32(t_row + Sh::TM_S, reinterpret_cast<uint32_t(&)[32]>(x[0]));
+        tmem_ld32(t_row + Sh::TM_S + 32, reinterpret_cast<uint32_t(&)[32]>(x[32]));
         tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.sfree);
+        if (i == (int32_t)first)
+          rs = scale * __uint_as_float((uint32_t)(sm.row_exp[nq & 1u][r] + 127) << 23);
         vref = meta.vref;
-        const int32_t j0 = i * BN + half * kCols;
-        float top = -GDN_INF;
-        const bool masked = (i + 1) * BN > min_limit;
+        const uint32_t absent = meta.absent;
+        if ((i + 1) * BN > min_limit || absent != 0) {
+          const int32_t room = limit - i * BN;
 #pragma unroll
-        for (int q = 0; q < kCols / 16; ++q) {
-          const float ks = meta.ks[half * (kCols / 16) + q], f = ks * rs;
+          for (int e = 0; e < BN; ++e)
+            if (e >= room || ((absent >> (e / 16)) & 1u)) x[e] = 0xff800000u;
+        }
+        // the tile's largest score: within a group of 16 tokens before its key scale
+        float f[kGroups], top = -GDN_INF;
 #pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            float2 y = mul2(make_float2(__uint_as_float(x[16 * q + e]),
-                                        __uint_as_float(x[16 * q + e + 1])),
-                            make_float2(f, f));
-            if (masked) {
-              if (j0 + 16 * q + e >= limit || ks < 0.f) y.x = -GDN_INF;
-              if (j0 + 16 * q + e + 1 >= limit || ks < 0.f) y.y = -GDN_INF;
-            } else if (ks < 0.f) {
-              y.x = y.y = -GDN_INF;
-            }
-            top = fmaxf(top, fmaxf(y.x, y.y));
-            x[16 * q + e] = __float_as_uint(y.x);
-            x[16 * q + e + 1] = __float_as_uint(y.y);
-          }
+        for (int q = 0; q < kGroups; ++q) {
+          f[q] = fmaxf(meta.ks[q] * rs, 1e-37f);  // above 0: what is masked stays -inf
+          float y = __uint_as_float(x[16 * q]);
+#pragma unroll
+          for (int e = 1; e < 16; ++e) y = fmaxf(y, __uint_as_float(x[16 * q + e]));
+          top = fmaxf(top, y * f[q]);
+        }
+        if (i > 0) {
+          pair_wait(from_other);
+          const float was = m;
+          m = sm.m[r];
+          l *= was == m ? 1.f : ex2(was - m);  // 0 before this group's first tile
         }
         const float vfac = meta.vfac;
-        if (named_any(kSoftBar, kSoftThreads, top > m + kLazyMax || (vfac != 1.f && i > 0))) {
-          // a new maximum for the rows, the accumulator and sum follow
-          sm.exchange[half][r] = top;
-          named_sync(kSoftBar, kSoftThreads);
-          const float both = fmaxf(fmaxf(sm.exchange[0][r], sm.exchange[1][r]), m);
-          const float f = both == -GDN_INF ? 1.f : ex2(m - both);
+        if (__any_sync(0xffffffffu, top > m + kLazyMax) || (vfac != 1.f && i > 0)) {
+          // a new maximum for these rows, the accumulator and sum follow
+          const float both = fmaxf(top, m);
+          const float fm = both == -GDN_INF ? 1.f : ex2(m - both);
           m = both;
-          l *= f;
+          l *= fm;
           if (i > 0) {
-            wait_or_die(&sm.odone[b ^ 1u], ((g - 1) >> 1) & 1u, sm, a.status);  // P V(g - 1)
+            const uint32_t o = j - 1;  // P V of the tile before
+            wait_or_die(&sm.odone[o % kDone], (o / kDone) & 1u, sm, a.status);
             tc_fence_after();
-            const float fo = f * vfac;
+            const float fo = fm * vfac;
 #pragma unroll 1
-            for (int c = 0; c < D / 2; c += 16) {
-              uint32_t o[16];
-              const uint32_t ad = tbase + lane_off + Sh::TM_O + half * (D / 2) + c;
-              tmem_ld16(ad, o);
+            for (int c = 0; c < D; c += 16) {
+              uint32_t y[16];
+              tmem_ld16(t_row + Sh::TM_O + c, y);
               tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * fo);
-              tmem_st16(ad, o);
+              for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * fo);
+              tmem_st16(t_row + Sh::TM_O + c, y);
             }
             tmem_st_wait();
           }
         }
+        if (i + 1 < u.tiles) {
+          sm.m[r] = m;
+          pair_arrive(to_other);
+        }
+        if (j >= 2) {  // P V(j - 2) has read this group's buffer
+          const uint32_t o = j - 2;
+          wait_or_die(&sm.odone[o % kDone], (o / kDone) & 1u, sm, a.status);
+          tc_fence_after();
+        }
+        // P = 2^(s - m + lv): weighted for the product, 2^-lv for the sum
         const float mu = m == -GDN_INF ? 0.f : m;
-        float2 sum = make_float2(0.f, 0.f);
-        uint32_t ph16[kCols / 2];
 #pragma unroll
-        for (int q = 0; q < kCols / 16; ++q) {
-          const float vr = meta.vr[half * (kCols / 16) + q];
+        for (int h = 0; h < 2; ++h) {
+          uint32_t ph[16];
 #pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            const float2 z = add2(make_float2(__uint_as_float(x[16 * q + e]),
-                                              __uint_as_float(x[16 * q + e + 1])),
-                                  make_float2(-mu, -mu));
-            const float2 pr = make_float2(ex2(z.x), ex2(z.y));
-            sum = add2(sum, pr);
-            const float2 pw = mul2(pr, make_float2(vr, vr));
-            ph16[8 * q + e / 2] = f16x2(pw.x, pw.y);
+          for (int q = 2 * h; q < 2 * h + 2; ++q) {
+            const float lv = meta.lv[q], off = lv - mu, fq = f[q];
+            float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int e = 16 * q; e < 16 * q + 16; e += 2) {
+              float2 z = make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+              z = fma2(z, make_float2(fq, fq), make_float2(off, off));
+              const float2 pr = make_float2(ex2(z.x), ex2(z.y));
+              sum = add2(sum, pr);
+              ph[e / 2 - 16 * h] = f16x2(pr.x, pr.y);
+            }
+            l = fmaf(sum.x + sum.y, ex2(-lv), l);
           }
+          tmem_st16(t_row + Sh::TM_P + b * (BN / 2) + 16 * h, ph);
         }
-        l += sum.x + sum.y;
-        if (g >= 2) {  // P V(g - 2) has read this buffer
-          wait_or_die(&sm.odone[b], ph ^ 1u, sm, a.status);
-        }
-        const uint32_t pa = tbase + lane_off + Sh::TM_P + b * (BN / 2) + half * (kCols / 2);
-        if constexpr (kCols == 64) tmem_st32(pa, reinterpret_cast<uint32_t(&)[32]>(ph16));
-        else tmem_st16(pa, reinterpret_cast<uint32_t(&)[16]>(ph16));
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.pfull[b]);
       }
-      // ---- output
+      g += u.tiles;
+      // ---- output: the groups' sums meet, each writes half of the row
       if (u.tiles > 0) {
         ++nq;
-        const uint32_t last = g - 1;
-        sm.exchange[half][r] = l;
+        const uint32_t last = g - 1, mine = (last & 1u) == grp;  // who has the final maximum
+        if (mine) {
+          sm.m[r] = m;
+          sm.exchange_v[r] = vref;
+        }
         named_sync(kSoftBar, kSoftThreads);
-        l = sm.exchange[0][r] + sm.exchange[1][r];
-        wait_or_die(&sm.odone[last & 1u], (last >> 1) & 1u, sm, a.status);
+        const float mf = sm.m[r];
+        vref = sm.exchange_v[r];
+        sm.exchange_l[grp][r] = m == -GDN_INF ? l : l * ex2(m - mf);
+        m = mf;
+        named_sync(kSoftBar, kSoftThreads);
+        l = sm.exchange_l[0][r] + sm.exchange_l[1][r];
+        wait_or_die(&sm.odone[last % kDone], (last / kDone) & 1u, sm, a.status);
         tc_fence_after();
       }
       const float inv = l == 0.f ? 0.f : vref / (l * kProbScale);
       const int64_t tok = u.row0 + query;
       const int hq = u.head * a.group + (row - query * a.group);
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) + tok * a.o_stride +
-                           (int64_t)hq * D + half * (D / 2);
+                           (int64_t)hq * D + grp * (D / 2);
 #pragma unroll 1
       for (int c = 0; c < D / 2; c += 32) {
         uint32_t o[32];
         if (u.tiles > 0) {
-          tmem_ld32(tbase + lane_off + Sh::TM_O + half * (D / 2) + c, o);
+          tmem_ld32(t_row + Sh::TM_O + grp * (D / 2) + c, o);
           tmem_ld_wait();
         } else {
 #pragma unroll
@@ -703,7 +781,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
           }
         }
       }
-      if (live && half == 0 && a.lse)
+      if (live && grp == 0 && a.lse)
         a.lse[tok * (a.hkv * a.group) + hq] = l == 0.f ? -GDN_INF : (m + log2f(l)) * kLn2;
       if (u.tiles > 0) {
         tc_fence_before();
@@ -725,9 +803,9 @@ int launch(const AttnArgs& a, const gdn_kv_cache& c, int num_sms, cudaStream_t s
   using Sh = Shape<D>;
   TileParams p;
   p.a = a;
-  const int box = std::min(c.page_size, Sh::BN);
-  if (!make_cache_map(&p.tk, c.k, c, box) || !make_cache_map(&p.tv, c.v, c, box))
-    return (int)cudaErrorInvalidValue;
+  const int box = std::min(c.page_size, BN);
+  if (!make_cache_map(&p.tk, c.k, c, box)) return (int)cudaErrorInvalidValue;
+  p.v = c.v;
   p.counter = a.counter;
   static std::atomic<int> ready[kMaxDevices];
   constexpr int kSmem = (int)Sh::kSmem;

@@ -166,6 +166,17 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const void* tmap, int32_t
       : "memory");
 }
 
+// Contiguous bytes (a multiple of 16, both addresses 16-byte aligned) from global to shared
+// memory.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // One box from shared memory to a tensor in global memory (bulk-group completion). The
 // source must be visible to the async proxy (fence_proxy_async_smem by its writers first).
 __device__ __forceinline__ void tma_store_2d(const void* tmap, const void* src, int32_t x,
@@ -338,13 +349,13 @@ __device__ __forceinline__ void warp_mma_f16_ts(uint32_t elected, uint32_t d_tme
 // 8-bit operands (e4m3 x e4m3, K = 32): the instruction descriptor has idesc_f16's fields,
 // with format 0 = e4m3; a 32-byte step along K is 32 elements, and in tensor memory a column
 // holds four of them.
-__device__ __forceinline__ void warp_mma_f8_ss(uint32_t elected, uint32_t d_tmem, uint64_t a_desc,
-                                               uint64_t b_desc, uint32_t idesc,
+__device__ __forceinline__ void warp_mma_f8_ts(uint32_t elected, uint32_t d_tmem,
+                                               uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                                uint32_t accumulate) {
   asm volatile(
       "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected)
+      " @q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected)
       : "memory");
 }
 
