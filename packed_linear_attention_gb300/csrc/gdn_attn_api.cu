@@ -402,6 +402,8 @@ gdn_status gdn_attn_paged(gdn_handle* h, const gdn_attn_config* cfg, const gdn_k
   a.page_size = cache->page_size;
   a.hkv = cache->num_kv_heads;
   a.group = cfg->num_q_heads / cache->num_kv_heads;
+  a.by_group = gdn::FastDiv((uint32_t)a.group);
+  while ((1 << a.page_shift) < a.page_size) ++a.page_shift;
   a.head_dim = cache->head_dim;
   a.num_seqs = num_seqs;
   a.num_tokens = num_tokens;

@@ -59,6 +59,22 @@ int launch_kv_append(const gdn_rope* rope, const AppendArgs& a, bool bf16, void*
 
 // Paged attention. Every request's queries are taken as rows r = query * group + head of one
 // key/value head (group = query heads per key/value head).
+// n / d for n in [0, 2^31) as a product and a shift: m = ceil(2^(31 + s) / d), s = ceil(log2 d),
+// is off by less than 2^s / d, at most one in n m / 2^(31 + s) before the floor's next step.
+struct FastDiv {
+  uint32_t d = 1, m = 0, s = 0;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t div) : d(div) {
+    while ((1u << s) < d) ++s;
+    if (s > 0) m = (uint32_t)((((uint64_t)1 << (31 + s)) + d - 1) / d);
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ int32_t operator()(int32_t n) const {
+    return s == 0 ? n : (int32_t)(__umulhi((uint32_t)n, m) >> (s - 1));
+  }
+#endif
+};
+
 struct AttnArgs {
   const void* q;
   void* o;
@@ -66,7 +82,8 @@ struct AttnArgs {
   int64_t q_stride, o_stride;  // elements
   const int32_t *cu_q, *kv_len, *block_table;
   const float *k_scale, *v_scale;
-  int32_t max_blocks, num_pages, page_size, hkv, group, head_dim;
+  int32_t max_blocks, num_pages, page_size, page_shift, hkv, group, head_dim;
+  FastDiv by_group;            // rows to queries
   int32_t num_seqs, num_tokens, max_q_len, max_kv_len;
   int32_t causal;
   float scale_log2;            // score scale times log2(e)

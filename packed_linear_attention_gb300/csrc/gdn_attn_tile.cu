@@ -26,10 +26,11 @@
 // the running maximum passes from one group to the other, warp by warp, through shared memory
 // and a pair of named barriers. 8-15 operands: V tiles, and the next unit's Q, whose bf16 rows
 // a bulk copy brings to shared memory while this unit runs and which moves to tensor memory
-// when its last S is done; 16 the producer (units, K tiles, Q rows); 17 the MMA issuer; two
-// idle (register shares move by whole groups of four warps). S is free again as soon as a
-// group holds it in registers, so S is issued two tiles ahead of P V. Units come from a
-// counter, heaviest rows of a request first.
+// when its last S is done; 16 the producer (units, K tiles, Q rows); 17 issues S, 18 P V (the
+// twenty products of a tile, issued one after another between the waits of both, took one warp
+// longer than the tensor pipe); one idle (register shares move by whole groups of four warps).
+// S is free again as soon as a group holds it in registers. Units come from a counter, heaviest
+// rows of a request first.
 // Every wait is bounded; after one gave up the block's warps leave at their unit's end.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -50,7 +51,7 @@ using namespace ptx;
 
 constexpr int kRows = kTileRows;          // query rows of a unit (the MMA's M)
 constexpr int kSoftWarps = 8, kAuxWarps = 8;
-constexpr int kProducer = kSoftWarps + kAuxWarps, kIssuer = kProducer + 1;
+constexpr int kProducer = kSoftWarps + kAuxWarps, kIssuerS = kProducer + 1, kIssuerO = kProducer + 2;
 constexpr int kWarps = 20, kThreads = 32 * kWarps;
 // Registers of a thread: 640 threads are launched with 96; the softmax warps take what the
 // others give (256 * 120 + 256 * 88 + 128 * 64 = 640 * 96).
@@ -98,7 +99,7 @@ constexpr int kDone = 4;
 struct Smem {
   uint64_t kfull[kMaxStages], kempty[kMaxStages];
   uint64_t pfull[2], sfull[2], odone[kDone], hfull[4];
-  uint64_t sfree, qfull, qempty, ofree, drain, rawfull, rawempty;
+  uint64_t sfree, qfull, qempty, ofree, drain[2], rawfull, rawempty;
   uint64_t mfull[kMeta];
   uint64_t ufull[2], uempty[2];
   Unit unit[2];
@@ -115,7 +116,7 @@ struct Smem {
 
 template <int D>
 struct Shape {
-  static constexpr int SK = D == 256 ? 5 : 8;                   // K stages
+  static constexpr int SK = D == 256 ? 4 : 8;                   // K stages
   static constexpr int NH = D == 256 ? 2 : 4;                   // V tiles in f16
   static constexpr uint32_t kTileBytes = BN * D;                // one e4m3 tile
   static constexpr uint32_t kHBytes = 2 * BN * D;
@@ -123,7 +124,8 @@ struct Shape {
   static constexpr uint32_t OFF_K = 0;
   static constexpr uint32_t OFF_H = OFF_K + SK * kTileBytes;
   static constexpr uint32_t OFF_RAW = OFF_H + NH * kHBytes;
-  static constexpr uint32_t OFF_SM = OFF_RAW + kRows * kRawPitch;
+  static constexpr uint32_t OFF_OUT = OFF_RAW + kRows * kRawPitch;  // a warp's rows on their way out
+  static constexpr uint32_t OFF_SM = OFF_OUT + kSoftWarps * 2048;
   static constexpr uint32_t kSmem = OFF_SM + sizeof(Smem);
   static_assert(kSmem <= 227 * 1024, "shared memory of a block");
   static constexpr uint32_t kRowPitch = D == 64 ? 64 : 128;     // bytes of a row in a region
@@ -139,29 +141,44 @@ struct TileParams {
   int32_t* counter;   // units taken
 };
 
+// Up to 1,024 polls of a phase in a short loop of assembly: there are twenty waits, the kernel's
+// roles share one instruction cache, and the same as C++ took 1 KB of it each.
+__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p, q;\n .reg .b32 n;\n"
+      " mov.u32 n, 1024;\n"
+      "POLL:\n"
+      " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " @p bra DONE;\n"
+      " sub.u32 n, n, 1;\n"
+      " setp.ne.u32 q, n, 0;\n"
+      " @q bra POLL;\n"
+      "DONE:\n"
+      " selp.b32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // A whole warp waits for a phase; one answer for the warp. After any wait of the block gave up
-// (a second), none waits again. (The slow part is not a function of its own: a call in the
-// softmax loop would leave too few registers.)
+// (about a second), none waits again.
 __device__ __forceinline__ bool wait_or_die(uint64_t* bar, uint32_t parity, Smem& sm,
                                             int32_t* status) {
-  bool ok = mbar_try_wait(bar, parity);
-  if (!__all_sync(0xffffffffu, ok)) {
-    volatile int32_t* dead = &sm.dead;
-    const uint64_t t0 = global_ns();
+  volatile int32_t* dead = &sm.dead;
+  bool ok = poll(smem_u32(bar), parity);
+  uint32_t t0 = 0;  // globaltimer's low word over 2^10: about microseconds
 #pragma unroll 1
-    for (uint32_t i = 1; !ok; ++i) {
-      ok = mbar_try_wait(bar, parity);
-      if ((i & 63u) == 0u && !ok) {
-        if (*dead) break;
-        if (global_ns() - t0 > kWaitNs) {
-          *dead = 1;
-          raise_status(status, GDN_ERR_DEVICE_TIMEOUT);
-        }
-      }
+  while (!ok && !*dead) {
+    const uint32_t t = (uint32_t)(global_ns() >> 10) | 1u;
+    if (t0 == 0) t0 = t;
+    if (t - t0 > (uint32_t)(kWaitNs >> 10)) {
+      *dead = 1;
+      raise_status(status, GDN_ERR_DEVICE_TIMEOUT);
     }
-    ok = __all_sync(0xffffffffu, ok);
+    ok = poll(smem_u32(bar), parity);
   }
-  return ok;
+  return __all_sync(0xffffffffu, ok);
 }
 
 __device__ __forceinline__ int32_t seq_units(const AttnArgs& a, const AttnSeq& s) {
@@ -183,6 +200,12 @@ __device__ __forceinline__ void pair_arrive(int id) {
 }
 __device__ __forceinline__ void pair_wait(int id) {
   asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
@@ -220,7 +243,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.pfull[i], kSoftWarps / 2);
       mbar_init(&sm.ufull[i], 1);
-      mbar_init(&sm.uempty[i], kSoftWarps + kAuxWarps + 1);
+      mbar_init(&sm.uempty[i], kSoftWarps + kAuxWarps + 2);
     }
     for (int i = 0; i < kDone; ++i) mbar_init(&sm.odone[i], 1);
     for (int i = 0; i < Sh::NH; ++i) mbar_init(&sm.hfull[i], kAuxWarps);
@@ -233,7 +256,8 @@ tile_kernel(const __grid_constant__ TileParams p) {
     mbar_init(&sm.ofree, kSoftWarps);
     mbar_init(&sm.rawfull, 1);
     mbar_init(&sm.rawempty, kAuxWarps);
-    mbar_init(&sm.drain, 1);
+    mbar_init(&sm.drain[0], 1);
+    mbar_init(&sm.drain[1], 1);
     fence_mbar_init();
   }
   const int chunks = (a.num_seqs + 31) / 32;
@@ -245,7 +269,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
     if (lane == 0) sm.coarse[c + 1] = n;
   }
   if (bad && blockIdx.x == 0) raise_status(a.status, GDN_ERR_INVALID_ARGUMENT);
-  if (warp == kIssuer) {
+  if (warp == kIssuerS) {
     tmem_alloc(&sm.tmem, 512);
     tmem_relinquish();
   }
@@ -320,7 +344,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
           u.first = (row_tiles - 1 - k % row_tiles) * kRows;  // the rows that see most come first
           last = min(u.q_len * a.group, u.first + kRows) - 1;
           const AttnSeq q = {u.row0, u.q_len, u.kv_len};
-          u.tiles = (attn_limit(a, q, last / a.group) + BN - 1) / BN;
+          u.tiles = (attn_limit(a, q, a.by_group(last)) + BN - 1) / BN;
         }
         const int slot = n & 1;
         if (!wait_or_die(&sm.uempty[slot], ((n >> 1) & 1u) ^ 1u, sm, a.status)) break;
@@ -337,7 +361,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
           mbar_arrive_expect_tx(&sm.rawfull, (uint32_t)(last - u.first + 1) * 2 * D);
         __syncwarp();
         for (int32_t r = u.first + lane; r <= last; r += 32) {
-          const int32_t i = r / a.group, h = r - i * a.group;
+          const int32_t i = a.by_group(r), h = r - i * a.group;
           bulk_load(smem + Sh::OFF_RAW + (r - u.first) * Sh::kRawPitch,
                     static_cast<const __nv_bfloat16*>(a.q) + (int64_t)(u.row0 + i) * a.q_stride +
                         (int64_t)(u.head * a.group + h) * D,
@@ -351,7 +375,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
           int32_t id = -1;
           float ks = 0.f, vs = 0.f;
           if (tok < u.kv_len && tok < u.tiles * BN) {
-            id = table[tok / a.page_size];
+            id = table[tok >> a.page_shift];
             if (id >= 0 && id < a.num_pages) {
               ks = a.k_scale[(int64_t)id * a.hkv + u.head];
               vs = a.v_scale[(int64_t)id * a.hkv + u.head];
@@ -362,6 +386,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
               raise_status(a.status, GDN_ERR_INVALID_ARGUMENT);
             }
           }
+#pragma unroll 1
           for (int j = 0; j < kBatchTiles && tb + j < u.tiles; ++j, ++it) {
             const int first = j * kGroups;
             const bool mine = lane >= first && lane < first + kGroups;
@@ -378,7 +403,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
             if (mine) {
               sm.meta[ms].ks[lane - first] = ks;
               sm.meta[ms].lv[lane - first] =
-                  log2f(fmaxf(vref > 0.f ? vs / vref : 0.f, kMinRatio) * kProbScale);
+                  __log2f(fmaxf(vref > 0.f ? __fdividef(vs, vref) : 0.f, kMinRatio) * kProbScale);
               sm.meta[ms].id[lane - first] = id;
             }
             if (lane == 0) {
@@ -410,11 +435,10 @@ tile_kernel(const __grid_constant__ TileParams p) {
                             kWaitLimit);
         if (raws > 0) mbar_wait_bounded(&sm.rawfull, (raws - 1) & 1u, kWaitLimit);
       }
-    } else if (warp == kIssuer) {
-      // ---- MMA issue
-      constexpr uint32_t id_s = idesc_f16(kRows, BN, 0, 0), id_o = idesc_f16(kRows, D, 0, 1);
+    } else if (warp == kIssuerS) {
+      // ---- S = Q K^T
+      constexpr uint32_t id_s = idesc_f16(kRows, BN, 0, 0);
       const uint64_t k_desc = f8_desc<D>(smem_u32(smem) + Sh::OFF_K);
-      const uint64_t h_desc = smem_desc_sw128(smem_u32(smem) + Sh::OFF_H, BN * 128, 1024);
       const uint32_t tm = __shfl_sync(0xffffffffu, tbase, 0), el = elect_lane();
       uint32_t g = 0, nq = 0;
       Unit u;
@@ -422,9 +446,12 @@ tile_kernel(const __grid_constant__ TileParams p) {
         const int32_t tiles = __shfl_sync(0xffffffffu, u.tiles, 0);
         if (tiles == 0) continue;
         bool ok = wait_or_die(&sm.qfull, nq & 1u, sm, a.status);
-        auto issue_s = [&](uint32_t j, bool last) {  // j: tile number since the start
-          const int st = j % Sh::SK;
-          ok = ok && wait_or_die(&sm.kfull[st], (j / Sh::SK) & 1u, sm, a.status) &&
+        ++nq;
+#pragma unroll 1
+        for (int32_t i = 0; i < tiles && ok; ++i) {
+          const uint32_t j = g + i;  // tile number since the start
+          const uint32_t st = j % Sh::SK;
+          ok = wait_or_die(&sm.kfull[st], (j / Sh::SK) & 1u, sm, a.status) &&
                wait_or_die(&sm.sfree, (j & 1u) ^ 1u, sm, a.status);
           tc_fence_after();
           if (ok) {
@@ -439,19 +466,34 @@ tile_kernel(const __grid_constant__ TileParams p) {
             if (el) {
               mma_commit(&sm.kempty[st]);
               mma_commit(&sm.sfull[j & 1u]);
-              if (last) mma_commit(&sm.qempty);
+              if (i + 1 == tiles) mma_commit(&sm.qempty);
             }
           }
           __syncwarp();
-        };
-        issue_s(g, tiles == 1);
-        if (tiles > 1) issue_s(g + 1, tiles == 2);
-        for (int32_t i = 0; i < tiles && ok; ++i, ++g) {
-          if (i + 2 < tiles) issue_s(g + 2, i + 3 == tiles);
-          const uint32_t b = g & 1u, hb = g % Sh::NH;
-          ok = ok && wait_or_die(&sm.hfull[hb], (g / Sh::NH) & 1u, sm, a.status) &&
-               wait_or_die(&sm.pfull[b], (g >> 1) & 1u, sm, a.status) &&
-               (i > 0 || wait_or_die(&sm.ofree, (nq & 1u) ^ 1u, sm, a.status));
+        }
+        g += tiles;
+        if (!ok) break;
+      }
+      // what was issued has completed before the block's memory goes
+      if (el) mma_commit(&sm.drain[0]);
+      mbar_wait_bounded(&sm.drain[0], 0, kWaitLimit);
+    } else if (warp == kIssuerO) {
+      // ---- O += P V
+      constexpr uint32_t id_o = idesc_f16(kRows, D, 0, 1);
+      const uint64_t h_desc = smem_desc_sw128(smem_u32(smem) + Sh::OFF_H, BN * 128, 1024);
+      const uint32_t tm = __shfl_sync(0xffffffffu, tbase, 0), el = elect_lane();
+      uint32_t g = 0, nq = 0;
+      Unit u;
+      while (next_unit(u)) {
+        const int32_t tiles = __shfl_sync(0xffffffffu, u.tiles, 0);
+        if (tiles == 0) continue;
+        bool ok = wait_or_die(&sm.ofree, (nq & 1u) ^ 1u, sm, a.status);
+        ++nq;
+#pragma unroll 1
+        for (int32_t i = 0; i < tiles && ok; ++i) {
+          const uint32_t j = g + i, b = j & 1u, hb = j % Sh::NH;
+          ok = wait_or_die(&sm.hfull[hb], (j / Sh::NH) & 1u, sm, a.status) &&
+               wait_or_die(&sm.pfull[b], (j >> 1) & 1u, sm, a.status);
           tc_fence_after();
           if (ok) {
             const uint64_t hd = h_desc + (uint32_t)(hb * (Sh::kHBytes / 16));
@@ -460,16 +502,15 @@ tile_kernel(const __grid_constant__ TileParams p) {
             for (int k = 0; k < BN / 16; ++k)
               warp_mma_f16_ts(el, tm + Sh::TM_O, pa + 8 * k, hd + k * (2048 / 16), id_o,
                               i > 0 || k > 0);
-            if (el) mma_commit(&sm.odone[g % kDone]);
+            if (el) mma_commit(&sm.odone[j % kDone]);
           }
           __syncwarp();
         }
-        ++nq;
+        g += tiles;
         if (!ok) break;
       }
-      // what was issued has completed before the block's memory goes
-      if (el) mma_commit(&sm.drain);
-      mbar_wait_bounded(&sm.drain, 0, kWaitLimit);
+      if (el) mma_commit(&sm.drain[1]);
+      mbar_wait_bounded(&sm.drain[1], 0, kWaitLimit);
     }
   } else if (warp >= kSoftWarps) {
     // ---- operands: Q of a unit, then its V tiles
@@ -564,32 +605,35 @@ tile_kernel(const __grid_constant__ TileParams p) {
           mbar_arrive(&sm.rawempty);
         }
         ++nq;
-        // V tiles: the next tile's loads are on their way while this one is stored
+        // V tiles: a tile's loads are on their way while the one before is stored
         uint4 v[kV];
-        auto load_v = [&](int32_t t, uint32_t j) {  // j: tile number since the start
-          ok = ok && wait_or_die(&sm.mfull[j % kMeta], (j / kMeta) & 1u, sm, a.status);
-          const TileMeta& m = sm.meta[j % kMeta];
-#pragma unroll
-          for (int k = 0; k < kV; ++k) {
-            const int32_t tok = vt + k * kStep, pos = t * BN + tok, id = m.id[tok >> 4];
-            v[k] = make_uint4(0, 0, 0, 0);  // past the cached tokens, or without a page: zeros
-            if (ok && id >= 0 && pos < u.kv_len)
-              v[k] = *reinterpret_cast<const uint4*>(
-                  vbase + ((int64_t)(id * a.hkv + u.head) * a.page_size + (pos & page_mask)) * D);
-          }
-        };
-        load_v(0, g);
-        for (int32_t t = 0; t < u.tiles && ok; ++t, ++g) {
-          const uint32_t hb = g % Sh::NH;
-          if (g >= Sh::NH) {  // P V(g - NH) has read this buffer
-            const uint32_t o = g - Sh::NH;
-            ok = wait_or_die(&sm.odone[o % kDone], (o / kDone) & 1u, sm, a.status);
-          }
-          uint8_t* dst = smem + Sh::OFF_H + hb * Sh::kHBytes;
+#pragma unroll 1
+        for (int32_t t = -1; t < u.tiles && ok; ++t) {
           uint4 cur[kV];
 #pragma unroll
           for (int k = 0; k < kV; ++k) cur[k] = v[k];
-          if (t + 1 < u.tiles) load_v(t + 1, g + 1);
+          if (t + 1 < u.tiles) {
+            const uint32_t j = g + t + 1;  // tile number since the start
+            ok = wait_or_die(&sm.mfull[j % kMeta], (j / kMeta) & 1u, sm, a.status);
+            const TileMeta& m = sm.meta[j % kMeta];
+            const int32_t pos = (t + 1) * BN + vt;
+#pragma unroll
+            for (int k = 0; k < kV; ++k) {
+              const int32_t id = m.id[(vt + k * kStep) >> 4];
+              v[k] = make_uint4(0, 0, 0, 0);  // past the cached tokens, or without a page: zeros
+              if (ok && id >= 0 && pos + k * kStep < u.kv_len)
+                v[k] = *reinterpret_cast<const uint4*>(
+                    vbase + ((int64_t)(id * a.hkv + u.head) * a.page_size +
+                             ((pos + k * kStep) & page_mask)) * D);
+            }
+          }
+          if (t < 0) continue;
+          const uint32_t j = g + t, hb = j % Sh::NH;
+          if (j >= Sh::NH) {  // P V(j - NH) has read this buffer
+            const uint32_t o = j - Sh::NH;
+            ok = wait_or_die(&sm.odone[o % kDone], (o / kDone) & 1u, sm, a.status) && ok;
+          }
+          uint8_t* dst = smem + Sh::OFF_H + hb * Sh::kHBytes;
 #pragma unroll
           for (int k = 0; k < kV; ++k) {
             const uint32_t s4[4] = {cur[k].x, cur[k].y, cur[k].z, cur[k].w};
@@ -608,6 +652,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.hfull[hb]);
         }
+        g += u.tiles;
       }
       more = next_unit(u);
     }
@@ -628,10 +673,10 @@ tile_kernel(const __grid_constant__ TileParams p) {
       if (named_any(kSoftBar, kSoftThreads, !more)) break;
       const int32_t rows = u.q_len * a.group, row = u.first + r;
       const bool live = row < rows;
-      const int32_t query = live ? row / a.group : 0;
+      const int32_t query = live ? a.by_group(row) : 0;
       const AttnSeq s = {u.row0, u.q_len, u.kv_len};
       const int32_t limit = live ? attn_limit(a, s, query) : u.kv_len;
-      const int32_t min_limit = attn_limit(a, s, u.first / a.group);
+      const int32_t min_limit = attn_limit(a, s, a.by_group(u.first));
       float m = -GDN_INF, l = 0.f, vref = 0.f, rs = 0.f;
       const uint32_t first = (g & 1u) ^ grp;  // this group's first tile of the unit
       for (int32_t i = (int32_t)first; i < u.tiles; i += 2) {
@@ -652,19 +697,27 @@ tile_kernel(const __grid_constant__ TileParams p) {
         vref = meta.vref;
         const uint32_t absent = meta.absent;
         if ((i + 1) * BN > min_limit || absent != 0) {
-          const int32_t room = limit - i * BN;
 #pragma unroll
-          for (int e = 0; e < BN; ++e)
-            if (e >= room || ((absent >> (e / 16)) & 1u)) x[e] = 0xff800000u;
+          for (int q = 0; q < kGroups; ++q) {
+            const int32_t room = (absent >> q) & 1u ? 0 : limit - i * BN - 16 * q;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (e >= room) x[16 * q + e] = 0xff800000u;
+          }
         }
         // the tile's largest score: within a group of 16 tokens before its key scale
         float f[kGroups], top = -GDN_INF;
 #pragma unroll
         for (int q = 0; q < kGroups; ++q) {
           f[q] = fmaxf(meta.ks[q] * rs, 1e-37f);  // above 0: what is masked stays -inf
-          float y = __uint_as_float(x[16 * q]);
+          float y = __uint_as_float(x[16 * q]), y2 = __uint_as_float(x[16 * q + 1]);
 #pragma unroll
-          for (int e = 1; e < 16; ++e) y = fmaxf(y, __uint_as_float(x[16 * q + e]));
+          for (int e = 2; e < 16; e += 4) {  // two chains of three-input maxima
+            y = max3(y, __uint_as_float(x[16 * q + e]), __uint_as_float(x[16 * q + e + 1]));
+            if (e + 2 < 16)
+              y2 = max3(y2, __uint_as_float(x[16 * q + e + 2]), __uint_as_float(x[16 * q + e + 3]));
+          }
+          y = fmaxf(y, y2);
           top = fmaxf(top, y * f[q]);
         }
         if (i > 0) {
@@ -754,8 +807,20 @@ tile_kernel(const __grid_constant__ TileParams p) {
       const float inv = l == 0.f ? 0.f : vref / (l * kProbScale);
       const int64_t tok = u.row0 + query;
       const int hq = u.head * a.group + (row - query * a.group);
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.o) + tok * a.o_stride +
-                           (int64_t)hq * D + grp * (D / 2);
+      // through shared memory, 32 columns at a time, so that four lanes store 64 consecutive
+      // bytes of a row (a thread storing its own row would touch 32 lines with every store)
+      uint8_t* stage = smem + Sh::OFF_OUT + warp * 2048;
+      __nv_bfloat16* out[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int32_t ro = u.first + 32 * (warp & 3) + 8 * k + (lane >> 2);
+        const int32_t qo = a.by_group(ro);
+        out[k] = ro < rows ? static_cast<__nv_bfloat16*>(a.o) +
+                                 (int64_t)(u.row0 + qo) * a.o_stride +
+                                 (int64_t)(u.head * a.group + ro - qo * a.group) * D +
+                                 grp * (D / 2) + 8 * (lane & 3)
+                           : nullptr;
+      }
 #pragma unroll 1
       for (int c = 0; c < D / 2; c += 32) {
         uint32_t o[32];
@@ -766,20 +831,28 @@ tile_kernel(const __grid_constant__ TileParams p) {
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0;
         }
-        if (live) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            uint32_t w[4];
+        for (int e = 0; e < 4; ++e) {
+          uint32_t w[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const __nv_bfloat162 y =
-                  __floats2bfloat162_rn(__uint_as_float(o[e + 2 * k]) * inv,
-                                        __uint_as_float(o[e + 2 * k + 1]) * inv);
-              w[k] = *reinterpret_cast<const uint32_t*>(&y);
-            }
-            *reinterpret_cast<uint4*>(out + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int k = 0; k < 4; ++k) {
+            const __nv_bfloat162 y =
+                __floats2bfloat162_rn(__uint_as_float(o[8 * e + 2 * k]) * inv,
+                                      __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
+            w[k] = *reinterpret_cast<const uint32_t*>(&y);
           }
+          *reinterpret_cast<uint4*>(stage + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4)) =
+              make_uint4(w[0], w[1], w[2], w[3]);
         }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int rr = 8 * k + (lane >> 2);
+          const uint4 w = *reinterpret_cast<const uint4*>(
+              stage + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4));
+          if (out[k]) *reinterpret_cast<uint4*>(out[k] + c) = w;
+        }
+        __syncwarp();
       }
       if (live && grp == 0 && a.lse)
         a.lse[tok * (a.hkv * a.group) + hq] = l == 0.f ? -GDN_INF : (m + log2f(l)) * kLn2;
@@ -792,7 +865,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kIssuer) {
+  if (warp == kIssuerS) {
     tc_fence_after();
     tmem_dealloc(tbase, 512);
   }
