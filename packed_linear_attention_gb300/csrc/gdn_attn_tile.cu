@@ -141,43 +141,34 @@ struct TileParams {
   int32_t* counter;   // units taken
 };
 
-// Up to 1,024 polls of a phase in a short loop of assembly: there are twenty waits, the kernel's
-// roles share one instruction cache, and the same as C++ took 1 KB of it each.
-__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity) {
+// A whole warp waits for a phase; one answer for the warp. At most 2^20 polls, of which one
+// that fails takes 0.8 us (measured), so about a second; after any wait of the block gave up,
+// none waits again. One short loop in assembly: there are twenty of these, the kernel's roles
+// share one instruction cache, and as C++ each took up to 1 KB of it.
+__device__ __forceinline__ bool wait_or_die(uint64_t* bar, uint32_t parity, Smem& sm,
+                                            int32_t* status) {
   uint32_t ok;
   asm volatile(
-      "{\n .reg .pred p, q;\n .reg .b32 n;\n"
-      " mov.u32 n, 1024;\n"
+      "{\n .reg .pred p, q;\n .reg .b32 n, d;\n"
+      " mov.u32 n, %5;\n"
       "POLL:\n"
       " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
       " @p bra DONE;\n"
+      " ld.volatile.shared.b32 d, [%3];\n"
+      " setp.ne.u32 q, d, 0;\n"
+      " @q bra DONE;\n"
       " sub.u32 n, n, 1;\n"
       " setp.ne.u32 q, n, 0;\n"
       " @q bra POLL;\n"
+      " st.volatile.shared.b32 [%3], 1;\n"
+      " setp.ne.u64 q, %4, 0;\n"
+      " @q red.global.max.s32 [%4], %6;\n"
       "DONE:\n"
       " selp.b32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
-      : "r"(bar), "r"(parity)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(smem_u32(&sm.dead)), "l"(status), "n"(1 << 20),
+        "n"((int)GDN_ERR_DEVICE_TIMEOUT)
       : "memory");
-  return ok != 0;
-}
-// A whole warp waits for a phase; one answer for the warp. After any wait of the block gave up
-// (about a second), none waits again.
-__device__ __forceinline__ bool wait_or_die(uint64_t* bar, uint32_t parity, Smem& sm,
-                                            int32_t* status) {
-  volatile int32_t* dead = &sm.dead;
-  bool ok = poll(smem_u32(bar), parity);
-  uint32_t t0 = 0;  // globaltimer's low word over 2^10: about microseconds
-#pragma unroll 1
-  while (!ok && !*dead) {
-    const uint32_t t = (uint32_t)(global_ns() >> 10) | 1u;
-    if (t0 == 0) t0 = t;
-    if (t - t0 > (uint32_t)(kWaitNs >> 10)) {
-      *dead = 1;
-      raise_status(status, GDN_ERR_DEVICE_TIMEOUT);
-    }
-    ok = poll(smem_u32(bar), parity);
-  }
   return __all_sync(0xffffffffu, ok);
 }
 
@@ -394,7 +385,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
             const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, box));
             const float top = __uint_as_float(
                 __reduce_max_sync(0xffffffffu, mine ? __float_as_uint(vs) : 0u));
-            const float fac = top > vref ? vref / top : 1.f;
+            const float fac = top > vref ? __fdividef(vref, top) : 1.f;
             vref = fmaxf(vref, top);
             const int ms = it % kMeta, kst = it % Sh::SK;
             const uint32_t gone = __ballot_sync(0xffffffffu, mine && id < 0) >> first;
@@ -804,7 +795,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
         wait_or_die(&sm.odone[last % kDone], (last / kDone) & 1u, sm, a.status);
         tc_fence_after();
       }
-      const float inv = l == 0.f ? 0.f : vref / (l * kProbScale);
+      const float inv = l == 0.f ? 0.f : __fdividef(vref, l * kProbScale);
       const int64_t tok = u.row0 + query;
       const int hq = u.head * a.group + (row - query * a.group);
       // through shared memory, 32 columns at a time, so that four lanes store 64 consecutive
@@ -855,7 +846,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
         __syncwarp();
       }
       if (live && grp == 0 && a.lse)
-        a.lse[tok * (a.hkv * a.group) + hq] = l == 0.f ? -GDN_INF : (m + log2f(l)) * kLn2;
+        a.lse[tok * (a.hkv * a.group) + hq] = l == 0.f ? -GDN_INF : (m + __log2f(l)) * kLn2;
       if (u.tiles > 0) {
         tc_fence_before();
         __syncwarp();
