@@ -58,9 +58,10 @@ constexpr int kWarps = 20, kThreads = 32 * kWarps;
 constexpr int kSoftRegs = 120, kAuxRegs = 88, kMiscRegs = 64;
 static_assert(256 * kSoftRegs + 256 * kAuxRegs + 128 * kMiscRegs == kThreads * 96, "registers");
 constexpr int kSoftThreads = 32 * kSoftWarps, kAuxThreads = 32 * kAuxWarps;
-constexpr int kMeta = 16;                 // ring of tile scales: K stages and three more
+// Scales and pages are looked up for a batch of tiles at a time, a 16-token group to a lane. The
+// ring holds 16 batches: at least 16 tiles, more than the roles are apart (K stages and four).
+constexpr int kBatch = 8, kBatches = 16;
 constexpr int kCoarse = kMaxSeqs / 32;    // prefix sums are kept for every 32 requests
-constexpr uint32_t kWaitLimit = 1u << 24;
 constexpr float kLazyMax = 8.f;
 constexpr float kProbScale = 128.f;
 constexpr float kMinRatio = 9.094947e-13f;  // 2^-40: value scales below that of vref count as it
@@ -100,10 +101,10 @@ struct Smem {
   uint64_t kfull[kMaxStages], kempty[kMaxStages];
   uint64_t pfull[2], sfull[2], odone[kDone], hfull[4];
   uint64_t sfree, qfull, qempty, ofree, drain[2], rawfull, rawempty;
-  uint64_t mfull[kMeta];
+  uint64_t mfull[kBatches];
   uint64_t ufull[2], uempty[2];
   Unit unit[2];
-  TileMeta meta[kMeta];
+  TileMeta meta[kBatches][kBatch];
   float m[kRows];            // running maximum on its way between the softmax groups
   float exchange_v[kRows];
   float exchange_l[2][kRows];
@@ -172,6 +173,13 @@ __device__ __forceinline__ bool wait_or_die(uint64_t* bar, uint32_t parity, Smem
   return __all_sync(0xffffffffu, ok);
 }
 
+// The same for what must have landed before the block ends, also after a wait gave up.
+__device__ __noinline__ void wait_landed(uint32_t bar, uint32_t parity) {
+#pragma unroll 1
+  for (uint32_t i = 0; i < (1u << 20); ++i)
+    if (mbar_try_wait(bar, parity)) return;
+}
+
 __device__ __forceinline__ int32_t seq_units(const AttnArgs& a, const AttnSeq& s) {
   if (s.q_len <= a.split_q) return 0;
   return a.hkv * ((s.q_len * a.group + kRows - 1) / kRows);
@@ -238,7 +246,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
     }
     for (int i = 0; i < kDone; ++i) mbar_init(&sm.odone[i], 1);
     for (int i = 0; i < Sh::NH; ++i) mbar_init(&sm.hfull[i], kAuxWarps);
-    for (int i = 0; i < kMeta; ++i) mbar_init(&sm.mfull[i], 1);
+    for (int i = 0; i < kBatches; ++i) mbar_init(&sm.mfull[i], 1);
     mbar_init(&sm.sfull[0], 1);  // a barrier for each softmax group: it waits for every second S
     mbar_init(&sm.sfull[1], 1);
     mbar_init(&sm.sfree, kSoftWarps / 2);
@@ -294,12 +302,11 @@ tile_kernel(const __grid_constant__ TileParams p) {
       // ---- units, pages and scales, Q rows, K tiles
       const int box_rows = min(a.page_size, BN), per_box = box_rows / 16;
       const uint32_t box_bytes = (uint32_t)box_rows * D;
-      constexpr int kBatchTiles = 32 / kGroups;
-      uint32_t it = 0, raws = 0;
+      static_assert(kBatch * kGroups == 32, "a group to a lane");
+      uint32_t it = 0, raws = 0, nb = 0;
+      int32_t next_x = lane == 0 ? atomicAdd(p.counter, 1) : 0;
       for (uint32_t n = 0;; ++n) {
-        int32_t x = 0;
-        if (lane == 0) x = atomicAdd(p.counter, 1);
-        x = __shfl_sync(0xffffffffu, x, 0);
+        const int32_t x = __shfl_sync(0xffffffffu, next_x, 0);
         Unit u = {-1, 0, 0, 0, 0, 0, 0, 0};
         int32_t last = 0;
         if (x < total) {
@@ -318,7 +325,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
             mine = seq_units(a, s);
           }
           int32_t inc = mine;
-#pragma unroll
+#pragma unroll 1
           for (int o = 1; o < 32; o <<= 1) {
             const int32_t y = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += y;
@@ -358,73 +365,89 @@ tile_kernel(const __grid_constant__ TileParams p) {
                         (int64_t)(u.head * a.group + h) * D,
                     2 * D, &sm.rawfull);
         }
+        if (lane == 0) next_x = atomicAdd(p.counter, 1);  // its answer has the unit's time
         const int32_t* table = a.block_table + (int64_t)u.seq * a.max_blocks;
-        float vref = 0.f;
-        bool ok = true;
-        for (int32_t tb = 0; tb < u.tiles && ok; tb += kBatchTiles) {
-          const int32_t tok = tb * BN + lane * 16;
-          int32_t id = -1;
-          float ks = 0.f, vs = 0.f;
-          if (tok < u.kv_len && tok < u.tiles * BN) {
-            id = table[tok >> a.page_shift];
-            if (id >= 0 && id < a.num_pages) {
-              ks = a.k_scale[(int64_t)id * a.hkv + u.head];
-              vs = a.v_scale[(int64_t)id * a.hkv + u.head];
-              if (!(ks >= 0.f)) ks = 0.f;
-              if (!(vs >= 0.f)) vs = 0.f;
-            } else {
-              id = -1;
-              raise_status(a.status, GDN_ERR_INVALID_ARGUMENT);
-            }
+        const int32_t end = min(u.kv_len, u.tiles * BN);
+        auto page_of = [&](int32_t tok) { return tok < end ? table[tok >> a.page_shift] : -1; };
+        auto scales_of = [&](int32_t tok, int32_t& id, float& ks, float& vs) {
+          ks = vs = 0.f;
+          if (id >= 0 && id < a.num_pages) {
+            ks = a.k_scale[(int64_t)id * a.hkv + u.head];
+            vs = a.v_scale[(int64_t)id * a.hkv + u.head];
+          } else {
+            if (tok < end) raise_status(a.status, GDN_ERR_INVALID_ARGUMENT);
+            id = -1;
           }
+        };
+        float ks, vs, vref = 0.f;
+        int32_t id = page_of(16 * lane);
+        scales_of(16 * lane, id, ks, vs);
+        bool ok = true;
 #pragma unroll 1
-          for (int j = 0; j < kBatchTiles && tb + j < u.tiles; ++j, ++it) {
-            const int first = j * kGroups;
-            const bool mine = lane >= first && lane < first + kGroups;
-            const bool box = mine && (lane - first) % per_box == 0 && id >= 0;
-            const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, box));
-            const float top = __uint_as_float(
-                __reduce_max_sync(0xffffffffu, mine ? __float_as_uint(vs) : 0u));
-            const float fac = top > vref ? __fdividef(vref, top) : 1.f;
-            vref = fmaxf(vref, top);
-            const int ms = it % kMeta, kst = it % Sh::SK;
-            const uint32_t gone = __ballot_sync(0xffffffffu, mine && id < 0) >> first;
+        for (int32_t tb = 0; tb < u.tiles && ok; tb += kBatch, ++nb) {
+          const int32_t tok = tb * BN + lane * 16;
+          // values that are no scales count as zeros
+          ks = ks >= 0.f ? ks : 0.f;
+          vs = vs >= 0.f ? vs : 0.f;
+          // largest value scale up to each tile of the batch
+          float top = fmaxf(vs, __shfl_xor_sync(0xffffffffu, vs, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) {
+            const float y = __shfl_up_sync(0xffffffffu, top, o);
+            if (lane >= o) top = fmaxf(top, y);
+          }
+          top = fmaxf(top, vref);
+          float before = __shfl_up_sync(0xffffffffu, top, 4);
+          if (lane < 4) before = vref;
+          vref = __shfl_sync(0xffffffffu, top, 31);
+          const uint32_t gone = __ballot_sync(0xffffffffu, id < 0);
+          TileMeta& m = sm.meta[nb % kBatches][lane >> 2];
+          m.ks[lane & 3] = ks;
+          m.lv[lane & 3] =
+              __log2f(fmaxf(top > 0.f ? __fdividef(vs, top) : 0.f, kMinRatio) * kProbScale);
+          m.id[lane & 3] = id;
+          if ((lane & 3) == 0) {
+            m.absent = (gone >> lane) & 15u;
+            m.vref = top;
+            m.vfac = top > before ? __fdividef(before, top) : 1.f;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.mfull[nb % kBatches]);
+          const bool box = (lane & (per_box - 1)) == 0 && id >= 0;
+          const uint32_t boxes = __ballot_sync(0xffffffffu, box);
+          const int32_t y = (int32_t)(((int64_t)id * a.hkv + u.head) * a.page_size +
+                                      (tok & (a.page_size - 1)));
+          const uint32_t at = (uint32_t)(lane & 3) * 16 * Sh::kRowPitch;
+          int32_t next_id = page_of(tok + kBatch * BN);
+#pragma unroll 1
+          for (int j = 0; j < kBatch && tb + j < u.tiles; ++j, ++it) {
+            const int kst = it % Sh::SK;
             ok = wait_or_die(&sm.kempty[kst], ((it / Sh::SK) & 1u) ^ 1u, sm, a.status);
             if (!ok) break;
-            if (mine) {
-              sm.meta[ms].ks[lane - first] = ks;
-              sm.meta[ms].lv[lane - first] =
-                  __log2f(fmaxf(vref > 0.f ? __fdividef(vs, vref) : 0.f, kMinRatio) * kProbScale);
-              sm.meta[ms].id[lane - first] = id;
-            }
-            if (lane == 0) {
-              sm.meta[ms].absent = gone & ((1u << kGroups) - 1);
-              sm.meta[ms].vref = vref;
-              sm.meta[ms].vfac = fac;
-            }
-            const int32_t y = (int32_t)(((int64_t)id * a.hkv + u.head) * a.page_size +
-                                        tok % a.page_size);
-            const uint32_t at = (uint32_t)(lane - first) * 16 * Sh::kRowPitch;
+            if (lane == 0)
+              mbar_arrive_expect_tx(&sm.kfull[kst],
+                                    __popc((boxes >> (kGroups * j)) & 15u) * box_bytes);
             __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(&sm.mfull[ms]);
-              mbar_arrive_expect_tx(&sm.kfull[kst], boxes * box_bytes);
-            }
-            __syncwarp();
-            if (box)
+            if (box && (lane >> 2) == j) {
+              uint8_t* dst = smem + Sh::OFF_K + kst * Sh::kTileBytes + at;
 #pragma unroll
               for (int r = 0; r < (D + 127) / 128; ++r)
-                tma_load_2d(smem + Sh::OFF_K + kst * Sh::kTileBytes + r * (BN * 128) + at, &p.tk,
-                            128 * r, y, &sm.kfull[kst]);
+                tma_load_2d(dst + r * (BN * 128), &p.tk, 128 * r, y, &sm.kfull[kst]);
+            }
           }
+          id = next_id;
+          scales_of(tok + kBatch * BN, id, ks, vs);
         }
         if (!ok) break;
       }
       if (sm.dead) {  // copies may be in flight: let them land
-        for (uint32_t k = 0; k < Sh::SK && k < it; ++k)
-          mbar_wait_bounded(&sm.kfull[(it - 1 - k) % Sh::SK], ((it - 1 - k) / Sh::SK) & 1u,
-                            kWaitLimit);
-        if (raws > 0) mbar_wait_bounded(&sm.rawfull, (raws - 1) & 1u, kWaitLimit);
+#pragma unroll 1
+        for (uint32_t k = 0; k < Sh::SK && k < it; ++k) {
+          const uint32_t x = it - 1 - k;
+          wait_landed(smem_u32(&sm.kfull[x % Sh::SK]), (x / Sh::SK) & 1u);
+        }
+        if (raws > 0) wait_landed(smem_u32(&sm.rawfull), (raws - 1) & 1u);
       }
     } else if (warp == kIssuerS) {
       // ---- S = Q K^T
@@ -467,7 +490,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
       }
       // what was issued has completed before the block's memory goes
       if (el) mma_commit(&sm.drain[0]);
-      mbar_wait_bounded(&sm.drain[0], 0, kWaitLimit);
+      wait_landed(smem_u32(&sm.drain[0]), 0);
     } else if (warp == kIssuerO) {
       // ---- O += P V
       constexpr uint32_t id_o = idesc_f16(kRows, D, 0, 1);
@@ -501,13 +524,13 @@ tile_kernel(const __grid_constant__ TileParams p) {
         if (!ok) break;
       }
       if (el) mma_commit(&sm.drain[1]);
-      mbar_wait_bounded(&sm.drain[1], 0, kWaitLimit);
+      wait_landed(smem_u32(&sm.drain[1]), 0);
     }
   } else if (warp >= kSoftWarps) {
     // ---- operands: Q of a unit, then its V tiles
     give_registers<kAuxRegs>();
     const int aw = warp - kSoftWarps, at = tid - kSoftThreads;
-    uint32_t g = 0, nq = 0;
+    uint32_t g = 0, nq = 0, nb = 0;
     Unit u;
     // a thread's place in V tiles: 16 channels of every (256 * 16 / D)-th token. Eight lanes
     // take four chunks of two neighbouring tokens, whose f16 chunks fall on distinct banks.
@@ -604,9 +627,10 @@ tile_kernel(const __grid_constant__ TileParams p) {
 #pragma unroll
           for (int k = 0; k < kV; ++k) cur[k] = v[k];
           if (t + 1 < u.tiles) {
-            const uint32_t j = g + t + 1;  // tile number since the start
-            ok = wait_or_die(&sm.mfull[j % kMeta], (j / kMeta) & 1u, sm, a.status);
-            const TileMeta& m = sm.meta[j % kMeta];
+            const uint32_t mb = nb + (uint32_t)(t + 1) / kBatch;
+            if ((t + 1) % kBatch == 0)
+              ok = wait_or_die(&sm.mfull[mb % kBatches], (mb / kBatches) & 1u, sm, a.status);
+            const TileMeta& m = sm.meta[mb % kBatches][(t + 1) % kBatch];
             const int32_t pos = (t + 1) * BN + vt;
 #pragma unroll
             for (int k = 0; k < kV; ++k) {
@@ -644,6 +668,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
           if (lane == 0) mbar_arrive(&sm.hfull[hb]);
         }
         g += u.tiles;
+        nb += (u.tiles + kBatch - 1) / kBatch;
       }
       more = next_unit(u);
     }
@@ -656,7 +681,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
     const int from_other = kPairBar + 2 * (warp & 3) + (int)grp,
               to_other = kPairBar + 2 * (warp & 3) + (int)(grp ^ 1u);
     const float scale = fabsf(a.scale_log2);
-    uint32_t g = 0, nq = 0;
+    uint32_t g = 0, nq = 0, nb = 0;
     Unit u;
     while (true) {
       const bool more = next_unit(u);
@@ -672,10 +697,12 @@ tile_kernel(const __grid_constant__ TileParams p) {
       const uint32_t first = (g & 1u) ^ grp;  // this group's first tile of the unit
       for (int32_t i = (int32_t)first; i < u.tiles; i += 2) {
         const uint32_t j = g + i, b = grp;  // tile number since the start; its P buffer
-        wait_or_die(&sm.mfull[j % kMeta], (j / kMeta) & 1u, sm, a.status);
+        const uint32_t mb = nb + (uint32_t)i / kBatch;
+        if (i % kBatch < 2)  // this group's first tile of the batch
+          wait_or_die(&sm.mfull[mb % kBatches], (mb / kBatches) & 1u, sm, a.status);
         wait_or_die(&sm.sfull[grp], (j >> 1) & 1u, sm, a.status);
         tc_fence_after();
-        const TileMeta& meta = sm.meta[j % kMeta];
+        const TileMeta& meta = sm.meta[mb % kBatches][i % kBatch];
         uint32_t x[BN];
         tmem_ld32(t_row + Sh::TM_S, reinterpret_cast<uint32_t(&)[32]>(x[0]));
         tmem_ld32(t_row + Sh::TM_S + 32, reinterpret_cast<uint32_t(&)[32]>(x[32]));
@@ -777,6 +804,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
         if (lane == 0) mbar_arrive(&sm.pfull[b]);
       }
       g += u.tiles;
+      nb += (u.tiles + kBatch - 1) / kBatch;
       // ---- output: the groups' sums meet, each writes half of the row
       if (u.tiles > 0) {
         ++nq;
