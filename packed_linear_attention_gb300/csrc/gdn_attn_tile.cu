@@ -84,13 +84,14 @@ struct Unit {
   int32_t tiles, pad;
 };
 
-struct TileMeta {
+struct __align__(16) TileMeta {
   float ks[kGroups];    // key scale of each 16-token group
   float lv[kGroups];    // log2 of what P is weighted with: value scale / vref * kProbScale
   int32_t id[kGroups];  // page; negative: absent, or past the cached tokens
   uint32_t absent;      // bit g: group g is absent
   float vref;           // largest value scale of the unit so far
   float vfac;           // what the accumulator is multiplied by as vref grew
+  float pad;
 };
 
 constexpr int kMaxStages = 8;
@@ -142,12 +143,12 @@ struct TileParams {
   int32_t* counter;   // units taken
 };
 
-// A whole warp waits for a phase; one answer for the warp. At most 2^20 polls, of which one
+// A lane's wait for a phase (wait_or_die: one answer for the warp). At most 2^20 polls, of which one
 // that fails takes 0.8 us (measured), so about a second; after any wait of the block gave up,
 // none waits again. One short loop in assembly: there are twenty of these, the kernel's roles
 // share one instruction cache, and as C++ each took up to 1 KB of it.
-__device__ __forceinline__ bool wait_or_die(uint64_t* bar, uint32_t parity, Smem& sm,
-                                            int32_t* status) {
+__device__ __forceinline__ uint32_t wait_lane(uint64_t* bar, uint32_t parity, Smem& sm,
+                                              int32_t* status) {
   uint32_t ok;
   asm volatile(
       "{\n .reg .pred p, q;\n .reg .b32 n, d;\n"
@@ -170,7 +171,17 @@ __device__ __forceinline__ bool wait_or_die(uint64_t* bar, uint32_t parity, Smem
       : "r"(smem_u32(bar)), "r"(parity), "r"(smem_u32(&sm.dead)), "l"(status), "n"(1 << 20),
         "n"((int)GDN_ERR_DEVICE_TIMEOUT)
       : "memory");
-  return __all_sync(0xffffffffu, ok);
+  return ok;
+}
+__device__ __forceinline__ bool wait_or_die(uint64_t* bar, uint32_t parity, Smem& sm,
+                                            int32_t* status) {
+  return __all_sync(0xffffffffu, wait_lane(bar, parity, sm, status));
+}
+// For the softmax warps, which run their unit's course whether or not a wait gave up.
+__device__ __forceinline__ void wait_on(uint64_t* bar, uint32_t parity, Smem& sm,
+                                        int32_t* status) {
+  wait_lane(bar, parity, sm, status);
+  __syncwarp();
 }
 
 // The same for what must have landed before the block ends, also after a wait gave up.
@@ -699,10 +710,18 @@ tile_kernel(const __grid_constant__ TileParams p) {
         const uint32_t j = g + i, b = grp;  // tile number since the start; its P buffer
         const uint32_t mb = nb + (uint32_t)i / kBatch;
         if (i % kBatch < 2)  // this group's first tile of the batch
-          wait_or_die(&sm.mfull[mb % kBatches], (mb / kBatches) & 1u, sm, a.status);
-        wait_or_die(&sm.sfull[grp], (j >> 1) & 1u, sm, a.status);
-        tc_fence_after();
+          wait_on(&sm.mfull[mb % kBatches], (mb / kBatches) & 1u, sm, a.status);
+        // the tile's scales, while S is on its way
         const TileMeta& meta = sm.meta[mb % kBatches][i % kBatch];
+        const float4 ks4 = *reinterpret_cast<const float4*>(meta.ks);
+        const float4 lv4 = *reinterpret_cast<const float4*>(meta.lv);
+        const uint32_t absent = meta.absent;
+        const float vfac = meta.vfac;
+        vref = meta.vref;
+        wait_on(&sm.sfull[grp], (j >> 1) & 1u, sm, a.status);
+        tc_fence_after();
+        if (i == (int32_t)first)
+          rs = scale * __uint_as_float((uint32_t)(sm.row_exp[nq & 1u][r] + 127) << 23);
         uint32_t x[BN];
         tmem_ld32(t_row + Sh::TM_S, reinterpret_cast<uint32_t(&)[32]>(x[0]));
         tmem_ld32(t_row + Sh::TM_S + 32, reinterpret_cast<uint32_t(&)[32]>(x[32]));
@@ -710,10 +729,6 @@ tile_kernel(const __grid_constant__ TileParams p) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.sfree);
-        if (i == (int32_t)first)
-          rs = scale * __uint_as_float((uint32_t)(sm.row_exp[nq & 1u][r] + 127) << 23);
-        vref = meta.vref;
-        const uint32_t absent = meta.absent;
         if ((i + 1) * BN > min_limit || absent != 0) {
 #pragma unroll
           for (int q = 0; q < kGroups; ++q) {
@@ -724,10 +739,12 @@ tile_kernel(const __grid_constant__ TileParams p) {
           }
         }
         // the tile's largest score: within a group of 16 tokens before its key scale
+        const float ksq[kGroups] = {ks4.x, ks4.y, ks4.z, ks4.w};
+        const float lvq[kGroups] = {lv4.x, lv4.y, lv4.z, lv4.w};
         float f[kGroups], top = -GDN_INF;
 #pragma unroll
         for (int q = 0; q < kGroups; ++q) {
-          f[q] = fmaxf(meta.ks[q] * rs, 1e-37f);  // above 0: what is masked stays -inf
+          f[q] = fmaxf(ksq[q] * rs, 1e-37f);  // above 0: what is masked stays -inf
           float y = __uint_as_float(x[16 * q]), y2 = __uint_as_float(x[16 * q + 1]);
 #pragma unroll
           for (int e = 2; e < 16; e += 4) {  // two chains of three-input maxima
@@ -744,7 +761,6 @@ tile_kernel(const __grid_constant__ TileParams p) {
           m = sm.m[r];
           l *= was == m ? 1.f : ex2(was - m);  // 0 before this group's first tile
         }
-        const float vfac = meta.vfac;
         if (__any_sync(0xffffffffu, top > m + kLazyMax) || (vfac != 1.f && i > 0)) {
           // a new maximum for these rows, the accumulator and sum follow
           const float both = fmaxf(top, m);
@@ -753,7 +769,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
           l *= fm;
           if (i > 0) {
             const uint32_t o = j - 1;  // P V of the tile before
-            wait_or_die(&sm.odone[o % kDone], (o / kDone) & 1u, sm, a.status);
+            wait_on(&sm.odone[o % kDone], (o / kDone) & 1u, sm, a.status);
             tc_fence_after();
             const float fo = fm * vfac;
 #pragma unroll 1
@@ -772,11 +788,6 @@ tile_kernel(const __grid_constant__ TileParams p) {
           sm.m[r] = m;
           pair_arrive(to_other);
         }
-        if (j >= 2) {  // P V(j - 2) has read this group's buffer
-          const uint32_t o = j - 2;
-          wait_or_die(&sm.odone[o % kDone], (o / kDone) & 1u, sm, a.status);
-          tc_fence_after();
-        }
         // P = 2^(s - m + lv): weighted for the product, 2^-lv for the sum
         const float mu = m == -GDN_INF ? 0.f : m;
 #pragma unroll
@@ -784,7 +795,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
           uint32_t ph[16];
 #pragma unroll
           for (int q = 2 * h; q < 2 * h + 2; ++q) {
-            const float lv = meta.lv[q], off = lv - mu, fq = f[q];
+            const float lv = lvq[q], off = lv - mu, fq = f[q];
             float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
             for (int e = 16 * q; e < 16 * q + 16; e += 2) {
@@ -795,6 +806,11 @@ tile_kernel(const __grid_constant__ TileParams p) {
               ph[e / 2 - 16 * h] = f16x2(pr.x, pr.y);
             }
             l = fmaf(sum.x + sum.y, ex2(-lv), l);
+          }
+          if (h == 0 && j >= 2) {  // P V(j - 2) has read this group's buffer
+            const uint32_t o = j - 2;
+            wait_on(&sm.odone[o % kDone], (o / kDone) & 1u, sm, a.status);
+            tc_fence_after();
           }
           tmem_st16(t_row + Sh::TM_P + b * (BN / 2) + 16 * h, ph);
         }
@@ -820,7 +836,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
         m = mf;
         named_sync(kSoftBar, kSoftThreads);
         l = sm.exchange_l[0][r] + sm.exchange_l[1][r];
-        wait_or_die(&sm.odone[last % kDone], (last / kDone) & 1u, sm, a.status);
+        wait_on(&sm.odone[last % kDone], (last / kDone) & 1u, sm, a.status);
         tc_fence_after();
       }
       const float inv = l == 0.f ? 0.f : __fdividef(vref, l * kProbScale);
@@ -840,38 +856,46 @@ tile_kernel(const __grid_constant__ TileParams p) {
                                  grp * (D / 2) + 8 * (lane & 3)
                            : nullptr;
       }
+      constexpr int kOut = D == 64 ? 32 : 64;  // columns loaded at a time
 #pragma unroll 1
-      for (int c = 0; c < D / 2; c += 32) {
-        uint32_t o[32];
+      for (int c = 0; c < D / 2; c += kOut) {
+        uint32_t o[kOut];
         if (u.tiles > 0) {
-          tmem_ld32(t_row + Sh::TM_O + grp * (D / 2) + c, o);
+#pragma unroll
+          for (int h = 0; h < kOut; h += 32)
+            tmem_ld32(t_row + Sh::TM_O + grp * (D / 2) + c + h,
+                      reinterpret_cast<uint32_t(&)[32]>(o[h]));
           tmem_ld_wait();
         } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0;
+          for (int e = 0; e < kOut; ++e) o[e] = 0;
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t w[4];
+        for (int h = 0; h < kOut; h += 32) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 z = mul2(make_float2(__uint_as_float(o[h + 8 * e + 2 * k]),
+                                                __uint_as_float(o[h + 8 * e + 2 * k + 1])),
+                                    make_float2(inv, inv));
+              const __nv_bfloat162 y = __floats2bfloat162_rn(z.x, z.y);
+              w[k] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+            *reinterpret_cast<uint4*>(stage + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          __syncwarp();
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const __nv_bfloat162 y =
-                __floats2bfloat162_rn(__uint_as_float(o[8 * e + 2 * k]) * inv,
-                                      __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
-            w[k] = *reinterpret_cast<const uint32_t*>(&y);
+            const int rr = 8 * k + (lane >> 2);
+            const uint4 w = *reinterpret_cast<const uint4*>(
+                stage + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4));
+            if (out[k]) *reinterpret_cast<uint4*>(out[k] + c + h) = w;
           }
-          *reinterpret_cast<uint4*>(stage + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4)) =
-              make_uint4(w[0], w[1], w[2], w[3]);
+          __syncwarp();
         }
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int rr = 8 * k + (lane >> 2);
-          const uint4 w = *reinterpret_cast<const uint4*>(
-              stage + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4));
-          if (out[k]) *reinterpret_cast<uint4*>(out[k] + c) = w;
-        }
-        __syncwarp();
       }
       if (live && grp == 0 && a.lse)
         a.lse[tok * (a.hkv * a.group) + hq] = l == 0.f ? -GDN_INF : (m + __log2f(l)) * kLn2;
