@@ -316,7 +316,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
       static_assert(kBatch * kGroups == 32, "a group to a lane");
       uint32_t it = 0, raws = 0, nb = 0;
       int32_t next_x = lane == 0 ? atomicAdd(p.counter, 1) : 0;
-      for (uint32_t n = 0;; ++n) {
+      for (uint32_t n = 0; n <= (uint32_t)total; ++n) {
         const int32_t x = __shfl_sync(0xffffffffu, next_x, 0);
         Unit u = {-1, 0, 0, 0, 0, 0, 0, 0};
         int32_t last = 0;
@@ -362,6 +362,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
           mbar_arrive(&sm.ufull[slot]);
         }
         if (u.seq < 0) break;
+        if (lane == 0) next_x = atomicAdd(p.counter, 1);  // its answer has the unit's time
         if (u.tiles == 0) continue;
         // the unit's rows of Q, one copy each, when the last unit's have moved on
         if (!wait_or_die(&sm.rawempty, (raws & 1u) ^ 1u, sm, a.status)) break;
@@ -376,7 +377,6 @@ tile_kernel(const __grid_constant__ TileParams p) {
                         (int64_t)(u.head * a.group + h) * D,
                     2 * D, &sm.rawfull);
         }
-        if (lane == 0) next_x = atomicAdd(p.counter, 1);  // its answer has the unit's time
         const int32_t* table = a.block_table + (int64_t)u.seq * a.max_blocks;
         const int32_t end = min(u.kv_len, u.tiles * BN);
         auto page_of = [&](int32_t tok) { return tok < end ? table[tok >> a.page_shift] : -1; };
