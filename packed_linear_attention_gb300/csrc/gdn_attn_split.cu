@@ -57,14 +57,9 @@ constexpr size_t kSmemPerCta = 112 * 1024;      // two blocks share an SM's 227 
 
 #define GDN_INF __int_as_float(0x7f800000)
 
-struct SplitDesc {  // what a worker's last, unfinished unit is; count 0: none
-  int32_t seq, head, row_tile, count;
-};
-
 struct SplitParams {
   AttnArgs a;
   CUtensorMap tk, tv;
-  SplitDesc* desc;    // [workers]
   float* part;        // [2 workers][RB (D + 2)]
   int32_t stages;
   uint32_t off_q, off_red, off_pre;  // shared-memory map after the stages
@@ -205,6 +200,7 @@ split_kernel(const __grid_constant__ SplitParams p) {
   float* red = reinterpret_cast<float*>(smem + p.off_red);  // [RB][kRed]
   int32_t* pre = reinterpret_cast<int32_t*>(smem + p.off_pre);  // [num_seqs + 1]
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the second kernel may come
   // ---- prefix sums of the requests' items (every block for itself)
   {
     const int per = (a.num_seqs + kThreads - 1) / kThreads, b0 = tid * per;
@@ -241,12 +237,9 @@ split_kernel(const __grid_constant__ SplitParams p) {
     if (b1 == a.num_seqs && b0 < b1) pre[a.num_seqs] = at;
     __syncthreads();
   }
-  // G workers share W items, every one at least one
+  // G workers share W items
   const int64_t W = pre[a.num_seqs], G = min((int64_t)gridDim.x, W);
-  if (blockIdx.x >= G) {
-    if (tid == 0) p.desc[blockIdx.x].count = 0;
-    return;
-  }
+  if (blockIdx.x >= G) return;
   const int32_t w0 = (int32_t)(W * blockIdx.x / G), w1 = (int32_t)(W * (blockIdx.x + 1) / G);
   uint32_t it = 0;  // tiles since the start: stage and phase
   const int S = p.stages;
@@ -265,7 +258,7 @@ split_kernel(const __grid_constant__ SplitParams p) {
         int32_t id = -1;
         float ks = -1.f, vs = 0.f;
         if (tok < s.kv_len && tok < g.t1 * kTile) {
-          id = table[tok / a.page_size];
+          id = table[tok >> a.page_shift];
           if (id >= 0 && id < a.num_pages) {
             ks = a.k_scale[(int64_t)id * a.hkv + g.head];
             vs = a.v_scale[(int64_t)id * a.hkv + g.head];
@@ -290,7 +283,7 @@ split_kernel(const __grid_constant__ SplitParams p) {
           if (box) {
             uint8_t* dk = smem + (uint32_t)st * 2 * kTileBytes;
             const int32_t y = (int32_t)(((int64_t)id * a.hkv + g.head) * a.page_size +
-                                        tok % a.page_size);
+                                        (tok & (a.page_size - 1)));
             const uint32_t row = (uint32_t)(lane - first) * 16;
 #pragma unroll
             for (int r = 0; r < (D + 127) / 128; ++r) {
@@ -313,20 +306,18 @@ split_kernel(const __grid_constant__ SplitParams p) {
 
   // ---- consumers
   const int c = lane & 3, n8 = lane >> 2;
-  SplitDesc desc = {0, 0, 0, 0};
   for (int32_t w = w0; w < w1;) {
     AttnSeq s;
     const Segment g = find_segment<RB>(a, pre, w, w1, s);
-    const int32_t wbeg = w;
     w += g.t1 - g.t0;
     const int32_t rows = s.q_len * a.group, r0 = g.row_tile * RB;
     // queries of the unit as f16 operands, a row per warp and round
     for (int r = warp; r < RB; r += kWarps) {
       const int32_t row = r0 + r;
       const bool live = row < rows;
-      const int32_t i = live ? row / a.group : 0;
+      const int32_t i = live ? a.by_group(row) : 0;
       const T* src = static_cast<const T*>(a.q) + (int64_t)(s.row0 + i) * a.q_stride +
-                     (int64_t)(g.head * a.group + (live ? row % a.group : 0)) * D;
+                     (int64_t)(g.head * a.group + (live ? (row - a.by_group(row) * a.group) : 0)) * D;
       constexpr int kQuads = (D / 4 + 31) / 32;
       float x[kQuads][4];
       float amax = 0.f;
@@ -552,7 +543,7 @@ split_kernel(const __grid_constant__ SplitParams p) {
         for (int x = 1; x < kWarps; ++x) M = fmaxf(M, sm.m[x][8 * n + 2 * c + e]);
         f[n][e] = m[n][e] == -GDN_INF ? 0.f : ex2(m[n][e] - M) * (vref / kProbScale);
       }
-    for (int x = 0; x < kWarps; ++x) {
+    for (int x = 0; x < kWarps; ++x) {  // in a fixed order
       if (warp == x) {
 #pragma unroll
         for (int k = 0; k < kSteps; ++k)
@@ -587,8 +578,8 @@ split_kernel(const __grid_constant__ SplitParams p) {
       for (int x = 0; x < kWarps; ++x)
         L += sm.m[x][r] == -GDN_INF ? sm.l[x][r] : sm.l[x][r] * ex2(sm.m[x][r] - M);
       const float inv = !whole ? 1.f : L == 0.f ? 0.f : 1.f / L;
-      const int64_t tok = s.row0 + row / a.group;
-      const int head = g.head * a.group + row % a.group;
+      const int64_t tok = s.row0 + a.by_group(row);
+      const int head = g.head * a.group + (row - a.by_group(row) * a.group);
       for (int quad = lane; quad < D / 4; quad += 32) {
         const float4 v = *reinterpret_cast<const float4*>(red + r * kRed + 4 * quad);
         const float y[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
@@ -604,92 +595,191 @@ split_kernel(const __grid_constant__ SplitParams p) {
         }
       }
     }
-    if (g.t0 == 0 && g.t1 < g.tiles) {  // the unit goes on in later blocks: up to which?
-      const int64_t last = (int64_t)wbeg + g.tiles - 1;
-      int64_t k = last * G / W;
-      while (W * (k + 1) / G <= last) ++k;
-      while (W * k / G > last) --k;
-      desc = {g.seq, g.head, g.row_tile, (int32_t)(k - blockIdx.x + 1)};
-    }
     named_sync(1, 32 * kWarps);  // the next unit writes the shared arrays again
   }
-  if (tid == 0) p.desc[blockIdx.x] = desc;
 }
 
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 constexpr int kMaxWorkers = kCtasPerSm * kMaxSms;
+constexpr int kMaxJoinBlocks = 16384, kBlockRows = 512;
 
-// Joins the pieces of the unit that worker blockIdx.x began and did not finish, row
-// blockIdx.y of it.
-template <typename T, int D, int RB>
+// Joins the pieces of the units that were cut. Where there are few rows (at most kBlockRows; one
+// long context: 152 pieces of 8 rows) a block joins 64 columns of a row, else a warp a row.
+// Which units were cut, and where, follows from the lengths alone, so every block works it out
+// while the first kernel still runs. Measured: 128 requests of 128 to 16,384 tokens 175 us with
+// blocks and 167 us with warps; one of 32,768 tokens 20.6 us with blocks, 31 us with warps.
+template <typename T, int D, int RB, bool kBlocks>
 __global__ void __launch_bounds__(kJoinThreads)
-join_kernel(AttnArgs a, const SplitDesc* desc, const float* part) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces are written
-  __shared__ float weight[kMaxWorkers];
-  __shared__ float red[kJoinThreads / 32];
-  __shared__ float4 sum[kJoinThreads];
-  const SplitDesc d = desc[blockIdx.x];
-  if (d.count == 0) return;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  bool bad = false;
-  const AttnSeq s = attn_seq(a, d.seq, bad);
-  const int r = blockIdx.y;
-  const int32_t row = d.row_tile * RB + r;
-  if (row >= s.q_len * a.group) return;
-  // piece i: the second slot of the first worker, then the first slots of the next ones
-  auto piece = [&](int i) {
-    return part + ((int64_t)2 * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * (RB * (D + 2));
+join_kernel(AttnArgs a, const float* part, int workers) {
+  extern __shared__ int32_t join_smem[];
+  __shared__ int32_t scan[kJoinWarps][2];
+  constexpr int kTeams = kBlocks ? 1 : kJoinWarps;  // rows that a block has in hand at a time
+  constexpr int kTeam = kJoinThreads / kTeams;       // threads of one
+  __shared__ float weight[kTeams][kMaxWorkers];
+  __shared__ float red[kJoinWarps];
+  __shared__ float4 sum[kBlocks ? kJoinThreads : 1];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = a.num_seqs;
+  int32_t* pre = join_smem;       // [n + 1] items before a request
+  int32_t* unit0 = pre + n + 1;   // [n + 1] units before it
+  {
+    const int per = (n + kJoinThreads - 1) / kJoinThreads, b0 = tid * per, b1 = min(n, b0 + per);
+    bool bad = false;
+    auto units_of = [&](const AttnSeq& s) {
+      return s.q_len == 0 || s.q_len > a.split_q ? 0 : a.hkv * ((s.q_len * a.group + RB - 1) / RB);
+    };
+    int32_t items = 0, units = 0;
+    for (int b = b0; b < b1; ++b) {
+      const AttnSeq s = attn_seq(a, b, bad);
+      items += seq_items<RB>(a, s);
+      units += units_of(s);
+    }
+    int32_t x = items, y = units;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) {
+        x += u;
+        y += v;
+      }
+    }
+    if (lane == 31) {
+      scan[warp][0] = x;
+      scan[warp][1] = y;
+    }
+    __syncthreads();
+    x -= items;
+    y -= units;
+    for (int w = 0; w < warp; ++w) {
+      x += scan[w][0];
+      y += scan[w][1];
+    }
+    for (int b = b0; b < b1; ++b) {
+      pre[b] = x;
+      unit0[b] = y;
+      const AttnSeq s = attn_seq(a, b, bad);
+      x += seq_items<RB>(a, s);
+      y += units_of(s);
+    }
+    if (b1 == n && b0 < b1) {
+      pre[n] = x;
+      unit0[n] = y;
+    }
+    __syncthreads();
+  }
+  const int64_t W = pre[n], G = min((int64_t)workers, W);
+  const int64_t jobs = (int64_t)unit0[n] * RB;
+  const int me = tid % kTeam;             // this thread in its row's team
+  float* const w = weight[tid / kTeam];
+  auto worker_of = [&](int64_t item) {
+    int64_t k = item * G / W;
+    while (W * (k + 1) / G <= item) ++k;
+    while (W * k / G > item) --k;
+    return (int)k;
   };
-  auto block_reduce = [&](float x, bool take_max) {
+  auto reduce = [&](float x, bool take_max) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       const float y = __shfl_xor_sync(0xffffffffu, x, o);
       x = take_max ? fmaxf(x, y) : x + y;
     }
-    __syncthreads();
-    if (lane == 0) red[warp] = x;
-    __syncthreads();
-    x = red[0];
+    if constexpr (kBlocks) {
+      __syncthreads();
+      if (lane == 0) red[warp] = x;
+      __syncthreads();
+      x = red[0];
 #pragma unroll
-    for (int w = 1; w < kJoinThreads / 32; ++w) x = take_max ? fmaxf(x, red[w]) : x + red[w];
+      for (int v = 1; v < kJoinWarps; ++v) x = take_max ? fmaxf(x, red[v]) : x + red[v];
+    }
     return x;
   };
-  float M = -GDN_INF;
-  for (int i = tid; i < d.count; i += kJoinThreads) M = fmaxf(M, piece(i)[RB * D + 2 * r]);
-  M = block_reduce(M, true);
-  float L = 0.f;
-  for (int i = tid; i < d.count; i += kJoinThreads) {
-    const float mi = piece(i)[RB * D + 2 * r];
-    const float f = mi == -GDN_INF ? 0.f : ex2(mi - M);
-    weight[i] = f;
-    L += piece(i)[RB * D + 2 * r + 1] * (mi == -GDN_INF ? 1.f : f);
-  }
-  L = block_reduce(L, false);
-  constexpr int kQuads = D / 4, kSets = kJoinThreads / kQuads;
-  const int quad = tid % kQuads, set = tid / kQuads;
-  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int i = set; i < d.count; i += kSets) {
-    const float4 v = *reinterpret_cast<const float4*>(piece(i) + r * D + 4 * quad);
-    const float f = weight[i];
-    y.x += v.x * f; y.y += v.y * f; y.z += v.z * f; y.w += v.w * f;
-  }
-  sum[tid] = y;
-  __syncthreads();
-  if (set == 0) {
-#pragma unroll
-    for (int k = 1; k < kSets; ++k) {
-      const float4 v = sum[k * kQuads + quad];
-      y.x += v.x; y.y += v.y; y.z += v.z; y.w += v.w;
+  bool waited = false;
+  for (int64_t job = (int64_t)blockIdx.x * kTeams + tid / kTeam; job < jobs;
+       job += (int64_t)gridDim.x * kTeams) {
+    const int32_t u = (int32_t)(job / RB), r = (int32_t)(job % RB);
+    int32_t lo = 0, hi = n - 1;
+    while (lo < hi) {  // the last request whose units begin at or before u
+      const int32_t mid = (lo + hi + 1) >> 1;
+      if (unit0[mid] <= u) lo = mid;
+      else hi = mid - 1;
     }
+    bool bad = false;
+    const AttnSeq s = attn_seq(a, lo, bad);
+    const int32_t row_tiles = (s.q_len * a.group + RB - 1) / RB, k = u - unit0[lo];
+    const int32_t row = k % row_tiles * RB + r;
+    if (row >= s.q_len * a.group) continue;  // the whole team, here and below
+    const int64_t tiles = max(1, (s.kv_len + kTile - 1) / kTile), item = pre[lo] + k * tiles;
+    const int w0 = worker_of(item), count = worker_of(item + tiles - 1) - w0 + 1;
+    if (count == 1) continue;  // written by its worker
+    if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");  // the pieces are written
+    waited = true;
+    // piece i: the second slot of the first worker, then the first slots of the next ones
+    auto piece = [&](int i) {
+      return part + ((int64_t)2 * (w0 + i) + (i == 0 ? 1 : 0)) * (RB * (D + 2));
+    };
+    constexpr int kStats = (kMaxWorkers + kTeam - 1) / kTeam;
+    float2 st[kStats];
+    float M = -GDN_INF, L = 0.f;
+#pragma unroll
+    for (int x = 0; x < kStats; ++x) {
+      const int i = me + x * kTeam;
+      st[x] = make_float2(-GDN_INF, 0.f);
+      if (i < count) st[x] = *reinterpret_cast<const float2*>(piece(i) + RB * D + 2 * r);
+      M = fmaxf(M, st[x].x);
+    }
+    M = reduce(M, true);
+#pragma unroll
+    for (int x = 0; x < kStats; ++x) {
+      const int i = me + x * kTeam;
+      const float f = st[x].x == -GDN_INF ? 0.f : ex2(st[x].x - M);
+      if (i < count) w[i] = f;
+      L += st[x].y * (st[x].x == -GDN_INF ? 1.f : f);
+    }
+    __syncwarp();
+    L = reduce(L, false);
     const float inv = L == 0.f ? 0.f : 1.f / L;
-    const int64_t tok = s.row0 + row / a.group;
-    const int head = d.head * a.group + row % a.group;
-    const float z[4] = {y.x * inv, y.y * inv, y.z * inv, y.w * inv};
-    store4(static_cast<T*>(a.o) + tok * a.o_stride + (int64_t)head * D + 4 * quad, z);
-    if (tid == 0 && a.lse)
+    const int32_t query = a.by_group(row);
+    const int64_t tok = s.row0 + query;
+    const int head = k / row_tiles * a.group + row - query * a.group;
+    T* out = static_cast<T*>(a.o) + tok * a.o_stride + (int64_t)head * D;
+    auto add = [&](float4& y, int i, int at) {
+      const float4 v = *reinterpret_cast<const float4*>(piece(i) + r * D + at);
+      const float f = w[i];
+      y.x += v.x * f; y.y += v.y * f; y.z += v.z * f; y.w += v.w * f;
+    };
+    auto put = [&](const float4& y, int at) {
+      const float z[4] = {y.x * inv, y.y * inv, y.z * inv, y.w * inv};
+      store4(out + at, z);
+    };
+    if constexpr (kBlocks) {  // 16 threads for 64 columns, 16 sets of pieces
+      const int at = 64 * blockIdx.y + 4 * (tid & 15), set = tid >> 4;
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+      for (int i = set; i < count; i += kJoinThreads / 16) add(y, i, at);
+      sum[tid] = y;
+      __syncthreads();
+      if (set == 0) {
+#pragma unroll
+        for (int x = 1; x < kJoinThreads / 16; ++x) {
+          const float4 v = sum[16 * x + tid];
+          y.x += v.x; y.y += v.y; y.z += v.z; y.w += v.w;
+        }
+        put(y, at);
+      }
+      __syncthreads();  // weights and sums are written again
+    } else {
+      for (int at = 4 * lane; at < D; at += 128) {
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int i = 0; i < count; ++i) add(y, i, at);
+        put(y, at);
+      }
+      __syncwarp();
+    }
+    if (me == 0 && blockIdx.y == 0 && a.lse)
       a.lse[tok * (a.hkv * a.group) + head] = L == 0.f ? -GDN_INF : (M + log2f(L)) * kLn2;
   }
+  // what follows in the stream waits for this kernel: let it stand for the first one too
+  if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -709,8 +799,7 @@ int launch(const AttnArgs& a, const gdn_kv_cache& c, int num_sms, cudaStream_t s
   const int64_t units = ((int64_t)a.num_tokens * a.group + RB - 1) / RB + a.num_seqs;
   const int64_t items = units * a.hkv * std::max(1, (a.max_kv_len + kTile - 1) / kTile);
   const int workers = (int)std::min<int64_t>((int64_t)kCtasPerSm * num_sms, items);
-  p.desc = reinterpret_cast<SplitDesc*>(a.partials);
-  p.part = a.partials + align_up(sizeof(SplitDesc) * kCtasPerSm * kMaxSms, 256) / sizeof(float);
+  p.part = a.partials;
   const size_t q = (size_t)kTerms * NT * D * 16, red = sizeof(float) * RB * (D + 8);
   const size_t fixed = q + red + align_up(sizeof(int32_t) * (a.num_seqs + 1), 16) + 1024 +
                        sizeof(SmemHead<NT>);
@@ -729,24 +818,32 @@ int launch(const AttnArgs& a, const gdn_kv_cache& c, int num_sms, cudaStream_t s
   split_kernel<T, D, NT><<<workers, kThreads, smem, stream>>>(p);
   if ((e = (int)cudaGetLastError()) != 0 || workers == 1) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(workers, RB);
+  // a unit's rows are at most those of the longest request that this kernel takes
+  const int64_t longest = ((int64_t)std::min(a.max_q_len, a.split_q) * a.group + RB - 1) / RB;
+  const int64_t jobs = std::min(units, a.num_seqs * longest) * a.hkv * RB;
+  const bool blocks = jobs <= kBlockRows;
+  cfg.gridDim = blocks ? dim3((unsigned)jobs, D / 64)
+                       : dim3((unsigned)std::min<int64_t>((jobs + kJoinWarps - 1) / kJoinWarps,
+                                                          kMaxJoinBlocks));
   cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = sizeof(int32_t) * 2 * (a.num_seqs + 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];  // its launch overlaps the first kernel's end
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return (int)cudaLaunchKernelEx(&cfg, join_kernel<T, D, RB>, a, (const SplitDesc*)p.desc,
-                                 (const float*)p.part);
+  return (int)(blocks ? cudaLaunchKernelEx(&cfg, join_kernel<T, D, RB, true>, a,
+                                           (const float*)p.part, workers)
+                      : cudaLaunchKernelEx(&cfg, join_kernel<T, D, RB, false>, a,
+                                           (const float*)p.part, workers));
 }
 
 }  // namespace
 
 size_t split_workspace(const gdn_attn_config& cfg, const gdn_kv_cache& c) {
   const size_t workers = (size_t)kCtasPerSm * kMaxSms;
-  return align_up(sizeof(SplitDesc) * workers, 256) +
-         2 * workers * 8 * max_tiles(c.head_dim) * (c.head_dim + 2) * sizeof(float);
+  return 2 * workers * 8 * max_tiles(c.head_dim) * (c.head_dim + 2) * sizeof(float);
 }
 
 int launch_attn_split(const AttnArgs& a, const gdn_kv_cache& c, bool bf16, int num_sms,

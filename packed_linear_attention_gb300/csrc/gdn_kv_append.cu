@@ -10,18 +10,23 @@
 // several heads of a token, so that the sine and cosine are formed once for them.
 //
 // Append. A unit is a run of rows that land in one page, for one head: keys by one half of a
-// block's 512 threads and values by the other, eight elements a thread, so the run is read
-// once, held in registers (rotated, fp32) while its largest magnitude is found, and stored as
-// codes. With power-of-two scales the division is exact, and a later, larger scale only moves
+// block's 512 threads and values by the other, eight elements a thread. The run's rows are held
+// in registers (rotated, fp32) while its largest magnitude is found, and stored as codes; what
+// a longer run has in front of the last four rows of a thread is read a second time, from L2.
+// (Eight rows a thread, every row read once, leave room for one block on an SM and took 226 us
+// where this takes 118: 32 x 1,024 tokens, 16 query heads over 2 of 256.) The run's sines and
+// cosines are formed once, by all threads, in shared memory. With power-of-two scales the division is exact, and a later, larger scale only moves
 // the exponents of the codes that are already there. No unit list is needed: a row begins a
 // run when its slot opens a page or does not follow the previous row's slot.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "gdn_attn_internal.h"
+#include "gdn_internal.h"
 
 namespace gdn {
 namespace {
@@ -29,7 +34,7 @@ namespace {
 constexpr int kRopeThreads = 256;
 constexpr int kHalf = 256;               // threads for the keys, and as many for the values
 constexpr int kAppendThreads = 2 * kHalf;
-constexpr int kBatch = 8;                // rows of a thread held in registers
+constexpr int kBatch = 4;                // rows of a thread held in registers
 constexpr int kMinExp = -100;            // exponent of the smallest scale
 
 struct RopeDev {  // gdn_rope without what the kernels do not need
@@ -213,7 +218,7 @@ struct AppendDev {
 };
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kAppendThreads)
+__global__ void __launch_bounds__(kAppendThreads, 2)
 append_kernel(const __grid_constant__ AppendDev p, const __grid_constant__ RopeDev r) {
   const AppendArgs& a = p.a;
   const int tid = threadIdx.x;
@@ -227,6 +232,7 @@ append_kernel(const __grid_constant__ AppendDev p, const __grid_constant__ RopeD
   __shared__ int s_nstart, s_n;
   __shared__ uint32_t s_amax[2];
   __shared__ uint32_t s_nan[4];            // rows of v that hold a NaN
+  extern __shared__ __align__(16) float2 s_turn[];  // cos, sin: [rows of a batch][R / 2]
   const int P = a.cache.page_size, H = a.cache.num_kv_heads;
   const int head = (int)(blockIdx.x % H);
   const int64_t row0 = (int64_t)(blockIdx.x / H) * p.rows_per_block;
@@ -238,7 +244,8 @@ append_kernel(const __grid_constant__ AppendDev p, const __grid_constant__ RopeD
   const int R = a.rotate && !is_v ? r.rotary_dim : 0;
   const bool rot = 8 * vec < R;
   // the chunk's pairs and, in the halves layout, the chunk that holds their other elements
-  const int half = R / 2, pair0 = r.adjacent ? 4 * vec : (8 * vec < half ? 8 * vec : 8 * vec - half);
+  const int half = R / 2, pairs = a.rotate ? r.rotary_dim / 2 : 0;
+  const int pair0 = r.adjacent ? 4 * vec : (8 * vec < half ? 8 * vec : 8 * vec - half);
   const int other = 8 * vec < half ? 8 * vec + half : 8 * vec - half;
 
   if (tid == 0) s_nstart = 0;
@@ -267,34 +274,42 @@ append_kernel(const __grid_constant__ AppendDev p, const __grid_constant__ RopeD
     __syncthreads();
     const int n = s_n;
 
-    // rows sub, sub + kRows, ...: the last kBatch passes stay in registers
-    auto fetch = [&](int i, float (&x)[8]) {
+    // cos and sin of a batch's rows (all threads)
+    auto turns = [&](int b) {
+      if (!pairs) return;
+      const int i0 = b * kBatch * kRows, rows = min(n - i0, kBatch * kRows);
+      __syncthreads();  // the batch before has been read
+      for (int x = tid; x < rows * pairs; x += kAppendThreads) {
+        const int i = x / pairs, e = x - i * pairs;
+        float c, s;
+        pair_angle(r, e, a.rope_args.positions + row + i0 + i, a.rope_args.pos_stride, c, s);
+        s_turn[x] = make_float2(c, s);
+      }
+      __syncthreads();
+    };
+    // row i of the run: this thread's eight elements, rotated
+    auto fetch = [&](int i, int b, float (&x)[8]) {
       const T* at = src + (row + i) * stride;
       Raw8<T> w;
       w.load(at + 8 * vec);
       w.get(x);
       if (rot) {
-        const int32_t* pos = a.rope_args.positions + row + i;
-        float c, s;
+        const float2* t = s_turn + (i - b * kBatch * kRows) * pairs + pair0;
         if (r.adjacent) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            pair_angle(r, pair0 + e, pos, a.rope_args.pos_stride, c, s);
             const float x0 = x[2 * e], y0 = x[2 * e + 1];
-            x[2 * e] = x0 * c - y0 * s;
-            x[2 * e + 1] = y0 * c + x0 * s;
+            x[2 * e] = x0 * t[e].x - y0 * t[e].y;
+            x[2 * e + 1] = y0 * t[e].x + x0 * t[e].y;
           }
         } else {
           Raw8<T> w2;
           float y[8];
           w2.load(at + other);
           w2.get(y);
-          const bool low = 8 * vec < half;
+          const float sign = 8 * vec < half ? -1.f : 1.f;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            pair_angle(r, pair0 + e, pos, a.rope_args.pos_stride, c, s);
-            x[e] = low ? x[e] * c - y[e] * s : x[e] * c + y[e] * s;
-          }
+          for (int e = 0; e < 8; ++e) x[e] = x[e] * t[e].x + y[e] * (sign * t[e].y);
         }
       }
     };
@@ -302,10 +317,11 @@ append_kernel(const __grid_constant__ AppendDev p, const __grid_constant__ RopeD
     float x[kBatch][8];
     float amax = 0.f;
     for (int b = 0; b < batches; ++b) {
+      turns(b);
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
         const int i = (b * kBatch + j) * kRows + sub;
-        if (i < n) fetch(i, x[j]);
+        if (i < n) fetch(i, b, x[j]);
       }
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
@@ -368,10 +384,12 @@ append_kernel(const __grid_constant__ AppendDev p, const __grid_constant__ RopeD
       const int i = ((batches - 1) * kBatch + j) * kRows + sub;
       if (i < n) put(i, x[j]);
     }
-    for (int i = sub; i < (batches - 1) * kBatch * kRows; i += kRows) {
-      float y[8];
-      fetch(i, y);
-      put(i, y);
+    for (int b = 0; b + 1 < batches; ++b) {
+      turns(b);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) fetch((b * kBatch + j) * kRows + sub, b, x[j]);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) put((b * kBatch + j) * kRows + sub, x[j]);
     }
     __syncthreads();  // every thread has read the old scale and the flags
     if (lt == 0) *sp = scale;
@@ -438,9 +456,19 @@ int launch_kv_append(const gdn_rope* rope, const AppendArgs& a, bool bf16, void*
   p.append_blocks = (int32_t)append;
   const unsigned blocks = (unsigned)(append + turn);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  int e = 0;
   auto run = [&](auto type, auto dim) {
     using T = decltype(type);
-    append_kernel<T, decltype(dim)::value><<<blocks, kAppendThreads, 0, s>>>(p, r);
+    constexpr int D = decltype(dim)::value;
+    // the rows of a batch: at most a page's
+    const int batch = std::min(a.cache.page_size, kBatch * (kHalf / (D / 8)));
+    const size_t smem = a.rotate ? sizeof(float2) * batch * (r.rotary_dim / 2) : 0;
+    static std::atomic<int> ready[kMaxDevices];
+    e = configure_once(ready, [] {
+      return (int)cudaFuncSetAttribute(append_kernel<T, D>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024);
+    });
+    if (e == 0) append_kernel<T, D><<<blocks, kAppendThreads, smem, s>>>(p, r);
   };
   auto pick = [&](auto type) {
     if (a.cache.head_dim == 64) run(type, std::integral_constant<int, 64>());
@@ -449,7 +477,7 @@ int launch_kv_append(const gdn_rope* rope, const AppendArgs& a, bool bf16, void*
   };
   if (bf16) pick(__nv_bfloat16());
   else pick(float());
-  return (int)cudaGetLastError();
+  return e != 0 ? e : (int)cudaGetLastError();
 }
 
 }  // namespace gdn
