@@ -10,14 +10,15 @@
 // several heads of a token, so that the sine and cosine are formed once for them.
 //
 // Append. A unit is a run of rows that land in one page, for one head: keys by one half of a
-// block's 512 threads and values by the other, eight elements a thread. The run's rows are held
-// in registers (rotated, fp32) while its largest magnitude is found, and stored as codes; what
-// a longer run has in front of the last four rows of a thread is read a second time, from L2.
-// (Eight rows a thread, every row read once, leave room for one block on an SM and took 226 us
-// where this takes 118: 32 x 1,024 tokens, 16 query heads over 2 of 256.) The run's sines and
-// cosines are formed once, by all threads, in shared memory. With power-of-two scales the division is exact, and a later, larger scale only moves
-// the exponents of the codes that are already there. No unit list is needed: a row begins a
-// run when its slot opens a page or does not follow the previous row's slot.
+// block's 512 threads and values by the other, eight elements of a row a thread. The run's rows
+// are loaded at once and stay in registers as they came while its largest magnitude is found;
+// the rotation is cheap enough to be done twice (its sines and cosines are formed once for the
+// run, by all threads, while the rows are on their way; the other half of a pair comes by a
+// shuffle, since a row never leaves a warp). Only runs longer than eight bf16 or four fp32 rows
+// a thread read their first rows a second time. With power-of-two scales the division is exact,
+// and a later, larger scale only moves the exponents of the codes that are already there. No
+// unit list is needed: a row begins a run when its slot opens a page or does not follow the
+// previous row's slot.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -34,7 +35,6 @@ namespace {
 constexpr int kRopeThreads = 256;
 constexpr int kHalf = 256;               // threads for the keys, and as many for the values
 constexpr int kAppendThreads = 2 * kHalf;
-constexpr int kBatch = 4;                // rows of a thread held in registers
 constexpr int kMinExp = -100;            // exponent of the smallest scale
 
 struct RopeDev {  // gdn_rope without what the kernels do not need
@@ -48,7 +48,17 @@ template <typename T>
 struct Raw8;
 template <>
 struct Raw8<__nv_bfloat16> {
+  static constexpr int kRows = 8;  // rows of a thread held in registers
   uint4 w;
+  __device__ Raw8 from_lane(int src) const {
+    Raw8 r;
+    r.w.x = __shfl_sync(0xffffffffu, w.x, src);
+    r.w.y = __shfl_sync(0xffffffffu, w.y, src);
+    r.w.z = __shfl_sync(0xffffffffu, w.z, src);
+    r.w.w = __shfl_sync(0xffffffffu, w.w, src);
+    return r;
+  }
+  __device__ void zero() { w = make_uint4(0, 0, 0, 0); }
   __device__ void load(const __nv_bfloat16* p) { w = *reinterpret_cast<const uint4*>(p); }
   __device__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = w; }
   __device__ void get(float (&x)[8]) const {
@@ -71,7 +81,21 @@ struct Raw8<__nv_bfloat16> {
 };
 template <>
 struct Raw8<float> {
+  static constexpr int kRows = 4;
   float4 a, b;
+  __device__ Raw8 from_lane(int src) const {
+    Raw8 r;
+    r.a.x = __shfl_sync(0xffffffffu, a.x, src);
+    r.a.y = __shfl_sync(0xffffffffu, a.y, src);
+    r.a.z = __shfl_sync(0xffffffffu, a.z, src);
+    r.a.w = __shfl_sync(0xffffffffu, a.w, src);
+    r.b.x = __shfl_sync(0xffffffffu, b.x, src);
+    r.b.y = __shfl_sync(0xffffffffu, b.y, src);
+    r.b.z = __shfl_sync(0xffffffffu, b.z, src);
+    r.b.w = __shfl_sync(0xffffffffu, b.w, src);
+    return r;
+  }
+  __device__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ void load(const float* p) {
     a = reinterpret_cast<const float4*>(p)[0];
     b = reinterpret_cast<const float4*>(p)[1];
@@ -90,8 +114,22 @@ struct Raw8<float> {
   }
 };
 
+// The table in shared memory: lanes look up different pairs, which constant memory would serve
+// one after another (8 us of a 79 us append).
+struct Turns {
+  uint64_t turns[GDN_ROPE_MAX_PAIRS];
+  uint8_t axis[GDN_ROPE_MAX_PAIRS];
+  __device__ void load(const RopeDev& r, int tid, int threads) {  // ends with the block together
+    for (int i = tid; i < r.rotary_dim / 2; i += threads) {
+      turns[i] = r.turns[i];
+      axis[i] = r.axis[i];
+    }
+    __syncthreads();
+  }
+};
+
 // cos and sin of pair i at a token whose positions start at `pos` (one row per axis).
-__device__ __forceinline__ void pair_angle(const RopeDev& r, int i, const int32_t* pos,
+__device__ __forceinline__ void pair_angle(const Turns& r, int i, const int32_t* pos,
                                            int64_t pos_stride, float& c, float& s) {
   const int64_t at = __ldg(pos + r.axis[i] * pos_stride);
   const uint64_t turn = (uint64_t)at * r.turns[i];
@@ -119,8 +157,9 @@ __device__ __forceinline__ void pair_angle(const RopeDev& r, int i, const int32_
 // followed by those of x[1]. Item i < R/16 are the pairs 8i..8i+7 (elements 8i.. and
 // R/2 + 8i.. in the halves layout, 16i.. in the adjacent one), the later items copy.
 template <typename T>
-__device__ __forceinline__ void rope_heads(const RopeDev& r, const RopeArgs& a, int64_t token,
-                                           int item, int head0, int head1) {
+__device__ __forceinline__ void rope_heads(const RopeDev& r, const Turns& table,
+                                           const RopeArgs& a, int64_t token, int item, int head0,
+                                           int head1) {
   const int D = r.head_dim, R = r.rotary_dim;
   const bool turn = 16 * item < R;
   const int lo = turn && !r.adjacent ? 8 * item : 16 * item;
@@ -129,7 +168,7 @@ __device__ __forceinline__ void rope_heads(const RopeDev& r, const RopeArgs& a, 
   if (turn) {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      pair_angle(r, 8 * item + e, a.positions + token, a.pos_stride, c[e], s[e]);
+      pair_angle(table, 8 * item + e, a.positions + token, a.pos_stride, c[e], s[e]);
   }
 #pragma unroll 4
   for (int h = head0; h < head1; ++h) {
@@ -174,20 +213,22 @@ __device__ __forceinline__ void rope_heads(const RopeDev& r, const RopeArgs& a, 
 
 // Block `block` of a rotation over num_tokens tokens, `slices` slices of the heads.
 template <typename T>
-__device__ __forceinline__ void rope_block(const RopeDev& r, const RopeArgs& a, int64_t block,
-                                           int slices, int threads, int tid) {
+__device__ __forceinline__ void rope_block(const RopeDev& r, Turns& table, const RopeArgs& a,
+                                           int64_t block, int slices, int threads, int tid) {
+  table.load(r, tid, threads);
   const int items = r.head_dim / 16, heads = a.x[0].heads + a.x[1].heads;
   const int64_t g = block / slices * threads + tid;
   const int64_t token = g / items;
   if (token >= a.num_tokens) return;
   const int slice = (int)(block % slices), per = (heads + slices - 1) / slices;
-  rope_heads<T>(r, a, token, (int)(g % items), slice * per, min(heads, (slice + 1) * per));
+  rope_heads<T>(r, table, a, token, (int)(g % items), slice * per, min(heads, (slice + 1) * per));
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kRopeThreads)
 rope_kernel(const __grid_constant__ RopeDev r, const __grid_constant__ RopeArgs a, int slices) {
-  rope_block<T>(r, a, blockIdx.x, slices, kRopeThreads, threadIdx.x);
+  __shared__ Turns table;
+  rope_block<T>(r, table, a, blockIdx.x, slices, kRopeThreads, threadIdx.x);
 }
 
 // Two fp32 values as e4m3 codes (nearest even, NaN kept, larger magnitudes to 448).
@@ -222,12 +263,16 @@ __global__ void __launch_bounds__(kAppendThreads, 2)
 append_kernel(const __grid_constant__ AppendDev p, const __grid_constant__ RopeDev r) {
   const AppendArgs& a = p.a;
   const int tid = threadIdx.x;
+  __shared__ Turns table;
   if ((int)blockIdx.x >= p.append_blocks) {
-    rope_block<T>(r, a.rope_args, blockIdx.x - p.append_blocks, p.rope_slices, kAppendThreads, tid);
+    rope_block<T>(r, table, a.rope_args, blockIdx.x - p.append_blocks, p.rope_slices,
+                  kAppendThreads, tid);
     return;
   }
   constexpr int kVec = D / 8;              // threads of a row
   constexpr int kRows = kHalf / kVec;      // rows of a pass
+  constexpr int kBatch = Raw8<T>::kRows;
+  __shared__ int64_t s_slot[1 + 256];      // slots from the row in front of the block's on
   __shared__ int s_start[128];
   __shared__ int s_nstart, s_n;
   __shared__ uint32_t s_amax[2];
@@ -239,98 +284,109 @@ append_kernel(const __grid_constant__ AppendDev p, const __grid_constant__ RopeD
   const int64_t nslots = (int64_t)a.cache.num_pages * P;
   const bool is_v = tid >= kHalf;
   const int lt = tid & (kHalf - 1), vec = lt % kVec, sub = lt / kVec;
-  const T* src = static_cast<const T*>(is_v ? a.v : a.k) + (int64_t)head * D;
+  const T* src = static_cast<const T*>(is_v ? a.v : a.k) + (int64_t)head * D + 8 * vec;
   const int64_t stride = is_v ? a.v_stride : a.k_stride;
-  const int R = a.rotate && !is_v ? r.rotary_dim : 0;
-  const bool rot = 8 * vec < R;
-  // the chunk's pairs and, in the halves layout, the chunk that holds their other elements
-  const int half = R / 2, pairs = a.rotate ? r.rotary_dim / 2 : 0;
-  const int pair0 = r.adjacent ? 4 * vec : (8 * vec < half ? 8 * vec : 8 * vec - half);
-  const int other = 8 * vec < half ? 8 * vec + half : 8 * vec - half;
+  const int R = a.rotate ? r.rotary_dim : 0, half = R / 2;
+  // this thread's chunk in the rotation: its first pair and, in the halves layout, the lane that
+  // holds the pairs' other elements
+  const bool rot = !is_v && 8 * vec < R, low = 8 * vec < half;
+  const int pair0 = r.adjacent ? 4 * vec : low ? 8 * vec : 8 * vec - half;
+  const int lane = tid & 31;
+  const int other = rot && !r.adjacent ? (low ? lane + half / 8 : lane - half / 8) : lane;
 
+  // the block's slots and a page's worth behind them: runs begin here and may end there
+  if (tid <= p.rows_per_block + P) {
+    const int64_t row = row0 + tid - 1;
+    s_slot[tid] = row >= 0 && row < a.num_tokens ? a.slots[row] : -1;
+  }
   if (tid == 0) s_nstart = 0;
-  __syncthreads();
-  if (tid < p.rows_per_block && row0 + tid < a.num_tokens) {
-    const int64_t row = row0 + tid, slot = a.slots[row];
-    if (slot >= nslots) {
+  if (R) table.load(r, tid, kAppendThreads);
+  else __syncthreads();
+  if (tid < p.rows_per_block) {
+    const int64_t slot = s_slot[tid + 1];
+    if (slot >= nslots)
       raise_status(a.status, GDN_ERR_INVALID_ARGUMENT);
-    } else if (slot >= 0 && (row == 0 || slot % P == 0 || a.slots[row - 1] != slot - 1)) {
+    else if (slot >= 0 && ((slot & (P - 1)) == 0 || s_slot[tid] != slot - 1))
       s_start[atomicAdd(&s_nstart, 1)] = tid;
-    }
   }
   __syncthreads();
   const int nstart = s_nstart;
   for (int u = 0; u < nstart; ++u) {  // in any order: the runs are independent
-    const int64_t row = row0 + s_start[u], slot = a.slots[row];
-    const int64_t page = slot / P;
-    const int off = (int)(slot % P);
+    const int at0 = s_start[u];
+    const int64_t row = row0 + at0, slot = s_slot[at0 + 1];
+    const int off = (int)(slot & (P - 1));
+    const int64_t page = (slot - off) / P;
     if (tid == 0) s_n = P - off;
     if (tid < 2) s_amax[tid] = 0;
     if (tid < 4) s_nan[tid] = 0;
     __syncthreads();
-    if (tid > 0 && tid < P - off &&
-        (row + tid >= a.num_tokens || a.slots[row + tid] != slot + tid))
-      atomicMin(&s_n, tid);
+    if (tid > 0 && tid < P - off && s_slot[at0 + 1 + tid] != slot + tid) atomicMin(&s_n, tid);
     __syncthreads();
     const int n = s_n;
+    const int passes = (n + kRows - 1) / kRows, batches = (passes + kBatch - 1) / kBatch;
 
-    // cos and sin of a batch's rows (all threads)
-    auto turns = [&](int b) {
-      if (!pairs) return;
+    Raw8<T> w[kBatch];
+    auto load = [&](int b) {  // rows b kBatch kRows + j kRows + sub
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int i = (b * kBatch + j) * kRows + sub;
+        w[j].zero();
+        if (i < n) w[j].load(src + (row + i) * stride);
+      }
+    };
+    auto turns = [&](int b) {  // cos and sin of the batch's rows (all threads)
+      if (!R) return;
       const int i0 = b * kBatch * kRows, rows = min(n - i0, kBatch * kRows);
       __syncthreads();  // the batch before has been read
-      for (int x = tid; x < rows * pairs; x += kAppendThreads) {
-        const int i = x / pairs, e = x - i * pairs;
-        float c, s;
-        pair_angle(r, e, a.rope_args.positions + row + i0 + i, a.rope_args.pos_stride, c, s);
-        s_turn[x] = make_float2(c, s);
+      const int teams = kAppendThreads / half;
+      if (tid < teams * half) {
+        const int e = tid % half;
+        for (int i = tid / half; i < rows; i += teams) {
+          float c, s;
+          pair_angle(table, e, a.rope_args.positions + row + i0 + i, a.rope_args.pos_stride, c, s);
+          s_turn[i * half + e] = make_float2(c, s);
+        }
       }
       __syncthreads();
     };
-    // row i of the run: this thread's eight elements, rotated
-    auto fetch = [&](int i, int b, float (&x)[8]) {
-      const T* at = src + (row + i) * stride;
-      Raw8<T> w;
-      w.load(at + 8 * vec);
-      w.get(x);
-      if (rot) {
-        const float2* t = s_turn + (i - b * kBatch * kRows) * pairs + pair0;
-        if (r.adjacent) {
+    // the eight elements of the batch's row j, rotated (whole warps; `live`: a row of the run)
+    auto values = [&](int j, bool live, float (&x)[8]) {
+      w[j].get(x);
+      if (!R) return;
+      const Raw8<T> o = w[j].from_lane(other);
+      if (!rot || !live) return;
+      const float2* t = s_turn + (j * kRows + sub) * half + pair0;
+      if (r.adjacent) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float x0 = x[2 * e], y0 = x[2 * e + 1];
-            x[2 * e] = x0 * t[e].x - y0 * t[e].y;
-            x[2 * e + 1] = y0 * t[e].x + x0 * t[e].y;
-          }
-        } else {
-          Raw8<T> w2;
-          float y[8];
-          w2.load(at + other);
-          w2.get(y);
-          const float sign = 8 * vec < half ? -1.f : 1.f;
+        for (int e = 0; e < 4; ++e) {
+          const float x0 = x[2 * e], y0 = x[2 * e + 1];
+          x[2 * e] = x0 * t[e].x - y0 * t[e].y;
+          x[2 * e + 1] = y0 * t[e].x + x0 * t[e].y;
+        }
+      } else {
+        float y[8];
+        o.get(y);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = x[e] * t[e].x + y[e] * (sign * t[e].y);
+        for (int e = 0; e < 8; ++e) {
+          const float s = low ? -t[e].y : t[e].y;
+          x[e] = x[e] * t[e].x + y[e] * s;
         }
       }
     };
-    const int passes = (n + kRows - 1) / kRows, batches = (passes + kBatch - 1) / kBatch;
-    float x[kBatch][8];
     float amax = 0.f;
     for (int b = 0; b < batches; ++b) {
+      load(b);
       turns(b);
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
         const int i = (b * kBatch + j) * kRows + sub;
-        if (i < n) fetch(i, b, x[j]);
-      }
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int i = (b * kBatch + j) * kRows + sub;
-        if (i < n) {
+        if ((b * kBatch + j) * kRows < n) {  // for the whole block
+          float x[8];
+          values(j, i < n, x);
           bool nan = false;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float m = fabsf(x[j][e]);
+            const float m = i < n ? fabsf(x[e]) : 0.f;
             nan = nan || m != m;
             if (m < __int_as_float(0x7f800000)) amax = fmaxf(amax, m);
           }
@@ -340,11 +396,11 @@ append_kernel(const __grid_constant__ AppendDev p, const __grid_constant__ RopeD
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    if ((tid & 31) == 0) atomicMax(&s_amax[is_v], __float_as_uint(amax));
+    if (lane == 0) atomicMax(&s_amax[is_v], __float_as_uint(amax));
     __syncthreads();
     float* sp = (is_v ? a.cache.v_scale : a.cache.k_scale) + page * H + head;
     uint8_t* codes = static_cast<uint8_t*>(is_v ? a.cache.v : a.cache.k) +
-                     ((page * H + head) * P) * (int64_t)D;
+                     ((page * H + head) * P) * (int64_t)D + 8 * vec;
     const float need = exp2_int(scale_exp(__uint_as_float(s_amax[is_v])));
     float scale = need;
     if (off > 0) {
@@ -353,9 +409,9 @@ append_kernel(const __grid_constant__ AppendDev p, const __grid_constant__ RopeD
       if (scale > old) {  // the rows in front move to the larger scale
         const float f = old / scale;
         for (int i = sub; i < off; i += kRows) {
-          uint2* c = reinterpret_cast<uint2*>(codes + (int64_t)i * D + 8 * vec);
-          uint2 w = *c;
-          uint32_t z[4] = {w.x & 0xFFFFu, w.x >> 16, w.y & 0xFFFFu, w.y >> 16};
+          uint2* c = reinterpret_cast<uint2*>(codes + (int64_t)i * D);
+          const uint2 z2 = *c;
+          uint32_t z[4] = {z2.x & 0xFFFFu, z2.x >> 16, z2.y & 0xFFFFu, z2.y >> 16};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float2 y = from_e4m3x2(z[e]);
@@ -366,30 +422,33 @@ append_kernel(const __grid_constant__ AppendDev p, const __grid_constant__ RopeD
       }
     }
     const float inv = 1.f / scale;  // exact: a power of two (or the caller's own old scale)
-    auto put = [&](int i, const float (&x)[8]) {
-      float y[8];
-      const bool bad = (s_nan[i >> 5] >> (i & 31)) & 1u;
+    auto store = [&](int b) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        y[e] = x[e] * inv;
-        if (is_v) y[e] = y[e] == y[e] ? y[e] : 0.f;
-        else if (bad) y[e] = __int_as_float(0x7fffffff);
+      for (int j = 0; j < kBatch; ++j) {
+        const int i = (b * kBatch + j) * kRows + sub;
+        if ((b * kBatch + j) * kRows < n) {  // for the whole block
+          float x[8];
+          values(j, i < n, x);
+          if (i < n) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] *= inv;
+            if ((s_nan[i >> 5] >> (i & 31)) & 1u) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                x[e] = !is_v ? __int_as_float(0x7fffffff) : x[e] == x[e] ? x[e] : 0.f;
+            }
+            *reinterpret_cast<uint2*>(codes + (int64_t)(off + i) * D) =
+                make_uint2(e4m3x2(x[0], x[1]) | e4m3x2(x[2], x[3]) << 16,
+                           e4m3x2(x[4], x[5]) | e4m3x2(x[6], x[7]) << 16);
+          }
+        }
       }
-      *reinterpret_cast<uint2*>(codes + (int64_t)(off + i) * D + 8 * vec) =
-          make_uint2(e4m3x2(y[0], y[1]) | e4m3x2(y[2], y[3]) << 16,
-                     e4m3x2(y[4], y[5]) | e4m3x2(y[6], y[7]) << 16);
     };
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const int i = ((batches - 1) * kBatch + j) * kRows + sub;
-      if (i < n) put(i, x[j]);
-    }
+    store(batches - 1);
     for (int b = 0; b + 1 < batches; ++b) {
+      load(b);
       turns(b);
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) fetch((b * kBatch + j) * kRows + sub, b, x[j]);
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) put((b * kBatch + j) * kRows + sub, x[j]);
+      store(b);
     }
     __syncthreads();  // every thread has read the old scale and the flags
     if (lt == 0) *sp = scale;
@@ -461,7 +520,7 @@ int launch_kv_append(const gdn_rope* rope, const AppendArgs& a, bool bf16, void*
     using T = decltype(type);
     constexpr int D = decltype(dim)::value;
     // the rows of a batch: at most a page's
-    const int batch = std::min(a.cache.page_size, kBatch * (kHalf / (D / 8)));
+    const int batch = std::min(a.cache.page_size, Raw8<T>::kRows * (kHalf / (D / 8)));
     const size_t smem = a.rotate ? sizeof(float2) * batch * (r.rotary_dim / 2) : 0;
     static std::atomic<int> ready[kMaxDevices];
     e = configure_once(ready, [] {
