@@ -254,7 +254,7 @@ __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint3
 struct AppendDev {
   AppendArgs a;
   int32_t rows_per_block;  // rows whose runs a block handles
-  int32_t append_blocks;   // the blocks after them rotate q
+  int32_t append_blocks;   // the others rotate q
   int32_t rope_slices;
 };
 
@@ -264,9 +264,11 @@ append_kernel(const __grid_constant__ AppendDev p, const __grid_constant__ RopeD
   const AppendArgs& a = p.a;
   const int tid = threadIdx.x;
   __shared__ Turns table;
-  if ((int)blockIdx.x >= p.append_blocks) {
-    rope_block<T>(r, table, a.rope_args, blockIdx.x - p.append_blocks, p.rope_slices,
-                  kAppendThreads, tid);
+  // the two kinds of blocks in turns: the append waits for memory where the rotation fills it
+  // (32 x 1,024 tokens: 152 us with the append's blocks first, 137 in turns)
+  const int64_t before = (int64_t)blockIdx.x * p.append_blocks / gridDim.x;
+  if (((int64_t)blockIdx.x + 1) * p.append_blocks / gridDim.x == before) {
+    rope_block<T>(r, table, a.rope_args, blockIdx.x - before, p.rope_slices, kAppendThreads, tid);
     return;
   }
   constexpr int kVec = D / 8;              // threads of a row
@@ -279,8 +281,8 @@ append_kernel(const __grid_constant__ AppendDev p, const __grid_constant__ RopeD
   __shared__ uint32_t s_nan[4];            // rows of v that hold a NaN
   extern __shared__ __align__(16) float2 s_turn[];  // cos, sin: [rows of a batch][R / 2]
   const int P = a.cache.page_size, H = a.cache.num_kv_heads;
-  const int head = (int)(blockIdx.x % H);
-  const int64_t row0 = (int64_t)(blockIdx.x / H) * p.rows_per_block;
+  const int head = (int)(before % H);
+  const int64_t row0 = before / H * p.rows_per_block;
   const int64_t nslots = (int64_t)a.cache.num_pages * P;
   const bool is_v = tid >= kHalf;
   const int lt = tid & (kHalf - 1), vec = lt % kVec, sub = lt / kVec;
