@@ -51,7 +51,8 @@ using namespace ptx;
 
 constexpr int kRows = kTileRows;          // query rows of a unit (the MMA's M)
 constexpr int kSoftWarps = 8, kAuxWarps = 8;
-constexpr int kProducer = kSoftWarps + kAuxWarps, kIssuerS = kProducer + 1, kIssuerO = kProducer + 2;
+constexpr int kProducer = kSoftWarps + kAuxWarps, kIssuerS = kProducer + 1, kIssuerO = kProducer + 2,
+              kScheduler = kProducer + 3;
 constexpr int kWarps = 20, kThreads = 32 * kWarps;
 // Registers of a thread: 640 threads are launched with 96; the softmax warps take what the
 // others give (256 * 120 + 256 * 88 + 128 * 64 = 640 * 96).
@@ -61,6 +62,7 @@ constexpr int kSoftThreads = 32 * kSoftWarps, kAuxThreads = 32 * kAuxWarps;
 // Scales and pages are looked up for a batch of tiles at a time, a 16-token group to a lane. The
 // ring holds 16 batches: at least 16 tiles, more than the roles are apart (K stages and four).
 constexpr int kBatch = 8, kBatches = 16;
+constexpr int kLead = 16;                 // K tiles of a unit left to load when the next is taken
 constexpr int kCoarse = kMaxSeqs / 32;    // prefix sums are kept for every 32 requests
 constexpr float kLazyMax = 8.f;
 constexpr float kProbScale = 128.f;
@@ -103,7 +105,7 @@ struct Smem {
   uint64_t pfull[2], sfull[2], odone[kDone], hfull[4];
   uint64_t sfree, qfull, qempty, ofree, drain[2], rawfull, rawempty;
   uint64_t mfull[kBatches];
-  uint64_t ufull[2], uempty[2];
+  uint64_t ufull[2], uempty[2], unext;
   Unit unit[2];
   TileMeta meta[kBatches][kBatch];
   float m[kRows];            // running maximum on its way between the softmax groups
@@ -253,7 +255,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.pfull[i], kSoftWarps / 2);
       mbar_init(&sm.ufull[i], 1);
-      mbar_init(&sm.uempty[i], kSoftWarps + kAuxWarps + 2);
+      mbar_init(&sm.uempty[i], kSoftWarps + kAuxWarps + 3);
     }
     for (int i = 0; i < kDone; ++i) mbar_init(&sm.odone[i], 1);
     for (int i = 0; i < Sh::NH; ++i) mbar_init(&sm.hfull[i], kAuxWarps);
@@ -265,6 +267,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
     mbar_init(&sm.qempty, 1);
     mbar_init(&sm.ofree, kSoftWarps);
     mbar_init(&sm.rawfull, 1);
+    mbar_init(&sm.unext, 1);
     mbar_init(&sm.rawempty, kAuxWarps);
     mbar_init(&sm.drain[0], 1);
     mbar_init(&sm.drain[1], 1);
@@ -295,7 +298,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
   const uint32_t tbase = sm.tmem;
   const int32_t total = sm.coarse[chunks];
 
-  // Takes the next unit of the block's list (every role but the producer).
+  // Takes the next unit of the block's list (every role but the scheduler).
   uint32_t nu = 0;
   auto next_unit = [&](Unit& u) {
     const int slot = nu & 1;
@@ -310,72 +313,16 @@ tile_kernel(const __grid_constant__ TileParams p) {
   if (warp >= kProducer) {
     give_registers<kMiscRegs>();
     if (warp == kProducer) {
-      // ---- units, pages and scales, Q rows, K tiles
+      // ---- pages and scales, K tiles
       const int box_rows = min(a.page_size, BN), per_box = box_rows / 16;
       const uint32_t box_bytes = (uint32_t)box_rows * D;
       static_assert(kBatch * kGroups == 32, "a group to a lane");
-      uint32_t it = 0, raws = 0, nb = 0;
-      int32_t next_x = lane == 0 ? atomicAdd(p.counter, 1) : 0;
-      for (uint32_t n = 0; n <= (uint32_t)total; ++n) {
-        const int32_t x = __shfl_sync(0xffffffffu, next_x, 0);
-        Unit u = {-1, 0, 0, 0, 0, 0, 0, 0};
-        int32_t last = 0;
-        if (x < total) {
-          int lo = 0, hi = chunks - 1;
-          while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (sm.coarse[mid] <= x) lo = mid;
-            else hi = mid - 1;
-          }
-          const int b = 32 * lo + lane;
-          bool cut = false;
-          AttnSeq s = {0, 0, 0};
-          int32_t mine = 0;
-          if (b < a.num_seqs) {
-            s = attn_seq(a, b, cut);
-            mine = seq_units(a, s);
-          }
-          int32_t inc = mine;
-#pragma unroll 1
-          for (int o = 1; o < 32; o <<= 1) {
-            const int32_t y = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += y;
-          }
-          const int32_t y = x - sm.coarse[lo];
-          const int src = __ffs(__ballot_sync(0xffffffffu, inc > y)) - 1;
-          u.seq = 32 * lo + src;
-          u.row0 = __shfl_sync(0xffffffffu, s.row0, src);
-          u.q_len = __shfl_sync(0xffffffffu, s.q_len, src);
-          u.kv_len = __shfl_sync(0xffffffffu, s.kv_len, src);
-          const int32_t k = y - __shfl_sync(0xffffffffu, inc - mine, src);
-          const int32_t row_tiles = (u.q_len * a.group + kRows - 1) / kRows;
-          u.head = k / row_tiles;
-          u.first = (row_tiles - 1 - k % row_tiles) * kRows;  // the rows that see most come first
-          last = min(u.q_len * a.group, u.first + kRows) - 1;
-          const AttnSeq q = {u.row0, u.q_len, u.kv_len};
-          u.tiles = (attn_limit(a, q, a.by_group(last)) + BN - 1) / BN;
-        }
-        const int slot = n & 1;
-        if (!wait_or_die(&sm.uempty[slot], ((n >> 1) & 1u) ^ 1u, sm, a.status)) break;
-        if (lane == 0) {
-          sm.unit[slot] = u;
-          mbar_arrive(&sm.ufull[slot]);
-        }
-        if (u.seq < 0) break;
-        if (lane == 0) next_x = atomicAdd(p.counter, 1);  // its answer has the unit's time
-        if (u.tiles == 0) continue;
-        // the unit's rows of Q, one copy each, when the last unit's have moved on
-        if (!wait_or_die(&sm.rawempty, (raws & 1u) ^ 1u, sm, a.status)) break;
-        ++raws;
-        if (lane == 0)
-          mbar_arrive_expect_tx(&sm.rawfull, (uint32_t)(last - u.first + 1) * 2 * D);
-        __syncwarp();
-        for (int32_t r = u.first + lane; r <= last; r += 32) {
-          const int32_t i = a.by_group(r), h = r - i * a.group;
-          bulk_load(smem + Sh::OFF_RAW + (r - u.first) * Sh::kRawPitch,
-                    static_cast<const __nv_bfloat16*>(a.q) + (int64_t)(u.row0 + i) * a.q_stride +
-                        (int64_t)(u.head * a.group + h) * D,
-                    2 * D, &sm.rawfull);
+      uint32_t it = 0, nb = 0;
+      Unit u;
+      while (next_unit(u)) {
+        if (u.tiles == 0) {
+          if (lane == 0) mbar_arrive(&sm.unext);
+          continue;
         }
         const int32_t* table = a.block_table + (int64_t)u.seq * a.max_blocks;
         const int32_t end = min(u.kv_len, u.tiles * BN);
@@ -396,6 +343,8 @@ tile_kernel(const __grid_constant__ TileParams p) {
         bool ok = true;
 #pragma unroll 1
         for (int32_t tb = 0; tb < u.tiles && ok; tb += kBatch, ++nb) {
+          if (lane == 0 && tb + kLead >= u.tiles && (tb == 0 || tb + kLead - kBatch < u.tiles))
+            mbar_arrive(&sm.unext);
           const int32_t tok = tb * BN + lane * 16;
           // values that are no scales count as zeros
           ks = ks >= 0.f ? ks : 0.f;
@@ -458,8 +407,75 @@ tile_kernel(const __grid_constant__ TileParams p) {
           const uint32_t x = it - 1 - k;
           wait_landed(smem_u32(&sm.kfull[x % Sh::SK]), (x / Sh::SK) & 1u);
         }
-        if (raws > 0) wait_landed(smem_u32(&sm.rawfull), (raws - 1) & 1u);
       }
+    } else if (warp == kScheduler) {
+      // ---- units and their rows of Q
+      uint32_t raws = 0;
+      for (uint32_t n = 0; n <= (uint32_t)total; ++n) {
+        // not long before its time, so that the last units go to the blocks that are free first
+        if (n > 0 && !wait_or_die(&sm.unext, (n - 1) & 1u, sm, a.status)) break;
+        int32_t x = lane == 0 ? atomicAdd(p.counter, 1) : 0;
+        x = __shfl_sync(0xffffffffu, x, 0);
+        Unit u = {-1, 0, 0, 0, 0, 0, 0, 0};
+        int32_t last = 0;
+        if (x < total) {
+          int lo = 0, hi = chunks - 1;
+          while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (sm.coarse[mid] <= x) lo = mid;
+            else hi = mid - 1;
+          }
+          const int b = 32 * lo + lane;
+          bool cut = false;
+          AttnSeq s = {0, 0, 0};
+          int32_t mine = 0;
+          if (b < a.num_seqs) {
+            s = attn_seq(a, b, cut);
+            mine = seq_units(a, s);
+          }
+          int32_t inc = mine;
+#pragma unroll 1
+          for (int o = 1; o < 32; o <<= 1) {
+            const int32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+          }
+          const int32_t y = x - sm.coarse[lo];
+          const int src = __ffs(__ballot_sync(0xffffffffu, inc > y)) - 1;
+          u.seq = 32 * lo + src;
+          u.row0 = __shfl_sync(0xffffffffu, s.row0, src);
+          u.q_len = __shfl_sync(0xffffffffu, s.q_len, src);
+          u.kv_len = __shfl_sync(0xffffffffu, s.kv_len, src);
+          const int32_t k = y - __shfl_sync(0xffffffffu, inc - mine, src);
+          const int32_t row_tiles = (u.q_len * a.group + kRows - 1) / kRows;
+          u.head = k / row_tiles;
+          u.first = (row_tiles - 1 - k % row_tiles) * kRows;  // the rows that see most come first
+          last = min(u.q_len * a.group, u.first + kRows) - 1;
+          const AttnSeq q = {u.row0, u.q_len, u.kv_len};
+          u.tiles = (attn_limit(a, q, a.by_group(last)) + BN - 1) / BN;
+        }
+        const int slot = n & 1;
+        if (!wait_or_die(&sm.uempty[slot], ((n >> 1) & 1u) ^ 1u, sm, a.status)) break;
+        if (lane == 0) {
+          sm.unit[slot] = u;
+          mbar_arrive(&sm.ufull[slot]);
+        }
+        if (u.seq < 0) break;
+        if (u.tiles == 0) continue;
+        // the unit's rows of Q, one copy each, when the last unit's have moved on
+        if (!wait_or_die(&sm.rawempty, (raws & 1u) ^ 1u, sm, a.status)) break;
+        ++raws;
+        if (lane == 0)
+          mbar_arrive_expect_tx(&sm.rawfull, (uint32_t)(last - u.first + 1) * 2 * D);
+        __syncwarp();
+        for (int32_t r = u.first + lane; r <= last; r += 32) {
+          const int32_t i = a.by_group(r), h = r - i * a.group;
+          bulk_load(smem + Sh::OFF_RAW + (r - u.first) * Sh::kRawPitch,
+                    static_cast<const __nv_bfloat16*>(a.q) + (int64_t)(u.row0 + i) * a.q_stride +
+                        (int64_t)(u.head * a.group + h) * D,
+                    2 * D, &sm.rawfull);
+        }
+      }
+      if (sm.dead && raws > 0) wait_landed(smem_u32(&sm.rawfull), (raws - 1) & 1u);
     } else if (warp == kIssuerS) {
       // ---- S = Q K^T
       constexpr uint32_t id_s = idesc_f16(kRows, BN, 0, 0);
@@ -559,77 +575,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
     while (true) {
       if (named_any(kAuxBar, kAuxThreads, !more)) break;  // these warps leave together
       if (u.tiles > 0) {
-        bool ok = wait_or_die(&sm.rawfull, nq & 1u, sm, a.status);
-        {
-          const bool live = u.first + qr < u.q_len * a.group;
-          // largest magnitude of the row: bf16 bit patterns without their signs order like
-          // integers
-          uint32_t top = 0;
-#pragma unroll 4
-          for (int c = 0; c < D; c += 16) {
-            const uint4 w = *reinterpret_cast<const uint4*>(raw + c);
-            top = __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
-                                         __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
-          }
-          sm.exchange_q[qhalf][qr] = (uint16_t)max(top & 0xffffu, top >> 16);
-          named_sync(kAuxBar, kAuxThreads);
-          top = max(sm.exchange_q[0][qr], sm.exchange_q[1][qr]);
-          int ex = (int)(top >> 7) - 127;        // [128, 256) after the scaling
-          const bool wild = ex == 128;           // an infinity or NaN: the row is NaN
-          ex = wild ? 7 : max(ex, -100);
-          if (!live) ex = 7;
-          float up = wild ? __int_as_float(0x7fffffff)
-                          : __uint_as_float((uint32_t)(7 - ex + 127) << 23);
-          if (a.scale_log2 < 0.f) up = -up;
-          // in place: eight values become eight e4m3 codes of each term
-#pragma unroll 2
-          for (int c = 0; c < D; c += 16) {
-            uint4* at8 = reinterpret_cast<uint4*>(raw + c);
-            const uint4 v = *at8;
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t h = f16x2(__uint_as_float(w[e] << 16) * up,
-                                       __uint_as_float(w[e] & 0xffff0000u) * up);
-              const uint16_t k = half2_to_e4m3(h);
-              const uint32_t back = e4m3_to_half2(k);
-              const __half2 rest = __hsub2(*reinterpret_cast<const __half2*>(&h),
-                                           *reinterpret_cast<const __half2*>(&back));
-              hi[e >> 1] |= (uint32_t)k << (16 * (e & 1));
-              lo[e >> 1] |= (uint32_t)half2_to_e4m3(h2_bits(rest)) << (16 * (e & 1));
-            }
-            *at8 = live ? make_uint4(hi[0], hi[1], lo[0], lo[1]) : make_uint4(0, 0, 0, 0);
-          }
-          if (qhalf == 0) sm.row_exp[nq & 1u][qr] = (int8_t)(ex - 7);
-        }
-        // to tensor memory, when the S products of the unit before have read theirs
-        ok = wait_or_die(&sm.qempty, (nq & 1u) ^ 1u, sm, a.status) && ok;
-        tc_fence_after();
-        {
-          const uint32_t tq = tbase + ((uint32_t)(32 * (warp & 3)) << 16) + Sh::TM_Q +
-                              qhalf * (D / 8);
-#pragma unroll 1
-          for (int c = 0; c < D / 64; ++c) {  // 32 elements: eight columns of each term
-            uint32_t hi[8], lo[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint4 w = *reinterpret_cast<const uint4*>(raw + 64 * c + 16 * e);
-              hi[2 * e] = w.x; hi[2 * e + 1] = w.y; lo[2 * e] = w.z; lo[2 * e + 1] = w.w;
-            }
-            tmem_st8(tq + 8 * c, hi);
-            tmem_st8(tq + D / 4 + 8 * c, lo);
-          }
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        fence_proxy_async_smem();  // the next rows come by the async proxy
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&sm.qfull);
-          mbar_arrive(&sm.rawempty);
-        }
-        ++nq;
+        bool ok = true;
         // V tiles: a tile's loads are on their way while the one before is stored
         uint4 v[kV];
 #pragma unroll 1
@@ -653,7 +599,81 @@ tile_kernel(const __grid_constant__ TileParams p) {
                              ((pos + k * kStep) & page_mask)) * D);
             }
           }
-          if (t < 0) continue;
+          if (t < 0) {  // Q, while the first V tile is on its way
+            ok = wait_or_die(&sm.rawfull, nq & 1u, sm, a.status) && ok;
+            int ex;
+            {
+              const bool live = u.first + qr < u.q_len * a.group;
+              // largest magnitude of the row: bf16 bit patterns without their signs order like
+              // integers
+              uint32_t top = 0;
+    #pragma unroll 4
+              for (int c = 0; c < D; c += 16) {
+                const uint4 w = *reinterpret_cast<const uint4*>(raw + c);
+                top = __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
+                                             __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
+              }
+              sm.exchange_q[qhalf][qr] = (uint16_t)max(top & 0xffffu, top >> 16);
+              named_sync(kAuxBar, kAuxThreads);
+              top = max(sm.exchange_q[0][qr], sm.exchange_q[1][qr]);
+              ex = (int)(top >> 7) - 127;           // [128, 256) after the scaling
+              const bool wild = ex == 128;           // an infinity or NaN: the row is NaN
+              ex = wild ? 7 : max(ex, -100);
+              if (!live) ex = 7;
+              float up = wild ? __int_as_float(0x7fffffff)
+                              : __uint_as_float((uint32_t)(7 - ex + 127) << 23);
+              if (a.scale_log2 < 0.f) up = -up;
+              // in place: eight values become eight e4m3 codes of each term
+    #pragma unroll 2
+              for (int c = 0; c < D; c += 16) {
+                uint4* at8 = reinterpret_cast<uint4*>(raw + c);
+                const uint4 v = *at8;
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+    #pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const uint32_t h = f16x2(__uint_as_float(w[e] << 16) * up,
+                                           __uint_as_float(w[e] & 0xffff0000u) * up);
+                  const uint16_t k = half2_to_e4m3(h);
+                  const uint32_t back = e4m3_to_half2(k);
+                  const __half2 rest = __hsub2(*reinterpret_cast<const __half2*>(&h),
+                                               *reinterpret_cast<const __half2*>(&back));
+                  hi[e >> 1] |= (uint32_t)k << (16 * (e & 1));
+                  lo[e >> 1] |= (uint32_t)half2_to_e4m3(h2_bits(rest)) << (16 * (e & 1));
+                }
+                *at8 = live ? make_uint4(hi[0], hi[1], lo[0], lo[1]) : make_uint4(0, 0, 0, 0);
+              }
+            }
+            // to tensor memory, when the S products of the unit before have read theirs
+            ok = wait_or_die(&sm.qempty, (nq & 1u) ^ 1u, sm, a.status) && ok;
+            tc_fence_after();
+            if (qhalf == 0) sm.row_exp[nq & 1u][qr] = (int8_t)(ex - 7);  // nor does one read this
+            {
+              const uint32_t tq = tbase + ((uint32_t)(32 * (warp & 3)) << 16) + Sh::TM_Q +
+                                  qhalf * (D / 8);
+    #pragma unroll 1
+              for (int c = 0; c < D / 64; ++c) {  // 32 elements: eight columns of each term
+                uint32_t hi[8], lo[8];
+    #pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const uint4 w = *reinterpret_cast<const uint4*>(raw + 64 * c + 16 * e);
+                  hi[2 * e] = w.x; hi[2 * e + 1] = w.y; lo[2 * e] = w.z; lo[2 * e + 1] = w.w;
+                }
+                tmem_st8(tq + 8 * c, hi);
+                tmem_st8(tq + D / 4 + 8 * c, lo);
+              }
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            fence_proxy_async_smem();  // the next rows come by the async proxy
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(&sm.qfull);
+              mbar_arrive(&sm.rawempty);
+            }
+            ++nq;
+            continue;
+          }
           const uint32_t j = g + t, hb = j % Sh::NH;
           if (j >= Sh::NH) {  // P V(j - NH) has read this buffer
             const uint32_t o = j - Sh::NH;
