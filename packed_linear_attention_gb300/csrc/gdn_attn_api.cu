@@ -435,9 +435,14 @@ int launch_attn(const AttnArgs& args, const gdn_kv_cache& c, bool bf16, void* st
   sms = std::min(sms, kMaxSms);
   // fp32 queries need more than the tile kernel's operands hold
   a.split_q = bf16 ? std::max(1, 64 / a.group) : a.max_q_len;
-  const int r = launch_attn_split(a, c, bf16, sms, stream);
-  if (r != 0 || a.max_q_len <= a.split_q) return r;
-  return launch_attn_tile(a, c, sms, stream);
+  // The kernels write different rows and may run at the same time; the counter of the second is
+  // cleared in front of both.
+  const bool tiles = a.max_q_len > a.split_q;
+  int r = 0;
+  if (tiles)
+    r = (int)cudaMemsetAsync(a.counter, 0, sizeof(int32_t), static_cast<cudaStream_t>(stream));
+  if (r == 0) r = launch_attn_split(a, c, bf16, sms, stream);
+  return r != 0 || !tiles ? r : launch_attn_tile(a, c, sms, stream);
 }
 
 }  // namespace gdn

@@ -611,6 +611,7 @@ constexpr int kMaxJoinBlocks = 16384, kBlockRows = 512;
 template <typename T, int D, int RB, bool kBlocks>
 __global__ void __launch_bounds__(kJoinThreads)
 join_kernel(AttnArgs a, const float* part, int workers) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the tile kernel may come
   extern __shared__ int32_t join_smem[];
   __shared__ int32_t scan[kJoinWarps][2];
   constexpr int kTeams = kBlocks ? 1 : kJoinWarps;  // rows that a block has in hand at a time

@@ -476,6 +476,8 @@ tile_kernel(const __grid_constant__ TileParams p) {
         }
       }
       if (sm.dead && raws > 0) wait_landed(smem_u32(&sm.rawfull), (raws - 1) & 1u);
+      // this kernel reads nothing of the ones before it in the call, but it must not end first
+      asm volatile("griddepcontrol.wait;" ::: "memory");
     } else if (warp == kIssuerS) {
       // ---- S = Q K^T
       constexpr uint32_t id_s = idesc_f16(kRows, BN, 0, 0);
@@ -950,11 +952,19 @@ int launch(const AttnArgs& a, const gdn_kv_cache& c, int num_sms, cudaStream_t s
                                      kSmem);
   });
   if (e != 0) return e;
-  if ((e = (int)cudaMemsetAsync(p.counter, 0, sizeof(int32_t), stream)) != 0) return e;
   const int64_t units =
       (((int64_t)a.num_tokens * a.group + kRows - 1) / kRows + a.num_seqs) * a.hkv;
-  tile_kernel<D><<<(unsigned)std::min<int64_t>(units, num_sms), kThreads, kSmem, stream>>>(p);
-  return (int)cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(units, num_sms));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];  // blocks may start as the kernels before leave SMs free
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return (int)cudaLaunchKernelEx(&cfg, tile_kernel<D>, p);
 }
 
 }  // namespace
