@@ -248,6 +248,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
   // ---- set-up: barriers, tensor memory, units before every 32nd request
   if (tid == 0) {
     sm.dead = 0;
+#pragma unroll 1
     for (int i = 0; i < Sh::SK; ++i) {
       mbar_init(&sm.kfull[i], 1);
       mbar_init(&sm.kempty[i], 1);
@@ -259,6 +260,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
     }
     for (int i = 0; i < kDone; ++i) mbar_init(&sm.odone[i], 1);
     for (int i = 0; i < Sh::NH; ++i) mbar_init(&sm.hfull[i], kAuxWarps);
+#pragma unroll 1
     for (int i = 0; i < kBatches; ++i) mbar_init(&sm.mfull[i], 1);
     mbar_init(&sm.sfull[0], 1);  // a barrier for each softmax group: it waits for every second S
     mbar_init(&sm.sfull[1], 1);
@@ -275,6 +277,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
   }
   const int chunks = (a.num_seqs + 31) / 32;
   bool bad = false;
+#pragma unroll 1
   for (int c = warp; c < chunks; c += kWarps) {
     const int b = 32 * c + lane;
     int32_t n = b < a.num_seqs ? seq_units(a, attn_seq(a, b, bad)) : 0;
@@ -291,6 +294,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
   if (tid == 0) {
     int32_t at = 0;
     sm.coarse[0] = 0;
+#pragma unroll 1
     for (int c = 1; c <= chunks; ++c) sm.coarse[c] = at += sm.coarse[c];
   }
   __syncthreads();
@@ -300,14 +304,20 @@ tile_kernel(const __grid_constant__ TileParams p) {
 
   // Takes the next unit of the block's list (every role but the scheduler).
   uint32_t nu = 0;
-  auto next_unit = [&](Unit& u) {
-    const int slot = nu & 1;
-    if (!wait_or_die(&sm.ufull[slot], (nu >> 1) & 1u, sm, a.status)) return false;
-    u = sm.unit[slot];
-    ++nu;
+  auto see_unit = [&] {
+    return wait_or_die(&sm.ufull[nu & 1], (nu >> 1) & 1u, sm, a.status) &&
+           *(volatile int32_t*)&sm.unit[nu & 1].seq >= 0;
+  };
+  auto take_unit = [&](Unit& u) {
+    u = sm.unit[nu & 1];
     __syncwarp();
-    if (lane == 0) mbar_arrive(&sm.uempty[slot]);
-    return u.seq >= 0;
+    if (lane == 0) mbar_arrive(&sm.uempty[nu & 1]);
+    ++nu;
+  };
+  auto next_unit = [&](Unit& u) {
+    if (!see_unit()) return false;
+    take_unit(u);
+    return true;
   };
 
   if (warp >= kProducer) {
@@ -420,6 +430,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
         int32_t last = 0;
         if (x < total) {
           int lo = 0, hi = chunks - 1;
+#pragma unroll 1
           while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
             if (sm.coarse[mid] <= x) lo = mid;
@@ -467,6 +478,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
         if (lane == 0)
           mbar_arrive_expect_tx(&sm.rawfull, (uint32_t)(last - u.first + 1) * 2 * D);
         __syncwarp();
+#pragma unroll 1
         for (int32_t r = u.first + lane; r <= last; r += 32) {
           const int32_t i = a.by_group(r), h = r - i * a.group;
           bulk_load(smem + Sh::OFF_RAW + (r - u.first) * Sh::kRawPitch,
@@ -609,7 +621,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
               // largest magnitude of the row: bf16 bit patterns without their signs order like
               // integers
               uint32_t top = 0;
-    #pragma unroll 4
+#pragma unroll 4
               for (int c = 0; c < D; c += 16) {
                 const uint4 w = *reinterpret_cast<const uint4*>(raw + c);
                 top = __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
@@ -626,13 +638,13 @@ tile_kernel(const __grid_constant__ TileParams p) {
                               : __uint_as_float((uint32_t)(7 - ex + 127) << 23);
               if (a.scale_log2 < 0.f) up = -up;
               // in place: eight values become eight e4m3 codes of each term
-    #pragma unroll 2
+#pragma unroll 2
               for (int c = 0; c < D; c += 16) {
                 uint4* at8 = reinterpret_cast<uint4*>(raw + c);
                 const uint4 v = *at8;
                 const uint32_t w[4] = {v.x, v.y, v.z, v.w};
                 uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
-    #pragma unroll
+#pragma unroll
                 for (int e = 0; e < 4; ++e) {
                   const uint32_t h = f16x2(__uint_as_float(w[e] << 16) * up,
                                            __uint_as_float(w[e] & 0xffff0000u) * up);
@@ -653,10 +665,10 @@ tile_kernel(const __grid_constant__ TileParams p) {
             {
               const uint32_t tq = tbase + ((uint32_t)(32 * (warp & 3)) << 16) + Sh::TM_Q +
                                   qhalf * (D / 8);
-    #pragma unroll 1
+#pragma unroll 1
               for (int c = 0; c < D / 64; ++c) {  // 32 elements: eight columns of each term
                 uint32_t hi[8], lo[8];
-    #pragma unroll
+#pragma unroll
                 for (int e = 0; e < 4; ++e) {
                   const uint4 w = *reinterpret_cast<const uint4*>(raw + 64 * c + 16 * e);
                   hi[2 * e] = w.x; hi[2 * e + 1] = w.y; lo[2 * e] = w.z; lo[2 * e + 1] = w.w;
@@ -716,10 +728,11 @@ tile_kernel(const __grid_constant__ TileParams p) {
     const float scale = fabsf(a.scale_log2);
     uint32_t g = 0, nq = 0, nb = 0;
     Unit u;
-    while (true) {
-      const bool more = next_unit(u);
-      // the warps leave together, so that none is left at a barrier
-      if (named_any(kSoftBar, kSoftThreads, !more)) break;
+    // the warps leave together, so that none is left at a barrier
+    bool more = see_unit();
+    more = !named_any(kSoftBar, kSoftThreads, !more);
+    while (more) {
+      take_unit(u);
       const int32_t rows = u.q_len * a.group, row = u.first + r;
       const bool live = row < rows;
       const int32_t query = live ? a.by_group(row) : 0;
@@ -843,11 +856,12 @@ tile_kernel(const __grid_constant__ TileParams p) {
       }
       g += u.tiles;
       nb += (u.tiles + kBatch - 1) / kBatch;
-      // ---- output: the groups' sums meet, each writes half of the row
+      // ---- output: the groups' sums meet, each writes half of the row. What needs only the sums
+      // is done while the last P V runs, and the look for the next unit falls into it.
+      const uint32_t last = g - 1;
       if (u.tiles > 0) {
         ++nq;
-        const uint32_t last = g - 1, mine = (last & 1u) == grp;  // who has the final maximum
-        if (mine) {
+        if ((last & 1u) == grp) {  // who has the final maximum
           sm.m[r] = m;
           sm.exchange_v[r] = vref;
         }
@@ -856,14 +870,14 @@ tile_kernel(const __grid_constant__ TileParams p) {
         vref = sm.exchange_v[r];
         sm.exchange_l[grp][r] = m == -GDN_INF ? l : l * ex2(m - mf);
         m = mf;
-        named_sync(kSoftBar, kSoftThreads);
-        l = sm.exchange_l[0][r] + sm.exchange_l[1][r];
-        wait_on(&sm.odone[last % kDone], (last / kDone) & 1u, sm, a.status);
-        tc_fence_after();
       }
+      more = see_unit();
+      more = !named_any(kSoftBar, kSoftThreads, !more);
+      if (u.tiles > 0) l = sm.exchange_l[0][r] + sm.exchange_l[1][r];
       const float inv = l == 0.f ? 0.f : __fdividef(vref, l * kProbScale);
-      const int64_t tok = u.row0 + query;
-      const int hq = u.head * a.group + (row - query * a.group);
+      if (live && grp == 0 && a.lse)
+        a.lse[(int64_t)(u.row0 + query) * (a.hkv * a.group) + u.head * a.group + row -
+              query * a.group] = l == 0.f ? -GDN_INF : (m + __log2f(l)) * kLn2;
       // through shared memory, 32 columns at a time, so that four lanes store 64 consecutive
       // bytes of a row (a thread storing its own row would touch 32 lines with every store)
       uint8_t* stage = smem + Sh::OFF_OUT + warp * 2048;
@@ -878,49 +892,44 @@ tile_kernel(const __grid_constant__ TileParams p) {
                                  grp * (D / 2) + 8 * (lane & 3)
                            : nullptr;
       }
-      constexpr int kOut = D == 64 ? 32 : 64;  // columns loaded at a time
+      if (u.tiles > 0) {
+        wait_on(&sm.odone[last % kDone], (last / kDone) & 1u, sm, a.status);
+        tc_fence_after();
+      }
 #pragma unroll 1
-      for (int c = 0; c < D / 2; c += kOut) {
-        uint32_t o[kOut];
+      for (int c = 0; c < D / 2; c += 32) {
+        uint32_t o[32];
         if (u.tiles > 0) {
-#pragma unroll
-          for (int h = 0; h < kOut; h += 32)
-            tmem_ld32(t_row + Sh::TM_O + grp * (D / 2) + c + h,
-                      reinterpret_cast<uint32_t(&)[32]>(o[h]));
+          tmem_ld32(t_row + Sh::TM_O + grp * (D / 2) + c, o);
           tmem_ld_wait();
         } else {
 #pragma unroll
-          for (int e = 0; e < kOut; ++e) o[e] = 0;
+          for (int e = 0; e < 32; ++e) o[e] = 0;
         }
 #pragma unroll
-        for (int h = 0; h < kOut; h += 32) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 z = mul2(make_float2(__uint_as_float(o[h + 8 * e + 2 * k]),
-                                                __uint_as_float(o[h + 8 * e + 2 * k + 1])),
-                                    make_float2(inv, inv));
-              const __nv_bfloat162 y = __floats2bfloat162_rn(z.x, z.y);
-              w[k] = *reinterpret_cast<const uint32_t*>(&y);
-            }
-            *reinterpret_cast<uint4*>(stage + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4)) =
-                make_uint4(w[0], w[1], w[2], w[3]);
-          }
-          __syncwarp();
+        for (int e = 0; e < 4; ++e) {
+          uint32_t w[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int rr = 8 * k + (lane >> 2);
-            const uint4 w = *reinterpret_cast<const uint4*>(
-                stage + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4));
-            if (out[k]) *reinterpret_cast<uint4*>(out[k] + c + h) = w;
+            const float2 z = mul2(make_float2(__uint_as_float(o[8 * e + 2 * k]),
+                                              __uint_as_float(o[8 * e + 2 * k + 1])),
+                                  make_float2(inv, inv));
+            const __nv_bfloat162 y = __floats2bfloat162_rn(z.x, z.y);
+            w[k] = *reinterpret_cast<const uint32_t*>(&y);
           }
-          __syncwarp();
+          *reinterpret_cast<uint4*>(stage + lane * 64 + ((e ^ ((lane >> 1) & 3)) << 4)) =
+              make_uint4(w[0], w[1], w[2], w[3]);
         }
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int rr = 8 * k + (lane >> 2);
+          const uint4 w = *reinterpret_cast<const uint4*>(
+              stage + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4));
+          if (out[k]) *reinterpret_cast<uint4*>(out[k] + c) = w;
+        }
+        __syncwarp();
       }
-      if (live && grp == 0 && a.lse)
-        a.lse[tok * (a.hkv * a.group) + hq] = l == 0.f ? -GDN_INF : (m + __log2f(l)) * kLn2;
       if (u.tiles > 0) {
         tc_fence_before();
         __syncwarp();
