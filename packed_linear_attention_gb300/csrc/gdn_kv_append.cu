@@ -40,7 +40,7 @@ constexpr int kMinExp = -100;            // exponent of the smallest scale
 struct RopeDev {  // gdn_rope without what the kernels do not need
   uint64_t turns[GDN_ROPE_MAX_PAIRS];
   uint8_t axis[GDN_ROPE_MAX_PAIRS];
-  int32_t head_dim, rotary_dim, adjacent;
+  int32_t head_dim, rotary_dim, adjacent, num_axes;
 };
 
 // Eight consecutive elements of a tensor, as loaded.
@@ -48,17 +48,9 @@ template <typename T>
 struct Raw8;
 template <>
 struct Raw8<__nv_bfloat16> {
-  static constexpr int kRows = 8;  // rows of a thread held in registers
+  static constexpr int kRows = 8, kParts = 1;  // rows that a thread of the append stages
   uint4 w;
-  __device__ Raw8 from_lane(int src) const {
-    Raw8 r;
-    r.w.x = __shfl_sync(0xffffffffu, w.x, src);
-    r.w.y = __shfl_sync(0xffffffffu, w.y, src);
-    r.w.z = __shfl_sync(0xffffffffu, w.z, src);
-    r.w.w = __shfl_sync(0xffffffffu, w.w, src);
-    return r;
-  }
-  __device__ void zero() { w = make_uint4(0, 0, 0, 0); }
+  __device__ void fetch(const uint4* p, int) { w = p[0]; }
   __device__ void load(const __nv_bfloat16* p) { w = *reinterpret_cast<const uint4*>(p); }
   __device__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = w; }
   __device__ void get(float (&x)[8]) const {
@@ -81,21 +73,12 @@ struct Raw8<__nv_bfloat16> {
 };
 template <>
 struct Raw8<float> {
-  static constexpr int kRows = 4;
+  static constexpr int kRows = 4, kParts = 2;
   float4 a, b;
-  __device__ Raw8 from_lane(int src) const {
-    Raw8 r;
-    r.a.x = __shfl_sync(0xffffffffu, a.x, src);
-    r.a.y = __shfl_sync(0xffffffffu, a.y, src);
-    r.a.z = __shfl_sync(0xffffffffu, a.z, src);
-    r.a.w = __shfl_sync(0xffffffffu, a.w, src);
-    r.b.x = __shfl_sync(0xffffffffu, b.x, src);
-    r.b.y = __shfl_sync(0xffffffffu, b.y, src);
-    r.b.z = __shfl_sync(0xffffffffu, b.z, src);
-    r.b.w = __shfl_sync(0xffffffffu, b.w, src);
-    return r;
+  __device__ void fetch(const uint4* p, int step) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *reinterpret_cast<const float4*>(p + step);
   }
-  __device__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ void load(const float* p) {
     a = reinterpret_cast<const float4*>(p)[0];
     b = reinterpret_cast<const float4*>(p)[1];
@@ -128,11 +111,9 @@ struct Turns {
   }
 };
 
-// cos and sin of pair i at a token whose positions start at `pos` (one row per axis).
-__device__ __forceinline__ void pair_angle(const Turns& r, int i, const int32_t* pos,
-                                           int64_t pos_stride, float& c, float& s) {
-  const int64_t at = __ldg(pos + r.axis[i] * pos_stride);
-  const uint64_t turn = (uint64_t)at * r.turns[i];
+// cos and sin of pair i at position `at` of its axis.
+__device__ __forceinline__ void pair_angle(const Turns& r, int i, int32_t at, float& c, float& s) {
+  const uint64_t turn = (uint64_t)(int64_t)at * r.turns[i];
   const uint32_t quarter = (uint32_t)((turn + (1ull << 61)) >> 62);
   // the rest in 2^-34 turns, in [-2^31, 2^31], times 2 pi 2^-34
   const float x = (float)(int32_t)((int64_t)(turn - ((uint64_t)quarter << 62)) >> 30) *
@@ -168,7 +149,8 @@ __device__ __forceinline__ void rope_heads(const RopeDev& r, const Turns& table,
   if (turn) {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      pair_angle(table, 8 * item + e, a.positions + token, a.pos_stride, c[e], s[e]);
+      pair_angle(table, 8 * item + e,
+                 __ldg(a.positions + table.axis[8 * item + e] * a.pos_stride + token), c[e], s[e]);
   }
 #pragma unroll 4
   for (int h = head0; h < head1; ++h) {
@@ -251,6 +233,13 @@ __device__ __forceinline__ int scale_exp(float amax) {
 }
 __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
+__device__ __forceinline__ void copy16_async(uint4* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(dst)),
+               "l"(src)
+               : "memory");
+}
+
 struct AppendDev {
   AppendArgs a;
   int32_t rows_per_block;  // rows whose runs a block handles
@@ -273,13 +262,16 @@ append_kernel(const __grid_constant__ AppendDev p, const __grid_constant__ RopeD
   }
   constexpr int kVec = D / 8;              // threads of a row
   constexpr int kRows = kHalf / kVec;      // rows of a pass
-  constexpr int kBatch = Raw8<T>::kRows;
+  constexpr int kBatch = Raw8<T>::kRows, kParts = Raw8<T>::kParts;
   __shared__ int64_t s_slot[1 + 256];      // slots from the row in front of the block's on
+  __shared__ int32_t s_pos[GDN_ROPE_MAX_AXES][256];  // positions of the rows from row0 on
   __shared__ int s_start[128];
   __shared__ int s_nstart, s_n;
   __shared__ uint32_t s_amax[2];
   __shared__ uint32_t s_nan[4];            // rows of v that hold a NaN
-  extern __shared__ __align__(16) float2 s_turn[];  // cos, sin: [rows of a batch][R / 2]
+  extern __shared__ uint4 stage[];         // [kBatch][kParts][thread]: rows as they came
+  float2* s_turn = reinterpret_cast<float2*>(stage + kBatch * kParts * kAppendThreads);
+  // cos, sin: [rows of a batch][R / 2]
   const int P = a.cache.page_size, H = a.cache.num_kv_heads;
   const int head = (int)(before % H);
   const int64_t row0 = before / H * p.rows_per_block;
@@ -290,7 +282,7 @@ append_kernel(const __grid_constant__ AppendDev p, const __grid_constant__ RopeD
   const int64_t stride = is_v ? a.v_stride : a.k_stride;
   const int R = a.rotate ? r.rotary_dim : 0, half = R / 2;
   // this thread's chunk in the rotation: its first pair and, in the halves layout, the lane that
-  // holds the pairs' other elements
+  // copies the pairs' other elements
   const bool rot = !is_v && 8 * vec < R, low = 8 * vec < half;
   const int pair0 = r.adjacent ? 4 * vec : low ? 8 * vec : 8 * vec - half;
   const int lane = tid & 31;
@@ -302,8 +294,16 @@ append_kernel(const __grid_constant__ AppendDev p, const __grid_constant__ RopeD
     s_slot[tid] = row >= 0 && row < a.num_tokens ? a.slots[row] : -1;
   }
   if (tid == 0) s_nstart = 0;
-  if (R) table.load(r, tid, kAppendThreads);
-  else __syncthreads();
+  if (R) {
+    for (int x = tid >> 8; x < r.num_axes; x += kAppendThreads / 256) {
+      const int i = tid & 255;
+      if (i < p.rows_per_block + P && row0 + i < a.num_tokens)
+        s_pos[x][i] = a.rope_args.positions[x * a.rope_args.pos_stride + row0 + i];
+    }
+    table.load(r, tid, kAppendThreads);
+  } else {
+    __syncthreads();
+  }
   if (tid < p.rows_per_block) {
     const int64_t slot = s_slot[tid + 1];
     if (slot >= nslots)
@@ -313,6 +313,7 @@ append_kernel(const __grid_constant__ AppendDev p, const __grid_constant__ RopeD
   }
   __syncthreads();
   const int nstart = s_nstart;
+#pragma unroll 1
   for (int u = 0; u < nstart; ++u) {  // in any order: the runs are independent
     const int at0 = s_start[u];
     const int64_t row = row0 + at0, slot = s_slot[at0 + 1];
@@ -327,14 +328,19 @@ append_kernel(const __grid_constant__ AppendDev p, const __grid_constant__ RopeD
     const int n = s_n;
     const int passes = (n + kRows - 1) / kRows, batches = (passes + kBatch - 1) / kBatch;
 
-    Raw8<T> w[kBatch];
     auto load = [&](int b) {  // rows b kBatch kRows + j kRows + sub
-#pragma unroll
+#pragma unroll 2
       for (int j = 0; j < kBatch; ++j) {
         const int i = (b * kBatch + j) * kRows + sub;
-        w[j].zero();
-        if (i < n) w[j].load(src + (row + i) * stride);
+        const char* from = reinterpret_cast<const char*>(src + (row + i) * stride);
+#pragma unroll
+        for (int x = 0; x < kParts; ++x)
+          if (i < n) copy16_async(stage + (j * kParts + x) * kAppendThreads + tid, from + 16 * x);
       }
+    };
+    auto landed = [&] {  // a row is copied and read by the same warp
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
     };
     auto turns = [&](int b) {  // cos and sin of the batch's rows (all threads)
       if (!R) return;
@@ -343,20 +349,22 @@ append_kernel(const __grid_constant__ AppendDev p, const __grid_constant__ RopeD
       const int teams = kAppendThreads / half;
       if (tid < teams * half) {
         const int e = tid % half;
+#pragma unroll 1
         for (int i = tid / half; i < rows; i += teams) {
           float c, s;
-          pair_angle(table, e, a.rope_args.positions + row + i0 + i, a.rope_args.pos_stride, c, s);
+          pair_angle(table, e, s_pos[table.axis[e]][at0 + i0 + i], c, s);
           s_turn[i * half + e] = make_float2(c, s);
         }
       }
       __syncthreads();
     };
-    // the eight elements of the batch's row j, rotated (whole warps; `live`: a row of the run)
-    auto values = [&](int j, bool live, float (&x)[8]) {
-      w[j].get(x);
-      if (!R) return;
-      const Raw8<T> o = w[j].from_lane(other);
-      if (!rot || !live) return;
+    // the eight elements of the batch's row j, rotated
+    auto values = [&](int j, float (&x)[8]) {
+      const uint4* at = stage + j * kParts * kAppendThreads + tid;
+      Raw8<T> w;
+      w.fetch(at, kAppendThreads);
+      w.get(x);
+      if (!rot) return;
       const float2* t = s_turn + (j * kRows + sub) * half + pair0;
       if (r.adjacent) {
 #pragma unroll
@@ -367,7 +375,8 @@ append_kernel(const __grid_constant__ AppendDev p, const __grid_constant__ RopeD
         }
       } else {
         float y[8];
-        o.get(y);
+        w.fetch(at + other - lane, kAppendThreads);
+        w.get(y);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float s = low ? -t[e].y : t[e].y;
@@ -376,19 +385,22 @@ append_kernel(const __grid_constant__ AppendDev p, const __grid_constant__ RopeD
       }
     };
     float amax = 0.f;
+#pragma unroll 1
     for (int b = 0; b < batches; ++b) {
+      if (b > 0) __syncwarp();  // the batch before has been read
       load(b);
       turns(b);
-#pragma unroll
+      landed();
+#pragma unroll 2
       for (int j = 0; j < kBatch; ++j) {
         const int i = (b * kBatch + j) * kRows + sub;
-        if ((b * kBatch + j) * kRows < n) {  // for the whole block
+        if (i < n) {
           float x[8];
-          values(j, i < n, x);
+          values(j, x);
           bool nan = false;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float m = i < n ? fabsf(x[e]) : 0.f;
+            const float m = fabsf(x[e]);
             nan = nan || m != m;
             if (m < __int_as_float(0x7f800000)) amax = fmaxf(amax, m);
           }
@@ -410,6 +422,7 @@ append_kernel(const __grid_constant__ AppendDev p, const __grid_constant__ RopeD
       scale = fmaxf(old, need);
       if (scale > old) {  // the rows in front move to the larger scale
         const float f = old / scale;
+#pragma unroll 1
         for (int i = sub; i < off; i += kRows) {
           uint2* c = reinterpret_cast<uint2*>(codes + (int64_t)i * D);
           const uint2 z2 = *c;
@@ -425,32 +438,34 @@ append_kernel(const __grid_constant__ AppendDev p, const __grid_constant__ RopeD
     }
     const float inv = 1.f / scale;  // exact: a power of two (or the caller's own old scale)
     auto store = [&](int b) {
-#pragma unroll
+#pragma unroll 2
       for (int j = 0; j < kBatch; ++j) {
         const int i = (b * kBatch + j) * kRows + sub;
-        if ((b * kBatch + j) * kRows < n) {  // for the whole block
+        if (i < n) {
           float x[8];
-          values(j, i < n, x);
-          if (i < n) {
+          values(j, x);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] *= inv;
-            if ((s_nan[i >> 5] >> (i & 31)) & 1u) {
+          for (int e = 0; e < 8; ++e) x[e] *= inv;
+          if ((s_nan[i >> 5] >> (i & 31)) & 1u) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                x[e] = !is_v ? __int_as_float(0x7fffffff) : x[e] == x[e] ? x[e] : 0.f;
-            }
-            *reinterpret_cast<uint2*>(codes + (int64_t)(off + i) * D) =
-                make_uint2(e4m3x2(x[0], x[1]) | e4m3x2(x[2], x[3]) << 16,
-                           e4m3x2(x[4], x[5]) | e4m3x2(x[6], x[7]) << 16);
+            for (int e = 0; e < 8; ++e)
+              x[e] = !is_v ? __int_as_float(0x7fffffff) : x[e] == x[e] ? x[e] : 0.f;
           }
+          *reinterpret_cast<uint2*>(codes + (int64_t)(off + i) * D) =
+              make_uint2(e4m3x2(x[0], x[1]) | e4m3x2(x[2], x[3]) << 16,
+                         e4m3x2(x[4], x[5]) | e4m3x2(x[6], x[7]) << 16);
         }
       }
     };
-    store(batches - 1);
-    for (int b = 0; b + 1 < batches; ++b) {
+    // the last batch's rows are still there; the others are loaded again
+#pragma unroll 1
+    for (int b = batches - 1;;) {
+      store(b);
+      if (--b < 0) break;
+      __syncwarp();
       load(b);
       turns(b);
-      store(b);
+      landed();
     }
     __syncthreads();  // every thread has read the old scale and the flags
     if (lt == 0) *sp = scale;
@@ -465,6 +480,7 @@ RopeDev device_rope(const gdn_rope& rope) {
   }
   r.head_dim = rope.head_dim;
   r.rotary_dim = rope.rotary_dim;
+  r.num_axes = rope.num_axes;
   r.adjacent = rope.pair_layout == GDN_ROPE_ADJACENT;
   return r;
 }
@@ -523,11 +539,12 @@ int launch_kv_append(const gdn_rope* rope, const AppendArgs& a, bool bf16, void*
     constexpr int D = decltype(dim)::value;
     // the rows of a batch: at most a page's
     const int batch = std::min(a.cache.page_size, Raw8<T>::kRows * (kHalf / (D / 8)));
-    const size_t smem = a.rotate ? sizeof(float2) * batch * (r.rotary_dim / 2) : 0;
+    const size_t smem = sizeof(uint4) * Raw8<T>::kRows * Raw8<T>::kParts * kAppendThreads +
+                        (a.rotate ? sizeof(float2) * batch * (r.rotary_dim / 2) : 0);
     static std::atomic<int> ready[kMaxDevices];
     e = configure_once(ready, [] {
       return (int)cudaFuncSetAttribute(append_kernel<T, D>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024);
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, 192 * 1024);
     });
     if (e == 0) append_kernel<T, D><<<blocks, kAppendThreads, smem, s>>>(p, r);
   };
