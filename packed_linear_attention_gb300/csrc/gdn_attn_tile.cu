@@ -89,7 +89,7 @@ struct Unit {
 struct __align__(16) TileMeta {
   float ks[kGroups];    // key scale of each 16-token group
   float lv[kGroups];    // log2 of what P is weighted with: value scale / vref * kProbScale
-  int32_t id[kGroups];  // page; negative: absent, or past the cached tokens
+  int32_t row[kGroups]; // the group's first row in the cache; negative: absent, or past its tokens
   uint32_t absent;      // bit g: group g is absent
   float vref;           // largest value scale of the unit so far
   float vfac;           // what the accumulator is multiplied by as vref grew
@@ -372,11 +372,13 @@ tile_kernel(const __grid_constant__ TileParams p) {
           if (lane < 4) before = vref;
           vref = __shfl_sync(0xffffffffu, top, 31);
           const uint32_t gone = __ballot_sync(0xffffffffu, id < 0);
+          const int32_t y = (int32_t)(((int64_t)id * a.hkv + u.head) * a.page_size +
+                                      (tok & (a.page_size - 1)));
           TileMeta& m = sm.meta[nb % kBatches][lane >> 2];
           m.ks[lane & 3] = ks;
           m.lv[lane & 3] =
               __log2f(fmaxf(top > 0.f ? __fdividef(vs, top) : 0.f, kMinRatio) * kProbScale);
-          m.id[lane & 3] = id;
+          m.row[lane & 3] = id < 0 ? -1 : y;
           if ((lane & 3) == 0) {
             m.absent = (gone >> lane) & 15u;
             m.vref = top;
@@ -386,8 +388,6 @@ tile_kernel(const __grid_constant__ TileParams p) {
           if (lane == 0) mbar_arrive(&sm.mfull[nb % kBatches]);
           const bool box = (lane & (per_box - 1)) == 0 && id >= 0;
           const uint32_t boxes = __ballot_sync(0xffffffffu, box);
-          const int32_t y = (int32_t)(((int64_t)id * a.hkv + u.head) * a.page_size +
-                                      (tok & (a.page_size - 1)));
           const uint32_t at = (uint32_t)(lane & 3) * 16 * Sh::kRowPitch;
           int32_t next_id = page_of(tok + kBatch * BN);
 #pragma unroll 1
@@ -581,7 +581,6 @@ tile_kernel(const __grid_constant__ TileParams p) {
     const uint32_t h0 = sw128_offset(vt, 16 * vc, BN), h1 = sw128_offset(vt, 16 * vc + 8, BN);
     static_assert(kStep % 8 == 0, "the swizzle repeats from step to step");
     const uint8_t* vbase = static_cast<const uint8_t*>(p.v) + 16 * vc;
-    const int page_mask = a.page_size - 1;
     // and in Q: half of a row
     const int qr = 32 * (warp & 3) + lane, qhalf = aw >> 2;
     uint8_t* raw = smem + Sh::OFF_RAW + qr * Sh::kRawPitch + qhalf * D;
@@ -602,15 +601,14 @@ tile_kernel(const __grid_constant__ TileParams p) {
             if ((t + 1) % kBatch == 0)
               ok = wait_or_die(&sm.mfull[mb % kBatches], (mb / kBatches) & 1u, sm, a.status);
             const TileMeta& m = sm.meta[mb % kBatches][(t + 1) % kBatch];
-            const int32_t pos = (t + 1) * BN + vt;
+            const int32_t left = u.kv_len - (t + 1) * BN - vt;
 #pragma unroll
             for (int k = 0; k < kV; ++k) {
-              const int32_t id = m.id[(vt + k * kStep) >> 4];
+              const int32_t r = m.row[(vt + k * kStep) >> 4];
               v[k] = make_uint4(0, 0, 0, 0);  // past the cached tokens, or without a page: zeros
-              if (ok && id >= 0 && pos + k * kStep < u.kv_len)
+              if (ok && r >= 0 && k * kStep < left)
                 v[k] = *reinterpret_cast<const uint4*>(
-                    vbase + ((int64_t)(id * a.hkv + u.head) * a.page_size +
-                             ((pos + k * kStep) & page_mask)) * D);
+                    vbase + (int64_t)(r + ((vt + k * kStep) & 15)) * D);
             }
           }
           if (t < 0) {  // Q, while the first V tile is on its way
