@@ -601,14 +601,20 @@ tile_kernel(const __grid_constant__ TileParams p) {
             if ((t + 1) % kBatch == 0)
               ok = wait_or_die(&sm.mfull[mb % kBatches], (mb / kBatches) & 1u, sm, a.status);
             const TileMeta& m = sm.meta[mb % kBatches][(t + 1) % kBatch];
-            const int32_t left = u.kv_len - (t + 1) * BN - vt;
+            auto row = [&](int k) {
+              return *reinterpret_cast<const uint4*>(
+                  vbase + (int64_t)(m.row[(vt + k * kStep) >> 4] + ((vt + k * kStep) & 15)) * D);
+            };
+            if (ok && m.absent == 0 && (t + 2) * BN <= u.kv_len) {
 #pragma unroll
-            for (int k = 0; k < kV; ++k) {
-              const int32_t r = m.row[(vt + k * kStep) >> 4];
-              v[k] = make_uint4(0, 0, 0, 0);  // past the cached tokens, or without a page: zeros
-              if (ok && r >= 0 && k * kStep < left)
-                v[k] = *reinterpret_cast<const uint4*>(
-                    vbase + (int64_t)(r + ((vt + k * kStep) & 15)) * D);
+              for (int k = 0; k < kV; ++k) v[k] = row(k);
+            } else {  // zeros past the cached tokens and without a page
+              const int32_t left = ok ? u.kv_len - (t + 1) * BN - vt : 0;
+#pragma unroll
+              for (int k = 0; k < kV; ++k) {
+                v[k] = make_uint4(0, 0, 0, 0);
+                if (k * kStep < left && m.row[(vt + k * kStep) >> 4] >= 0) v[k] = row(k);
+              }
             }
           }
           if (t < 0) {  // Q, while the first V tile is on its way
