@@ -671,10 +671,12 @@ gdn_status gdn_attn_workspace_size(const gdn_attn_config* cfg, const gdn_kv_cach
  *  lse          [num_tokens][num_q_heads] fp32 out, or NULL: log of the sum of exponentials.
  * A query that sees no token gives o = 0 and lse = -inf. Pages out of range count as absent
  * (status raised). Rows outside every request are not written. Scores, softmax sums and
- * outputs are accumulated in fp32; products take fp16 operands: the cache's codes and the
- * powers-of-two-normalised bf16 queries exactly, probabilities rounded to 11 bits (fp32 io:
- * queries and probabilities as two fp16 terms, 22 bits). Results do not depend on atomics:
- * the same call gives the same bits. At most 4,096 requests.
+ * outputs are accumulated in fp32. The cache's codes enter the products exactly, and so do bf16
+ * queries, but for values below 2^-10 of their row's largest where a request has many queries:
+ * those are off by at most 2^-17 of the largest. Probabilities are rounded to fp16's 11 bits;
+ * a value scale below 2^-40 of the largest of its request and head counts as that much. With
+ * fp32 io queries and probabilities are two fp16 terms, 22 bits. Results do not depend on
+ * atomics: the same call gives the same bits. At most 4,096 requests.
  * Errors: INVALID_ARGUMENT, UNSUPPORTED, WORKSPACE_TOO_SMALL, CUDA. */
 gdn_status gdn_attn_paged(gdn_handle* handle, const gdn_attn_config* cfg,
                           const gdn_kv_cache* cache, int32_t num_seqs, int32_t num_tokens,

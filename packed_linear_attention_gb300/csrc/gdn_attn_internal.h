@@ -87,9 +87,8 @@ struct AttnArgs {
   int32_t num_seqs, num_tokens, max_q_len, max_kv_len;
   int32_t causal;
   float scale_log2;            // score scale times log2(e)
-  // Requests of at most split_q queries (split_queries in gdn_attn_api.cu) go to the split kernel
-  // (gdn_attn_split.cu), longer ones
-  // to the tile kernel (gdn_attn_tile.cu).
+  // Requests of at most split_q queries go to the split kernel (gdn_attn_split.cu), longer ones
+  // to the tile kernel (gdn_attn_tile.cu); split_queries in gdn_attn_api.cu has the rule.
   int32_t split_q;
   int32_t* status;
   float* partials;             // workspace of the split kernel

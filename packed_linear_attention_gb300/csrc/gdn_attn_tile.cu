@@ -8,11 +8,11 @@
 //   O (128 x D)  += P V,  P = 2^(S - m)
 //
 // Operands. K enters as it lies in the cache: e4m3 tiles come by TMA into the swizzled layout
-// that kind::f8f6f4 reads. Q stays in tensor memory for the whole unit and is split into two e4m3 terms, q 2^k = hi + lo (hi to four
-// significant bits, lo the rest; the row's power of two brings its largest value to [128,
-// 256)): a bf16 value has eight bits, so the two terms are exact down to 2^-10 of the row's
-// largest value and off by at most 2^-18 of it below. Two e4m3 products cost what one f16
-// product costs, and no K tile is converted. Such a split of P would lose the small
+// that kind::f8f6f4 reads. Q stays in tensor memory for the whole unit and is split into two
+// e4m3 terms, q 2^k = hi + lo (hi to four significant bits, lo the rest; the row's power of two
+// brings its largest value to [128, 256)): a bf16 value has eight bits, so the two terms are
+// exact down to 2^-10 of the row's largest value and off by at most 2^-17 of it below. Two e4m3
+// products cost what one f16 product costs, and no K tile is converted. Such a split of P would lose the small
 // probabilities of a long context, so P is f16 (from registers to TMEM, as the A operand) and
 // V is widened to f16 on its way from the cache to shared memory (exact). Shared memory is what
 // a tile would be bound by otherwise: with Q and a staged e4m3 V read from it, a tile of 64
@@ -26,12 +26,25 @@
 // the running maximum passes from one group to the other, warp by warp, through shared memory
 // and a pair of named barriers. 8-15 operands: V tiles, and the next unit's Q, whose bf16 rows
 // a bulk copy brings to shared memory while this unit runs and which moves to tensor memory
-// when its last S is done; 16 the producer (units, K tiles, Q rows); 17 issues S, 18 P V (the
+// when its last S is done; 16 the producer (pages, scales, K tiles); 17 issues S, 18 P V (the
 // twenty products of a tile, issued one after another between the waits of both, took one warp
-// longer than the tensor pipe); one idle (register shares move by whole groups of four warps).
+// longer than the tensor pipe); 19 takes the units and copies their rows of Q, so that they are
+// there when the unit before ends.
 // S is free again as soon as a group holds it in registers. Units come from a counter, heaviest
 // rows of a request first.
 // Every wait is bounded; after one gave up the block's warps leave at their unit's end.
+//
+// Bound and measured (16 query and 2 key/value heads of 256, causal). 4 x 8,192 tokens: 1,481 us
+// for 2.20 TFLOP, 79% of the measured bf16 peak. A tile takes 1,540 clocks where its products
+// take 1,024: tensor memory holds one S beside O and Q, so S(j + 1) waits until S(j) is read, and
+// P V stands in the same queue. 32 x 1,024 tokens: 325 us, 45%; a unit has 8.5 tiles, and its
+// start and end (Q to two terms, the output, the next first scores) take as long as six. 32 and 8
+// heads of 128, 8 requests of 190 to 1,789 tokens behind up to 1,537: 250 us, 41%; the products take 512
+// clocks of a tile, the two softmax groups 1,200. Half of the issue slots and 42% of the ALU are
+// taken, so instructions of any role cost time: page arithmetic in the operand warps cost 5% of
+// the first case. Tried and dropped: a second S at D <= 128 (no change), tiles of 128 tokens there
+// (265 us: scores read twice), V tiles taken in turns by two operand groups with the next unit's Q
+// converted between them (long 1,572, but 383 and 283: 7 KB more code), Q rows and V by one warp.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -7,18 +7,23 @@
 // the rest, at most an eighth of a turn, is one fp32 number, and the Taylor series of sine and
 // cosine to r^9 and r^10 leave less than 2^-28. Both kernels are bound by HBM
 // (every element is read and written once); a thread of the rotation takes the same pairs of
-// several heads of a token, so that the sine and cosine are formed once for them.
+// several heads of a token, so that the sine and cosine are formed once for them. Measured: 18
+// heads of 256 of 32,768 tokens 101 us, 6.0 TB/s, 88% of the measured copy rate.
 //
 // Append. A unit is a run of rows that land in one page, for one head: keys by one half of a
 // block's 512 threads and values by the other, eight elements of a row a thread. The run's rows
-// are loaded at once and stay in registers as they came while its largest magnitude is found;
-// the rotation is cheap enough to be done twice (its sines and cosines are formed once for the
-// run, by all threads, while the rows are on their way; the other half of a pair comes by a
-// shuffle, since a row never leaves a warp). Only runs longer than eight bf16 or four fp32 rows
-// a thread read their first rows a second time. With power-of-two scales the division is exact,
+// are copied to shared memory at once, asynchronously, and stay there as they came while its
+// largest magnitude is found; the rotation is cheap enough to be done twice (its sines and
+// cosines are formed once for the run, by all threads, while the rows are on their way; the other
+// half of a pair is read beside, since a row never leaves a warp). Only runs longer than eight
+// bf16 or four fp32 rows a thread read their first rows a second time. With power-of-two scales the division is exact,
 // and a later, larger scale only moves the exponents of the codes that are already there. No
 // unit list is needed: a row begins a run when its slot opens a page or does not follow the
-// previous row's slot.
+// previous row's slot. Measured: 32 x 1,024 tokens, 16 query heads rotated beside 2 + 2 heads of
+// 256, 129 us, 4.9 TB/s, 73% of the copy rate; keys and values alone 33 us, 46 with rotation,
+// where a block's chain of slots, rows, maximum and store is what bounds it (two blocks an SM).
+// Rows in registers took 137 us, three blocks an SM 152 (spills), and asking for the rows before
+// the slots are known changed nothing.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
