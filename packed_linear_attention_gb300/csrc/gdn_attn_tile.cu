@@ -234,6 +234,9 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ __nv_bfloat162 bf16x2(uint32_t x) {
+  return *reinterpret_cast<const __nv_bfloat162*>(&x);
+}
 __device__ __forceinline__ uint32_t e4m3_to_half2(uint16_t x) {
   uint32_t r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(x));
@@ -635,25 +638,33 @@ tile_kernel(const __grid_constant__ TileParams p) {
             int ex;
             {
               const bool live = u.first + qr < u.q_len * a.group;
-              // largest magnitude of the row: bf16 bit patterns without their signs order like
-              // integers
-              uint32_t top = 0;
+              // largest magnitude of the row, NaN if there is one
+              __nv_bfloat162 big = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll 4
               for (int c = 0; c < D; c += 16) {
                 const uint4 w = *reinterpret_cast<const uint4*>(raw + c);
-                top = __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
-                                             __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
+                big = __hmax2_nan(big, __habs2(bf16x2(w.x)));
+                big = __hmax2_nan(big, __habs2(bf16x2(w.y)));
+                big = __hmax2_nan(big, __habs2(bf16x2(w.z)));
+                big = __hmax2_nan(big, __habs2(bf16x2(w.w)));
               }
+              uint32_t top = *reinterpret_cast<const uint32_t*>(&big);
               sm.exchange_q[qhalf][qr] = (uint16_t)max(top & 0xffffu, top >> 16);
               named_sync(kAuxBar, kAuxThreads);
               top = max(sm.exchange_q[0][qr], sm.exchange_q[1][qr]);
-              ex = (int)(top >> 7) - 127;           // [128, 256) after the scaling
-              const bool wild = ex == 128;           // an infinity or NaN: the row is NaN
+              ex = (int)(top >> 7) - 127;            // [128, 256) after the scaling
+              const bool wild = live && ex == 128;   // an infinity or NaN: the row is NaN
               ex = wild ? 7 : max(ex, -100);
               if (!live) ex = 7;
               float up = wild ? __int_as_float(0x7fffffff)
                               : __uint_as_float((uint32_t)(7 - ex + 127) << 23);
               if (a.scale_log2 < 0.f) up = -up;
+              const __nv_bfloat162 up2 = __floats2bfloat162_rn(up, up);  // exact: a power of two
+              if (!live) {  // the row may hold anything
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16)
+                  *reinterpret_cast<uint4*>(raw + c) = make_uint4(0, 0, 0, 0);
+              }
               // in place: eight values become eight e4m3 codes of each term
 #pragma unroll 2
               for (int c = 0; c < D; c += 16) {
@@ -663,8 +674,10 @@ tile_kernel(const __grid_constant__ TileParams p) {
                 uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                  const uint32_t h = f16x2(__uint_as_float(w[e] << 16) * up,
-                                           __uint_as_float(w[e] & 0xffff0000u) * up);
+                  const __nv_bfloat162 y = __hmul2(bf16x2(w[e]), up2);
+                  const uint32_t yb = *reinterpret_cast<const uint32_t*>(&y);
+                  const uint32_t h =
+                      f16x2(__uint_as_float(yb << 16), __uint_as_float(yb & 0xffff0000u));
                   const uint16_t k = half2_to_e4m3(h);
                   const uint32_t back = e4m3_to_half2(k);
                   const __half2 rest = __hsub2(*reinterpret_cast<const __half2*>(&h),
@@ -672,7 +685,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
                   hi[e >> 1] |= (uint32_t)k << (16 * (e & 1));
                   lo[e >> 1] |= (uint32_t)half2_to_e4m3(h2_bits(rest)) << (16 * (e & 1));
                 }
-                *at8 = live ? make_uint4(hi[0], hi[1], lo[0], lo[1]) : make_uint4(0, 0, 0, 0);
+                *at8 = make_uint4(hi[0], hi[1], lo[0], lo[1]);
               }
             }
             // to tensor memory, when the S products of the unit before have read theirs
