@@ -44,7 +44,7 @@
 // taken, so instructions of any role cost time: page arithmetic in the operand warps cost 5% of
 // the first case. Tried and dropped: a second S at D <= 128 (no change), tiles of 128 tokens there
 // (265 us: scores read twice), V tiles taken in turns by two operand groups with the next unit's Q
-// converted between them (long 1,572, but 383 and 283: 7 KB more code), Q rows and V by one warp.
+// converted between them (1,572, 383 and 283 us in the order of the cases: 7 KB more code).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
