@@ -114,22 +114,24 @@ int device_sms(int* out);
 
 #ifdef __CUDACC__
 // Request b's range, made safe: first row, queries, cached tokens. Raises `bad` when the
-// caller's numbers had to be cut.
+// caller's numbers had to be cut. Both ends are cut to [0, num_tokens] before the subtraction,
+// which would wrap for an end far below 0. (For the host too, where its test runs it.)
 struct AttnSeq {
   int32_t row0, q_len, kv_len;
 };
-__device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, int b, bool& bad) {
+__host__ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, int b, bool& bad) {
   const int32_t r0 = a.cu_q[b], r1 = a.cu_q[b + 1], kv = a.kv_len[b];
   AttnSeq s;
   s.row0 = min(max(r0, 0), a.num_tokens);
-  s.q_len = min(max(min(r1, a.num_tokens) - s.row0, 0), a.max_q_len);
+  s.q_len = min(max(min(max(r1, 0), a.num_tokens) - s.row0, 0), a.max_q_len);
   const int64_t room = (int64_t)a.max_blocks * a.page_size;
   s.kv_len = (int32_t)min((int64_t)min(max(kv, 0), a.max_kv_len), room);
   bad = bad || s.row0 != r0 || s.q_len != (int64_t)r1 - r0 || s.kv_len != kv;
   return s;
 }
 // Cached tokens that query i of the request sees.
-__device__ __forceinline__ int32_t attn_limit(const AttnArgs& a, const AttnSeq& s, int32_t i) {
+__host__ __device__ __forceinline__ int32_t attn_limit(const AttnArgs& a, const AttnSeq& s,
+                                                       int32_t i) {
   return a.causal ? min(max(s.kv_len - s.q_len + i + 1, 0), s.kv_len) : s.kv_len;
 }
 

@@ -1,0 +1,47 @@
+"""Ranges of the attention calls' requests, as the kernels work them out from the caller's
+device-side numbers: the kernels' own arithmetic, built for the host."""
+import ctypes
+import itertools
+import os
+import subprocess
+
+import numpy as np
+import pytest
+
+from packed_linear_attention_gb300 import build
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+LO, HI = -2**31, 2**31 - 1
+
+
+@pytest.fixture(scope="module")
+def ranges(tmp_path_factory):
+    so = str(tmp_path_factory.mktemp("ranges") / "libattn_ranges.so")
+    subprocess.run([build.nvcc(), *build.ARCH, "-O1", "-std=c++17", "-Xcompiler",
+                    "-fPIC,-fwrapv", "-shared", "-I", build.INCLUDE, "-o", so,
+                    os.path.join(HERE, "cuda", "attn_ranges.cu")], check=True,
+                   capture_output=True)
+    fn = ctypes.CDLL(so).attn_ranges
+
+    def call(cu, kv, tokens, max_q, max_kv, blocks=HI, page=16):
+        n = len(kv)
+        out = np.empty((4, n), np.int32)
+        cu, kv = np.asarray(cu, np.int32), np.asarray(kv, np.int32)
+        p = lambda x: x.ctypes.data_as(ctypes.c_void_p)  # noqa: E731
+        fn(n, tokens, max_q, max_kv, blocks, page, p(cu), p(kv), *(p(x) for x in out))
+        return out.astype(np.int64)
+
+    return call
+
+
+def test_rows_stay_inside_the_arrays(ranges):
+    """Any two numbers as a request's first and last row: its rows are rows of the arrays, and
+    the request is flagged unless the numbers were in order."""
+    ends = [LO, LO + 1, LO + 5, -7, -1, 0, 1, 5, 6, 7, 100, HI - 1, HI]
+    for tokens, max_q in ((6, 3), (6, HI), (0, 4), (1, 0), (HI, HI)):
+        for r0, r1 in itertools.product(ends, ends):
+            (row0,), (q,), _, (bad,) = ranges([r0, r1], [4], tokens, max_q, 100)
+            assert 0 <= row0 <= tokens and 0 <= q <= max_q and row0 + q <= tokens, (r0, r1, tokens)
+            lo, hi = max(r0, 0), min(r1, tokens)
+            assert q == min(max(hi - min(lo, tokens), 0), max_q)
+            assert bad == (not (0 <= r0 <= r1 <= tokens and r1 - r0 <= max_q))
