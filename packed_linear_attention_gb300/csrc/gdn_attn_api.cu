@@ -128,7 +128,9 @@ gdn_status check_attn(const gdn_attn_config* cfg, const gdn_kv_cache* c, int32_t
   const double group = cfg->num_q_heads / c->num_kv_heads;
   const double items = ((double)num_tokens * group / 8 + num_seqs) * c->num_kv_heads *
                        (max_kv_len / (double)gdn::kSplitTile + 1);
-  if ((double)num_tokens * group > (double)INT32_MAX || items > (double)INT32_MAX)
+  const double units = ((double)num_tokens * group / gdn::kTileRows + num_seqs) * c->num_kv_heads;
+  if ((double)num_tokens * group > (double)INT32_MAX || items >= (double)INT32_MAX ||
+      units >= (double)gdn::kMaxUnits)
     return GDN_ERR_UNSUPPORTED;
   return GDN_OK;
 }

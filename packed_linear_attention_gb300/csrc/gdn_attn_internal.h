@@ -96,6 +96,9 @@ struct AttnArgs {
 };
 constexpr int kSplitTile = 64;     // cached tokens of a work item of the split kernel
 constexpr int kTileRows = 128;     // query rows of a unit of the tile kernel
+// Units of the tile kernel in one call: 32 requests' sum fits 32 bits. (2^26 units of 128 rows of
+// 64 bf16 values would be a terabyte of queries.)
+constexpr int kMaxUnits = 1 << 26;
 
 constexpr int kMaxSms = 160;       // the workspace is sized without asking the device
 
@@ -133,6 +136,14 @@ __host__ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, int b, b
 __host__ __device__ __forceinline__ int32_t attn_limit(const AttnArgs& a, const AttnSeq& s,
                                                        int32_t i) {
   return a.causal ? min(max(s.kv_len - s.q_len + i + 1, 0), s.kv_len) : s.kv_len;
+}
+
+// Sum of two counts of work items (or units), held at kTooMany. The host check keeps those of
+// requests in order below it; requests whose rows overlap can ask for more, and get none.
+constexpr int32_t kTooMany = INT32_MAX;
+__host__ __device__ __forceinline__ int32_t add_items(int32_t x, int32_t y) {
+  const uint32_t sum = (uint32_t)x + (uint32_t)y;
+  return sum < (uint32_t)kTooMany ? (int32_t)sum : kTooMany;
 }
 
 __device__ __forceinline__ void raise_status(int32_t* status, int32_t code) {

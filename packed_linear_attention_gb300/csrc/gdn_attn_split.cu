@@ -110,7 +110,7 @@ struct SmemHead {
   float row_scale[8 * NT];
   int32_t row_limit[8 * NT];
   float m[kWarps][8 * NT], l[kWarps][8 * NT], vref[kWarps];
-  int64_t scan[8];
+  int32_t scan[8];
   int32_t dead;
 };
 
@@ -212,14 +212,14 @@ split_kernel(const __grid_constant__ SplitParams p) {
     bool bad = false;
     for (int b = b0; b < b1; ++b) {
       const AttnSeq s = attn_seq(a, b, bad);
-      sum += seq_items<RB>(a, s);
+      sum = add_items(sum, seq_items<RB>(a, s));
     }
     if (bad && blockIdx.x == 0) raise_status(a.status, GDN_ERR_INVALID_ARGUMENT);
     int32_t inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int32_t y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
+      if (lane >= o) inc = add_items(inc, y);
     }
     if (lane == 31) sm.scan[warp] = inc;
     if (tid == 0) {
@@ -232,16 +232,17 @@ split_kernel(const __grid_constant__ SplitParams p) {
     }
     __syncthreads();
     int32_t at = inc - sum;
-    for (int w = 0; w < warp; ++w) at += (int32_t)sm.scan[w];
+    for (int w = 0; w < warp; ++w) at = add_items(at, sm.scan[w]);
     for (int b = b0; b < b1; ++b) {
       pre[b] = at;
-      at += seq_items<RB>(a, attn_seq(a, b, bad));
+      at = add_items(at, seq_items<RB>(a, attn_seq(a, b, bad)));
     }
     if (b1 == a.num_seqs && b0 < b1) pre[a.num_seqs] = at;
     __syncthreads();
   }
   // G workers share W items
-  const int64_t W = pre[a.num_seqs], G = min((int64_t)gridDim.x, W);
+  const int64_t W = pre[a.num_seqs] == kTooMany ? 0 : pre[a.num_seqs],
+                G = min((int64_t)gridDim.x, W);
   if (blockIdx.x >= G) return;
   const int32_t w0 = (int32_t)(W * blockIdx.x / G), w1 = (int32_t)(W * (blockIdx.x + 1) / G);
   uint32_t it = 0;  // tiles since the start: stage and phase
@@ -634,16 +635,16 @@ join_kernel(AttnArgs a, const float* part, int workers) {
     int32_t items = 0, units = 0;
     for (int b = b0; b < b1; ++b) {
       const AttnSeq s = attn_seq(a, b, bad);
-      items += seq_items<RB>(a, s);
-      units += units_of(s);
+      items = add_items(items, seq_items<RB>(a, s));
+      units = add_items(units, units_of(s));
     }
     int32_t x = items, y = units;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int32_t u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
       if (lane >= o) {
-        x += u;
-        y += v;
+        x = add_items(x, u);
+        y = add_items(y, v);
       }
     }
     if (lane == 31) {
@@ -654,15 +655,15 @@ join_kernel(AttnArgs a, const float* part, int workers) {
     x -= items;
     y -= units;
     for (int w = 0; w < warp; ++w) {
-      x += scan[w][0];
-      y += scan[w][1];
+      x = add_items(x, scan[w][0]);
+      y = add_items(y, scan[w][1]);
     }
     for (int b = b0; b < b1; ++b) {
       pre[b] = x;
       unit0[b] = y;
       const AttnSeq s = attn_seq(a, b, bad);
-      x += seq_items<RB>(a, s);
-      y += units_of(s);
+      x = add_items(x, seq_items<RB>(a, s));
+      y = add_items(y, units_of(s));
     }
     if (b1 == n && b0 < b1) {
       pre[n] = x;
@@ -671,7 +672,7 @@ join_kernel(AttnArgs a, const float* part, int workers) {
     __syncthreads();
   }
   const int64_t W = pre[n], G = min((int64_t)workers, W);
-  const int64_t jobs = (int64_t)unit0[n] * RB;
+  const int64_t jobs = W == kTooMany ? 0 : (int64_t)unit0[n] * RB;
   const int me = tid % kTeam;             // this thread in its row's team
   float* const w = weight[tid / kTeam];
   auto worker_of = [&](int64_t item) {

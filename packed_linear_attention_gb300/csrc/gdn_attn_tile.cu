@@ -297,7 +297,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
   for (int c = warp; c < chunks; c += kWarps) {
     const int b = 32 * c + lane;
     int32_t n = b < a.num_seqs ? seq_units(a, attn_seq(a, b, bad)) : 0;
-    n = __reduce_add_sync(0xffffffffu, n);
+    n = __reduce_add_sync(0xffffffffu, n);  // each below kMaxUnits
     if (lane == 0) sm.coarse[c + 1] = n;
   }
   if (bad && blockIdx.x == 0) raise_status(a.status, GDN_ERR_INVALID_ARGUMENT);
@@ -311,12 +311,12 @@ tile_kernel(const __grid_constant__ TileParams p) {
     int32_t at = 0;
     sm.coarse[0] = 0;
 #pragma unroll 1
-    for (int c = 1; c <= chunks; ++c) sm.coarse[c] = at += sm.coarse[c];
+    for (int c = 1; c <= chunks; ++c) sm.coarse[c] = at = add_items(at, sm.coarse[c]);
   }
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = sm.tmem;
-  const int32_t total = sm.coarse[chunks];
+  const int32_t total = sm.coarse[chunks] == kTooMany ? 0 : sm.coarse[chunks];
 
   // Takes the next unit of the block's list (every role but the scheduler).
   uint32_t nu = 0;

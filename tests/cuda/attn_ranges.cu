@@ -1,4 +1,4 @@
-// Host build of the attention kernels' range arithmetic (attn_seq, attn_limit), so that it can
+// Host build of the attention kernels' range arithmetic (attn_seq, add_items), so that it can
 // be checked for every kind of caller's numbers without a GPU.
 #include "../../packed_linear_attention_gb300/csrc/gdn_attn_internal.h"
 
@@ -22,4 +22,10 @@ extern "C" void attn_ranges(int num_seqs, int num_tokens, int max_q_len, int max
     kv[b] = s.kv_len;
     bad[b] = cut;
   }
+}
+
+extern "C" int attn_items_sum(int n, const int* items) {
+  int sum = 0;
+  for (int i = 0; i < n; ++i) sum = gdn::add_items(sum, items[i]);
+  return sum;
 }

@@ -21,7 +21,8 @@ def ranges(tmp_path_factory):
                     "-fPIC,-fwrapv", "-shared", "-I", build.INCLUDE, "-o", so,
                     os.path.join(HERE, "cuda", "attn_ranges.cu")], check=True,
                    capture_output=True)
-    fn = ctypes.CDLL(so).attn_ranges
+    lib = ctypes.CDLL(so)
+    fn = lib.attn_ranges
 
     def call(cu, kv, tokens, max_q, max_kv, blocks=HI, page=16):
         n = len(kv)
@@ -31,6 +32,7 @@ def ranges(tmp_path_factory):
         fn(n, tokens, max_q, max_kv, blocks, page, p(cu), p(kv), *(p(x) for x in out))
         return out.astype(np.int64)
 
+    call.lib = lib
     return call
 
 
@@ -45,3 +47,15 @@ def test_rows_stay_inside_the_arrays(ranges):
             lo, hi = max(r0, 0), min(r1, tokens)
             assert q == min(max(hi - min(lo, tokens), 0), max_q)
             assert bad == (not (0 <= r0 <= r1 <= tokens and r1 - r0 <= max_q))
+
+
+def test_item_counts_stop_at_the_end_of_32_bits(ranges):
+    """Overlapping requests may ask for any number of work items: the sum never wraps."""
+    rng = np.random.default_rng(0)
+    total = lambda x: ranges.lib.attn_items_sum(  # noqa: E731
+        len(x), np.asarray(x, np.int32).ctypes.data_as(ctypes.c_void_p))
+    assert total([HI - 5, 3]) == HI - 2 and total([HI - 5, 5]) == HI
+    assert total([2304 * 1024] * 2048) == HI and total([HI] * 100) == HI
+    for _ in range(200):
+        x = rng.integers(0, rng.integers(1, HI), 40)
+        assert total(x) == min(int(x.sum()), HI)

@@ -54,3 +54,30 @@ def test_ends_far_out_of_range(io, lengths, max_q):
         outside = torch.from_numpy(~inside).cuda()
         assert (o[outside] == 5).all() and (lse[outside] == 7).all()
         assert torch.isfinite(o).all()  # the guard rows of q are NaN
+
+
+def test_overlapping_requests_that_ask_for_too_much():
+    """2,048 requests, each over all rows of the call: their work items pass 32 bits. Nothing is
+    computed, the status is raised, and the next call is right."""
+    torch = torch_cuda()
+    seqs, tokens, hq, dim, page, kv = 4096, 2304, 16, 64, 16, 65536
+    i32 = dict(dtype=torch.int32, device="cuda")
+    codes = [torch.zeros(4, 1, page, dim, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    scales = [torch.ones(4, 1, device="cuda") for _ in range(2)]
+    cache = gdn.make_kv_cache(*codes, *scales)
+    cfg = gdn.make_attn_config(hq, scale=1.0, io_dtype=gdn.GDN_F32)
+    cu = torch.zeros(seqs + 1, **i32)
+    cu[1::2] = tokens
+    table = torch.zeros(seqs, kv // page, **i32)
+    kv_len = torch.full((seqs,), kv, **i32)
+    q = torch.zeros(tokens, hq * dim, device="cuda")
+    o = torch.full_like(q, 5.0)
+    size = gdn.gdn_attn_workspace_size(cfg, cache, seqs, tokens, tokens, kv)
+    work = torch.empty(size, dtype=torch.uint8, device="cuda")
+    status = torch.zeros(1, **i32)
+    gdn.gdn_attn_paged(handle(), cfg, cache, seqs, tokens, tokens, kv, cu, kv_len, table,
+                       kv // page, q, hq * dim, o, hq * dim, None, work, size, status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == gdn.GDN_ERR_INVALID_ARGUMENT
+    assert (o == 5).all()
+    Case(32, [3, 40], [100, 40], 8, 2, 64, 16, "f32").check(torch)
