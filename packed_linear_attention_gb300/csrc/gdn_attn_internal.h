@@ -100,6 +100,10 @@ constexpr int kTileRows = 128;     // query rows of a unit of the tile kernel
 // 64 bf16 values would be a terabyte of queries.)
 constexpr int kMaxUnits = 1 << 26;
 
+// Longest request: tokens are numbered in 32 bits, by batches of 512 and a batch ahead. (A cache
+// has fewer than 2^31 tokens in all.)
+constexpr int32_t kMaxKvLen = INT32_MAX - 4096;
+
 constexpr int kMaxSms = 160;       // the workspace is sized without asking the device
 
 size_t attn_workspace(const gdn_attn_config& cfg, const gdn_kv_cache& c);
@@ -128,7 +132,7 @@ __host__ __device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, int b, b
   s.row0 = min(max(r0, 0), a.num_tokens);
   s.q_len = min(max(min(max(r1, 0), a.num_tokens) - s.row0, 0), a.max_q_len);
   const int64_t room = (int64_t)a.max_blocks * a.page_size;
-  s.kv_len = (int32_t)min((int64_t)min(max(kv, 0), a.max_kv_len), room);
+  s.kv_len = (int32_t)min((int64_t)min(max(kv, 0), min(a.max_kv_len, kMaxKvLen)), room);
   bad = bad || s.row0 != r0 || s.q_len != (int64_t)r1 - r0 || s.kv_len != kv;
   return s;
 }

@@ -804,7 +804,8 @@ int launch(const AttnArgs& a, const gdn_kv_cache& c, int num_sms, cudaStream_t s
     return (int)cudaErrorInvalidValue;
   // one block per SM slot, no more than there can be items
   const int64_t units = ((int64_t)a.num_tokens * a.group + RB - 1) / RB + a.num_seqs;
-  const int64_t items = units * a.hkv * std::max(1, (a.max_kv_len + kTile - 1) / kTile);
+  const int64_t items = units * a.hkv *
+                        std::max<int64_t>(1, ((int64_t)a.max_kv_len + kTile - 1) / kTile);
   const int workers = (int)std::min<int64_t>((int64_t)kCtasPerSm * num_sms, items);
   p.part = a.partials;
   const size_t q = (size_t)kTerms * NT * D * 16, red = sizeof(float) * RB * (D + 8);

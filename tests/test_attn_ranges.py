@@ -49,6 +49,19 @@ def test_rows_stay_inside_the_arrays(ranges):
             assert bad == (not (0 <= r0 <= r1 <= tokens and r1 - r0 <= max_q))
 
 
+def test_tokens_can_be_numbered_past_the_last_one(ranges):
+    """The kernels number tokens by whole batches of 512, a batch ahead: no such number passes 32
+    bits, whatever length the caller states, and a length that was cut is flagged."""
+    for kv in (LO, -1, 0, 1, 1 << 30, HI - 4096, HI - 4095, HI - 1023, HI):
+        for max_kv in (0, 100, HI - 2000, HI):
+            for blocks in (1, HI):
+                _, _, (length,), (bad,) = ranges([0, 1], [kv], 1, 1, max_kv, blocks)
+                assert 0 <= length <= min(max(kv, 0), max_kv, 16 * blocks)
+                assert -(-length // 512) * 512 + 2 * 512 <= HI
+                assert length == min(max(kv, 0), max_kv, 16 * blocks, HI - 4096)
+                assert bad == (length != kv)
+
+
 def test_item_counts_stop_at_the_end_of_32_bits(ranges):
     """Overlapping requests may ask for any number of work items: the sum never wraps."""
     rng = np.random.default_rng(0)
