@@ -523,7 +523,8 @@ gdn_status gdn_split_segment_auto(int32_t num_seqs, const int32_t* cu_seqlens_ho
  * wait that gave up raises it to GDN_ERR_DEVICE_TIMEOUT. */
 
 /* A paged cache of e4m3 values with one fp32 scale for each page and head. A cached value is
- * its e4m3 code times its page's and head's scale. All arrays are device memory, k and v
+ * its e4m3 code times its page's and head's scale; v holds no NaN codes (gdn_kv_append puts a
+ * token's NaN into its key alone). All arrays are device memory, k and v
  * 16-byte aligned. Supported: page_size 16, 32, 64 or 128, head_dim 64, 128 or 256,
  * num_pages * num_kv_heads * page_size <= INT32_MAX. */
 typedef struct gdn_kv_cache {
@@ -675,10 +676,13 @@ gdn_status gdn_attn_workspace_size(const gdn_attn_config* cfg, const gdn_kv_cach
  * together they ask for 2^31 work items. Scores, softmax sums and
  * outputs are accumulated in fp32. The cache's codes enter the products exactly, and so do bf16
  * queries, but for values below 2^-10 of their row's largest where a request has many queries:
- * those are off by at most 2^-17 of the largest. Probabilities are rounded to fp16's 11 bits;
- * a value scale below 2^-40 of the largest of its request and head counts as that much. With
- * fp32 io queries and probabilities are two fp16 terms, 22 bits. Results do not depend on
- * atomics: the same call gives the same bits. At most 4,096 requests.
+ * those are off by at most 2^-17 of the largest. A token's weight, its probability times its
+ * value scale, is rounded to fp16's 11 bits, or to 2^-31 of the largest weight of its row where
+ * that is more: tokens that a row does not see, or gives no weight, change nothing of it. With
+ * fp32 io queries and weights are two fp16 terms, 22 bits (weights to 2^-31 of the row's
+ * largest). Value scales count as at least 2^-100 and at most 2^120, the range in which
+ * gdn_kv_append keeps them. Results do not depend on atomics: the same call gives the same bits.
+ * At most 4,096 requests.
  * Errors: INVALID_ARGUMENT, UNSUPPORTED, WORKSPACE_TOO_SMALL, CUDA. */
 gdn_status gdn_attn_paged(gdn_handle* handle, const gdn_attn_config* cfg,
                           const gdn_kv_cache* cache, int32_t num_seqs, int32_t num_tokens,

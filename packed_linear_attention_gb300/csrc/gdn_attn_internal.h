@@ -94,6 +94,24 @@ struct AttnArgs {
   float* partials;             // workspace of the split kernel
   int32_t* counter;            // workspace of the tile kernel: units taken
 };
+// Value scales enter the exponents, not the accumulator. With s a token's score (log2) and z = s +
+// log2(its value scale) + kScaleShift, a row keeps two running maxima over the tokens that it sees:
+// ms of s, to which its softmax sum refers, and mz of z, to which the accumulator does. P is
+// 2^(z - mz), so that the row's largest weight (probability times value scale) fills the f16 range
+// whatever the scales of other pages are; the sum takes P times 2^(mz - ms + s - z), one factor
+// for 16 tokens. Both maxima are looked at when a z passes mz by kLazyMax (log2 units), or when a
+// scale lies 2^kNear below the row's (mz - ms); in between scores stay below ms + kLazyMax + kNear.
+// For a scale that far below, the exponent is raised to at least -kFar - ms + s: P is 0 in f16 all
+// the same, and the probability is not lost from the sum. The shift brings scales of ordinary
+// values (2^-6) to z = s. Scales count as at least 2^-100 (the append's least) and at most 2^120
+// (its largest).
+constexpr float kScaleShift = 6.f;
+constexpr float kLazyMax = 8.f, kNear = 40.f, kFar = 45.f;
+constexpr float kNoMax = -3.402823466e38f;  // maxima of a row that has seen no token (finite, so
+                                            // that differences are no NaN)
+constexpr float kMinValueScale = 7.8886090522101181e-31f;  // 2^-100
+constexpr float kMaxValueScale = 1.3292279957849159e36f;   // 2^120
+
 constexpr int kSplitTile = 64;     // cached tokens of a work item of the split kernel
 constexpr int kTileRows = 128;     // query rows of a unit of the tile kernel
 // Units of the tile kernel in one call: 32 requests' sum fits 32 bits. (2^26 units of 128 rows of

@@ -25,9 +25,9 @@
 // token's row; V^T is read with transposing 16-bit ldmatrix (two channels to an element) and
 // one byte permutation. The queries are scaled by a power of two per row into the f16 range
 // (bf16 fits exactly); fp32 queries and probabilities are two f16 terms.
-// The running maximum is only raised when a score passes it by 2^8 (in log2 units, 8): until
-// then probabilities stay below 2^8 and no cross-lane reduction is needed. Value scales enter
-// as ratios to the largest met so far, so that probabilities fill the f16 range.
+// The running maxima (of scores and of exponents with the value scales, see kScaleShift in
+// gdn_attn_internal.h) are only raised when one is passed by 8 (in log2 units): until then
+// weights stay below 2^8 and no cross-lane reduction is needed.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -52,8 +52,9 @@ constexpr int kGroups = kTile / 16;             // 16-token groups of a tile, on
 constexpr int kCtasPerSm = 2;
 constexpr int kMaxStages = 8;
 constexpr uint32_t kWaitLimit = 1u << 20;       // a poll that fails takes 0.8 us: about a second
-constexpr float kLazyMax = 8.f;                 // log2 units
-constexpr float kProbScale = 128.f;             // probabilities times this, at most 2^15 in f16
+constexpr float kProbScale = 64.f;              // weights times this and a scale's fraction: at
+                                                // most 2^15 in f16
+constexpr float kOutShift = 6.f + kScaleShift;  // log2 of kProbScale and the scales' shift
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kStatusTimeout = GDN_ERR_DEVICE_TIMEOUT;
 constexpr size_t kSmemPerCta = 112 * 1024;      // two blocks share an SM's 227 KB
@@ -63,7 +64,7 @@ constexpr size_t kSmemPerCta = 112 * 1024;      // two blocks share an SM's 227 
 struct SplitParams {
   AttnArgs a;
   CUtensorMap tk, tv;
-  float* part;        // [2 workers][RB (D + 2)]
+  float* part;        // [2 workers][RB (D + 4)]: rows, then their maxima (z, s) and sum
   int32_t stages;
   uint32_t off_q, off_red, off_pre;  // shared-memory map after the stages
 };
@@ -99,8 +100,10 @@ __device__ __forceinline__ uint32_t tile_offset(int row, int chunk) {
   else return (chunk >> 3) * (kTile * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
 }
 
-struct GroupMeta {
-  float ks, vs;   // ks < 0: the group's page is absent
+struct __align__(16) GroupMeta {
+  float ks;       // key scale; below 0: the group's page is absent
+  float lv;       // exponent of the value scale, shifted
+  float pv;       // its fraction, in [1, 2), times kProbScale
 };
 
 template <int NT>
@@ -109,7 +112,7 @@ struct SmemHead {
   GroupMeta meta[kMaxStages][kGroups];
   float row_scale[8 * NT];
   int32_t row_limit[8 * NT];
-  float m[kWarps][8 * NT], l[kWarps][8 * NT], vref[kWarps];
+  float mz[kWarps][8 * NT], ms[kWarps][8 * NT], l[kWarps][8 * NT];
   int32_t scan[8];
   int32_t dead;
 };
@@ -260,7 +263,7 @@ split_kernel(const __grid_constant__ SplitParams p) {
       for (int32_t tb = g.t0; tb < g.t1; tb += 8) {  // 8 tiles' pages and scales, one group a lane
         const int32_t tok = tb * kTile + lane * 16;
         int32_t id = -1;
-        float ks = -1.f, vs = 0.f;
+        float ks = -1.f, vs = 0.f;  // a value scale that is none counts as the smallest
         if (tok < s.kv_len && tok < g.t1 * kTile) {
           id = table[tok >> a.page_shift];
           if (id >= 0 && id < a.num_pages) {
@@ -272,11 +275,15 @@ split_kernel(const __grid_constant__ SplitParams p) {
             raise_status(a.status, GDN_ERR_INVALID_ARGUMENT);
           }
         }
+        const uint32_t vb = __float_as_uint(fminf(fmaxf(vs, kMinValueScale), kMaxValueScale));
+        const int lv = (int)(vb >> 23) - 127 + (int)kScaleShift;
+        const GroupMeta group = {
+            ks, (float)lv, __uint_as_float((vb & 0x7FFFFFu) | 0x3F800000u) * kProbScale};
         for (int j = 0; j < 8 && tb + j < g.t1; ++j, ++it) {
           const int st = it % S;
           wait_or_die(&sm.empty[st], ((it / S) & 1u) ^ 1u, &sm.dead, a.status);
           const int first = j * kGroups;
-          if (lane >= first && lane < first + kGroups) sm.meta[st][lane - first] = {ks, vs};
+          if (lane >= first && lane < first + kGroups) sm.meta[st][lane - first] = group;
           // one lane per box: the lanes that hold its first group
           const bool box = lane >= first && lane < first + kGroups &&
                            (lane - first) % per_box == 0 && id >= 0;
@@ -378,11 +385,12 @@ split_kernel(const __grid_constant__ SplitParams p) {
       }
 
     float O[kSteps][NT][4];
-    float m[NT][2], l[NT][2], vref = 0.f;
+    float mz[NT][2], apart[NT][2], l[NT][2];  // apart: mz - ms
+    float most = kNoMax;                      // largest apart of this thread's rows
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      m[t][0] = m[t][1] = -GDN_INF;
-      l[t][0] = l[t][1] = 0.f;
+      mz[t][0] = mz[t][1] = kNoMax;
+      apart[t][0] = apart[t][1] = l[t][0] = l[t][1] = 0.f;
 #pragma unroll
       for (int k = 0; k < kSteps; ++k)
 #pragma unroll
@@ -429,32 +437,39 @@ split_kernel(const __grid_constant__ SplitParams p) {
               }
           }
         }
-        // ---- scores, running maximum, probabilities
-        float s4[NT][4];
-        bool over = false;
+        // ---- exponents, running maxima, weights
+        float z4[NT][4];
+        bool over = most > meta.lv + kNear;
         const bool masked = j0 + 16 > min_limit;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            float x = (acc[0][n][e] + acc[1][n][e]) * (meta.ks * rs[n][e & 1]);
-            if (masked && j0 + n8 + (e >= 2 ? 8 : 0) >= lim[n][e & 1]) x = -GDN_INF;
-            s4[n][e] = x;
-            over = over || x > m[n][e & 1] + kLazyMax;
+            float z = fmaf(acc[0][n][e] + acc[1][n][e], meta.ks * rs[n][e & 1], meta.lv);
+            if (masked && j0 + n8 + (e >= 2 ? 8 : 0) >= lim[n][e & 1]) z = -GDN_INF;
+            z4[n][e] = z;
+            over = over || z > mz[n][e & 1] + kLazyMax;
           }
         if (__any_sync(0xffffffffu, over)) {
+          most = kNoMax;
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float x = fmaxf(s4[n][e], s4[n][e + 2]);
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-              x = fmaxf(x, m[n][e]);
-              const float f = x == -GDN_INF ? 1.f : ex2(m[n][e] - x);
-              m[n][e] = x;
-              l[n][e] *= f;
+              float z = fmaxf(z4[n][e], z4[n][e + 2]);
+              z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 4));
+              z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 8));
+              z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 16));
+              const float was = mz[n][e] - apart[n][e], ms = fmaxf(z - meta.lv, was);
+              l[n][e] *= ex2(was - ms);
+              z = fmaxf(z, mz[n][e]);
+              const float f = ex2(mz[n][e] - z);
+              mz[n][e] = z;
+              apart[n][e] = z - ms;
+              most = fmaxf(most, z - ms);
+              const float up = fmaxf(apart[n][e] - kFar - meta.lv, 0.f);  // a scale far below
+              z4[n][e] += up;
+              z4[n][e + 2] += up;
 #pragma unroll
               for (int k = 0; k < kSteps; ++k) {
                 O[k][n][e] *= f;
@@ -462,27 +477,15 @@ split_kernel(const __grid_constant__ SplitParams p) {
               }
             }
         }
-        if (meta.vs > vref) {
-          const float f = vref / meta.vs;
-          vref = meta.vs;
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int k = 0; k < kSteps; ++k)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) O[k][n][e] *= f;
-        }
-        const float pv = vref > 0.f ? meta.vs / vref * kProbScale : 0.f;
         uint32_t B[kTerms][NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           float y[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float mu = m[n][e & 1] == -GDN_INF ? 0.f : m[n][e & 1];
-            const float pr = ex2(s4[n][e] - mu);
-            l[n][e & 1] += pr;
-            y[e] = pr * pv;
+            const float pr = ex2(z4[n][e] - mz[n][e & 1]);
+            l[n][e & 1] = fmaf(pr, ex2(fminf(apart[n][e & 1] - meta.lv, kFar)), l[n][e & 1]);
+            y[e] = pr * meta.pv;
           }
           const uint32_t h0 = f16x2(y[0], y[1]), h1 = f16x2(y[2], y[3]);
           B[0][n][0] = movmatrix_trans(h0);
@@ -532,7 +535,8 @@ split_kernel(const __grid_constant__ SplitParams p) {
         x += __shfl_xor_sync(0xffffffffu, x, 8);
         x += __shfl_xor_sync(0xffffffffu, x, 16);
         if (n8 == 0) {
-          sm.m[warp][8 * n + 2 * c + e] = m[n][e];
+          sm.mz[warp][8 * n + 2 * c + e] = mz[n][e];
+          sm.ms[warp][8 * n + 2 * c + e] = mz[n][e] - apart[n][e];
           sm.l[warp][8 * n + 2 * c + e] = x;
         }
       }
@@ -542,10 +546,10 @@ split_kernel(const __grid_constant__ SplitParams p) {
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float M = sm.m[0][8 * n + 2 * c + e];
+        float M = sm.mz[0][8 * n + 2 * c + e];
 #pragma unroll
-        for (int x = 1; x < kWarps; ++x) M = fmaxf(M, sm.m[x][8 * n + 2 * c + e]);
-        f[n][e] = m[n][e] == -GDN_INF ? 0.f : ex2(m[n][e] - M) * (vref / kProbScale);
+        for (int x = 1; x < kWarps; ++x) M = fmaxf(M, sm.mz[x][8 * n + 2 * c + e]);
+        f[n][e] = ex2(mz[n][e] - M);
       }
     for (int x = 0; x < kWarps; ++x) {  // in a fixed order
       if (warp == x) {
@@ -570,18 +574,20 @@ split_kernel(const __grid_constant__ SplitParams p) {
     }
     // ---- write the output, or the piece
     const bool whole = g.t0 == 0 && g.t1 == g.tiles;
-    float* part = p.part + ((int64_t)2 * blockIdx.x + (g.t0 > 0 ? 0 : 1)) * (RB * (D + 2));
+    float* part = p.part + ((int64_t)2 * blockIdx.x + (g.t0 > 0 ? 0 : 1)) * (RB * (D + 4));
     for (int r = warp; r < RB; r += kWarps) {
       const int32_t row = r0 + r;
       if (row >= rows) break;
-      float M = sm.m[0][r];
+      float MZ = sm.mz[0][r], MS = sm.ms[0][r];
 #pragma unroll
-      for (int x = 1; x < kWarps; ++x) M = fmaxf(M, sm.m[x][r]);
-      float L = 0.f;  // a warp without a maximum has a sum of 0, or NaN where a key was
+      for (int x = 1; x < kWarps; ++x) {
+        MZ = fmaxf(MZ, sm.mz[x][r]);
+        MS = fmaxf(MS, sm.ms[x][r]);
+      }
+      float L = 0.f;
 #pragma unroll
-      for (int x = 0; x < kWarps; ++x)
-        L += sm.m[x][r] == -GDN_INF ? sm.l[x][r] : sm.l[x][r] * ex2(sm.m[x][r] - M);
-      const float inv = !whole ? 1.f : L == 0.f ? 0.f : 1.f / L;
+      for (int x = 0; x < kWarps; ++x) L += sm.l[x][r] * ex2(sm.ms[x][r] - MS);
+      const float inv = !whole ? 1.f : L == 0.f ? 0.f : ex2(MZ - MS - kOutShift) / L;
       const int64_t tok = s.row0 + a.by_group(row);
       const int head = g.head * a.group + (row - a.by_group(row) * a.group);
       for (int quad = lane; quad < D / 4; quad += 32) {
@@ -592,10 +598,9 @@ split_kernel(const __grid_constant__ SplitParams p) {
       }
       if (lane == 0) {
         if (!whole) {
-          part[RB * D + 2 * r] = M;
-          part[RB * D + 2 * r + 1] = L;
+          *reinterpret_cast<float4*>(part + RB * D + 4 * r) = make_float4(MZ, MS, L, 0.f);
         } else if (a.lse) {
-          a.lse[tok * (a.hkv * a.group) + head] = L == 0.f ? -GDN_INF : (M + log2f(L)) * kLn2;
+          a.lse[tok * (a.hkv * a.group) + head] = L == 0.f ? -GDN_INF : (MS + log2f(L)) * kLn2;
         }
       }
     }
@@ -719,29 +724,30 @@ join_kernel(AttnArgs a, const float* part, int workers) {
     waited = true;
     // piece i: the second slot of the first worker, then the first slots of the next ones
     auto piece = [&](int i) {
-      return part + ((int64_t)2 * (w0 + i) + (i == 0 ? 1 : 0)) * (RB * (D + 2));
+      return part + ((int64_t)2 * (w0 + i) + (i == 0 ? 1 : 0)) * (RB * (D + 4));
     };
     constexpr int kStats = (kMaxWorkers + kTeam - 1) / kTeam;
-    float2 st[kStats];
-    float M = -GDN_INF, L = 0.f;
+    float4 st[kStats];
+    float MZ = kNoMax, MS = kNoMax, L = 0.f;
 #pragma unroll
     for (int x = 0; x < kStats; ++x) {
       const int i = me + x * kTeam;
-      st[x] = make_float2(-GDN_INF, 0.f);
-      if (i < count) st[x] = *reinterpret_cast<const float2*>(piece(i) + RB * D + 2 * r);
-      M = fmaxf(M, st[x].x);
+      st[x] = make_float4(kNoMax, kNoMax, 0.f, 0.f);
+      if (i < count) st[x] = *reinterpret_cast<const float4*>(piece(i) + RB * D + 4 * r);
+      MZ = fmaxf(MZ, st[x].x);
+      MS = fmaxf(MS, st[x].y);
     }
-    M = reduce(M, true);
+    MZ = reduce(MZ, true);
+    MS = reduce(MS, true);
 #pragma unroll
     for (int x = 0; x < kStats; ++x) {
       const int i = me + x * kTeam;
-      const float f = st[x].x == -GDN_INF ? 0.f : ex2(st[x].x - M);
-      if (i < count) w[i] = f;
-      L += st[x].y * (st[x].x == -GDN_INF ? 1.f : f);
+      if (i < count) w[i] = ex2(st[x].x - MZ);
+      L += st[x].z * ex2(st[x].y - MS);
     }
     __syncwarp();
     L = reduce(L, false);
-    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const float inv = L == 0.f ? 0.f : ex2(MZ - MS - kOutShift) / L;
     const int32_t query = a.by_group(row);
     const int64_t tok = s.row0 + query;
     const int head = k / row_tiles * a.group + row - query * a.group;
@@ -781,7 +787,7 @@ join_kernel(AttnArgs a, const float* part, int workers) {
       __syncwarp();
     }
     if (me == 0 && blockIdx.y == 0 && a.lse)
-      a.lse[tok * (a.hkv * a.group) + head] = L == 0.f ? -GDN_INF : (M + log2f(L)) * kLn2;
+      a.lse[tok * (a.hkv * a.group) + head] = L == 0.f ? -GDN_INF : (MS + log2f(L)) * kLn2;
   }
   // what follows in the stream waits for this kernel: let it stand for the first one too
   if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -851,7 +857,7 @@ int launch(const AttnArgs& a, const gdn_kv_cache& c, int num_sms, cudaStream_t s
 
 size_t split_workspace(const gdn_attn_config& cfg, const gdn_kv_cache& c) {
   const size_t workers = (size_t)kCtasPerSm * kMaxSms;
-  return 2 * workers * 8 * kMaxRowTiles * (c.head_dim + 2) * sizeof(float);
+  return 2 * workers * 8 * kMaxRowTiles * (c.head_dim + 4) * sizeof(float);
 }
 
 int launch_attn_split(const AttnArgs& a, const gdn_kv_cache& c, bool bf16, int num_sms,

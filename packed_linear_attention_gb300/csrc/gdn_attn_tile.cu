@@ -18,8 +18,8 @@
 // a tile would be bound by otherwise: with Q and a staged e4m3 V read from it, a tile of 64
 // tokens at D = 256 moved 208 KB through 128 bytes a clock against 1,024 clocks of products;
 // this way it moves 112 KB.
-// The maximum is raised only when a score passes it by 2^8 (see gdn_attn_split.cu); value
-// scales enter P as ratios to the largest that the unit has met.
+// The running maxima (of scores and of exponents with the value scales, see kScaleShift in
+// gdn_attn_internal.h) are raised only when one is passed by 8 (see gdn_attn_split.cu).
 //
 // Block: 20 warps. 0-3 and 4-7 softmax, tile by tile in turns, a row to a thread: the latency
 // of a tile (tensor memory loads, 64 exponentials, the store of P) is then two tiles long. Only
@@ -77,9 +77,8 @@ constexpr int kSoftThreads = 32 * kSoftWarps, kAuxThreads = 32 * kAuxWarps;
 constexpr int kBatch = 8, kBatches = 16;
 constexpr int kLead = 16;                 // K tiles of a unit left to load when the next is taken
 constexpr int kCoarse = kMaxSeqs / 32;    // prefix sums are kept for every 32 requests
-constexpr float kLazyMax = 8.f;
-constexpr float kProbScale = 128.f;
-constexpr float kMinRatio = 9.094947e-13f;  // 2^-40: value scales below that of vref count as it
+constexpr float kProbShift = 7.f;  // P = 2^(z - m + this), at most 2^15 in f16
+constexpr float kOutShift = kProbShift + kScaleShift;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kSoftBar = 2, kAuxBar = 3;  // named barriers of the softmax and operand warps
 constexpr int kPairBar = 4;               // 4-11: a pair of softmax warps, either direction
@@ -101,12 +100,11 @@ struct Unit {
 
 struct __align__(16) TileMeta {
   float ks[kGroups];    // key scale of each 16-token group
-  float lv[kGroups];    // log2 of what P is weighted with: value scale / vref * kProbScale
+  float lv[kGroups];    // log2 of its value scale, shifted
   int32_t row[kGroups]; // the group's first row in the cache; negative: absent, or past its tokens
   uint32_t absent;      // bit g: group g is absent
-  float vref;           // largest value scale of the unit so far
-  float vfac;           // what the accumulator is multiplied by as vref grew
-  float pad;
+  float lvmin;          // least lv of the groups that are there
+  uint32_t pad[2];
 };
 
 constexpr int kMaxStages = 8;
@@ -121,8 +119,7 @@ struct Smem {
   uint64_t ufull[2], uempty[2], unext;
   Unit unit[2];
   TileMeta meta[kBatches][kBatch];
-  float m[kRows];            // running maximum on its way between the softmax groups
-  float exchange_v[kRows];
+  float2 m[kRows];           // running maxima on their way between the softmax groups
   float exchange_l[2][kRows];
   uint16_t exchange_q[2][kRows];
   int8_t row_exp[2][kRows];  // power of two of a row of Q (two units' worth)
@@ -363,7 +360,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
             id = -1;
           }
         };
-        float ks, vs, vref = 0.f;
+        float ks, vs;
         int32_t id = page_of(16 * lane);
         scales_of(16 * lane, id, ks, vs);
         bool ok = true;
@@ -372,33 +369,22 @@ tile_kernel(const __grid_constant__ TileParams p) {
           if (lane == 0 && tb + kLead >= u.tiles && (tb == 0 || tb + kLead - kBatch < u.tiles))
             mbar_arrive(&sm.unext);
           const int32_t tok = tb * BN + lane * 16;
-          // values that are no scales count as zeros
-          ks = ks >= 0.f ? ks : 0.f;
-          vs = vs >= 0.f ? vs : 0.f;
-          // largest value scale up to each tile of the batch
-          float top = fmaxf(vs, __shfl_xor_sync(0xffffffffu, vs, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) {
-            const float y = __shfl_up_sync(0xffffffffu, top, o);
-            if (lane >= o) top = fmaxf(top, y);
-          }
-          top = fmaxf(top, vref);
-          float before = __shfl_up_sync(0xffffffffu, top, 4);
-          if (lane < 4) before = vref;
-          vref = __shfl_sync(0xffffffffu, top, 31);
+          ks = ks >= 0.f ? ks : 0.f;  // values that are no scales count as the smallest
           const uint32_t gone = __ballot_sync(0xffffffffu, id < 0);
           const int32_t y = (int32_t)(((int64_t)id * a.hkv + u.head) * a.page_size +
                                       (tok & (a.page_size - 1)));
           TileMeta& m = sm.meta[nb % kBatches][lane >> 2];
           m.ks[lane & 3] = ks;
-          m.lv[lane & 3] =
-              __log2f(fmaxf(top > 0.f ? __fdividef(vs, top) : 0.f, kMinRatio) * kProbScale);
+          const float lv =
+              id < 0 ? 127.f
+                     : __log2f(fminf(fmaxf(vs, kMinValueScale), kMaxValueScale)) + kScaleShift;
+          float least = fminf(lv, __shfl_xor_sync(0xffffffffu, lv, 1));
+          least = fminf(least, __shfl_xor_sync(0xffffffffu, least, 2));
+          m.lv[lane & 3] = lv;
           m.row[lane & 3] = id < 0 ? -1 : y;
           if ((lane & 3) == 0) {
             m.absent = (gone >> lane) & 15u;
-            m.vref = top;
-            m.vfac = top > before ? __fdividef(before, top) : 1.f;
+            m.lvmin = least;
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm.mfull[nb % kBatches]);
@@ -769,7 +755,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
       const AttnSeq s = {u.row0, u.q_len, u.kv_len};
       const int32_t limit = live ? attn_limit(a, s, query) : u.kv_len;
       const int32_t min_limit = attn_limit(a, s, a.by_group(u.first));
-      float m = -GDN_INF, l = 0.f, vref = 0.f, rs = 0.f;
+      float mz = kNoMax, ms = kNoMax, l = 0.f, rs = 0.f;
       const uint32_t first = (g & 1u) ^ grp;  // this group's first tile of the unit
       for (int32_t i = (int32_t)first; i < u.tiles; i += 2) {
         const uint32_t j = g + i, b = grp;  // tile number since the start; its P buffer
@@ -781,8 +767,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
         const float4 ks4 = *reinterpret_cast<const float4*>(meta.ks);
         const float4 lv4 = *reinterpret_cast<const float4*>(meta.lv);
         const uint32_t absent = meta.absent;
-        const float vfac = meta.vfac;
-        vref = meta.vref;
+        const float lvmin = meta.lvmin;
         wait_on(&sm.sfull[grp], (j >> 1) & 1u, sm, a.status);
         tc_fence_after();
         if (i == (int32_t)first)
@@ -803,10 +788,10 @@ tile_kernel(const __grid_constant__ TileParams p) {
               if (e >= room) x[16 * q + e] = 0xff800000u;
           }
         }
-        // the tile's largest score: within a group of 16 tokens before its key scale
+        // the tile's largest exponents: within a group of 16 tokens before the group's scales
         const float ksq[kGroups] = {ks4.x, ks4.y, ks4.z, ks4.w};
-        const float lvq[kGroups] = {lv4.x, lv4.y, lv4.z, lv4.w};
-        float f[kGroups], top = -GDN_INF;
+        float lvq[kGroups] = {lv4.x, lv4.y, lv4.z, lv4.w};
+        float f[kGroups], zq[kGroups];
 #pragma unroll
         for (int q = 0; q < kGroups; ++q) {
           f[q] = fmaxf(ksq[q] * rs, 1e-37f);  // above 0: what is masked stays -inf
@@ -818,49 +803,59 @@ tile_kernel(const __grid_constant__ TileParams p) {
               y2 = max3(y2, __uint_as_float(x[16 * q + e + 2]), __uint_as_float(x[16 * q + e + 3]));
           }
           y = fmaxf(y, y2);
-          top = fmaxf(top, y * f[q]);
+          zq[q] = fmaf(y, f[q], lvq[q]);
         }
+        const float top = fmaxf(fmaxf(zq[0], zq[1]), fmaxf(zq[2], zq[3]));
         if (i > 0) {
           pair_wait(from_other);
-          const float was = m;
-          m = sm.m[r];
-          l *= was == m ? 1.f : ex2(was - m);  // 0 before this group's first tile
+          const float was = ms;
+          const float2 m = sm.m[r];
+          mz = m.x;
+          ms = m.y;
+          l *= ex2(was - ms);
         }
-        if (__any_sync(0xffffffffu, top > m + kLazyMax) || (vfac != 1.f && i > 0)) {
-          // a new maximum for these rows, the accumulator and sum follow
-          const float both = fmaxf(top, m);
-          const float fm = both == -GDN_INF ? 1.f : ex2(m - both);
-          m = both;
-          l *= fm;
-          if (i > 0) {
+        float apart = mz - ms;
+        if (__any_sync(0xffffffffu, top > mz + kLazyMax || lvmin < apart - kNear)) {
+          // new maxima for these rows, the accumulator and sum follow
+          float top_s = ms;
+#pragma unroll
+          for (int q = 0; q < kGroups; ++q) top_s = fmaxf(top_s, zq[q] - lvq[q]);
+          const float top_z = fmaxf(top, mz);
+          const float fm = ex2(mz - top_z);
+          l *= ex2(ms - top_s);
+          ms = top_s;
+          mz = top_z;
+          apart = mz - ms;
+#pragma unroll
+          for (int q = 0; q < kGroups; ++q) lvq[q] = fmaxf(lvq[q], apart - kFar);
+          if (i > 0 && __any_sync(0xffffffffu, fm != 1.f)) {
             const uint32_t o = j - 1;  // P V of the tile before
             wait_on(&sm.odone[o % kDone], (o / kDone) & 1u, sm, a.status);
             tc_fence_after();
-            const float fo = fm * vfac;
 #pragma unroll 1
             for (int c = 0; c < D; c += 16) {
               uint32_t y[16];
               tmem_ld16(t_row + Sh::TM_O + c, y);
               tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * fo);
+              for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * fm);
               tmem_st16(t_row + Sh::TM_O + c, y);
             }
             tmem_st_wait();
           }
         }
         if (i + 1 < u.tiles) {
-          sm.m[r] = m;
+          sm.m[r] = make_float2(mz, ms);
           pair_arrive(to_other);
         }
-        // P = 2^(s - m + lv): weighted for the product, 2^-lv for the sum
-        const float mu = m == -GDN_INF ? 0.f : m;
+        // P = 2^(z - mz + kProbShift)
+        const float mu = mz - kProbShift;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t ph[16];
 #pragma unroll
           for (int q = 2 * h; q < 2 * h + 2; ++q) {
-            const float lv = lvq[q], off = lv - mu, fq = f[q];
+            const float off = lvq[q] - mu, fq = f[q];
             float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
             for (int e = 16 * q; e < 16 * q + 16; e += 2) {
@@ -870,7 +865,7 @@ tile_kernel(const __grid_constant__ TileParams p) {
               sum = add2(sum, pr);
               ph[e / 2 - 16 * h] = f16x2(pr.x, pr.y);
             }
-            l = fmaf(sum.x + sum.y, ex2(-lv), l);
+            l = fmaf(sum.x + sum.y, ex2(apart - kProbShift - lvq[q]), l);
           }
           if (h == 0 && j >= 2) {  // P V(j - 2) has read this group's buffer
             const uint32_t o = j - 2;
@@ -891,23 +886,20 @@ tile_kernel(const __grid_constant__ TileParams p) {
       const uint32_t last = g - 1;
       if (u.tiles > 0) {
         ++nq;
-        if ((last & 1u) == grp) {  // who has the final maximum
-          sm.m[r] = m;
-          sm.exchange_v[r] = vref;
-        }
+        if ((last & 1u) == grp) sm.m[r] = make_float2(mz, ms);  // who has the final maxima
         named_sync(kSoftBar, kSoftThreads);
-        const float mf = sm.m[r];
-        vref = sm.exchange_v[r];
-        sm.exchange_l[grp][r] = m == -GDN_INF ? l : l * ex2(m - mf);
-        m = mf;
+        const float2 m = sm.m[r];
+        sm.exchange_l[grp][r] = l * ex2(ms - m.y);
+        mz = m.x;
+        ms = m.y;
       }
       more = see_unit();
       more = !named_any(kSoftBar, kSoftThreads, !more);
       if (u.tiles > 0) l = sm.exchange_l[0][r] + sm.exchange_l[1][r];
-      const float inv = l == 0.f ? 0.f : __fdividef(vref, l * kProbScale);
+      const float inv = l == 0.f ? 0.f : __fdividef(ex2(mz - ms - kOutShift), l);
       if (live && grp == 0 && a.lse)
         a.lse[(int64_t)(u.row0 + query) * (a.hkv * a.group) + u.head * a.group + row -
-              query * a.group] = l == 0.f ? -GDN_INF : (m + __log2f(l)) * kLn2;
+              query * a.group] = l == 0.f ? -GDN_INF : (ms + __log2f(l)) * kLn2;
       // through shared memory, 32 columns at a time, so that four lanes store 64 consecutive
       // bytes of a row (a thread storing its own row would touch 32 lines with every store)
       uint8_t* stage = smem + Sh::OFF_OUT + warp * 2048;
