@@ -556,7 +556,10 @@ typedef struct gdn_kv_cache {
  * append then stores nothing for it, and the attention gives it zeros), and status is raised
  * to GDN_ERR_POOL_EXHAUSTED when the stack ran out (no later request that needs a page is
  * served then), or to GDN_ERR_INVALID_ARGUMENT for lengths below 0, more pages than
- * max_blocks, rows past num_tokens, or a page out of range. At most 4,096 requests.
+ * max_blocks, rows past num_tokens, or a page out of range: the half-filled one that its first
+ * new tokens go to, or one on the stack (the stack counts as ending in front of it, so no later
+ * request that needs a page is served either). A caller keeps such a request's ctx_len as it
+ * was: its table row is untouched. At most 4,096 requests.
  * Errors: INVALID_ARGUMENT, UNSUPPORTED, CUDA. */
 gdn_status gdn_kv_plan(gdn_handle* handle, int32_t page_size, int32_t num_seqs,
                        int32_t num_tokens, const int32_t* ctx_len, const int32_t* new_len,

@@ -26,11 +26,16 @@ def plan(ctx, new, table, free, count, page, num_tokens, num_pages):
     if not 0 <= count <= num_pages:
         status, count = INVALID, min(max(count, 0), num_pages)
     cu, kv, positions, slots = [0], [], [0] * num_tokens, [-1] * num_tokens
+    inside = lambda p: 0 <= p < num_pages  # noqa: E731
+    # pages on the stack, from its top, in front of the first that is none
+    usable = next((k for k in range(count) if not inside(int(free[count - 1 - k]))), count)
     row, asked, taken = 0, 0, 0
     for b, (c, m) in enumerate(zip(ctx, new)):
         c, m = int(c), int(m)
         end = row + max(m, 0)
         good = c >= 0 and m >= 0 and end <= num_tokens and c + m <= max_blocks * page
+        if good and m and c % page and not inside(table[b][c // page]):
+            good = False  # the page that its first new tokens go to
         if not good:
             status = max(status, INVALID)
         else:
@@ -38,26 +43,19 @@ def plan(ctx, new, table, free, count, page, num_tokens, num_pages):
             need = ceil_div(c + m, page) - have
             first = asked
             asked += need
-            if need and asked > count:
+            if need and asked > usable:
                 good = False
-                status = max(status, EXHAUSTED)
+                status = max(status, EXHAUSTED if asked > count else INVALID)
             elif need:
                 taken = asked
                 for j in range(need):
-                    p = int(free[count - 1 - first - j])
-                    if not 0 <= p < num_pages:
-                        status, p = max(status, INVALID), -1
-                    table[b][have + j] = p
+                    table[b][have + j] = int(free[count - 1 - first - j])
         kv.append(c + m if good else 0)
         if good:
             for i in range(m):
                 pos = c + i
-                p = table[b][pos // page]
                 positions[row + i] = pos
-                if 0 <= p < num_pages:
-                    slots[row + i] = p * page + pos % page
-                else:
-                    status = max(status, INVALID)
+                slots[row + i] = table[b][pos // page] * page + pos % page
         row = end
         cu.append(min(row, num_tokens))
     return table, cu, kv, positions, slots, count - taken, status

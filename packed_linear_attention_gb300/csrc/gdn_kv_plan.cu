@@ -5,13 +5,15 @@
 // ceil((c + n) / P) - ceil(c / P) more. With the exclusive sums of the needs, page number k
 // handed out in the step is the free stack's entry count - 1 - k, so every table entry and
 // every slot is an independent lookup after two prefix sums over the requests, and the result
-// does not depend on the order in which threads run.
+// does not depend on the order in which threads run. Pages are looked at before anything is
+// decided: a request whose half-filled page is out of range asks for none, and the stack counts
+// as ending in front of its first entry out of range. (The loads fall into the prefix sums.)
 //
 // One launch of one thread-block cluster (1 to 8 blocks of 1,024 threads): every block forms
 // the prefix sums itself (at most 4,096 requests, four per thread), then the blocks share the
 // rows. The free count may be updated in place, so block 0 writes it only after the cluster
 // has met, when every block has read it. A decode step's plan is bound by the launch and a
-// chain of dependent loads: 8.2 us for 256 requests of one token, 12.3 for 512 that bring 33,000
+// chain of dependent loads: 8.2 us for 256 requests of one token, 12.6 for 512 that bring 33,000
 // tokens.
 #include <cuda_runtime.h>
 
@@ -36,7 +38,8 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 
-// Exclusive sum over the block (64-bit: lengths are the caller's and may be any int32).
+// Exclusive sum over the block (64-bit: lengths are the caller's and may be any int32), the whole
+// sum in warp_sums[32].
 __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* warp_sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t inc = x;
@@ -56,6 +59,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* warp_sums) {
       if (lane >= o) t += y;
     }
     warp_sums[lane] = t - s;
+    if (lane == 31) warp_sums[32] = t;
   }
   __syncthreads();
   return warp_sums[warp] + inc - x;
@@ -78,8 +82,8 @@ __device__ __forceinline__ int32_t owner(const int32_t* start, int32_t n, int32_
 
 __global__ void __launch_bounds__(kThreads) plan_kernel(PlanArgs p) {
   extern __shared__ int32_t sh[];
-  __shared__ int64_t warp_sums[32];
-  __shared__ int32_t taken;
+  __shared__ int64_t warp_sums[33];
+  __shared__ int32_t taken, usable;  // pages handed out; pages in front of the first bad one
   const int n = p.num_seqs, tid = threadIdx.x, P = p.page_size;
   int32_t* cu = sh;               // [n + 1] first rows
   int32_t* page0 = cu + n + 1;    // [n + 1] first page handed out
@@ -91,11 +95,25 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanArgs p) {
     raise = GDN_ERR_INVALID_ARGUMENT;
     free_count = free_count < 0 ? 0 : p.num_pages;
   }
-  if (tid == 0) taken = 0;
+  if (tid == 0) {
+    taken = 0;
+    usable = INT32_MAX;
+  }
+  auto bad_page = [&](int32_t k) {  // the k-th page from the top
+    const int32_t id = p.free_pages[free_count - 1 - k];
+    return id < 0 || id >= p.num_pages;
+  };
+  int32_t bad_at = INT32_MAX;  // this thread's first, of the 4,096 that most steps do with
+#pragma unroll
+  for (int i = kPerThread - 1; i >= 0; --i) {
+    const int32_t k = tid + i * kThreads;
+    if (k < free_count && bad_page(k)) bad_at = k;
+  }
 
   // rows: exclusive sums of the new lengths
   const int per = (n + kThreads - 1) / kThreads, b0 = tid * per;
   int32_t c[kPerThread], m[kPerThread];
+  bool ok[kPerThread];
   int64_t sum = 0;
 #pragma unroll
   for (int i = 0; i < kPerThread; ++i) {
@@ -104,19 +122,23 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanArgs p) {
     c[i] = in ? p.ctx_len[b] : 0;
     m[i] = in ? p.new_len[b] : 0;
     sum += max(m[i], 0);
+    ok[i] = in;
+    if (m[i] > 0 && c[i] > 0 && (c[i] & (P - 1)) != 0 && c[i] / P < p.max_blocks) {
+      const int32_t id = p.block_table[(size_t)b * p.max_blocks + c[i] / P];
+      ok[i] = id >= 0 && id < p.num_pages;
+    }
   }
   int64_t row = block_scan(sum, warp_sums);
+  if (bad_at < INT32_MAX) atomicMin(&usable, bad_at);  // read behind the next sum's barriers
   int64_t need = 0;
-  bool ok[kPerThread];
 #pragma unroll
   for (int i = 0; i < kPerThread; ++i) {
     const int b = b0 + i;
-    ok[i] = false;
     if (i < per && b < n) {
       const int64_t end = row + max(m[i], 0), len = (int64_t)c[i] + m[i];
       cu[b] = (int32_t)min(row, (int64_t)p.num_tokens);
       if (b == n - 1) cu[n] = (int32_t)min(end, (int64_t)p.num_tokens);
-      ok[i] = c[i] >= 0 && m[i] >= 0 && end <= p.num_tokens &&
+      ok[i] = ok[i] && c[i] >= 0 && m[i] >= 0 && end <= p.num_tokens &&
               len <= (int64_t)p.max_blocks * P && len <= INT32_MAX;
       if (!ok[i]) raise = GDN_ERR_INVALID_ARGUMENT;
       else need += ceil_div(c[i] + m[i], P) - ceil_div(c[i], P);
@@ -125,6 +147,13 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanArgs p) {
   }
   // pages: exclusive sums of the needs; a request is served while the stack covers its sum
   int64_t page = block_scan(need, warp_sums);
+  const int64_t asked = warp_sums[32];
+  if (asked > kMaxSeqs) {  // the rest of the pages that may be handed out
+    for (int32_t k = kMaxSeqs + tid; k < min(asked, (int64_t)free_count); k += kThreads)
+      if (bad_page(k)) atomicMin(&usable, k);
+    __syncthreads();
+  }
+  const int32_t have = min(usable, free_count);
 #pragma unroll
   for (int i = 0; i < kPerThread; ++i) {
     const int b = b0 + i;
@@ -134,9 +163,10 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanArgs p) {
       page += want;
       if (b == n - 1) page0[n] = (int32_t)min(page, (int64_t)INT32_MAX);
       if (want > 0) {
-        if (page > free_count) {
+        if (page > have) {
           ok[i] = false;
-          raise = max(raise, (int32_t)GDN_ERR_POOL_EXHAUSTED);
+          raise = max(raise, page > free_count ? (int32_t)GDN_ERR_POOL_EXHAUSTED
+                                               : (int32_t)GDN_ERR_INVALID_ARGUMENT);
         } else {
           atomicMax(&taken, (int32_t)page);
         }
@@ -153,14 +183,12 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanArgs p) {
 
   const int gtid = (int)(blockIdx.x * kThreads) + tid, all = (int)(gridDim.x * kThreads);
   // new table entries
-  const int32_t out = min(page0[n], free_count);
+  const int32_t out = min(page0[n], have);
   for (int32_t k = gtid; k < out; k += all) {
     const int b = owner(page0, n, k);
-    if (ctx[b] < 0) continue;
-    const int32_t id = p.free_pages[free_count - 1 - k];
-    const bool good = id >= 0 && id < p.num_pages;
-    if (!good) raise_status(p.status, GDN_ERR_INVALID_ARGUMENT);
-    p.block_table[(size_t)b * p.max_blocks + ceil_div(ctx[b], P) + k - page0[b]] = good ? id : -1;
+    if (ctx[b] >= 0)
+      p.block_table[(size_t)b * p.max_blocks + ceil_div(ctx[b], P) + k - page0[b]] =
+          p.free_pages[free_count - 1 - k];
   }
   // slots and positions
   const int32_t rows = cu[n];
@@ -171,12 +199,11 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanArgs p) {
       const int b = owner(cu, n, r);
       if (ctx[b] >= 0) {
         pos = ctx[b] + r - cu[b];
-        const int32_t blk = pos / P, have = ceil_div(ctx[b], P);
-        const int32_t id = blk < have
+        const int32_t blk = pos / P, old = ceil_div(ctx[b], P);
+        const int32_t id = blk < old
                                ? p.block_table[(size_t)b * p.max_blocks + blk]
-                               : p.free_pages[free_count - 1 - (page0[b] + blk - have)];
-        if (id >= 0 && id < p.num_pages) slot = (int64_t)id * P + (pos - blk * P);
-        else raise_status(p.status, GDN_ERR_INVALID_ARGUMENT);
+                               : p.free_pages[free_count - 1 - (page0[b] + blk - old)];
+        slot = (int64_t)id * P + (pos - blk * P);
       }
     }
     p.slots[r] = slot;
@@ -188,7 +215,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanArgs p) {
 
 __global__ void __launch_bounds__(kThreads) release_kernel(ReleaseArgs p) {
   extern __shared__ int32_t sh[];
-  __shared__ int64_t warp_sums[32];
+  __shared__ int64_t warp_sums[33];
   __shared__ int32_t pushed;
   const int n = p.num_seqs, tid = threadIdx.x, lane = tid & 31;
   int32_t* cnt = sh;        // [n] pages of a row that is given back
