@@ -6,7 +6,8 @@ layer behind every three, random weights, prompts and one-token steps in the sam
 A step's pages, slots and positions are planned on the GPU once; every full-attention layer
 then appends its keys and values to its paged 8-bit cache (rotating keys and queries on the
 way) and attends over it; every linear layer reads and writes its states in its pool. The
-projections are plain matrix products.
+projections are plain matrix products. Requests for whose rows there are no pages sit out the
+step, in every layer, and are tried again in the next one.
 """
 import argparse
 import os
@@ -31,13 +32,18 @@ def _norm(x):
     return torch.nn.functional.rms_norm(x, x.shape[-1:])
 
 
+def _pages_of(tokens):
+    return -(-tokens // PAGE)
+
+
 class Pages:
     """Page tables of `slots` requests and the stack of free pages: they serve every layer,
-    since the layers' caches have the same pages."""
+    since the layers' caches have the same pages. The host knows the lengths too, and so which
+    requests a step has pages for."""
 
     def __init__(self, slots, num_pages, max_tokens):
         i32 = dict(dtype=torch.int32, device="cuda")
-        self.slots, self.num_pages, self.max_blocks = slots, num_pages, -(-max_tokens // PAGE)
+        self.slots, self.num_pages, self.max_blocks = slots, num_pages, _pages_of(max_tokens)
         self.max_tokens = max_tokens
         self.table = torch.full((slots, self.max_blocks), -1, **i32)
         self.free = torch.arange(num_pages, **i32)
@@ -46,10 +52,23 @@ class Pages:
         self.kv_len = torch.zeros(slots, **i32)
         self.cu = torch.zeros(slots + 1, **i32)
         self.status = torch.zeros(1, **i32)
+        self.length, self.left = [0] * slots, num_pages  # ctx and count, as the host has them
+
+    def admit(self, new_len):
+        """new_len without the requests that there are no pages for, in the plan's order."""
+        taken, kept = 0, []
+        for length, n in zip(self.length, new_len):
+            if length + n > self.max_tokens:
+                raise gdn.GdnError(gdn.GDN_ERR_INVALID_ARGUMENT, "serve: request too long")
+            need = _pages_of(length + n) - _pages_of(length)
+            fits = taken + need <= self.left
+            taken += need if fits else 0
+            kept.append(n if fits else 0)
+        return kept
 
     def plan(self, handle, new_len):
         """Pages for new_len[slot] tokens of every slot (host list); the rows' positions/slots."""
-        self.rows, self.longest = sum(new_len), max(new_len)
+        self.rows, self.longest, self.new = sum(new_len), max(new_len), new_len
         new = torch.tensor(new_len, dtype=torch.int32).cuda()
         self.positions = torch.empty(self.rows, dtype=torch.int32, device="cuda")
         self.places = torch.empty(self.rows, dtype=torch.int64, device="cuda")
@@ -58,7 +77,11 @@ class Pages:
                         self.cu, self.kv_len, self.positions, self.places, self.status)
 
     def advance(self):
-        self.ctx.copy_(self.kv_len)
+        # kv_len is 0 for a request that the plan refused: it keeps its context
+        self.ctx.copy_(torch.where(self.kv_len > 0, self.kv_len, self.ctx))
+        for s, n in enumerate(self.new):
+            self.left -= _pages_of(self.length[s] + n) - _pages_of(self.length[s])
+            self.length[s] += n
 
     def release(self, handle, ended):
         flags = torch.zeros(self.slots, dtype=torch.int32)
@@ -67,6 +90,9 @@ class Pages:
         gdn.gdn_kv_release(handle, PAGE, self.slots, self.ctx, flags, self.table,
                            self.max_blocks, self.num_pages, self.free, self.count, self.status)
         self.ctx *= 1 - flags
+        for s in ended:
+            self.left += _pages_of(self.length[s])
+            self.length[s] = 0
 
 
 class FullAttention:
@@ -120,7 +146,8 @@ class LinearAttention:
 
 class Server:
     """`slots` requests at a time. step() takes the new rows of some of them (a prompt or a
-    single token each) and gives each one's last row back."""
+    single token each) and gives each one's last row back; a request without pages is left out
+    of the step and of its results."""
 
     def __init__(self, slots=8, num_pages=128, max_tokens=2048, layers="LLLF"):
         self.handle = gdn.gdn_handle_create(torch.cuda.current_device())
@@ -128,11 +155,16 @@ class Server:
         self.layers = [FullAttention(self.pages) if c == "F" else LinearAttention(slots)
                        for c in layers]
         self.known = [False] * slots
+        self.waiting = []  # requests that the last step had no pages for
 
     def step(self, rows):
         """rows: {slot: [n, HIDDEN] bf16}. A slot that was free takes a new request."""
-        used = sorted(rows)
-        new = [rows[s].shape[0] if s in rows else 0 for s in range(self.pages.slots)]
+        new = self.pages.admit([rows[s].shape[0] if s in rows else 0
+                                for s in range(self.pages.slots)])
+        used = [s for s in sorted(rows) if new[s]]
+        self.waiting = [s for s in sorted(rows) if not new[s]]
+        if not used:
+            return {}
         cu = [0]
         for s in used:
             cu.append(cu[-1] + new[s])
@@ -156,7 +188,7 @@ class Server:
 
     def check(self):
         """Raise what the kernels found (pages that ran out, values out of range)."""
-        status = int(self.pages.status.item())
+        status = gdn.GDN_ERR_POOL_EXHAUSTED if self.waiting else int(self.pages.status.item())
         if status != gdn.GDN_OK:
             raise gdn.GdnError(status, "serve")
 
@@ -167,18 +199,21 @@ class Server:
 
 def serve(server, prompts, answer):
     """Every prompt and `answer` steps behind it; a freed slot takes the next prompt, whose rows
-    share the step with the others' single ones. Returns the prompts' last rows, in order."""
+    share the step with the others' single ones. What gets no pages waits for the others to end;
+    where nothing can run, check() raises. Returns the prompts' last rows, in order."""
     waiting, running, last = list(range(len(prompts))), {}, [None] * len(prompts)
     left = [answer] * len(prompts)
     while waiting or running:
-        rows = {s: last[r] for s, r in running.items()}
+        rows = {s: last[r] if server.known[s] else prompts[r] for s, r in running.items()}
         for s in range(server.pages.slots):
             if s not in running and waiting:
                 running[s] = waiting.pop(0)
                 rows[s] = prompts[running[s]]
         out = server.step(rows)
+        if not out:
+            server.check()
         ended = []
-        for s, r in list(running.items()):
+        for s, r in [(s, r) for s, r in running.items() if s in out]:
             last[r] = out[s]
             left[r] -= 1
             if left[r] < 0:
