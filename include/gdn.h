@@ -685,7 +685,10 @@ gdn_status gdn_attn_workspace_size(const gdn_attn_config* cfg, const gdn_kv_cach
  * fp32 io queries and weights are two fp16 terms, 22 bits (weights to 2^-31 of the row's
  * largest). Value scales count as at least 2^-100 and at most 2^120, the range in which
  * gdn_kv_append keeps them. Results do not depend on atomics: the same call gives the same bits.
- * At most 4,096 requests.
+ * UNSUPPORTED: more than 4,096 requests, 2^31 or more query rows of a key/value head, or more than
+ * 2^31 work items, for which every 8 query rows count max_kv_len / 64 + 1 times num_kv_heads: with
+ * fp32 io all rows (a prompt of 131,072 tokens over as many, 16 query and 2 key/value heads, is
+ * within), with bf16 at most 256 (or twice the heads of a group) of each request.
  * Errors: INVALID_ARGUMENT, UNSUPPORTED, WORKSPACE_TOO_SMALL, CUDA. */
 gdn_status gdn_attn_paged(gdn_handle* handle, const gdn_attn_config* cfg,
                           const gdn_kv_cache* cache, int32_t num_seqs, int32_t num_tokens,

@@ -124,9 +124,14 @@ gdn_status check_attn(const gdn_attn_config* cfg, const gdn_kv_cache* c, int32_t
       num_tokens < 0 || max_q_len < 0 || max_kv_len < 0)
     return GDN_ERR_INVALID_ARGUMENT;
   if (num_seqs > gdn::kMaxSeqs) return GDN_ERR_UNSUPPORTED;
-  // query rows and work items are counted in 32 bits
+  // query rows and the split kernel's work items are counted in 32 bits. With fp32 io it takes
+  // all rows, with bf16 at most max(kTileRows, group) of a request (split_queries; twice that is
+  // counted, so that the rule can move without a call being refused).
   const double group = cfg->num_q_heads / c->num_kv_heads;
-  const double items = ((double)num_tokens * group / 8 + num_seqs) * c->num_kv_heads *
+  double split_rows = (double)num_tokens * group;
+  if (cfg->io_dtype == GDN_BF16)
+    split_rows = std::min(split_rows, num_seqs * 2.0 * std::max((double)gdn::kTileRows, group));
+  const double items = (split_rows / 8 + num_seqs) * c->num_kv_heads *
                        (max_kv_len / (double)gdn::kSplitTile + 1);
   const double units = ((double)num_tokens * group / gdn::kTileRows + num_seqs) * c->num_kv_heads;
   if ((double)num_tokens * group > (double)INT32_MAX || items >= (double)INT32_MAX ||

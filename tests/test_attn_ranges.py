@@ -8,7 +8,7 @@ import subprocess
 import numpy as np
 import pytest
 
-from packed_linear_attention_gb300 import build
+from packed_linear_attention_gb300 import build, gdn
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LO, HI = -2**31, 2**31 - 1
@@ -72,3 +72,44 @@ def test_item_counts_stop_at_the_end_of_32_bits(ranges):
     for _ in range(200):
         x = rng.integers(0, rng.integers(1, HI), 40)
         assert total(x) == min(int(x.sum()), HI)
+
+
+def _call(tokens, seqs=1, hq=16, hkv=2, dim=256, io=gdn.GDN_BF16, kv=None, max_q=None, page=64):
+    """Status of a call's host checks (its NULL handle is refused after them)."""
+    build.build()
+    kv = tokens if kv is None else kv
+    cache = gdn.gdn_kv_cache(min(HI // (hkv * page), 1 << 20), page, hkv, dim, 1 << 24, 1 << 25,
+                             1 << 26, 1 << 27)
+    cfg = gdn.gdn_attn_config(hq, 1, io, 0.1)
+    at = lambda i: i << 44  # noqa: E731
+    size = ctypes.c_size_t()
+    sized = gdn.load().gdn_attn_workspace_size(ctypes.byref(cfg), ctypes.byref(cache), seqs,
+                                               tokens, tokens if max_q is None else max_q, kv,
+                                               ctypes.byref(size))
+    st = gdn.gdn_attn_paged(None, cfg, cache, seqs, tokens, tokens if max_q is None else max_q, kv,
+                            at(1), at(2), at(3), 1 << 20, at(4), hq * dim, at(5), hq * dim, at(6),
+                            at(7), size.value - 1 if sized == 0 else 0, None,
+                            raise_on_error=False)
+    assert st == (gdn.GDN_ERR_WORKSPACE_TOO_SMALL if sized == 0 else sized)
+    return sized
+
+
+@pytest.mark.parametrize("tokens,seqs,hq,hkv,dim,kv", [
+    (262144, 1, 16, 2, 256, None), (262144, 1, 64, 8, 128, None), (131072, 1, 64, 8, 128, None),
+    (262144, 8, 32, 8, 128, 262144), (1 << 20, 4096, 16, 2, 256, 262144), (1000000, 1, 8, 1, 64, None)])
+def test_long_prompts_are_taken(tokens, seqs, hq, hkv, dim, kv):
+    """bf16 prompts of the longest contexts: only requests of few queries count work items over
+    the cached tokens."""
+    assert _call(tokens, seqs, hq, hkv, dim, kv=kv) == gdn.GDN_OK
+
+
+def test_calls_of_more_work_items_than_32_bits_are_refused():
+    f32 = dict(io=gdn.GDN_F32)
+    # fp32: every row counts, 8 rows and 64 cached tokens an item
+    assert _call(100000, kv=100000, **f32) == gdn.GDN_OK
+    assert _call(262144, kv=262144, **f32) == gdn.GDN_ERR_UNSUPPORTED
+    # bf16: many requests of few queries over the longest lengths
+    assert _call(4096, 4096, 16, 2, 256, kv=1 << 20, max_q=1) == gdn.GDN_OK
+    assert _call(65536, 4096, 16, 16, 256, kv=1 << 28, max_q=16) == gdn.GDN_ERR_UNSUPPORTED
+    # rows
+    assert _call(1 << 30, hq=64, hkv=8, kv=64) == gdn.GDN_ERR_UNSUPPORTED
