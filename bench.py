@@ -71,12 +71,12 @@ MEASURED_TRAFFIC = {
         "packed_linear_attention_gb300/csrc/gdn_chunk_util.cuh":
             "79a2646b770efccd02ab41cc732b8ffe6c5c890479fc9c579353bcf415d15a2f",
         "packed_linear_attention_gb300/csrc/ptx_sm103.cuh":
-            "762c9e7ef68fa3e883aaeb592d47ce09eed2b387cc7b6e46fa74fa53d9b1da60",
+            "eef0851575db3d180e6940fec26e8bbdd5ebf72ae5d2e392aea373f1304fc435",
         "packed_linear_attention_gb300/csrc/gdn_tma.cu":
-            "b97a465a15c3850359ec63c6925ea5d4f1962a058db1f247ccd5c0a9055e72f2",
+            "3ce935c111cbc0241ecf938d60413ace6dbdf8b5eb58eae1391f8b7c546ce3a3",
     },
-    "read_bytes": 545.9e6,
-    "write_bytes": 356.8e6,
+    "read_bytes": 546.0e6,
+    "write_bytes": 356.6e6,
 }
 
 
