@@ -439,8 +439,9 @@ size_t attn_workspace(const gdn_attn_config& cfg, const gdn_kv_cache& c) {
 // kernel once for every 128, a unit to an SM. So the split kernel is the faster one while the
 // passes are few: up to about 64 for each round of units over the SMs at head_dim 256, 128 below.
 // Measured with 2,000 cached tokens, split / tile in us of a call: 32 requests of 16 query and 2
-// key/value heads (D 256) 56 / 54 with 16 rows, 66 / 54 with 32, 92 / 54 with 64; 4 such requests
-// 31 / 50, 37 / 51, 54 / 51 and 56 / 54 with 128; 32 of 32 and 8 heads (D 128) 56 / 72 with 16.
+// key/value heads (D 256) 47 / 45 with 16 rows, 57 / 45 with 32, 83 / 46 with 64; 4 such requests
+// 21 / 37, 27 / 38, 43 / 39 and 42 / 41 with 128; 32 of 32 and 8 heads (D 128) 52 / 62 with 16,
+// 86 / 62 with 32.
 // One query of a group of 16 always counts as few.
 int split_queries(const AttnArgs& a, int sms) {
   const int64_t units = (int64_t)a.num_seqs * a.hkv;

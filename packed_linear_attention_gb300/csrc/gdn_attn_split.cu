@@ -10,7 +10,7 @@
 // second kernel joins them in order, so the result does not depend on timing.
 //
 // Bound: HBM (16 query and 2 key/value heads of 256, one query each: 128 requests of 128 to 16,384
-// tokens 165 us, 88% of the measured copy rate; one of 32,768 tokens 20 us of which the read is 5
+// tokens 164 us, 89% of the measured copy rate; one of 32,768 tokens 19 us of which the read is 5
 // and the rest two launches, the pipeline's start and the join). A cached token is read once for
 // all query rows of its head, up to 16. One producer warp
 // keeps the stages' TMA copies in flight (page ids and scales are fetched 512 tokens ahead);
@@ -795,8 +795,10 @@ join_kernel(AttnArgs a, const float* part, int workers) {
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
-// Row tiles of 8 in a unit. Four of them do not fit the registers: 32 requests of 32 rows behind
-// 2,000 tokens (D 128, 8 key/value heads) took 142 us with four and 93 with two passes of two.
+// Row tiles of 8 in a unit. Two fit the registers up to D = 128 (12 bytes of spills in bf16); at 256
+// the accumulator alone takes 128 of the 168 and 360 bytes spill. Four spill everywhere: 32 requests
+// of 32 rows behind 2,000 tokens (D 128, 8 key/value heads) took 142 us with four and 93 with two
+// passes of two.
 constexpr int kMaxRowTiles = 2;
 
 template <typename T, int D, int NT>

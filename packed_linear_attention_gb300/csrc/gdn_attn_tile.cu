@@ -34,12 +34,12 @@
 // rows of a request first.
 // Every wait is bounded; after one gave up the block's warps leave at their unit's end.
 //
-// Bound and measured (16 query and 2 key/value heads of 256, causal). 4 x 8,192 tokens: 1,479 us
-// for 2.20 TFLOP, 79% of the measured bf16 peak. A tile takes 1,540 clocks where its products
+// Bound and measured (16 query and 2 key/value heads of 256, causal). 4 x 8,192 tokens: 1,470 us
+// for 2.20 TFLOP, 80% of the measured bf16 peak. A tile takes 1,530 clocks where its products
 // take 1,024: tensor memory holds one S beside O and Q, so S(j + 1) waits until S(j) is read, and
-// P V stands in the same queue. 32 x 1,024 tokens: 318 us, 46%; a unit has 8.5 tiles, and its
+// P V stands in the same queue. 32 x 1,024 tokens: 312 us, 47%; a unit has 8.5 tiles, and its
 // start and end (Q to two terms, the output, the next first scores) take as long as six. 32 and 8
-// heads of 128, 8 requests of 190 to 1,789 tokens behind up to 1,537: 246 us, 42%; the products take 512
+// heads of 128, 8 requests of 190 to 1,789 tokens behind up to 1,537: 243 us, 42%; the products take 512
 // clocks of a tile, the two softmax groups 1,200. Half of the issue slots and 42% of the ALU are
 // taken, so instructions of any role cost time: page arithmetic in the operand warps cost 5% of
 // the first case. Tried and dropped: a second S at D <= 128 (no change), tiles of 128 tokens there

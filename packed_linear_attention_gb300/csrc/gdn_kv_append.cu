@@ -16,11 +16,12 @@
 // largest magnitude is found; the rotation is cheap enough to be done twice (its sines and
 // cosines are formed once for the run, by all threads, while the rows are on their way; the other
 // half of a pair is read beside, since a row never leaves a warp). Only runs longer than eight
-// bf16 or four fp32 rows a thread read their first rows a second time. With power-of-two scales the division is exact,
-// and a later, larger scale only moves the exponents of the codes that are already there. No
+// bf16 or four fp32 rows a thread read their first rows a second time. With power-of-two scales
+// the division is exact, and a later, larger scale only moves the exponents of the codes that are
+// already there. No
 // unit list is needed: a row begins a run when its slot opens a page or does not follow the
 // previous row's slot. Measured: 32 x 1,024 tokens, 16 query heads rotated beside 2 + 2 heads of
-// 256, 129 us, 4.9 TB/s, 73% of the copy rate; keys and values alone 33 us, 46 with rotation,
+// 256, 129 us, 4.9 TB/s, 73% of the copy rate; keys and values alone 37 us, 15 more rotated,
 // where a block's chain of slots, rows, maximum and store is what bounds it (two blocks an SM).
 // Rows in registers took 137 us, three blocks an SM 152 (spills), and asking for the rows before
 // the slots are known changed nothing.
