@@ -683,8 +683,8 @@ gdn_status gdn_attn_workspace_size(const gdn_attn_config* cfg, const gdn_kv_cach
  * value scale, is rounded to fp16's 11 bits, or to 2^-31 of the largest weight of its row where
  * that is more: tokens that a row does not see, or gives no weight, change nothing of it. With
  * fp32 io queries and weights are two fp16 terms, 22 bits (weights to 2^-31 of the row's
- * largest). Value scales count as at least 2^-100 and at most 2^120, the range in which
- * gdn_kv_append keeps them. Results do not depend on atomics: the same call gives the same bits.
+ * largest). Value scales below 2^-100 count as 0 and those above 2^120 as 2^120 (gdn_kv_append
+ * keeps them in that range). Results do not depend on atomics: the same call gives the same bits.
  * UNSUPPORTED: more than 4,096 requests, 2^31 or more query rows of a key/value head, or more than
  * 2^31 work items, for which every 8 query rows count max_kv_len / 64 + 1 times num_kv_heads: with
  * fp32 io all rows (a prompt of 131,072 tokens over as many, 16 query and 2 key/value heads, is

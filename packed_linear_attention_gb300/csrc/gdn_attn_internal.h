@@ -103,8 +103,8 @@ struct AttnArgs {
 // scale lies 2^kNear below the row's (mz - ms); in between scores stay below ms + kLazyMax + kNear.
 // For a scale that far below, the exponent is raised to at least -kFar - ms + s: P is 0 in f16 all
 // the same, and the probability is not lost from the sum. The shift brings scales of ordinary
-// values (2^-6) to z = s. Scales count as at least 2^-100 (the append's least) and at most 2^120
-// (its largest).
+// values (2^-6) to z = s. Scales below 2^-100 (the append's least) count as 0: their tokens have the
+// exponent of 2^-100 and zeros for values. Scales above 2^120 (its largest) count as that.
 constexpr float kScaleShift = 6.f;
 constexpr float kLazyMax = 8.f, kNear = 40.f, kFar = 45.f;
 constexpr float kNoMax = -3.402823466e38f;  // maxima of a row that has seen no token (finite, so

@@ -103,7 +103,7 @@ __device__ __forceinline__ uint32_t tile_offset(int row, int chunk) {
 struct __align__(16) GroupMeta {
   float ks;       // key scale; below 0: the group's page is absent
   float lv;       // exponent of the value scale, shifted
-  float pv;       // its fraction, in [1, 2), times kProbScale
+  float pv;       // its fraction, in [1, 2), times kProbScale; 0 for no value
 };
 
 template <int NT>
@@ -263,7 +263,7 @@ split_kernel(const __grid_constant__ SplitParams p) {
       for (int32_t tb = g.t0; tb < g.t1; tb += 8) {  // 8 tiles' pages and scales, one group a lane
         const int32_t tok = tb * kTile + lane * 16;
         int32_t id = -1;
-        float ks = -1.f, vs = 0.f;  // a value scale that is none counts as the smallest
+        float ks = -1.f, vs = 0.f;
         if (tok < s.kv_len && tok < g.t1 * kTile) {
           id = table[tok >> a.page_shift];
           if (id >= 0 && id < a.num_pages) {
@@ -277,8 +277,10 @@ split_kernel(const __grid_constant__ SplitParams p) {
         }
         const uint32_t vb = __float_as_uint(fminf(fmaxf(vs, kMinValueScale), kMaxValueScale));
         const int lv = (int)(vb >> 23) - 127 + (int)kScaleShift;
-        const GroupMeta group = {
-            ks, (float)lv, __uint_as_float((vb & 0x7FFFFFu) | 0x3F800000u) * kProbScale};
+        const GroupMeta group = {ks, (float)lv,
+                                 vs >= kMinValueScale  // what is no scale counts as 0
+                                     ? __uint_as_float((vb & 0x7FFFFFu) | 0x3F800000u) * kProbScale
+                                     : 0.f};
         for (int j = 0; j < 8 && tb + j < g.t1; ++j, ++it) {
           const int st = it % S;
           wait_or_die(&sm.empty[st], ((it / S) & 1u) ^ 1u, &sm.dead, a.status);

@@ -101,8 +101,8 @@ struct Unit {
 struct __align__(16) TileMeta {
   float ks[kGroups];    // key scale of each 16-token group
   float lv[kGroups];    // log2 of its value scale, shifted
-  int32_t row[kGroups]; // the group's first row in the cache; negative: absent, or past its tokens
-  uint32_t absent;      // bit g: group g is absent
+  int32_t row[kGroups]; // the group's first row of values in the cache; negative: zeros
+  uint32_t absent;      // bit g: group g is absent; bit 4 + g: its values are zeros
   float lvmin;          // least lv of the groups that are there
   uint32_t pad[2];
 };
@@ -369,7 +369,8 @@ tile_kernel(const __grid_constant__ TileParams p) {
           if (lane == 0 && tb + kLead >= u.tiles && (tb == 0 || tb + kLead - kBatch < u.tiles))
             mbar_arrive(&sm.unext);
           const int32_t tok = tb * BN + lane * 16;
-          ks = ks >= 0.f ? ks : 0.f;  // values that are no scales count as the smallest
+          ks = ks >= 0.f ? ks : 0.f;  // values that are no scales count as zeros
+          const bool empty = !(vs >= kMinValueScale);
           const uint32_t gone = __ballot_sync(0xffffffffu, id < 0);
           const int32_t y = (int32_t)(((int64_t)id * a.hkv + u.head) * a.page_size +
                                       (tok & (a.page_size - 1)));
@@ -381,9 +382,10 @@ tile_kernel(const __grid_constant__ TileParams p) {
           float least = fminf(lv, __shfl_xor_sync(0xffffffffu, lv, 1));
           least = fminf(least, __shfl_xor_sync(0xffffffffu, least, 2));
           m.lv[lane & 3] = lv;
-          m.row[lane & 3] = id < 0 ? -1 : y;
+          m.row[lane & 3] = id < 0 || empty ? -1 : y;
+          const uint32_t zeros = __ballot_sync(0xffffffffu, empty);
           if ((lane & 3) == 0) {
-            m.absent = (gone >> lane) & 15u;
+            m.absent = ((gone >> lane) & 15u) | ((zeros >> lane) & 15u) << 4;
             m.lvmin = least;
           }
           __syncwarp();

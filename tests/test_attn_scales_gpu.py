@@ -128,3 +128,33 @@ def test_scales_over_the_whole_range(shape, io):
 def test_nearly_one_hot_rows(io, dim):
     """Scores of hundreds."""
     _check(torch_cuda(), Case(8, [1, 2, 40, 130], [100, 77, 200, 130], 4, 2, dim, 16, io, scale=3.0))
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_scales_of_zero(io, shape):
+    """A value scale of 0, or below 2^-100, makes zeros of any codes, and the tokens keep their
+    part of the softmax sum; everywhere, in first pages, and in turns."""
+    hq, hkv, dim, page = shape
+    torch = torch_cuda()
+    c = Case(65, [1, 5, 140], [300, 70, 140], hq, hkv, dim, page, io)
+    c.scales[1][:] = 0
+    o, lse, status = c.run(torch)
+    assert status == 0 and (o == 0).all()
+    _, want_lse, _, size, _, _ = _reference(c)
+    assert (np.abs(lse - want_lse) <= 2 * (dim + 8) * 2.0 ** -24 * size + 2.0 ** -13).all()
+    for small in (0.0, 2.0 ** -101, 2.0 ** -140):
+        c.scales[1][:] = 2.0 ** -7
+        for b in range(3):
+            pages = c.table[b][:-(-c.kv_len[b] // page)]
+            c.scales[1][pages[:1]] = small
+            c.scales[1][pages[2::2]] = small
+        keep = c.scales[1]
+        c.scales[1] = np.where(keep == 2.0 ** -7, keep, 0).astype(np.float32)
+        want = _reference(c)[0]
+        c.scales[1] = keep
+        o, _, status = c.run(torch)
+        none = (want == 0).all(-1)
+        assert status == 0 and none.any() and (o[none] == 0).all()
+        c.scales[1] = np.where(keep == 2.0 ** -7, keep, 0).astype(np.float32)
+        _check(torch, c)
