@@ -797,10 +797,10 @@ join_kernel(AttnArgs a, const float* part, int workers) {
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
-// Row tiles of 8 in a unit. Two fit the registers up to D = 128 (12 bytes of spills in bf16); at 256
-// the accumulator alone takes 128 of the 168 and 360 bytes spill. Four spill everywhere: 32 requests
-// of 32 rows behind 2,000 tokens (D 128, 8 key/value heads) took 142 us with four and 93 with two
-// passes of two.
+// Row tiles of 8 in a unit. Two fit the registers up to D = 128 (12 bytes of spills in bf16); at
+// D = 256 the accumulator alone takes 128 of the 168, and 360 bytes spill. Four do not fit at 128:
+// 32 requests of 32 rows behind 2,000 tokens (8 key/value heads) took 142 us with four and 93 with
+// two passes of two.
 constexpr int kMaxRowTiles = 2;
 
 template <typename T, int D, int NT>

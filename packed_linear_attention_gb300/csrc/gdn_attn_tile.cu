@@ -23,8 +23,8 @@
 //
 // Block: 20 warps. 0-3 and 4-7 softmax, tile by tile in turns, a row to a thread: the latency
 // of a tile (tensor memory loads, 64 exponentials, the store of P) is then two tiles long. Only
-// the running maximum passes from one group to the other, warp by warp, through shared memory
-// and a pair of named barriers. 8-15 operands: V tiles, and the next unit's Q, whose bf16 rows
+// the running maxima pass from one group to the other, warp by warp, through shared memory and
+// a pair of named barriers. 8-15 operands: V tiles, and the next unit's Q, whose bf16 rows
 // a bulk copy brings to shared memory while this unit runs and which moves to tensor memory
 // when its last S is done; 16 the producer (pages, scales, K tiles); 17 issues S, 18 P V (the
 // twenty products of a tile, issued one after another between the waits of both, took one warp
