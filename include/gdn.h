@@ -678,8 +678,8 @@ gdn_status gdn_attn_workspace_size(const gdn_attn_config* cfg, const gdn_kv_cach
  * of order, status raised) write their common rows in any order, and nothing is written where
  * together they ask for 2^31 work items.
  * Scores, softmax sums and outputs are accumulated in fp32. The cache's codes enter the products
- * exactly, and so do bf16 queries, but for values below 2^-10 of their row's largest where a request has many queries:
- * those are off by at most 2^-17 of the largest. A token's weight, its probability times its
+ * exactly, and so do bf16 queries, but for values below 2^-10 of their row's largest where a
+ * request has many queries: those are off by at most 2^-17 of the largest. A token's weight, its probability times its
  * value scale, is rounded to fp16's 11 bits, or to 2^-31 of the largest weight of its row where
  * that is more: tokens that a row does not see, or gives no weight, change nothing of it. With
  * fp32 io queries and weights are two fp16 terms, 22 bits (weights to 2^-31 of the row's
