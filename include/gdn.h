@@ -698,6 +698,189 @@ gdn_status gdn_attn_paged(gdn_handle* handle, const gdn_attn_config* cfg,
                           int64_t o_stride, float* lse, void* workspace,
                           size_t workspace_bytes, int32_t* status, void* stream);
 
+/* ---- around the recurrent layers: convolution, selective scan, norm, sampling ---------- */
+
+/* The rest of a hybrid model's serving step. In front of a recurrent layer (the gated delta rule
+ * above, or the selective scan here) stands a short causal convolution over its channels; its
+ * output passes a root-mean-square norm, and so does the residual stream in front of every
+ * projection, which may take it in 8 bits; the last projection's logits are sampled. Serving
+ * forms only, like every call of this library.
+ *
+ * Requests of the two packed calls are given on the device, as gdn_kv_plan's, so that a step can
+ * be captured in a CUDA graph: request n is rows [cu[n], cu[n+1]) and its state lives in slot
+ * slot_idx[n] of the caller's pool, where it is updated in place. Any mix of prompts and single
+ * tokens is served. A request whose rows or slot are out of range, or that is longer than max_len,
+ * is refused whole (nothing of it is read or written); a slot below 0 skips its request. Rows
+ * outside every request served are not written. Where `status` is a non-NULL device int32 the
+ * kernels raise it (atomic maximum) to GDN_ERR_INVALID_ARGUMENT when they refused something; they
+ * never clear it. Distinct slots and disjoint rows are the caller's duty: requests that share a
+ * slot or rows (cu out of order, status raised) race for them, and some of them may be left out. */
+typedef struct gdn_requests {
+  int32_t num_seqs;          /* 1 .. 4,096 requests                                          */
+  int32_t num_tokens;        /* rows of the call's arrays, cu[num_seqs] or more              */
+  int32_t max_len;           /* host bound of the requests' lengths                          */
+  int32_t num_slots;         /* slots of the state pool                                      */
+  const int32_t* cu;         /* [num_seqs + 1] first rows; a request of no rows is allowed   */
+  const int32_t* slot_idx;   /* [num_seqs], or NULL: request n uses slot n                   */
+  const int32_t* start_zero; /* [num_seqs] nonzero: start from zeros, not from the slot; NULL:
+                                every request starts from its slot                           */
+  const int32_t* ckpt_cu;    /* [num_seqs + 1] CSR over ckpt_pos, or NULL: no checkpoints    */
+  const int32_t* ckpt_pos;   /* positions p in [1, length], rising within a request: checkpoint
+                                j receives the state after the request's first p rows        */
+  int32_t num_ckpt;          /* checkpoints the arrays hold (others are refused)             */
+} gdn_requests;
+
+typedef enum gdn_activation { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1 } gdn_activation;
+
+/* Causal convolution of each channel by itself:
+ *     y[t][c] = act(bias[c] + sum_j weight[c][j] * x[t - width + 1 + j][c])
+ * summed in fp32 and rounded once. Rows in front of a request's first come from its state: the
+ * last width - 1 inputs of the request so far, oldest first, [width - 1][channels] io_dtype. */
+typedef struct gdn_conv_config {
+  int32_t channels;     /* C >= 1 */
+  int32_t width;        /* taps, 2 .. 4 */
+  int32_t activation;   /* gdn_activation; silu(v) = v / (1 + exp(-v)) */
+  int32_t io_dtype;     /* gdn_dtype of x, y and the states */
+  const float* weight;  /* [C][width] device; the last tap multiplies the current row */
+  const float* bias;    /* [C] device, or NULL */
+} gdn_conv_config;
+
+/* The convolution of a pack of requests (one kernel).
+ *  x, y        row t's channels at x + t * x_stride (elements); no overlap of x and y.
+ *  state_pool  [num_slots][width - 1][C] io_dtype, updated in place.
+ *  ckpt_states [num_ckpt][width - 1][C] io_dtype, or NULL without checkpoints.
+ * Pointers 16-byte aligned, strides multiples of 16 bytes and at least C (so x may be a column
+ * range of a projection's output). Results do not depend on the pack around a request.
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED (width, more than 4,096 requests), CUDA. */
+gdn_status gdn_conv_packed(gdn_handle* handle, const gdn_conv_config* cfg,
+                           const gdn_requests* req, const void* x, int64_t x_stride, void* y,
+                           int64_t y_stride, void* state_pool, void* ckpt_states,
+                           int32_t* status, void* stream);
+
+/* One token of `batch` decoding requests (one kernel): row b with the state in slot slot_idx[b]
+ * (device; below 0: the row is skipped; slots distinct). y may be x with the same stride.
+ * Otherwise as gdn_conv_packed. */
+gdn_status gdn_conv_step(gdn_handle* handle, const gdn_conv_config* cfg, int32_t batch,
+                         const void* x, int64_t x_stride, void* y, int64_t y_stride,
+                         void* state_pool, int32_t num_slots, const int32_t* slot_idx,
+                         int32_t* status, void* stream);
+
+/* Selective scan: for every channel c with group g = c / (C / num_groups),
+ *     dt = softplus(delta[t][c] + delta_bias[c])    (without softplus when delta_softplus is 0)
+ *     h[n] = exp(dt * a[c][n]) * h[n] + dt * x[t][c] * b[t][g][n]
+ *     y[t][c] = (sum_n c[t][g][n] * h[n] + d[c] * x[t][c]) * silu(z[t][c])
+ * in fp32, y rounded once; states fp32 [C][state_dim]. */
+typedef struct gdn_ssm_config {
+  int32_t channels;        /* C >= 1, a multiple of num_groups */
+  int32_t num_groups;
+  int32_t state_dim;       /* N, 1 .. 128 */
+  int32_t io_dtype;        /* gdn_dtype of x, delta, b, c, z and y */
+  int32_t delta_softplus;
+  const float* a;          /* [C][N] device (negative: decaying) */
+  const float* d;          /* [C] device, or NULL: no skip term */
+  const float* delta_bias; /* [C] device, or NULL */
+} gdn_ssm_config;
+
+/* The rows of a scan: row t of an array at its pointer + t * its stride (elements). x, delta, z
+ * and y hold C elements a row (pointers 16-byte aligned, strides multiples of 16 bytes); b and c
+ * [num_groups][N], at any alignment of their elements. z NULL: no gate. y may be x, delta or z
+ * with the same stride; no other overlap. */
+typedef struct gdn_ssm_rows {
+  const void* x;
+  const void* delta;
+  const void* b;
+  const void* c;
+  const void* z;
+  void* y;
+  int64_t x_stride, delta_stride, b_stride, c_stride, z_stride, y_stride;
+} gdn_ssm_rows;
+
+/* Device workspace of gdn_ssm_packed for such requests (multiple of 256; the host fields of req
+ * alone are read). */
+gdn_status gdn_ssm_workspace_size(const gdn_ssm_config* cfg, const gdn_requests* req,
+                                  size_t* bytes);
+
+/* The scan of a pack of requests.
+ *  state_pool  [num_slots][C][N] fp32, updated in place.
+ *  ckpt_states [num_ckpt][C][N] fp32, or NULL without checkpoints.
+ *  workspace   256-byte aligned; not to be used by other work before this call's has finished.
+ * Where the call has too few channels and requests to fill the GPU, requests longer than a
+ * segment (chosen from num_tokens, max_len, C and N, never from device values) are cut: a first
+ * kernel finds each segment's end state from zeros and its decay, a second runs the segments
+ * from the joined states; results then differ from the uncut ones by fp32 rounding. The same call
+ * gives the same bits. Inputs that are not finite spoil their own channel of their own request.
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED (state_dim above 128, more than 4,096 requests),
+ * WORKSPACE_TOO_SMALL, CUDA. */
+gdn_status gdn_ssm_packed(gdn_handle* handle, const gdn_ssm_config* cfg, const gdn_requests* req,
+                          const gdn_ssm_rows* rows, float* state_pool, float* ckpt_states,
+                          void* workspace, size_t workspace_bytes, int32_t* status,
+                          void* stream);
+
+/* One token of `batch` decoding requests (one kernel): row b with the state in slot slot_idx[b]
+ * (device; below 0: the row is skipped; slots distinct), updated in place. */
+gdn_status gdn_ssm_step(gdn_handle* handle, const gdn_ssm_config* cfg, int32_t batch,
+                        const gdn_ssm_rows* rows, float* state_pool, int32_t num_slots,
+                        const int32_t* slot_idx, int32_t* status, void* stream);
+
+/* Root-mean-square norm of every head of every token, with the residual's addition in front and
+ * a gate and an 8-bit output behind:
+ *     s = x + residual                              (sum receives s rounded to io_dtype)
+ *     v = s / sqrt(mean(s^2) + eps) * (weight + weight_offset) * silu(gate)
+ *     y = v rounded to io_dtype; codes = v / scale rounded to e4m3
+ * in fp32 from the unrounded s. A scale covers scale_group columns, or with 0 the token's whole
+ * row: max|v| / 448 over its finite values, or with scale_pow2 the least power of two at least
+ * that; 2^-100 at least. Infinities are held as the largest finite value; a NaN stays NaN. */
+typedef struct gdn_norm_config {
+  int32_t num_heads;     /* heads of a row, each normalised by itself (1: the row) */
+  int32_t dim;           /* elements of a head: any with one head, else 64, 128 or 256 */
+  int32_t io_dtype;      /* gdn_dtype of x, residual, sum, gate and y */
+  int32_t scale_group;   /* 0, 32, 64 or 128 (dividing dim) */
+  int32_t scale_pow2;
+  float eps;             /* >= 0 */
+  float weight_offset;   /* 1 where the model keeps weight - 1 */
+  const float* weight;   /* [dim] device, or NULL: ones (and no offset) */
+} gdn_norm_config;
+
+/* The norm of num_tokens rows of num_heads * dim elements (at most 32,768), one kernel.
+ *  residual, sum, gate  NULL where not wanted (sum needs residual). y NULL where codes are given.
+ *  codes   [num_tokens] rows of e4m3 at codes + t * codes_stride (bytes), with
+ *  scales  [num_tokens][num_heads * dim / scale_group, or 1] fp32; or both NULL.
+ * Pointers 16-byte aligned (scales 4), strides multiples of 16 bytes. sum and y may each be x,
+ * residual or gate with the same stride (in place); no other overlap.
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED, CUDA. */
+gdn_status gdn_rms_norm(gdn_handle* handle, const gdn_norm_config* cfg, int32_t num_tokens,
+                        const void* x, int64_t x_stride, const void* residual,
+                        int64_t residual_stride, void* sum, int64_t sum_stride, const void* gate,
+                        int64_t gate_stride, void* y, int64_t y_stride, void* codes,
+                        int64_t codes_stride, float* scales, void* stream);
+
+/* Draw a token from every row of logits (one kernel). With l the row's logits, m their maximum
+ * and w_i = exp((l_i - m) / temperature), tokens in the order of falling logits, equal ones by
+ * rising index:
+ *   top_k  > 0: the first top_k tokens are kept;
+ *   top_p  < 1: of these the shortest beginning whose weight reaches top_p of theirs (the first
+ *          token at least);
+ *   min_p  > 0: of these the tokens with w_i >= min_p (values above 1 count as 1).
+ * The token drawn is the first, by index, at which the kept tokens' weights sum to more than u
+ * times their total; logprob is the logarithm of its share of that total. temperature 0: the
+ * token of the maximum, lowest index first, logprob 0.
+ *  logits       row r at logits + r * stride (elements), io_dtype, any alignment of elements.
+ *  temperature, top_k, top_p, min_p  [num_rows] device, or NULL: 1, off, off, off.
+ *  u            [num_rows] device, random numbers of [0, 1) (others count as the nearest).
+ *  token        [num_rows] int32 out; logprob [num_rows] fp32 out, or NULL.
+ * A logit of -inf or NaN is never drawn; where a row has +inf, those alone are drawn from. A row
+ * without any other logit, or with a temperature below 0 or a NaN among its settings, gives token
+ * -1 and logprob -inf and raises status (may be NULL) to GDN_ERR_INVALID_ARGUMENT.
+ * Weights are fixed-point numbers of 2^-44 of the maximum's, right to 2^-30 of their own value
+ * (or half a unit), and their sums are exact: results depend on no order of additions, and the same
+ * call gives the same bits. Supported: vocab 1 .. 262,144.
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED, CUDA. */
+gdn_status gdn_sample(gdn_handle* handle, int32_t io_dtype, int32_t num_rows, int32_t vocab,
+                      const void* logits, int64_t stride, const float* temperature,
+                      const int32_t* top_k, const float* top_p, const float* min_p,
+                      const float* u, int32_t* token, float* logprob, int32_t* status,
+                      void* stream);
+
 /* ---- host-side scheduling policy (no device work) ---------------------------------- */
 
 /* Prefix-cache checkpoint position of a prompt of `len` tokens on a grid of `block`

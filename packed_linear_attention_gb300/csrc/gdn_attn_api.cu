@@ -9,15 +9,13 @@
 #include <cstring>
 
 #include "../../include/gdn.h"
+#include "gdn_args.h"
 #include "gdn_attn_internal.h"
 #include "gdn_internal.h"
 
 namespace {
 
-bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
-bool known_dtype(int32_t t) { return t == GDN_F32 || t == GDN_BF16; }
-size_t item_size(int32_t dtype) { return dtype == GDN_BF16 ? 2 : 4; }
+using namespace gdn::args;
 
 gdn_status check_page_size(int32_t p) {
   if (p <= 0) return GDN_ERR_INVALID_ARGUMENT;
@@ -49,35 +47,6 @@ gdn_status check_cache(const gdn_kv_cache* c) {
   return GDN_OK;
 }
 
-// Rows of `heads` heads: pointer, alignment and stride.
-bool rows_ok(const void* p, int64_t stride, int32_t heads, int32_t head_dim, int32_t dtype) {
-  return p && aligned(p, 16) && stride >= (int64_t)heads * head_dim &&
-         stride % (int64_t)(16 / item_size(dtype)) == 0 && stride <= (int64_t)1 << 40;
-}
-
-struct Span {
-  uintptr_t lo, hi;
-};
-// The bytes that `tokens` rows of a strided tensor reach over.
-Span span_of(const void* p, int64_t tokens, int64_t stride, int64_t row, size_t item) {
-  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-  return {lo, tokens > 0 ? lo + (uintptr_t)((tokens - 1) * stride + row) * item : lo};
-}
-bool overlap(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi; }
-
-// Two strided tensors share memory unless their rows lie beside one another in rows of the
-// same stride (column ranges of one array).
-bool rows_overlap(const void* p, int64_t ps, int64_t prow, const void* q, int64_t qs,
-                  int64_t qrow, int64_t tokens, size_t item) {
-  if (!overlap(span_of(p, tokens, ps, prow, item), span_of(q, tokens, qs, qrow, item)))
-    return false;
-  if (ps != qs) return true;
-  const int64_t stride = ps * (int64_t)item;
-  int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(q) - reinterpret_cast<uintptr_t>(p)) % stride;
-  if (d < 0) d += stride;
-  return d < prow * (int64_t)item || d + qrow * (int64_t)item > stride;
-}
-
 gdn_status check_rope(const gdn_rope* r) {
   if (!r) return GDN_ERR_INVALID_ARGUMENT;
   const gdn_status s = check_head_dim(r->head_dim);
@@ -100,18 +69,6 @@ bool rope_heads_ok(const void* in, int64_t in_stride, int32_t heads, const void*
   if (in == out && in_stride == out_stride) return true;
   const int64_t row = (int64_t)heads * head_dim;
   return !rows_overlap(in, in_stride, row, out, out_stride, row, tokens, item_size(dtype));
-}
-
-// Runs `launch` with the handle's device current.
-template <class F>
-gdn_status on_device(const gdn_handle* h, F launch) {
-  const int device = gdn::handle_device(h);
-  int prev = 0;
-  if (cudaGetDevice(&prev) != cudaSuccess) return GDN_ERR_CUDA;
-  if (prev != device && cudaSetDevice(device) != cudaSuccess) return GDN_ERR_CUDA;
-  const int e = launch();
-  if (prev != device) cudaSetDevice(prev);
-  return e == 0 ? GDN_OK : GDN_ERR_CUDA;
 }
 
 gdn_status check_attn(const gdn_attn_config* cfg, const gdn_kv_cache* c, int32_t num_seqs,

@@ -1,0 +1,540 @@
+// gdn_ssm.cu — the selective scan, for packs of requests and for single tokens.
+//
+//     dt = softplus(delta + bias)
+//     h[n] = exp(dt a[n]) h[n] + dt x b[n]          (fp32, N states a channel)
+//     y = (sum_n c[n] h[n] + d x) silu(z)
+//
+// Channels are independent and their states short, so a thread owns a channel (or SPLIT lanes
+// share one, NS states each), keeps its states and decay rates in registers and walks down the
+// rows. b and c are the same for all channels of a group: a block stages them in shared memory,
+// kTile rows at a time. exp is one multiplication (the rates are held times log2 e) and one
+// ex2; the rest are fused multiply-adds on pairs of states (f32x2).
+#include <algorithm>
+#include <climits>
+
+#include "gdn_step_internal.h"
+
+namespace gdn {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kAhead = 4;  // rows whose x, delta and z are loaded ahead
+constexpr float kLog2e = 1.4426950408889634f;
+
+using f32x2 = unsigned long long;  // two fp32 in a register pair
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(f32x2 p, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ f32x2 ex2(f32x2 x) {
+  float lo, hi;
+  unpair(x, lo, hi);
+  return pair(ex2(lo), ex2(hi));
+}
+
+// log(1 + exp(x)) = max(x, 0) + log1p(e), e = exp(-|x|) in (0, 1], and with s = e / (2 + e),
+// log1p(e) = 2 atanh(s) = 2 s (1 + s^2/3 + s^4/5 + ...): s^2 <= 1/9, so seven terms leave 2e-8 of
+// it, and small values keep their relative precision.
+__device__ __forceinline__ float softplus(float x) {
+  const float e = ex2(-kLog2e * fabsf(x));
+  const float s = __fdividef(e, 2.f + e), q = s * s;
+  float p = fmaf(q, 1.f / 13.f, 1.f / 11.f);
+  p = fmaf(q, p, 1.f / 9.f);
+  p = fmaf(q, p, 1.f / 7.f);
+  p = fmaf(q, p, 1.f / 5.f);
+  p = fmaf(q, p, 1.f / 3.f);
+  p = fmaf(q, p, 1.f);
+  return fmaf(2.f * s, p, fmaxf(x, 0.f));
+}
+
+constexpr int tile_rows(int padded) { return padded <= 32 ? 32 : 16; }
+
+// The states of one thread: NS of channel c, chunks of four that the SPLIT lanes take in turn
+// (so that the lanes' reads of b and c in shared memory lie side by side).
+template <int NS, int SPLIT>
+struct States {
+  f32x2 h[NS / 2], a[NS / 2];
+
+  __device__ __forceinline__ static int chunk(int i, int part) { return 4 * (i * SPLIT + part); }
+
+  __device__ __forceinline__ void rates(const float* a_row, int part, int n) {
+#pragma unroll
+    for (int i = 0; i < NS / 4; ++i) {
+      float f[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int at = chunk(i, part) + e;
+        f[e] = at < n ? kLog2e * __ldg(a_row + at) : 0.f;
+      }
+      a[2 * i] = pair(f[0], f[1]);
+      a[2 * i + 1] = pair(f[2], f[3]);
+    }
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < NS / 2; ++i) h[i] = 0;
+  }
+  // row: N floats; 16-byte accesses where N is a multiple of 4
+  __device__ __forceinline__ void load(const float* row, int part, int n) {
+#pragma unroll
+    for (int i = 0; i < NS / 4; ++i) {
+      const int at = chunk(i, part);
+      float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (n % 4 == 0) {
+        if (at < n) f = *reinterpret_cast<const float4*>(row + at);
+      } else {
+        if (at < n) f.x = row[at];
+        if (at + 1 < n) f.y = row[at + 1];
+        if (at + 2 < n) f.z = row[at + 2];
+        if (at + 3 < n) f.w = row[at + 3];
+      }
+      h[2 * i] = pair(f.x, f.y);
+      h[2 * i + 1] = pair(f.z, f.w);
+    }
+  }
+  __device__ __forceinline__ void store(float* row, int part, int n) const {
+#pragma unroll
+    for (int i = 0; i < NS / 4; ++i) {
+      const int at = chunk(i, part);
+      float4 f;
+      unpair(h[2 * i], f.x, f.y);
+      unpair(h[2 * i + 1], f.z, f.w);
+      if (n % 4 == 0) {
+        if (at < n) *reinterpret_cast<float4*>(row + at) = f;
+      } else {
+        if (at < n) row[at] = f.x;
+        if (at + 1 < n) row[at + 1] = f.y;
+        if (at + 2 < n) row[at + 2] = f.z;
+        if (at + 3 < n) row[at + 3] = f.w;
+      }
+    }
+  }
+  // one row; b and c: the padded row in shared memory. Returns this thread's part of c . h.
+  template <bool OUT>
+  __device__ __forceinline__ float step(float dt, float dtx, const float* b, const float* c,
+                                        int part) {
+    const f32x2 t = pair(dt, dt), u = pair(dtx, dtx);
+    f32x2 acc[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < NS / 4; ++i) {
+      const ulonglong2 bv = *reinterpret_cast<const ulonglong2*>(b + chunk(i, part));
+      h[2 * i] = fma2(ex2(mul2(t, a[2 * i])), h[2 * i], mul2(u, bv.x));
+      h[2 * i + 1] = fma2(ex2(mul2(t, a[2 * i + 1])), h[2 * i + 1], mul2(u, bv.y));
+      if (OUT) {
+        const ulonglong2 cv = *reinterpret_cast<const ulonglong2*>(c + chunk(i, part));
+        acc[0] = fma2(cv.x, h[2 * i], acc[0]);
+        acc[1] = fma2(cv.y, h[2 * i + 1], acc[1]);
+      }
+    }
+    float s0, s1, s2, s3;
+    unpair(acc[0], s0, s1);
+    unpair(acc[1], s2, s3);
+    return (s0 + s1) + (s2 + s3);
+  }
+};
+
+// What a block scans: rows [lo, lo + len) of request `seq` from `state`.
+struct Span {
+  int32_t seq, lo, len, first;  // first: rows of the request in front of them
+};
+
+template <typename T, int NS, int SPLIT>
+struct Scan {
+  static constexpr int kPadded = NS * SPLIT;
+  static constexpr int kTile = tile_rows(kPadded);
+  static constexpr int kChannels = kThreads / SPLIT;
+  struct Shared {
+    float b[2][kTile][kPadded], c[2][kTile][kPadded];
+  };
+
+  const SsmArgs& p;
+  Shared& sm;
+  int group, channel, part;
+  bool live;
+  States<NS, SPLIT> s;
+  float skip, bias, total = 0.f;
+
+  __device__ __forceinline__ Scan(const SsmArgs& args, Shared& shared, int block)
+      : p(args), sm(shared) {
+    const int per = p.cfg.channels / p.cfg.num_groups;
+    const int tiles = (per + kChannels - 1) / kChannels;
+    group = block / tiles;
+    const int c = block % tiles * kChannels + (int)threadIdx.x / SPLIT;
+    live = c < per;
+    channel = group * per + min(c, per - 1);
+    part = threadIdx.x % SPLIT;
+    s.rates(p.cfg.a + (size_t)channel * p.cfg.state_dim, part, p.cfg.state_dim);
+    skip = p.cfg.d ? __ldg(p.cfg.d + channel) : 0.f;
+    bias = p.cfg.delta_bias ? __ldg(p.cfg.delta_bias + channel) : 0.f;
+  }
+
+  __device__ __forceinline__ size_t state_row(int64_t slot) const {
+    return ((size_t)slot * p.cfg.channels + channel) * p.cfg.state_dim;
+  }
+
+  // b and c of rows [row, row + kTile) into buffer `buf`; zeros past the states and the rows
+  __device__ __forceinline__ void stage(int64_t row, int rows, int buf) {
+    const int n = p.cfg.state_dim;
+    const T* b = static_cast<const T*>(p.rows.b) + row * p.rows.b_stride + (size_t)group * n;
+    const T* c = static_cast<const T*>(p.rows.c) + row * p.rows.c_stride + (size_t)group * n;
+#pragma unroll
+    for (int i = 0; i < kTile * kPadded / kThreads; ++i) {
+      const int at = i * kThreads + threadIdx.x, t = at / kPadded, k = at % kPadded;
+      const bool in = t < rows && k < n;
+      sm.b[buf][t][k] = in ? to_f32(b[(size_t)t * p.rows.b_stride + k]) : 0.f;
+      sm.c[buf][t][k] = in ? to_f32(c[(size_t)t * p.rows.c_stride + k]) : 0.f;
+    }
+  }
+
+  // The rows of `span`, from the states in s. OUT: y and the checkpoints; else the sum of dt.
+  template <bool OUT>
+  __device__ __forceinline__ void run(const Span& span, bool report) {
+    const T* x = static_cast<const T*>(p.rows.x) + (size_t)span.lo * p.rows.x_stride + channel;
+    const T* delta =
+        static_cast<const T*>(p.rows.delta) + (size_t)span.lo * p.rows.delta_stride + channel;
+    const T* z = p.rows.z
+                     ? static_cast<const T*>(p.rows.z) + (size_t)span.lo * p.rows.z_stride + channel
+                     : nullptr;
+    T* y = static_cast<T*>(p.rows.y) + (size_t)span.lo * p.rows.y_stride + channel;
+    const int len = span.len;
+
+    // the first checkpoint past the rows in front (rows counted from span.lo from here on)
+    int2 ck = make_int2(0, 0);
+    int mark = INT_MAX, before = 0;
+    auto next_mark = [&] {
+      mark = INT_MAX;
+      for (; ck.x < ck.y; ++ck.x) {
+        const int pos = p.req.ckpt_pos[ck.x];
+        if (pos <= before || pos > p.req.cu[span.seq + 1] - p.req.cu[span.seq]) {
+          if (report) raise_status(p.status, GDN_ERR_INVALID_ARGUMENT);
+          continue;
+        }
+        before = pos;
+        if (pos > span.first) {
+          mark = pos - span.first;
+          return;
+        }
+      }
+    };
+    if (OUT) {
+      ck = load_checkpoints(p.req, span.seq, report ? p.status : nullptr);
+      next_mark();
+    }
+
+    T xr[kAhead], dr[kAhead], zr[kAhead];
+    auto fetch = [&](int t) {
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (t + i < len) {
+          xr[i] = x[(size_t)(t + i) * p.rows.x_stride];
+          dr[i] = delta[(size_t)(t + i) * p.rows.delta_stride];
+          if (OUT && z) zr[i] = z[(size_t)(t + i) * p.rows.z_stride];
+        }
+      }
+    };
+    const bool soft = p.cfg.delta_softplus != 0;
+    auto one = [&](int t, int buf, int row, T xv, T dv, T zv) {
+      const float xf = to_f32(xv);
+      float dt = to_f32(dv) + bias;
+      if (soft) dt = softplus(dt);
+      if (!OUT) total += dt;
+      float sum = s.template step<OUT>(dt, dt * xf, sm.b[buf][row], sm.c[buf][row], part);
+      if (OUT) {
+#pragma unroll
+        for (int off = SPLIT / 2; off > 0; off >>= 1)
+          sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        sum = fmaf(skip, xf, sum);
+        if (z) sum *= silu(to_f32(zv));
+        if (live && part == 0) y[(size_t)t * p.rows.y_stride] = from_f32<T>(sum);
+      }
+    };
+    fetch(0);
+    stage(span.lo, min(len, kTile), 0);
+    __syncthreads();
+    for (int t0 = 0, buf = 0; t0 < len; t0 += kTile, buf ^= 1) {
+      if (t0 + kTile < len) stage(span.lo + t0 + kTile, min(len - t0 - kTile, kTile), buf ^ 1);
+      const int rows = min(len - t0, kTile);
+      for (int r = 0; r < rows; r += kAhead) {
+        T xv[kAhead], dv[kAhead], zv[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          xv[i] = xr[i];
+          dv[i] = dr[i];
+          zv[i] = zr[i];
+        }
+        const int t = t0 + r;
+        fetch(t + kAhead);
+        if (r + kAhead <= rows && (!OUT || mark > t + kAhead)) {
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i) one(t + i, buf, r + i, xv[i], dv[i], zv[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i) {
+            if (r + i < rows) {
+              one(t + i, buf, r + i, xv[i], dv[i], zv[i]);
+              if (OUT && mark == t + i + 1) {
+                if (live) s.store(p.ckpt + state_row(ck.x), part, p.cfg.state_dim);
+                ++ck.x;
+                next_mark();
+              }
+            }
+          }
+        }
+      }
+      __syncthreads();
+    }
+  }
+};
+
+// pass 0: whole requests, a unit each. With requests cut into segments, pass 1 runs every
+// request's first segment and finds the end states of its middle ones from zeros; pass 2 joins
+// them and runs the segments behind the first. exp(a dt_1) ... exp(a dt_k) is exp(a sum dt), so a
+// segment's decay needs only its sum of dt.
+template <typename T, int NS, int SPLIT>
+__global__ void __launch_bounds__(kThreads) ssm_kernel(SsmArgs p, int channel_blocks, int pass) {
+  using S = Scan<T, NS, SPLIT>;
+  __shared__ __align__(16) typename S::Shared sm;
+  const int unit = blockIdx.x / channel_blocks;
+  int32_t* status = blockIdx.x == 0 && pass < 2 ? p.status : nullptr;
+  const int seg = p.segment;
+  const int cap = seg ? p.req.num_tokens / seg : 0;  // end states the workspace holds
+  Unit u = {unit, 0, 0};
+  if (pass > 0) {
+    const auto behind = [&](int n) {  // segments behind the first
+      const Request q = load_request(p.req, n, nullptr);
+      return q.len <= 0 ? 0 : (q.len - 1) / seg;
+    };
+    u = find_unit<kThreads>(
+        p.req.num_seqs, unit,
+        [&](int n) {
+          const Request q = load_request(p.req, n, status);
+          if (q.len < 0) return 0;
+          const int k = q.len == 0 ? 0 : (q.len - 1) / seg;
+          return pass == 1 ? max(1, k) : k;
+        },
+        behind);
+    if (u.seq < 0) return;
+  } else {
+    status = blockIdx.x % channel_blocks == 0 && threadIdx.x == 0 ? p.status : nullptr;
+  }
+  const Request q = load_request(p.req, u.seq, pass == 0 ? status : nullptr);
+  if (q.len < 0) return;
+  const int later = seg && q.len > 0 ? (q.len - 1) / seg : 0;
+  const int k = pass == 2 ? u.place + 1 : u.place;  // this block's segment
+  if (later > 0 && u.extra + later > cap) {  // only where requests overlap
+    if (threadIdx.x == 0) raise_status(p.status, GDN_ERR_INVALID_ARGUMENT);
+    return;
+  }
+  S scan(p, sm, blockIdx.x % channel_blocks);
+  const int n = p.cfg.state_dim;
+  const Span span = {u.seq, q.lo + k * seg, seg ? min(q.len - k * seg, seg) : q.len, k * seg};
+  const size_t ends = (size_t)u.extra;  // the request's first end state
+  scan.s.clear();
+  if (k == 0) {
+    if (!q.zero) scan.s.load(p.pool + scan.state_row(q.slot), scan.part, n);
+  } else if (pass == 2) {
+    scan.s.load(p.ends + scan.state_row(ends), scan.part, n);
+    for (int j = 1; j < k; ++j) {
+      States<NS, SPLIT> end;
+      end.load(p.ends + scan.state_row(ends + j), scan.part, n);
+      const float dt = p.steps[(ends + j) * p.cfg.channels + scan.channel];
+#pragma unroll
+      for (int i = 0; i < NS / 2; ++i)
+        scan.s.h[i] = fma2(ex2(mul2(pair(dt, dt), scan.s.a[i])), scan.s.h[i], end.h[i]);
+    }
+  }
+  const bool report = blockIdx.x % channel_blocks == 0 && threadIdx.x == 0;
+  if (pass == 1 && k > 0) {
+    scan.template run<false>(span, false);
+    if (scan.live && scan.part == 0)
+      p.steps[(ends + k) * p.cfg.channels + scan.channel] = scan.total;
+  } else {
+    scan.template run<true>(span, report);
+  }
+  if (!scan.live) return;
+  if (k == later) scan.s.store(p.pool + scan.state_row(q.slot), scan.part, n);
+  else if (pass == 1) scan.s.store(p.ends + scan.state_row(ends + k), scan.part, n);
+}
+
+// One token: LANES lanes a channel, four states each, so that a state goes through as 16-byte
+// accesses side by side. Bound by HBM (the states, in and out).
+template <typename T>
+__device__ __forceinline__ float4 load_four(const T* p, int count, bool aligned) {
+  float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (aligned && count >= 4) {
+    if (sizeof(T) == 4) return *reinterpret_cast<const float4*>(p);
+    const uint2 w = *reinterpret_cast<const uint2*>(p);
+    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
+                       __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+  }
+  if (count > 0) f.x = to_f32(p[0]);
+  if (count > 1) f.y = to_f32(p[1]);
+  if (count > 2) f.z = to_f32(p[2]);
+  if (count > 3) f.w = to_f32(p[3]);
+  return f;
+}
+
+template <typename T, int LANES>
+__global__ void __launch_bounds__(kThreads) ssm_step_kernel(SsmArgs p, int channel_blocks,
+                                                            bool aligned) {
+  const int row = blockIdx.x / channel_blocks;
+  const int c = blockIdx.x % channel_blocks * (kThreads / LANES) + (int)threadIdx.x / LANES;
+  const int part = threadIdx.x % LANES, n0 = 4 * part, n = p.cfg.state_dim;
+  const int slot = p.req.slot_idx[row];
+  if (slot < 0 || slot >= p.req.num_slots) {
+    if (slot >= 0) raise_status(p.status, GDN_ERR_INVALID_ARGUMENT);
+    return;
+  }
+  const bool live = c < p.cfg.channels;
+  const int ch = min(c, p.cfg.channels - 1);
+  const int count = n - n0;
+  float* state = p.pool + ((size_t)slot * p.cfg.channels + ch) * n + n0;
+  const bool whole = n % 4 == 0;
+  float4 h = load_four(state, count, whole);
+  const float4 a = load_four(p.cfg.a + (size_t)ch * n + n0, count, whole);
+  const int group = ch / (p.cfg.channels / p.cfg.num_groups);
+  const float4 b = load_four(
+      static_cast<const T*>(p.rows.b) + (size_t)row * p.rows.b_stride + group * n + n0, count, aligned);
+  const float4 cc = load_four(
+      static_cast<const T*>(p.rows.c) + (size_t)row * p.rows.c_stride + group * n + n0, count, aligned);
+  const float x = to_f32(static_cast<const T*>(p.rows.x)[(size_t)row * p.rows.x_stride + ch]);
+  float dt = to_f32(static_cast<const T*>(p.rows.delta)[(size_t)row * p.rows.delta_stride + ch]);
+  if (p.cfg.delta_bias) dt += __ldg(p.cfg.delta_bias + ch);
+  if (p.cfg.delta_softplus) dt = softplus(dt);
+  const float t = kLog2e * dt, dtx = dt * x;
+  h.x = fmaf(ex2(t * a.x), h.x, dtx * b.x);
+  h.y = fmaf(ex2(t * a.y), h.y, dtx * b.y);
+  h.z = fmaf(ex2(t * a.z), h.z, dtx * b.z);
+  h.w = fmaf(ex2(t * a.w), h.w, dtx * b.w);
+  float sum = fmaf(cc.x, h.x, cc.y * h.y) + fmaf(cc.z, h.z, cc.w * h.w);
+#pragma unroll
+  for (int off = LANES / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  if (!live) return;
+  if (whole) {
+    if (count >= 4) *reinterpret_cast<float4*>(state) = h;
+  } else {
+    if (count > 0) state[0] = h.x;
+    if (count > 1) state[1] = h.y;
+    if (count > 2) state[2] = h.z;
+    if (count > 3) state[3] = h.w;
+  }
+  if (part == 0) {
+    if (p.cfg.d) sum = fmaf(__ldg(p.cfg.d + ch), x, sum);
+    if (p.rows.z)
+      sum *= silu(to_f32(static_cast<const T*>(p.rows.z)[(size_t)row * p.rows.z_stride + ch]));
+    static_cast<T*>(p.rows.y)[(size_t)row * p.rows.y_stride + ch] = from_f32<T>(sum);
+  }
+}
+
+// states of a thread and lanes of a channel
+struct Shape {
+  int ns, split;
+};
+Shape shape_of(int n) {
+  if (n <= 4) return {4, 1};
+  if (n <= 8) return {8, 1};
+  int split = 1;
+  while (16 * split < n) split *= 2;
+  return {16, split};
+}
+
+template <typename T, int NS, int SPLIT>
+int launch_scan(const SsmArgs& a, cudaStream_t s) {
+  const int per = a.cfg.channels / a.cfg.num_groups, ch = kThreads / SPLIT;
+  const int cb = a.cfg.num_groups * ((per + ch - 1) / ch);
+  if (a.segment == 0) {
+    ssm_kernel<T, NS, SPLIT><<<(unsigned)((int64_t)a.req.num_seqs * cb), kThreads, 0, s>>>(a, cb, 0);
+    return (int)cudaGetLastError();
+  }
+  // disjoint requests: at most a segment more than their whole ones each
+  const int64_t behind = a.req.num_tokens / a.segment;
+  ssm_kernel<T, NS, SPLIT>
+      <<<(unsigned)((behind + a.req.num_seqs) * cb), kThreads, 0, s>>>(a, cb, 1);
+  if (behind > 0)
+    ssm_kernel<T, NS, SPLIT><<<(unsigned)(behind * cb), kThreads, 0, s>>>(a, cb, 2);
+  return (int)cudaGetLastError();
+}
+
+template <typename T>
+int scan_by_shape(const SsmArgs& a, cudaStream_t s) {
+  const Shape k = shape_of(a.cfg.state_dim);
+  if (k.ns == 4) return launch_scan<T, 4, 1>(a, s);
+  if (k.ns == 8) return launch_scan<T, 8, 1>(a, s);
+  switch (k.split) {
+    case 1: return launch_scan<T, 16, 1>(a, s);
+    case 2: return launch_scan<T, 16, 2>(a, s);
+    case 4: return launch_scan<T, 16, 4>(a, s);
+    case 8: return launch_scan<T, 16, 8>(a, s);
+  }
+  return (int)cudaErrorInvalidValue;
+}
+
+template <typename T, int LANES>
+int launch_one(const SsmArgs& a, cudaStream_t s) {
+  const int ch = kThreads / LANES, cb = (a.cfg.channels + ch - 1) / ch;
+  const auto at = [](const void* p, int64_t stride) {
+    return reinterpret_cast<uintptr_t>(p) % (4 * sizeof(T)) == 0 && stride % 4 == 0;
+  };
+  const bool aligned = at(a.rows.b, a.rows.b_stride) && at(a.rows.c, a.rows.c_stride) &&
+                       a.cfg.state_dim % 4 == 0;
+  ssm_step_kernel<T, LANES>
+      <<<(unsigned)((int64_t)a.req.num_tokens * cb), kThreads, 0, s>>>(a, cb, aligned);
+  return (int)cudaGetLastError();
+}
+template <typename T>
+int step_by_lanes(const SsmArgs& a, cudaStream_t s) {
+  const int n = a.cfg.state_dim;
+  if (n <= 4) return launch_one<T, 1>(a, s);
+  if (n <= 8) return launch_one<T, 2>(a, s);
+  if (n <= 16) return launch_one<T, 4>(a, s);
+  if (n <= 32) return launch_one<T, 8>(a, s);
+  if (n <= 64) return launch_one<T, 16>(a, s);
+  return launch_one<T, 32>(a, s);
+}
+
+}  // namespace
+
+// Warps that run side by side: those of a request's channels, times the requests that the rows
+// make up at their longest. Below kFew the GPU's 608 schedulers have too little to do.
+int32_t ssm_segment(const gdn_ssm_config& cfg, const gdn_requests& req) {
+  constexpr int64_t kFew = 1216, kWanted = 2432;
+  if (req.max_len < 1) return 0;
+  const int64_t warps = ((int64_t)cfg.channels * shape_of(cfg.state_dim).split + 31) / 32;
+  const int64_t side = std::max<int64_t>(1, std::min<int64_t>(req.num_seqs, req.num_tokens / req.max_len));
+  if (warps * side > kFew) return 0;
+  const int64_t pieces = std::min<int64_t>(32, kWanted / (warps * side));
+  const int64_t seg = std::max<int64_t>(128, ((int64_t)req.max_len + pieces - 1) / pieces + 31) / 32 * 32;
+  return req.max_len >= 2 * seg ? (int32_t)seg : 0;
+}
+
+int launch_ssm_packed(const SsmArgs& a, void* stream) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return a.cfg.io_dtype == GDN_BF16 ? scan_by_shape<__nv_bfloat16>(a, s) : scan_by_shape<float>(a, s);
+}
+
+int launch_ssm_step(const SsmArgs& a, void* stream) {
+  if (a.req.num_tokens == 0) return 0;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return a.cfg.io_dtype == GDN_BF16 ? step_by_lanes<__nv_bfloat16>(a, s) : step_by_lanes<float>(a, s);
+}
+
+}  // namespace gdn

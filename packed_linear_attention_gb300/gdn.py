@@ -39,6 +39,8 @@ GDN_ROPE_INTERLEAVED = 1
 GDN_ROPE_HALVES = 0
 GDN_ROPE_ADJACENT = 1
 GDN_ROPE_MAX_PAIRS = 128
+GDN_ACT_NONE = 0
+GDN_ACT_SILU = 1
 
 # every symbol include/gdn.h declares
 EXPORTS = (
@@ -55,6 +57,8 @@ EXPORTS = (
     "gdn_checkpoint_copy_join", "gdn_noalloc_read_status", "gdn_noalloc_set_test_hook",
     "gdn_split_segment_auto", "gdn_kv_plan", "gdn_kv_release", "gdn_rope_init",
     "gdn_rope_apply", "gdn_kv_append", "gdn_attn_workspace_size", "gdn_attn_paged",
+    "gdn_conv_packed", "gdn_conv_step", "gdn_ssm_workspace_size", "gdn_ssm_packed",
+    "gdn_ssm_step", "gdn_rms_norm", "gdn_sample",
 )
 
 
@@ -98,6 +102,40 @@ class gdn_attn_config(ctypes.Structure):
                 ("io_dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
+class gdn_requests(ctypes.Structure):
+    _fields_ = [("num_seqs", ctypes.c_int32), ("num_tokens", ctypes.c_int32),
+                ("max_len", ctypes.c_int32), ("num_slots", ctypes.c_int32),
+                ("cu", ctypes.c_void_p), ("slot_idx", ctypes.c_void_p),
+                ("start_zero", ctypes.c_void_p), ("ckpt_cu", ctypes.c_void_p),
+                ("ckpt_pos", ctypes.c_void_p), ("num_ckpt", ctypes.c_int32)]
+
+
+class gdn_conv_config(ctypes.Structure):
+    _fields_ = [("channels", ctypes.c_int32), ("width", ctypes.c_int32),
+                ("activation", ctypes.c_int32), ("io_dtype", ctypes.c_int32),
+                ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
+
+
+class gdn_ssm_config(ctypes.Structure):
+    _fields_ = [("channels", ctypes.c_int32), ("num_groups", ctypes.c_int32),
+                ("state_dim", ctypes.c_int32), ("io_dtype", ctypes.c_int32),
+                ("delta_softplus", ctypes.c_int32), ("a", ctypes.c_void_p),
+                ("d", ctypes.c_void_p), ("delta_bias", ctypes.c_void_p)]
+
+
+class gdn_ssm_rows(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in ("x", "delta", "b", "c", "z", "y")] + \
+        [(name, ctypes.c_int64) for name in ("x_stride", "delta_stride", "b_stride", "c_stride",
+                                             "z_stride", "y_stride")]
+
+
+class gdn_norm_config(ctypes.Structure):
+    _fields_ = [("num_heads", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("io_dtype", ctypes.c_int32), ("scale_group", ctypes.c_int32),
+                ("scale_pow2", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("weight_offset", ctypes.c_float), ("weight", ctypes.c_void_p)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -118,6 +156,9 @@ def load(path: str = LIB_PATH):
         I64 = ctypes.c_int64
         CACHE, ROPE = ctypes.POINTER(gdn_kv_cache), ctypes.POINTER(gdn_rope)
         ACFG = ctypes.POINTER(gdn_attn_config)
+        REQ, CONV = ctypes.POINTER(gdn_requests), ctypes.POINTER(gdn_conv_config)
+        SSM, SROWS = ctypes.POINTER(gdn_ssm_config), ctypes.POINTER(gdn_ssm_rows)
+        NORM = ctypes.POINTER(gdn_norm_config)
         sig = {
             "gdn_abi_version": (I32, []),
             "gdn_status_string": (ctypes.c_char_p, [I32]),
@@ -179,6 +220,14 @@ def load(path: str = LIB_PATH):
                                               ctypes.POINTER(SZ)]),
             "gdn_attn_paged": (I32, [P, ACFG, CACHE, I32, I32, I32, I32, P, P, P, I32, P, I64, P,
                                      I64, P, P, SZ, P, P]),
+            "gdn_conv_packed": (I32, [P, CONV, REQ, P, I64, P, I64, P, P, P, P]),
+            "gdn_conv_step": (I32, [P, CONV, I32, P, I64, P, I64, P, I32, P, P, P]),
+            "gdn_ssm_workspace_size": (I32, [SSM, REQ, ctypes.POINTER(SZ)]),
+            "gdn_ssm_packed": (I32, [P, SSM, REQ, SROWS, P, P, P, SZ, P, P]),
+            "gdn_ssm_step": (I32, [P, SSM, I32, SROWS, P, I32, P, P, P]),
+            "gdn_rms_norm": (I32, [P, NORM, I32, P, I64, P, I64, P, I64, P, I64, P, I64, P, I64, P,
+                                   P]),
+            "gdn_sample": (I32, [P, I32, I32, I32, P, I64, P, P, P, P, P, P, P, P, P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -697,6 +746,137 @@ def gdn_attn_paged(handle, cfg, cache, num_seqs, num_tokens, max_q_len, max_kv_l
         o_stride, _addr(lse), _addr(workspace), workspace_bytes, _addr(status), _stream(stream))
     if raise_on_error:
         _check(st, "gdn_attn_paged")
+    return st
+
+
+# ---- around the recurrent layers: convolution, selective scan, norm, sampling --------------
+
+def make_requests(cu, num_tokens, max_len, num_slots, *, slot_idx=None, start_zero=None,
+                  ckpt_cu=None, ckpt_pos=None, num_ckpt=0, num_seqs=None) -> gdn_requests:
+    """The requests of a packed call: device int32 tensors (num_seqs: by default those of cu),
+    which must outlive every call using the record."""
+    n = len(cu) - 1 if num_seqs is None else num_seqs
+    return gdn_requests(int(n), int(num_tokens), int(max_len), int(num_slots), _addr(cu),
+                        _addr(slot_idx), _addr(start_zero), _addr(ckpt_cu), _addr(ckpt_pos),
+                        int(num_ckpt))
+
+
+def make_conv_config(weight, bias=None, *, activation=GDN_ACT_SILU,
+                     io_dtype=GDN_BF16) -> gdn_conv_config:
+    """Convolution with fp32 device weights [channels, width] and biases; they must outlive every
+    call using the config."""
+    _floats(weight, 2, "weight")
+    _floats(bias, 1, "bias")
+    return gdn_conv_config(weight.shape[0], weight.shape[1], int(activation), int(io_dtype),
+                           _addr(weight), _addr(bias))
+
+
+def make_ssm_config(a, d=None, delta_bias=None, *, num_groups=1, delta_softplus=True,
+                    io_dtype=GDN_BF16) -> gdn_ssm_config:
+    """Selective scan with fp32 device rates a [channels, state_dim], skip weights d and biases of
+    delta; they must outlive every call using the config."""
+    _floats(a, 2, "a")
+    _floats(d, 1, "d")
+    _floats(delta_bias, 1, "delta_bias")
+    return gdn_ssm_config(a.shape[0], int(num_groups), a.shape[1], int(io_dtype),
+                          1 if delta_softplus else 0, _addr(a), _addr(d), _addr(delta_bias))
+
+
+def make_ssm_rows(x, delta, b, c, y, z=None) -> gdn_ssm_rows:
+    """The rows of a scan: 2-D device tensors (column ranges of wider ones are fine)."""
+    width = lambda t: 0 if t is None else t.stride(0)  # noqa: E731
+    return gdn_ssm_rows(_addr(x), _addr(delta), _addr(b), _addr(c), _addr(z), _addr(y), width(x),
+                        width(delta), width(b), width(c), width(z), width(y))
+
+
+def make_norm_config(dim, weight=None, *, num_heads=1, eps=1e-6, weight_offset=0.0, scale_group=0,
+                     scale_pow2=False, io_dtype=GDN_BF16) -> gdn_norm_config:
+    """Root-mean-square norm with fp32 device weights [dim]; they must outlive every call using
+    the config."""
+    _floats(weight, 1, "weight")
+    return gdn_norm_config(int(num_heads), int(dim), int(io_dtype), int(scale_group),
+                           1 if scale_pow2 else 0, float(eps), float(weight_offset), _addr(weight))
+
+
+def _floats(t, dims, name):
+    """fp32 weights lie as the library reads them (raw addresses are taken as they are)."""
+    if t is not None and not isinstance(t, int) and \
+            (str(t.dtype) != "torch.float32" or t.dim() != dims or not t.is_contiguous()):
+        raise ValueError(f"{name}: a contiguous float32 tensor of {dims} dimensions is needed")
+
+
+def gdn_conv_packed(handle, cfg, requests, x, x_stride, y, y_stride, state_pool, ckpt_states=None,
+                    status=None, stream=None, *, raise_on_error=True) -> int:
+    """Short causal convolution of a pack of requests, states in pool slots."""
+    st = load().gdn_conv_packed(handle, _ref(cfg), _ref(requests), _addr(x), x_stride, _addr(y),
+                                y_stride, _addr(state_pool), _addr(ckpt_states), _addr(status),
+                                _stream(stream))
+    if raise_on_error:
+        _check(st, "gdn_conv_packed")
+    return st
+
+
+def gdn_conv_step(handle, cfg, batch, x, x_stride, y, y_stride, state_pool, num_slots, slot_idx,
+                  status=None, stream=None, *, raise_on_error=True) -> int:
+    """One token of `batch` requests through the convolution."""
+    st = load().gdn_conv_step(handle, _ref(cfg), batch, _addr(x), x_stride, _addr(y), y_stride,
+                              _addr(state_pool), num_slots, _addr(slot_idx), _addr(status),
+                              _stream(stream))
+    if raise_on_error:
+        _check(st, "gdn_conv_step")
+    return st
+
+
+def gdn_ssm_workspace_size(cfg, requests) -> int:
+    n = ctypes.c_size_t()
+    _check(load().gdn_ssm_workspace_size(_ref(cfg), _ref(requests), ctypes.byref(n)),
+           "gdn_ssm_workspace_size")
+    return n.value
+
+
+def gdn_ssm_packed(handle, cfg, requests, rows, state_pool, ckpt_states, workspace,
+                   workspace_bytes, status=None, stream=None, *, raise_on_error=True) -> int:
+    """Selective scan of a pack of requests, states in pool slots."""
+    st = load().gdn_ssm_packed(handle, _ref(cfg), _ref(requests), _ref(rows), _addr(state_pool),
+                               _addr(ckpt_states), _addr(workspace), workspace_bytes,
+                               _addr(status), _stream(stream))
+    if raise_on_error:
+        _check(st, "gdn_ssm_packed")
+    return st
+
+
+def gdn_ssm_step(handle, cfg, batch, rows, state_pool, num_slots, slot_idx, status=None,
+                 stream=None, *, raise_on_error=True) -> int:
+    """One token of `batch` requests through the selective scan."""
+    st = load().gdn_ssm_step(handle, _ref(cfg), batch, _ref(rows), _addr(state_pool), num_slots,
+                             _addr(slot_idx), _addr(status), _stream(stream))
+    if raise_on_error:
+        _check(st, "gdn_ssm_step")
+    return st
+
+
+def gdn_rms_norm(handle, cfg, num_tokens, x, x_stride, residual=None, residual_stride=0, sum=None,
+                 sum_stride=0, gate=None, gate_stride=0, y=None, y_stride=0, codes=None,
+                 codes_stride=0, scales=None, stream=None, *, raise_on_error=True) -> int:
+    """RMS norm of rows, with residual, gate and an 8-bit output where given."""
+    st = load().gdn_rms_norm(handle, _ref(cfg), num_tokens, _addr(x), x_stride, _addr(residual),
+                             residual_stride, _addr(sum), sum_stride, _addr(gate), gate_stride,
+                             _addr(y), y_stride, _addr(codes), codes_stride, _addr(scales),
+                             _stream(stream))
+    if raise_on_error:
+        _check(st, "gdn_rms_norm")
+    return st
+
+
+def gdn_sample(handle, io_dtype, num_rows, vocab, logits, row_stride, temperature, top_k, top_p, min_p,
+               u, token, logprob=None, status=None, stream=None, *,
+               raise_on_error=True) -> int:
+    """Draw a token from every row of logits; `row_stride` in elements from row to row."""
+    st = load().gdn_sample(handle, io_dtype, num_rows, vocab, _addr(logits), row_stride,
+                           _addr(temperature), _addr(top_k), _addr(top_p), _addr(min_p), _addr(u),
+                           _addr(token), _addr(logprob), _addr(status), _stream(stream))
+    if raise_on_error:
+        _check(st, "gdn_sample")
     return st
 
 
