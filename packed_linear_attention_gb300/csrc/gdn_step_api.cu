@@ -272,9 +272,7 @@ gdn_status gdn_rms_norm(gdn_handle* h, const gdn_norm_config* cfg, int32_t num_t
   if (group > 0 && d % group != 0) return GDN_ERR_INVALID_ARGUMENT;
   if ((codes == nullptr) != (scales == nullptr) || (!y && !codes) || (sum && !residual))
     return GDN_ERR_INVALID_ARGUMENT;
-  if ((group != 0 && group != 32 && group != 64 && group != 128) ||
-      (heads > 1 && d != 64 && d != 128 && d != 256) || row > gdn::kMaxNormRow)
-    return GDN_ERR_UNSUPPORTED;
+  if (row > INT32_MAX) return GDN_ERR_UNSUPPORTED;
   if (num_tokens > 0) {
     const size_t e = item_size(cfg->io_dtype);
     const int32_t io = cfg->io_dtype, n = (int32_t)row;
@@ -309,6 +307,9 @@ gdn_status gdn_rms_norm(gdn_handle* h, const gdn_norm_config* cfg, int32_t num_t
       }
     }
   }
+  if ((group != 0 && group != 32 && group != 64 && group != 128) ||
+      (heads > 1 && d != 64 && d != 128 && d != 256) || row > gdn::kMaxNormRow)
+    return GDN_ERR_UNSUPPORTED;
   if (!h) return GDN_ERR_INVALID_ARGUMENT;
   const gdn::NormArgs a = {*cfg, num_tokens, x, residual, gate, sum, y, codes, x_stride,
                            residual_stride, gate_stride, sum_stride, y_stride, codes_stride, scales};

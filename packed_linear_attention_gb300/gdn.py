@@ -754,48 +754,58 @@ def gdn_attn_paged(handle, cfg, cache, num_seqs, num_tokens, max_q_len, max_kv_l
 def make_requests(cu, num_tokens, max_len, num_slots, *, slot_idx=None, start_zero=None,
                   ckpt_cu=None, ckpt_pos=None, num_ckpt=0, num_seqs=None) -> gdn_requests:
     """The requests of a packed call: device int32 tensors (num_seqs: by default those of cu),
-    which must outlive every call using the record."""
+    which the record keeps alive."""
     n = len(cu) - 1 if num_seqs is None else num_seqs
-    return gdn_requests(int(n), int(num_tokens), int(max_len), int(num_slots), _addr(cu),
-                        _addr(slot_idx), _addr(start_zero), _addr(ckpt_cu), _addr(ckpt_pos),
-                        int(num_ckpt))
+    r = gdn_requests(int(n), int(num_tokens), int(max_len), int(num_slots), _addr(cu),
+                     _addr(slot_idx), _addr(start_zero), _addr(ckpt_cu), _addr(ckpt_pos),
+                     int(num_ckpt))
+    r.tensors = (cu, slot_idx, start_zero, ckpt_cu, ckpt_pos)
+    return r
 
 
 def make_conv_config(weight, bias=None, *, activation=GDN_ACT_SILU,
                      io_dtype=GDN_BF16) -> gdn_conv_config:
-    """Convolution with fp32 device weights [channels, width] and biases; they must outlive every
-    call using the config."""
+    """Convolution with fp32 device weights [channels, width] and biases, which the config keeps
+    alive."""
     _floats(weight, 2, "weight")
     _floats(bias, 1, "bias")
-    return gdn_conv_config(weight.shape[0], weight.shape[1], int(activation), int(io_dtype),
-                           _addr(weight), _addr(bias))
+    cfg = gdn_conv_config(weight.shape[0], weight.shape[1], int(activation), int(io_dtype),
+                          _addr(weight), _addr(bias))
+    cfg.tensors = (weight, bias)
+    return cfg
 
 
 def make_ssm_config(a, d=None, delta_bias=None, *, num_groups=1, delta_softplus=True,
                     io_dtype=GDN_BF16) -> gdn_ssm_config:
     """Selective scan with fp32 device rates a [channels, state_dim], skip weights d and biases of
-    delta; they must outlive every call using the config."""
+    delta, which the config keeps alive."""
     _floats(a, 2, "a")
     _floats(d, 1, "d")
     _floats(delta_bias, 1, "delta_bias")
-    return gdn_ssm_config(a.shape[0], int(num_groups), a.shape[1], int(io_dtype),
-                          1 if delta_softplus else 0, _addr(a), _addr(d), _addr(delta_bias))
+    cfg = gdn_ssm_config(a.shape[0], int(num_groups), a.shape[1], int(io_dtype),
+                         1 if delta_softplus else 0, _addr(a), _addr(d), _addr(delta_bias))
+    cfg.tensors = (a, d, delta_bias)
+    return cfg
 
 
 def make_ssm_rows(x, delta, b, c, y, z=None) -> gdn_ssm_rows:
-    """The rows of a scan: 2-D device tensors (column ranges of wider ones are fine)."""
+    """The rows of a scan: 2-D device tensors (column ranges of wider ones are fine), which the
+    record keeps alive."""
     width = lambda t: 0 if t is None else t.stride(0)  # noqa: E731
-    return gdn_ssm_rows(_addr(x), _addr(delta), _addr(b), _addr(c), _addr(z), _addr(y), width(x),
-                        width(delta), width(b), width(c), width(z), width(y))
+    r = gdn_ssm_rows(_addr(x), _addr(delta), _addr(b), _addr(c), _addr(z), _addr(y), width(x),
+                     width(delta), width(b), width(c), width(z), width(y))
+    r.tensors = (x, delta, b, c, z, y)
+    return r
 
 
 def make_norm_config(dim, weight=None, *, num_heads=1, eps=1e-6, weight_offset=0.0, scale_group=0,
                      scale_pow2=False, io_dtype=GDN_BF16) -> gdn_norm_config:
-    """Root-mean-square norm with fp32 device weights [dim]; they must outlive every call using
-    the config."""
+    """Root-mean-square norm with fp32 device weights [dim], which the config keeps alive."""
     _floats(weight, 1, "weight")
-    return gdn_norm_config(int(num_heads), int(dim), int(io_dtype), int(scale_group),
-                           1 if scale_pow2 else 0, float(eps), float(weight_offset), _addr(weight))
+    cfg = gdn_norm_config(int(num_heads), int(dim), int(io_dtype), int(scale_group),
+                          1 if scale_pow2 else 0, float(eps), float(weight_offset), _addr(weight))
+    cfg.tensors = (weight,)
+    return cfg
 
 
 def _floats(t, dims, name):
