@@ -6,9 +6,14 @@
 //
 // Channels are independent and their states short, so a thread owns a channel (or SPLIT lanes
 // share one, NS states each), keeps its states and decay rates in registers and walks down the
-// rows. b and c are the same for all channels of a group: a block stages them in shared memory,
-// kTile rows at a time. exp is one multiplication (the rates are held times log2 e) and one
-// ex2; the rest are fused multiply-adds on pairs of states (f32x2).
+// rows. exp is one multiplication (the rates are held times log2 e) and one ex2; the rest are fused
+// multiply-adds on pairs of states (f32x2).
+//
+// A block takes kCh channels of one request, kTile rows at a time, in two turns. In the first its
+// threads share out the tile 8 elements each, 16-byte accesses side by side: dt and dt x go to shared
+// memory, and what the last tile's scan left there is gated and stored; b and c, the same for all
+// channels of a group, are widened to fp32. In the second every thread scans its channel from shared
+// memory, at offsets known when compiled: what it costs is its 16 states, not their addresses.
 #include <algorithm>
 #include <climits>
 
@@ -18,7 +23,6 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kAhead = 4;  // rows whose x, delta and z are loaded ahead
 constexpr float kLog2e = 1.4426950408889634f;
 
 using f32x2 = unsigned long long;  // two fp32 in a register pair
@@ -40,6 +44,11 @@ __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -51,22 +60,45 @@ __device__ __forceinline__ f32x2 ex2(f32x2 x) {
   return pair(ex2(lo), ex2(hi));
 }
 
-// log(1 + exp(x)) = max(x, 0) + log1p(e), e = exp(-|x|) in (0, 1], and with s = e / (2 + e),
-// log1p(e) = 2 atanh(s) = 2 s (1 + s^2/3 + s^4/5 + ...): s^2 <= 1/9, so seven terms leave 2e-8 of
-// it, and small values keep their relative precision.
-__device__ __forceinline__ float softplus(float x) {
-  const float e = ex2(-kLog2e * fabsf(x));
-  const float s = __fdividef(e, 2.f + e), q = s * s;
-  float p = fmaf(q, 1.f / 13.f, 1.f / 11.f);
-  p = fmaf(q, p, 1.f / 9.f);
-  p = fmaf(q, p, 1.f / 7.f);
-  p = fmaf(q, p, 1.f / 5.f);
-  p = fmaf(q, p, 1.f / 3.f);
-  p = fmaf(q, p, 1.f);
-  return fmaf(2.f * s, p, fmaxf(x, 0.f));
+// exp of dt times a rate (held times log2 e). Just below 0 the ex2 instruction errs low by 2e-8 on
+// average, which slow decays would sum up; 3e-8 in its argument leaves 5e-9 (and 2^0 at 1).
+constexpr float kNudge = 3e-8f;
+__device__ __forceinline__ f32x2 decay(f32x2 dt, f32x2 a) {
+  return ex2(fma2(dt, a, pair(kNudge, kNudge)));
+}
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
-constexpr int tile_rows(int padded) { return padded <= 32 ? 32 : 16; }
+// log(1 + exp(x)) = max(x, 0) + log1p(e), e = exp(-|x|) in (0, 1]. log1p(e) is e times a polynomial
+// fitted to log1p(e) / e (least squares, reweighted towards an even relative error, 3e-8), so that
+// small values keep their relative precision.
+__device__ constexpr float kLog1p[9] = {0.99999994f,  -0.49999493f, 0.33319095f,   -0.24842976f, 0.1910598f,
+                             -0.13663195f, 0.07822535f,  -0.029504869f, 0.0052326024f};
+__device__ __forceinline__ f32x2 both(float v) { return pair(v, v); }
+__device__ __forceinline__ f32x2 softplus(f32x2 x) {
+  float x0, x1;
+  unpair(x, x0, x1);
+  const f32x2 e = pair(ex2(-kLog2e * fabsf(x0)), ex2(-kLog2e * fabsf(x1)));
+  f32x2 p = both(kLog1p[8]);
+#pragma unroll
+  for (int i = 7; i >= 0; --i) p = fma2(e, p, both(kLog1p[i]));
+  return fma2(e, p, pair(fmaxf(x0, 0.f), fmaxf(x1, 0.f)));
+}
+__device__ __forceinline__ float softplus(float x) {
+  float a, b;
+  unpair(softplus(pair(x, x)), a, b);
+  return a;
+}
+// v / (1 + exp(-v)); past 2^126 the reciprocal is 0, and so is the result to 1e-36
+__device__ __forceinline__ float gate(float v) { return v * rcp(1.f + ex2(-kLog2e * v)); }
+__device__ __forceinline__ f32x2 gate(f32x2 v) {
+  float a, b;
+  unpair(add2(ex2(mul2(v, both(-kLog2e))), both(1.f)), a, b);
+  return mul2(v, pair(rcp(a), rcp(b)));
+}
 
 // The states of one thread: NS of channel c, chunks of four that the SPLIT lanes take in turn
 // (so that the lanes' reads of b and c in shared memory lie side by side).
@@ -137,18 +169,17 @@ struct States {
 #pragma unroll
     for (int i = 0; i < NS / 4; ++i) {
       const ulonglong2 bv = *reinterpret_cast<const ulonglong2*>(b + chunk(i, part));
-      h[2 * i] = fma2(ex2(mul2(t, a[2 * i])), h[2 * i], mul2(u, bv.x));
-      h[2 * i + 1] = fma2(ex2(mul2(t, a[2 * i + 1])), h[2 * i + 1], mul2(u, bv.y));
+      h[2 * i] = fma2(decay(t, a[2 * i]), h[2 * i], mul2(u, bv.x));
+      h[2 * i + 1] = fma2(decay(t, a[2 * i + 1]), h[2 * i + 1], mul2(u, bv.y));
       if (OUT) {
         const ulonglong2 cv = *reinterpret_cast<const ulonglong2*>(c + chunk(i, part));
-        acc[0] = fma2(cv.x, h[2 * i], acc[0]);
-        acc[1] = fma2(cv.y, h[2 * i + 1], acc[1]);
+        acc[0] = i == 0 ? mul2(cv.x, h[0]) : fma2(cv.x, h[2 * i], acc[0]);
+        acc[1] = i == 0 ? mul2(cv.y, h[1]) : fma2(cv.y, h[2 * i + 1], acc[1]);
       }
     }
-    float s0, s1, s2, s3;
-    unpair(acc[0], s0, s1);
-    unpair(acc[1], s2, s3);
-    return (s0 + s1) + (s2 + s3);
+    float lo, hi;
+    unpair(add2(acc[0], acc[1]), lo, hi);
+    return lo + hi;
   }
 };
 
@@ -160,63 +191,109 @@ struct Span {
 template <typename T, int NS, int SPLIT>
 struct Scan {
   static constexpr int kPadded = NS * SPLIT;
-  static constexpr int kTile = tile_rows(kPadded);
-  static constexpr int kChannels = kThreads / SPLIT;
+  static constexpr int kCh = kThreads / SPLIT;
+  // a tile of 8 elements a thread, while b and c stay within 16 KB
+  static constexpr int kTile = SPLIT == 8 ? 16 : 8 * SPLIT;
+  static constexpr int kTasks = kTile * kCh / 8;
+  static constexpr int kVecs = 8 / Vec<T>::N;
+  static constexpr int kShare = (kTile * kPadded + kThreads - 1) / kThreads;  // of b and of c
+  static constexpr bool kAhead = kShare <= 4;
   struct Shared {
-    float b[2][kTile][kPadded], c[2][kTile][kPadded];
+    float4 f[kTile][kCh / 2];  // dt and dt x of two channels, at pair_at
+    float4 y[kTile][kCh / 4];  // at quad_at
+    float b[kTile][kPadded], c[kTile][kPadded];
+    float4 bias[kCh / 4], skip[kCh / 4];  // at quad_at
+    uint4 x[kVecs][kTasks], z[kVecs][kTasks];  // of the rows being scanned
+  };
+  // Where 16 bytes of a row lie, so that neither the 8 channels of a thread's share nor the channels
+  // of a warp's lanes meet in a bank: chunk q of pairs, chunk q of fours.
+  __device__ __forceinline__ static int pair_at(int q) { return q ^ ((q >> 3) & 3); }
+  __device__ __forceinline__ static int quad_at(int q) { return q ^ ((q >> 3) & 1); }
+
+  struct Eight {
+    Vec<T> v[kVecs];
+    __device__ __forceinline__ void load(const T* p, int count, bool whole) {
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i)
+        v[i] = load_vec(p + i * Vec<T>::N, count - i * Vec<T>::N, whole);
+    }
+    __device__ __forceinline__ void values(float* f) const {
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) unpack(v[i], f + i * Vec<T>::N);
+    }
   };
 
   const SsmArgs& p;
   Shared& sm;
-  int group, channel, part;
+  int group, channel, part, local;
+  int my_f, my_y;  // this thread's channel in a row of f and of y
   bool live;
+  // this thread's share of a tile: 8 channels of a row
+  int task_row, task_col, task_channel, count;
+  bool whole;
   States<NS, SPLIT> s;
-  float skip, bias, total = 0.f;
+  float total = 0.f;
 
   __device__ __forceinline__ Scan(const SsmArgs& args, Shared& shared, int block)
       : p(args), sm(shared) {
     const int per = p.cfg.channels / p.cfg.num_groups;
-    const int tiles = (per + kChannels - 1) / kChannels;
+    const int tiles = (per + kCh - 1) / kCh;
     group = block / tiles;
-    const int c = block % tiles * kChannels + (int)threadIdx.x / SPLIT;
-    live = c < per;
-    channel = group * per + min(c, per - 1);
+    const int first = block % tiles * kCh;  // of the group
+    local = threadIdx.x / SPLIT;
     part = threadIdx.x % SPLIT;
+    live = first + local < per;
+    channel = group * per + min(first + local, per - 1);
+    task_row = threadIdx.x / (kCh / 8);
+    task_col = threadIdx.x % (kCh / 8) * 8;
+    task_channel = group * per + first + task_col;
+    count = threadIdx.x < kTasks ? max(0, min(8, per - first - task_col)) : 0;
+    whole = count == 8 && (p.cfg.num_groups == 1 || per % Vec<T>::N == 0);
     s.rates(p.cfg.a + (size_t)channel * p.cfg.state_dim, part, p.cfg.state_dim);
-    skip = p.cfg.d ? __ldg(p.cfg.d + channel) : 0.f;
-    bias = p.cfg.delta_bias ? __ldg(p.cfg.delta_bias + channel) : 0.f;
+    my_f = 2 * pair_at(local / 2) + local % 2;
+    my_y = 4 * quad_at(local / 4) + local % 4;
+    if (part == 0) {
+      reinterpret_cast<float*>(sm.bias)[my_y] = p.cfg.delta_bias ? __ldg(p.cfg.delta_bias + channel) : 0.f;
+      reinterpret_cast<float*>(sm.skip)[my_y] = p.cfg.d ? __ldg(p.cfg.d + channel) : 0.f;
+    }
   }
 
   __device__ __forceinline__ size_t state_row(int64_t slot) const {
     return ((size_t)slot * p.cfg.channels + channel) * p.cfg.state_dim;
   }
 
-  // b and c of rows [row, row + kTile) into buffer `buf`; zeros past the states and the rows
-  __device__ __forceinline__ void stage(int64_t row, int rows, int buf) {
+  // b and c of rows [row, row + kTile) on their way to a buffer; zeros past the states and the rows
+  struct Shares {
+    T b[kShare], c[kShare];
+  };
+  __device__ __forceinline__ void load_bc(Shares& w, int64_t row, int rows) {
     const int n = p.cfg.state_dim;
     const T* b = static_cast<const T*>(p.rows.b) + row * p.rows.b_stride + (size_t)group * n;
     const T* c = static_cast<const T*>(p.rows.c) + row * p.rows.c_stride + (size_t)group * n;
 #pragma unroll
-    for (int i = 0; i < kTile * kPadded / kThreads; ++i) {
+    for (int i = 0; i < kShare; ++i) {
       const int at = i * kThreads + threadIdx.x, t = at / kPadded, k = at % kPadded;
       const bool in = t < rows && k < n;
-      sm.b[buf][t][k] = in ? to_f32(b[(size_t)t * p.rows.b_stride + k]) : 0.f;
-      sm.c[buf][t][k] = in ? to_f32(c[(size_t)t * p.rows.c_stride + k]) : 0.f;
+      w.b[i] = in ? b[(size_t)t * p.rows.b_stride + k] : from_f32<T>(0.f);
+      w.c[i] = in ? c[(size_t)t * p.rows.c_stride + k] : from_f32<T>(0.f);
+    }
+  }
+  __device__ __forceinline__ void store_bc(const Shares& w) {
+#pragma unroll
+    for (int i = 0; i < kShare; ++i) {
+      const int at = i * kThreads + threadIdx.x;
+      if (kTile * kPadded % kThreads == 0 || at < kTile * kPadded) {
+        (&sm.b[0][0])[at] = to_f32(w.b[i]);
+        (&sm.c[0][0])[at] = to_f32(w.c[i]);
+      }
     }
   }
 
   // The rows of `span`, from the states in s. OUT: y and the checkpoints; else the sum of dt.
   template <bool OUT>
   __device__ __forceinline__ void run(const Span& span, bool report) {
-    const T* x = static_cast<const T*>(p.rows.x) + (size_t)span.lo * p.rows.x_stride + channel;
-    const T* delta =
-        static_cast<const T*>(p.rows.delta) + (size_t)span.lo * p.rows.delta_stride + channel;
-    const T* z = p.rows.z
-                     ? static_cast<const T*>(p.rows.z) + (size_t)span.lo * p.rows.z_stride + channel
-                     : nullptr;
-    T* y = static_cast<T*>(p.rows.y) + (size_t)span.lo * p.rows.y_stride + channel;
     const int len = span.len;
-
+    const bool gated = OUT && p.rows.z;
     // the first checkpoint past the rows in front (rows counted from span.lo from here on)
     int2 ck = make_int2(0, 0);
     int mark = INT_MAX, before = 0;
@@ -240,77 +317,138 @@ struct Scan {
       next_mark();
     }
 
-    T xr[kAhead], dr[kAhead], zr[kAhead];
-    auto fetch = [&](int t) {
+    // Addresses are worked out anew for each tile: registers are what is short while it is scanned.
+    auto row_of = [&](const void* base, int64_t stride, int t0) {
+      int row = task_row;
+      asm volatile("" : "+r"(row));
+      return static_cast<const T*>(base) + (int64_t)(span.lo + t0 + row) * stride + task_channel;
+    };
+    Eight xn, dn, zn;  // the next tile's rows
+    auto fetch = [&](int t0) {
+      if (t0 + task_row < len && count > 0) {
+        xn.load(row_of(p.rows.x, p.rows.x_stride, t0), count, whole);
+        dn.load(row_of(p.rows.delta, p.rows.delta_stride, t0), count, whole);
+        if (gated) zn.load(row_of(p.rows.z, p.rows.z_stride, t0), count, whole);
+      }
+    };
+    // this thread's 8 channels in a row of fours, as pairs
+    auto quads = [&](const float4* row, f32x2* f) {
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        if (t + i < len) {
-          xr[i] = x[(size_t)(t + i) * p.rows.x_stride];
-          dr[i] = delta[(size_t)(t + i) * p.rows.delta_stride];
-          if (OUT && z) zr[i] = z[(size_t)(t + i) * p.rows.z_stride];
+      for (int i = 0; i < 2; ++i) {
+        const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(&row[quad_at(task_col / 4 + i)]);
+        f[2 * i] = v.x;
+        f[2 * i + 1] = v.y;
+      }
+    };
+    // dt and dt x of this thread's share
+    auto prepare = [&] {
+      float xf[8], df[8];
+      f32x2 bias[4];
+      xn.values(xf);
+      dn.values(df);
+      quads(sm.bias, bias);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f32x2 dt = add2(pair(df[2 * i], df[2 * i + 1]), bias[i]);
+        if (p.cfg.delta_softplus) dt = softplus(dt);
+        float4 f;
+        unpair(dt, f.x, f.z);
+        unpair(mul2(dt, pair(xf[2 * i], xf[2 * i + 1])), f.y, f.w);
+        sm.f[task_row][pair_at(task_col / 2 + i)] = f;
+      }
+      if (OUT) {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+          sm.x[i][threadIdx.x] = xn.v[i].raw;
+          if (gated) sm.z[i][threadIdx.x] = zn.v[i].raw;
         }
       }
     };
-    const bool soft = p.cfg.delta_softplus != 0;
-    auto one = [&](int t, int buf, int row, T xv, T dv, T zv) {
-      const float xf = to_f32(xv);
-      float dt = to_f32(dv) + bias;
-      if (soft) dt = softplus(dt);
-      if (!OUT) total += dt;
-      float sum = s.template step<OUT>(dt, dt * xf, sm.b[buf][row], sm.c[buf][row], part);
+    auto finish = [&](int t0) {
+      if (t0 + task_row >= len || count <= 0) return;
+      float f[8], out[8];
+      f32x2 skip[4], sum[4];
+      Eight h;
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) h.v[i].raw = sm.x[i][threadIdx.x];
+      h.values(f);
+      quads(sm.skip, skip);
+      quads(sm.y[task_row], sum);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[i] = fma2(skip[i], pair(f[2 * i], f[2 * i + 1]), sum[i]);
+      if (gated) {
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) h.v[i].raw = sm.z[i][threadIdx.x];
+        h.values(f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[i] = mul2(sum[i], gate(pair(f[2 * i], f[2 * i + 1])));
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) unpair(sum[i], out[2 * i], out[2 * i + 1]);
+      T* y = const_cast<T*>(row_of(p.rows.y, p.rows.y_stride, t0));
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i)
+        store_vec(y + i * Vec<T>::N, pack<T>(out + i * Vec<T>::N), count - i * Vec<T>::N, whole);
+    };
+    auto one = [&](int r) {
+      const float2 f = reinterpret_cast<const float2*>(sm.f[r])[my_f];
+      if (!OUT) total += f.x;
+      float sum = s.template step<OUT>(f.x, f.y, sm.b[r], sm.c[r], part);
       if (OUT) {
 #pragma unroll
         for (int off = SPLIT / 2; off > 0; off >>= 1)
           sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        sum = fmaf(skip, xf, sum);
-        if (z) sum *= silu(to_f32(zv));
-        if (live && part == 0) y[(size_t)t * p.rows.y_stride] = from_f32<T>(sum);
+        if (part == 0) reinterpret_cast<float*>(sm.y[r])[my_y] = sum;
       }
     };
+
+    Shares w;  // the next tile's b and c, where a thread's share of them is small
+    if (kAhead) load_bc(w, span.lo, min(len, kTile));
     fetch(0);
-    stage(span.lo, min(len, kTile), 0);
-    __syncthreads();
-    for (int t0 = 0, buf = 0; t0 < len; t0 += kTile, buf ^= 1) {
-      if (t0 + kTile < len) stage(span.lo + t0 + kTile, min(len - t0 - kTile, kTile), buf ^ 1);
+    __syncthreads();  // bias and skip
+    for (int t0 = 0; t0 < len; t0 += kTile) {
+      const bool more = t0 + kTile < len;
+      if (!kAhead) load_bc(w, span.lo + t0, min(len - t0, kTile));
+      if (OUT && t0 > 0) finish(t0 - kTile);
+      if (t0 + task_row < len && count > 0) prepare();
+      store_bc(w);
+      if (more) {
+        fetch(t0 + kTile);
+        if (kAhead) load_bc(w, span.lo + t0 + kTile, min(len - t0 - kTile, kTile));
+      }
+      __syncthreads();
       const int rows = min(len - t0, kTile);
-      for (int r = 0; r < rows; r += kAhead) {
-        T xv[kAhead], dv[kAhead], zv[kAhead];
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-          xv[i] = xr[i];
-          dv[i] = dr[i];
-          zv[i] = zr[i];
-        }
-        const int t = t0 + r;
-        fetch(t + kAhead);
-        if (r + kAhead <= rows && (!OUT || mark > t + kAhead)) {
-#pragma unroll
-          for (int i = 0; i < kAhead; ++i) one(t + i, buf, r + i, xv[i], dv[i], zv[i]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < kAhead; ++i) {
-            if (r + i < rows) {
-              one(t + i, buf, r + i, xv[i], dv[i], zv[i]);
-              if (OUT && mark == t + i + 1) {
-                if (live) s.store(p.ckpt + state_row(ck.x), part, p.cfg.state_dim);
-                ++ck.x;
-                next_mark();
-              }
-            }
+      if (rows == kTile && (!OUT || mark > t0 + kTile)) {
+#pragma unroll 8
+        for (int r = 0; r < kTile; ++r) one(r);
+      } else {
+        for (int r = 0; r < rows; ++r) {
+          one(r);
+          if (OUT && mark == t0 + r + 1) {
+            if (live) s.store(p.ckpt + state_row(ck.x), part, p.cfg.state_dim);
+            ++ck.x;
+            next_mark();
           }
         }
       }
       __syncthreads();
     }
+    if (OUT && len > 0) finish((len - 1) / kTile * kTile);
   }
 };
+
+// Blocks of an SM: 128 registers a thread hold 16 states, their rates and the next rows without
+// spilling. At 96 (five blocks) a wave of 32 x 1,024 x 4,096 channels takes 648 us against 620; fp32
+// rows and wide shares of b and c want more.
+template <typename T, int SPLIT>
+constexpr int kResident = sizeof(T) == 2 && SPLIT < 4 ? 4 : 3;
 
 // pass 0: whole requests, a unit each. With requests cut into segments, pass 1 runs every
 // request's first segment and finds the end states of its middle ones from zeros; pass 2 joins
 // them and runs the segments behind the first. exp(a dt_1) ... exp(a dt_k) is exp(a sum dt), so a
 // segment's decay needs only its sum of dt.
 template <typename T, int NS, int SPLIT>
-__global__ void __launch_bounds__(kThreads) ssm_kernel(SsmArgs p, int channel_blocks, int pass) {
+__global__ void __launch_bounds__(kThreads, kResident<T, SPLIT>) ssm_kernel(SsmArgs p, int channel_blocks, int pass) {
   using S = Scan<T, NS, SPLIT>;
   __shared__ __align__(16) typename S::Shared sm;
   const int unit = blockIdx.x / channel_blocks;
@@ -359,7 +497,7 @@ __global__ void __launch_bounds__(kThreads) ssm_kernel(SsmArgs p, int channel_bl
       const float dt = p.steps[(ends + j) * p.cfg.channels + scan.channel];
 #pragma unroll
       for (int i = 0; i < NS / 2; ++i)
-        scan.s.h[i] = fma2(ex2(mul2(pair(dt, dt), scan.s.a[i])), scan.s.h[i], end.h[i]);
+        scan.s.h[i] = fma2(decay(pair(dt, dt), scan.s.a[i]), scan.s.h[i], end.h[i]);
     }
   }
   const bool report = blockIdx.x % channel_blocks == 0 && threadIdx.x == 0;
@@ -420,11 +558,11 @@ __global__ void __launch_bounds__(kThreads) ssm_step_kernel(SsmArgs p, int chann
   float dt = to_f32(static_cast<const T*>(p.rows.delta)[(size_t)row * p.rows.delta_stride + ch]);
   if (p.cfg.delta_bias) dt += __ldg(p.cfg.delta_bias + ch);
   if (p.cfg.delta_softplus) dt = softplus(dt);
-  const float t = kLog2e * dt, dtx = dt * x;
-  h.x = fmaf(ex2(t * a.x), h.x, dtx * b.x);
-  h.y = fmaf(ex2(t * a.y), h.y, dtx * b.y);
-  h.z = fmaf(ex2(t * a.z), h.z, dtx * b.z);
-  h.w = fmaf(ex2(t * a.w), h.w, dtx * b.w);
+  const float dtx = dt * x;
+  h.x = fmaf(ex2(fmaf(dt, kLog2e * a.x, kNudge)), h.x, dtx * b.x);
+  h.y = fmaf(ex2(fmaf(dt, kLog2e * a.y, kNudge)), h.y, dtx * b.y);
+  h.z = fmaf(ex2(fmaf(dt, kLog2e * a.z, kNudge)), h.z, dtx * b.z);
+  h.w = fmaf(ex2(fmaf(dt, kLog2e * a.w, kNudge)), h.w, dtx * b.w);
   float sum = fmaf(cc.x, h.x, cc.y * h.y) + fmaf(cc.z, h.z, cc.w * h.w);
 #pragma unroll
   for (int off = LANES / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
@@ -440,21 +578,30 @@ __global__ void __launch_bounds__(kThreads) ssm_step_kernel(SsmArgs p, int chann
   if (part == 0) {
     if (p.cfg.d) sum = fmaf(__ldg(p.cfg.d + ch), x, sum);
     if (p.rows.z)
-      sum *= silu(to_f32(static_cast<const T*>(p.rows.z)[(size_t)row * p.rows.z_stride + ch]));
+      sum *= gate(to_f32(static_cast<const T*>(p.rows.z)[(size_t)row * p.rows.z_stride + ch]));
     static_cast<T*>(p.rows.y)[(size_t)row * p.rows.y_stride + ch] = from_f32<T>(sum);
   }
 }
 
-// states of a thread and lanes of a channel
+// States of a thread and lanes of a channel. 16 states a thread cost the least in all; 8 are done
+// sooner where the GPU's 608 schedulers have less than four warps each (a prompt of 4,096 rows and
+// 4,096 channels: 542 against 704 us; a wave, which has seven: 710 against 620).
 struct Shape {
   int ns, split;
 };
+constexpr int64_t kSchedulers = 608;
 Shape shape_of(int n) {
   if (n <= 4) return {4, 1};
   if (n <= 8) return {8, 1};
   int split = 1;
   while (16 * split < n) split *= 2;
   return {16, split};
+}
+// Warps that run side by side: those of a request's channels, times the requests that the rows
+// make up at their longest.
+int64_t warps_of(const gdn_ssm_config& cfg, const gdn_requests& req) {
+  const int64_t warps = ((int64_t)cfg.channels * shape_of(cfg.state_dim).split + 31) / 32;
+  return warps * std::max<int64_t>(1, std::min<int64_t>(req.num_seqs, req.num_tokens / std::max(1, req.max_len)));
 }
 
 template <typename T, int NS, int SPLIT>
@@ -479,6 +626,9 @@ int scan_by_shape(const SsmArgs& a, cudaStream_t s) {
   const Shape k = shape_of(a.cfg.state_dim);
   if (k.ns == 4) return launch_scan<T, 4, 1>(a, s);
   if (k.ns == 8) return launch_scan<T, 8, 1>(a, s);
+  const int64_t pieces = a.segment ? (a.req.max_len + a.segment - 1) / a.segment : 1;
+  if (k.split == 1 && warps_of(a.cfg, a.req) * pieces < 4 * kSchedulers)
+    return launch_scan<T, 8, 2>(a, s);
   switch (k.split) {
     case 1: return launch_scan<T, 16, 1>(a, s);
     case 2: return launch_scan<T, 16, 2>(a, s);
@@ -513,16 +663,16 @@ int step_by_lanes(const SsmArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// Warps that run side by side: those of a request's channels, times the requests that the rows
-// make up at their longest. Below kFew the GPU's 608 schedulers have too little to do.
+// Cutting does the exponentials of most rows twice, so it pays where the schedulers have less than
+// three quarters of a warp each: 32,768 rows of 2,048 channels take 3,620 us whole and 540 in 57
+// pieces, four requests of 4,096 rows and 4,096 channels 542 and 550. Shorter pieces than 64 rows
+// spend more on their starts than they win (a prompt of 100 rows: 17 us whole, 21 in four).
 int32_t ssm_segment(const gdn_ssm_config& cfg, const gdn_requests& req) {
-  constexpr int64_t kFew = 1216, kWanted = 2432;
-  if (req.max_len < 1) return 0;
-  const int64_t warps = ((int64_t)cfg.channels * shape_of(cfg.state_dim).split + 31) / 32;
-  const int64_t side = std::max<int64_t>(1, std::min<int64_t>(req.num_seqs, req.num_tokens / req.max_len));
-  if (warps * side > kFew) return 0;
-  const int64_t pieces = std::min<int64_t>(32, kWanted / (warps * side));
-  const int64_t seg = std::max<int64_t>(128, ((int64_t)req.max_len + pieces - 1) / pieces + 31) / 32 * 32;
+  constexpr int64_t kFew = kSchedulers * 3 / 4, kWanted = 6 * kSchedulers, kLeast = 64, kMost = 64;
+  const int64_t warps = warps_of(cfg, req);
+  if (req.max_len < 1 || warps > kFew) return 0;
+  const int64_t pieces = std::min<int64_t>(kMost, kWanted / warps);
+  const int64_t seg = std::max<int64_t>(kLeast, ((int64_t)req.max_len + pieces - 1) / pieces + 31) / 32 * 32;
   return req.max_len >= 2 * seg ? (int32_t)seg : 0;
 }
 
