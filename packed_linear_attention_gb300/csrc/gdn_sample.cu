@@ -4,12 +4,13 @@
 // A row belongs to one cluster of blocks: each holds a slice of it in shared memory, so the logits
 // are read from memory once, however many passes the filters take. Nothing is sorted: every filter
 // keeps a beginning of the order (falling logits, equal ones by rising index), so it is enough to
-// find the last token kept. A histogram over the distance from the maximum gives its bin; the
-// bin's tokens, when few, are ranked against one another, else their bits are cut into 2,048 finer
-// bins, until they are few or all equal.
+// find the last token kept. The tokens are counted in bins of their distance from the maximum. For
+// top-k the counts say which bin it is in; for top-p they bound the weights to about 1.5% and say
+// between which bins. The tokens there, when few, are ranked against one another, else their bits
+// are cut into 2,048 finer bins, until they are few or all equal.
 //
 // Weights are integers, 2^44 for the maximum, so that their sums are exact and depend on no order:
-// exp((l - m) / T) = 2^-y, and 2^-y is a table entry times 1 + a polynomial of the last 1/64 of y.
+// exp((l - m) / T) = 2^-y, and 2^-y is a table entry times 1 + a polynomial of the last 1/32 of y.
 // l - m and y carry a second fp32 term, since errors of 2^-24 would move borders that u or
 // top_p may fall next to: weights are right to 2^-30 (2^-32 from the polynomial, the rest from y).
 #include <cooperative_groups.h>
@@ -29,14 +30,38 @@ using u64 = unsigned long long;
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 2048, kBinsOf = kBins / kThreads;  // bins of a thread
-constexpr int kList = kThreads;                          // tokens ranked against one another
+static_assert(kBinsOf == 4, "a thread's counts are read 16 bytes at a time");
+constexpr int kList = 128;                               // tokens ranked against one another
 constexpr float kRange = 44.f;                           // 2^-44 of the maximum: weight 1
 constexpr int kMaxCluster = 8;
+constexpr size_t kMostMemory = 227 * 1024;               // shared memory of a block, and of an SM
 
-struct Bins {
-  u64 weight[kBins];
-  u32 count[kBins];
+// 2^(31 - j/32), j = 0 .. 31, as a whole number and as fp32. One entry a bank: lanes may look up what
+// they like.
+struct Powers {
+  u32 whole[32], factor[32];
 };
+constexpr double root_of(double x) {
+  double r = x;
+  for (int i = 0; i < 60; ++i) r = 0.5 * (r + x / r);
+  return r;
+}
+constexpr Powers make_powers() {
+  double step = 0.5;  // 2^(-1/32): five square roots of a half
+  for (int i = 0; i < 5; ++i) step = root_of(step);
+  Powers t = {};
+  double p = 2147483648.0;
+  for (int j = 0; j < 32; ++j, p *= step) {
+    t.whole[j] = (u32)(p + 0.5);
+    // bits of the fp32 number nearest to p in [2^30, 2^31]: 24 bits from 2^7 (or 2^8) on
+    const double unit = j == 0 ? 256.0 : 128.0;
+    const u32 m = (u32)(p / unit + 0.5);
+    t.factor[j] = ((j == 0 ? 158u : 157u) << 23) + (m - (1u << 23));
+  }
+  return t;
+}
+__device__ const Powers kPowers = make_powers();
+
 struct Entry {
   u64 weight;
   u32 key, at;
@@ -46,43 +71,62 @@ struct List {
   u32 count;
 };
 struct Found {
-  u64 before_weight, weight;
+  u64 before_weight;
   u32 bin, before, count;
 };
 struct Shared {
-  Bins bins;
+  u32 count[kBins];  // tokens at each distance from the maximum
   union {
-    Bins finer;
+    u32 finer[kBins];
     List list;
   };
-  u64 table[64];      // 2^(36 - j/64)
-  float factor[64];   // the same
+  Powers table;
   u64 box[2];         // what the cluster's blocks tell one another, in turns
   u64 warp_weight[kWarps];
   u32 warp_count[kWarps];
   Found found;
-  Entry chosen;       // weight: of all tokens up to the chosen one
+  u32 window[2];
+  Entry chosen;       // the last token kept
 };
 
-// Orders floats as unsigned numbers (-0 as 0).
+// x times `total` for x in [0, 1), rounded down or up: exact, in whole numbers (fp64 arithmetic is
+// two lanes a clock here).
+__device__ __forceinline__ u64 share(float x, u64 total, bool up) {
+  const u32 bits = __float_as_uint(x), e = bits >> 23;
+  const u64 m = e ? (bits & 0x7fffffu) | 0x800000u : bits & 0x7fffffu;  // x = m 2^-s
+  const int s = 150 - max((int)e, 1);                                   // 24 .. 149
+  const u64 hi = __umul64hi(m, total), lo = m * total;
+  if (s >= 128) return up && (hi | lo) ? 1 : 0;
+  u64 q, rest;
+  if (s >= 64) {
+    q = s == 64 ? hi : hi >> (s - 64);
+    rest = lo | (s == 64 ? 0 : hi << (128 - s));
+  } else {
+    q = lo >> s | hi << (64 - s);
+    rest = lo << (64 - s);
+  }
+  return q + (up && rest ? 1 : 0);
+}
+
+// Orders logits as unsigned numbers (-0 as 0): 32 bits of an fp32 value, 16 of a bf16 one.
+template <typename T>
 __device__ __forceinline__ u32 key_of(float x) {
-  const u32 b = __float_as_uint(x + 0.f);
-  return b ^ ((u32)((int32_t)b >> 31) | 0x80000000u);
+  const u32 b = __float_as_uint(x + 0.f), k = b ^ ((u32)((int32_t)b >> 31) | 0x80000000u);
+  return sizeof(T) == 2 ? k >> 16 : k;
+}
+template <typename T>
+__device__ __forceinline__ float value_of(u32 key) {
+  const u32 k = sizeof(T) == 4 ? key : key << 16 | (key & 0x8000u ? 0 : 0xffffu);
+  return __uint_as_float(k ^ ((u32)((int32_t)~k >> 31) | 0x80000000u));
 }
 
 // Weights of one row.
 struct Weights {
   float top, hi, lo;   // the maximum; log2(e) / temperature
-  bool infinite;       // the maximum is +inf: such logits share the row
-  const u64* table;
-  const float* factor;
+  const Powers* table;
 
   // -log2 of the weight, y + rest; kRange or more (or NaN): weight 0
   __device__ __forceinline__ float distance(float l, float& rest) const {
-    if (infinite) {
-      rest = 0.f;
-      return l == top ? 0.f : 2.f * kRange;
-    }
     const float d = top - l, b = d - top;
     const float err = (top - (d - b)) - (l + b);  // top - l = d + err
     const float y = d * hi;
@@ -90,39 +134,61 @@ struct Weights {
     return y;
   }
   __device__ __forceinline__ float distance(float l) const {
-    return infinite ? (l == top ? 0.f : 2.f * kRange) : (top - l) * hi;
+    return (top - l) * hi;
   }
+  // No branches: a thread's elements are worked out side by side.
   __device__ __forceinline__ u64 operator()(float l) const {
     float rest;
-    const float y = distance(l, rest);
-    if (!(y < kRange)) return 0;
-    const int n = (int)(y * 64.f);
-    const float r = fmaf((float)n, -1.f / 64.f, y) + rest;  // the difference is exact
-    // 2^-r - 1, r < 1/64: powers of r ln 2 over factorials, the next one below 2^-38
+    const float y = distance(l, rest), held = fminf(y, kRange);
+    constexpr float kMagic = 0x1.8p23f;  // 32 y to the nearest whole number, in the low bits
+    const float shifted = fmaf(held, 32.f, kMagic);
+    const u32 n = __float_as_uint(shifted) & 0x7ffu;
+    const float r = fmaf(shifted - kMagic, -1.f / 32.f, held) + rest;  // the difference is exact
+    // 2^-r - 1, |r| <= 1/64: powers of r ln 2 over factorials, the next one below 2^-39
     float q = fmaf(r, 0.0096181291f, -0.0555041087f);
     q = fmaf(r, q, 0.2402265070f);
     q = fmaf(r, q, -0.6931471806f);
-    q *= r;
-    const int j = n & 63;
-    const u64 w = table[j] + (u64)(int64_t)__float2int_rn(factor[j] * q);
-    return (w << 8) >> (n >> 6);
+    const u32 w = table->whole[n & 31] +
+                  (u32)__float2int_rn(__uint_as_float(table->factor[n & 31]) * (r * q));
+    return y < kRange ? (u64)w << 13 >> (n >> 5) : 0;
   }
 };
 
+// A block's part of a row. A thread owns `each` neighbouring vectors (an odd number of them, so that
+// the lanes' reads do not meet in a bank): sums over threads run in the order of the row.
 template <typename T>
 struct Slice {
   static constexpr int N = Vec<T>::N;
   const Vec<T>* data;
-  int vecs;       // of this block
-  u32 first;      // place of its first element in the row
+  int vecs, per_thread;
+  u32 first;      // place of the block's first element in the row
   // f(value, place) for every element
   template <class F>
   __device__ __forceinline__ void each(F f) const {
-    for (int v = threadIdx.x; v < vecs; v += kThreads) {
+    const int v1 = min(vecs, ((int)threadIdx.x + 1) * per_thread);
+    for (int v = threadIdx.x * per_thread; v < v1; ++v) {
       float x[N];
       unpack(data[v], x);
 #pragma unroll
       for (int i = 0; i < N; ++i) f(x[i], first + v * N + i);
+    }
+  }
+  // f(value, place) for the elements that are wanted, where they are few: looked for side by side,
+  // then taken one by one.
+  template <class Want, class F>
+  __device__ __forceinline__ void some(Want want, F f) const {
+    const int v1 = min(vecs, ((int)threadIdx.x + 1) * per_thread);
+    for (int v = threadIdx.x * per_thread; v < v1; ++v) {
+      float x[N];
+      unpack(data[v], x);
+      u32 mask = 0;
+#pragma unroll
+      for (int i = 0; i < N; ++i) mask |= want(x[i], first + v * N + i) ? 1u << i : 0;
+      while (mask) {
+        const int i = __ffs(mask) - 1;
+        mask &= mask - 1;
+        f(to_f32(reinterpret_cast<const T*>(data + v)[i]), first + v * N + i);
+      }
     }
   }
 };
@@ -131,6 +197,15 @@ template <typename V>
 __device__ __forceinline__ V warp_sum(V v) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
+__device__ __forceinline__ u64 warp_upto(u64 v) {
+  const int lane = threadIdx.x % 32;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const u64 o = __shfl_up_sync(0xffffffffu, v, off);
+    if (lane >= off) v += o;
+  }
   return v;
 }
 
@@ -145,257 +220,330 @@ struct Row {
 
   __device__ __forceinline__ Row(Shared& s) : cluster(cg::this_cluster()), sh(s) {}
 
-  // Every block's value (thread 0's), combined by f in the blocks' order.
-  template <class F>
-  __device__ __forceinline__ void exchange(u64 mine, F f) {
+  // Every block's value (thread 0's): lane r of every warp has block r's, others 0. Read side by side:
+  // a read from another block takes about 300 ns.
+  __device__ __forceinline__ u64 exchange(u64 mine) {
     if (threadIdx.x == 0) sh.box[turn] = mine;
     cluster.sync();
-    for (unsigned r = 0; r < cluster.num_blocks(); ++r)
-      f(r, *cluster.map_shared_rank(&sh.box[turn], r));
+    const unsigned lane = threadIdx.x % 32;
+    const u64 v = lane < cluster.num_blocks() ? *cluster.map_shared_rank(&sh.box[turn], lane) : 0;
     turn ^= 1;
+    return v;
+  }
+  __device__ __forceinline__ u64 in_front(u64 of_block) {  // of exchanged values, those of the blocks in front
+    return warp_sum(threadIdx.x % 32 < cluster.block_rank() ? of_block : 0);
   }
 
+  // Sum in front of this thread, and of the whole block.
+  __device__ __forceinline__ u64 scan(u64 v, u64& all) {
+    const u64 upto = warp_upto(v);
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    __syncthreads();
+    if (lane == 31) sh.warp_weight[warp] = upto;
+    __syncthreads();
+    const u64 w = warp_upto(lane < kWarps ? sh.warp_weight[lane] : 0);
+    all = __shfl_sync(0xffffffffu, w, kWarps - 1);
+    const u64 front = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
+    return (warp > 0 ? front : 0) + upto - v;
+  }
   __device__ __forceinline__ u64 block_sum(u64 v) {
     v = warp_sum(v);
     __syncthreads();
     if (threadIdx.x % 32 == 0) sh.warp_weight[threadIdx.x / 32] = v;
     __syncthreads();
-    u64 s = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) s += sh.warp_weight[w];
-    return s;
+    return warp_sum(threadIdx.x % 32 < kWarps ? sh.warp_weight[threadIdx.x % 32] : 0);
   }
-  __device__ __forceinline__ u64 block_max(u64 v) {
+  __device__ __forceinline__ u64 cluster_sum(u64 v) {
+    return warp_sum(exchange(block_sum(v)));
+  }
+  __device__ __forceinline__ static u64 warp_max(u64 x) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
-      const u64 o = __shfl_xor_sync(0xffffffffu, v, off);
-      v = o > v ? o : v;
+      const u64 o = __shfl_xor_sync(0xffffffffu, x, off);
+      x = o > x ? o : x;
     }
+    return x;
+  }
+  __device__ __forceinline__ u64 block_max(u64 v) {
+    v = warp_max(v);
     __syncthreads();
     if (threadIdx.x % 32 == 0) sh.warp_weight[threadIdx.x / 32] = v;
     __syncthreads();
-    u64 s = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) s = sh.warp_weight[w] > s ? sh.warp_weight[w] : s;
-    return s;
-  }
-
-  __device__ __forceinline__ void clear(Bins& b) {
-    for (int i = threadIdx.x; i < kBins; i += kThreads) {
-      b.weight[i] = 0;
-      b.count[i] = 0;
-    }
-    __syncthreads();
-  }
-
-  // Sums in front of this thread (exclusive), and of the whole block.
-  __device__ __forceinline__ void scan(u32 c, u64 w, u32& before_c, u64& before_w, u32& all_c,
-                                       u64& all_w) {
-    u32 upc = c;
-    u64 upw = w;
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const u32 a = __shfl_up_sync(0xffffffffu, upc, off);
-      const u64 b = __shfl_up_sync(0xffffffffu, upw, off);
-      if (lane >= off) {
-        upc += a;
-        upw += b;
-      }
-    }
-    __syncthreads();
-    if (lane == 31) {
-      sh.warp_count[warp] = upc;
-      sh.warp_weight[warp] = upw;
-    }
-    __syncthreads();
-    before_c = upc - c;
-    before_w = upw - w;
-    all_c = 0;
-    all_w = 0;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-      if (i == warp) {
-        before_c += all_c;
-        before_w += all_w;
-      }
-      all_c += sh.warp_count[i];
-      all_w += sh.warp_weight[i];
-    }
-  }
-
-  // The cluster's bins: the sums of all, and the first bin at which the count (or weight) reaches
-  // a target, which may follow from the sums.
-  template <class Target>
-  __device__ __forceinline__ Found find(Bins& mine, bool by_weight, u32 before, u64 before_weight,
-                                        Target target, u32& all_c, u64& all_w) {
-    u32 c[kBinsOf] = {}, sum_c = 0, at_c;
-    u64 w[kBinsOf] = {}, sum_w = 0, at_w;
-    for (unsigned r = 0; r < cluster.num_blocks(); ++r) {
-      const Bins& b = *cluster.map_shared_rank(&mine, r);
-#pragma unroll
-      for (int i = 0; i < kBinsOf; ++i) {
-        c[i] += b.count[threadIdx.x * kBinsOf + i];
-        w[i] += b.weight[threadIdx.x * kBinsOf + i];
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kBinsOf; ++i) {
-      sum_c += c[i];
-      sum_w += w[i];
-    }
-    scan(sum_c, sum_w, at_c, at_w, all_c, all_w);
-    const u64 goal = target(all_c, all_w);
-    at_c += before;
-    at_w += before_weight;
-#pragma unroll
-    for (int i = 0; i < kBinsOf; ++i) {
-      const u64 front = by_weight ? at_w : at_c, back = front + (by_weight ? w[i] : c[i]);
-      if (front < goal && goal <= back)
-        sh.found = {at_w, w[i], (u32)(threadIdx.x * kBinsOf + i), at_c, c[i]};
-      at_c += c[i];
-      at_w += w[i];
-    }
-    __syncthreads();
-    return sh.found;
-  }
-
-  // The first place at which the cumulative g passes target (total: what it passes in the end).
-  template <class G>
-  __device__ __forceinline__ bool select(u64 target, u64 before, G g, u32& place, u64& value) {
-    constexpr int N = Slice<T>::N;
-    for (int v0 = 0; v0 < slice.vecs; v0 += kThreads) {
-      const int v = v0 + threadIdx.x;
-      float x[N];
-      u64 w[N], sum = 0, at, all;
-      if (v < slice.vecs) unpack(slice.data[v], x);
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        w[i] = v < slice.vecs ? g(x[i], slice.first + v * N + i) : 0;
-        sum += w[i];
-      }
-      u32 none, none2;
-      scan(0, sum, none, at, none2, all);
-      at += before;
-      if (at <= target && target < at + sum) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          if (at <= target && target < at + w[i]) {
-            place = slice.first + v * N + i;
-            value = w[i];
-            return true;
-          }
-          at += w[i];
-        }
-      }
-      before += all;
-      if (target < before) return false;  // another thread has it
-    }
-    return false;
-  }
-
-  // The last token kept, when the bin `f` of the first histogram holds it: the one at which the
-  // count (or weight) of the order reaches goal. at: its place; weight: of all up to it.
-  __device__ __forceinline__ Entry resolve(Found f, bool by_weight, u64 goal) {
-    u32 hi = 0, lo = 0xffffffffu;
-    slice.each([&](float x, u32) {
-      const float y = weight.distance(x);
-      if (y < kRange && bin_of(y) == f.bin) {
-        const u32 k = key_of(x);
-        hi = max(hi, k);
-        lo = min(lo, k);
-      }
-    });
-    u32 inv = __reduce_max_sync(0xffffffffu, ~lo);
-    hi = __reduce_max_sync(0xffffffffu, hi);
-    __syncthreads();
-    if (threadIdx.x % 32 == 0) sh.warp_weight[threadIdx.x / 32] = (u64)hi << 32 | inv;
-    __syncthreads();
-    for (int w = 0; w < kWarps; ++w) {
-      hi = max(hi, (u32)(sh.warp_weight[w] >> 32));
-      inv = max(inv, (u32)sh.warp_weight[w]);
-    }
-    exchange((u64)hi << 32 | inv, [&](unsigned, u64 o) {
-      hi = max(hi, (u32)(o >> 32));
-      inv = max(inv, (u32)o);
-    });
-    lo = ~inv;
-    while (f.count > kList && lo < hi) {
-      const int shift = max(0, 21 - __clz(hi - lo));  // (hi - lo) >> shift is below 2,048
-      clear(sh.finer);
-      slice.each([&](float x, u32) {
-        const u32 k = key_of(x);
-        if (k >= lo && k <= hi) {
-          atomicAdd(&sh.finer.count[(hi - k) >> shift], 1u);
-          atomicAdd(&sh.finer.weight[(hi - k) >> shift], weight(x));
-        }
-      });
-      cluster.sync();
-      u32 c;
-      u64 w;
-      f = find(sh.finer, by_weight, f.before, f.before_weight, [&](u32, u64) { return goal; }, c, w);
-      hi -= f.bin << shift;
-      lo = max(lo, hi - ((1u << shift) - 1));
-      cluster.sync();  // the bins have been read
-    }
-    if (f.count <= kList) {
-      if (threadIdx.x == 0) sh.list.count = 0;
-      __syncthreads();
-      slice.each([&](float x, u32 at) {
-        const u32 k = key_of(x);
-        if (k >= lo && k <= hi) sh.list.mine[atomicAdd(&sh.list.count, 1u)] = {weight(x), k, at};
-      });
-      cluster.sync();
-      u32 i = threadIdx.x;
-      for (unsigned r = 0; r < cluster.num_blocks(); ++r) {
-        const List& l = *cluster.map_shared_rank(&sh.list, r);
-        const u32 n = l.count;
-        if (i < n) {
-          sh.list.all[threadIdx.x] = l.mine[i];
-          break;
-        }
-        i -= n;
-      }
-      __syncthreads();
-      if (threadIdx.x < f.count) {
-        const Entry me = sh.list.all[threadIdx.x];
-        u64 c = f.before, w = f.before_weight;
-        for (u32 j = 0; j < f.count; ++j) {
-          const Entry o = sh.list.all[j];
-          if (o.key > me.key || (o.key == me.key && o.at < me.at)) {
-            ++c;
-            w += o.weight;
-          }
-        }
-        const u64 front = by_weight ? w : c, back = front + (by_weight ? me.weight : 1);
-        if (front < goal && goal <= back) sh.chosen = {w + me.weight, me.key, me.at};
-      }
-      __syncthreads();
-    } else {  // all equal: the first of them, by place
-      const u64 each = f.weight / f.count;
-      const u64 n = by_weight ? (goal - f.before_weight + each - 1) / each : goal - f.before;
-      u64 mine = 0, before = 0;
-      slice.each([&](float x, u32) { mine += key_of(x) == lo; });
-      mine = block_sum(mine);
-      exchange(mine, [&](unsigned r, u64 o) { before += r < cluster.block_rank() ? o : 0; });
-      u32 at;
-      u64 one;
-      if (before < n && n <= before + mine &&
-          select(n - 1, before, [&](float x, u32) { return (u64)(key_of(x) == lo); }, at, one))
-        for (unsigned r = 0; r < cluster.num_blocks(); ++r)
-          *cluster.map_shared_rank(&sh.chosen, r) = {f.before_weight + n * each, lo, at};
-      cluster.sync();
-    }
-    return sh.chosen;
+    return warp_max(threadIdx.x % 32 < kWarps ? sh.warp_weight[threadIdx.x % 32] : 0);
   }
 
   __device__ __forceinline__ static u32 bin_of(float y) {
     return min((u32)(y * (kBins / kRange)), (u32)kBins - 1);
   }
+
+  // The cluster's counts of this thread's bins.
+  __device__ __forceinline__ void counts(u32* mine, u32 (&c)[kBinsOf]) {
+    uint4 o[kMaxCluster];
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) {
+      o[r] = make_uint4(0, 0, 0, 0);
+      if (r < cluster.num_blocks())
+        o[r] = reinterpret_cast<const uint4*>(cluster.map_shared_rank(mine, r))[threadIdx.x];
+    }
+#pragma unroll
+    for (int i = 0; i < kBinsOf; ++i) c[i] = 0;
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) {
+      c[0] += o[r].x;
+      c[1] += o[r].y;
+      c[2] += o[r].z;
+      c[3] += o[r].w;
+    }
+  }
+
+  // The bin at which the cumulative count reaches goal (`before`: what lies in front of the bins), and
+  // the tokens in all; nothing found: bin kBins.
+  __device__ __forceinline__ Found find(const u32 (&c)[kBinsOf], u32 before, u64 goal, u64& all) {
+    u64 sum = 0;
+#pragma unroll
+    for (int i = 0; i < kBinsOf; ++i) sum += c[i];
+    u64 at = scan(sum, all) + before;
+    if (threadIdx.x == 0) sh.found.bin = kBins;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kBinsOf; ++i) {
+      if (at < goal && goal <= at + c[i]) sh.found = {0, (u32)(threadIdx.x * kBinsOf + i), (u32)at, c[i]};
+      at += c[i];
+    }
+    __syncthreads();
+    return sh.found;
+  }
+
+  // The tokens in front of the bins first .. last, and in them.
+  __device__ __forceinline__ Found tokens(const u32 (&c)[kBinsOf], u32 first, u32 last) {
+    u64 v = 0;  // front and inside, 32 bits each
+#pragma unroll
+    for (int i = 0; i < kBinsOf; ++i) {
+      const u32 b = threadIdx.x * kBinsOf + i;
+      v += b < first ? (u64)c[i] << 32 : b <= last ? c[i] : 0;
+    }
+    v = block_sum(v);
+    return {0, first, (u32)(v >> 32), (u32)v};
+  }
+
+  // The bins first .. last, one of which the cumulative weight reaches goal in, from bounds of the
+  // bins' weights: goal lies between least(sums of lo, of hi) and most(...).
+  template <class Goal>
+  __device__ __forceinline__ void window(const u64 (&lo)[kBinsOf], const u64 (&hi)[kBinsOf], u64 before,
+                                         Goal goal, u32& first, u32& last) {
+    u64 sum_hi = 0, sum_lo = 0, all_hi, all_lo, least, most;
+#pragma unroll
+    for (int i = 0; i < kBinsOf; ++i) {
+      sum_hi += hi[i];
+      sum_lo += lo[i];
+    }
+    u64 at_hi = scan(sum_hi, all_hi) + before, at_lo = scan(sum_lo, all_lo) + before;
+    goal(all_lo, all_hi, least, most);
+    if (threadIdx.x == 0) {
+      sh.window[0] = 0;
+      sh.window[1] = kBins - 1;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kBinsOf; ++i) {
+      if (at_hi < least && least <= at_hi + hi[i]) sh.window[0] = threadIdx.x * kBinsOf + i;
+      if (at_lo < most && most <= at_lo + lo[i]) sh.window[1] = threadIdx.x * kBinsOf + i;
+      at_hi += hi[i];
+      at_lo += lo[i];
+    }
+    __syncthreads();
+    first = sh.window[0];
+    last = sh.window[1];
+  }
+
+  // The first place at which the cumulative g passes target, given this thread's sum of g and what
+  // lies in front of it. One warp finds it and runs `got` on one of its lanes.
+  template <class G, class Got>
+  __device__ __forceinline__ void select(u64 target, u64 front, u64 sum, G g, Got got) {
+    constexpr int N = Slice<T>::N;
+    const u32 owner = __ballot_sync(0xffffffffu, front <= target && target < front + sum);
+    if (owner == 0) return;
+    const int lane = threadIdx.x % 32, src = __ffs(owner) - 1;
+    u64 at = __shfl_sync(0xffffffffu, front, src);
+    const int v0 = (threadIdx.x - lane + src) * slice.per_thread;
+    const int items = (min(slice.vecs, v0 + slice.per_thread) - v0) * N;
+    const T* data = reinterpret_cast<const T*>(slice.data + v0);
+    for (int i0 = 0; i0 < items; i0 += 32) {
+      const int i = i0 + lane;
+      const u32 place = slice.first + v0 * N + i;
+      const u64 w = i < items ? g(to_f32(data[i]), place) : 0;
+      const u64 upto = at + warp_upto(w);
+      if (upto - w <= target && target < upto) got(place, w);
+      at = __shfl_sync(0xffffffffu, upto, 31);
+      if (target < at) return;
+    }
+  }
+
+  // The weight of the keys above `low`, up to `high`.
+  __device__ __forceinline__ u64 weight_between(u32 low, u32 high) {
+    u64 sum = 0;
+    const float v0 = value_of<T>(low), v1 = value_of<T>(high);
+    slice.some([&](float x, u32) { return x > v0 && x <= v1; },
+               [&](float x, u32) { sum += weight(x); });
+    return cluster_sum(sum);
+  }
+
+  // The last token kept, which one of the bins first .. last of the distances holds: the one at which
+  // the count (or weight) of the order reaches goal. f: what lies in front of those bins, and the
+  // tokens in them.
+  __device__ __forceinline__ Entry resolve(u32 first, u32 last, Found f, bool by_weight, u64 goal) {
+    bool by_key = false;
+    u32 hi = 0, lo = 0;            // by_key: the keys lo .. hi
+    float above = 0.f, below = 0.f;  // and their values
+    const auto member = [&](float x, u32) {
+      if (by_key) return x >= above && x <= below;
+      const float y = weight.distance(x);
+      const u32 b = bin_of(fminf(y, kRange));
+      return y < kRange && b >= first && b <= last;
+    };
+    if (f.count > kList) {
+      above = INFINITY;
+      below = -INFINITY;
+      slice.each([&](float x, u32 at) {
+        const bool in = member(x, at);
+        below = in ? fmaxf(below, x) : below;
+        above = in ? fminf(above, x) : above;
+      });
+      u32 inv = ~key_of<T>(above);
+      hi = key_of<T>(below);
+      hi = __reduce_max_sync(0xffffffffu, hi);
+      inv = __reduce_max_sync(0xffffffffu, inv);
+      __syncthreads();
+      if (threadIdx.x % 32 == 0) sh.warp_weight[threadIdx.x / 32] = (u64)hi << 32 | inv;
+      __syncthreads();
+      const u64 of = sh.warp_weight[threadIdx.x % kWarps];
+      hi = __reduce_max_sync(0xffffffffu, (u32)(of >> 32));
+      inv = __reduce_max_sync(0xffffffffu, (u32)of);
+      const u64 both = exchange((u64)hi << 32 | inv);
+      hi = __reduce_max_sync(0xffffffffu, (u32)(both >> 32));
+      inv = __reduce_max_sync(0xffffffffu, (u32)both);
+      lo = ~inv;
+      by_key = true;
+      above = value_of<T>(lo);
+      below = value_of<T>(hi);
+    }
+    while (f.count > kList && lo < hi) {  // the keys left are halved at least
+      const int shift = max(0, 21 - __clz(hi - lo));  // (hi - lo) >> shift is below 2,048
+      for (int i = threadIdx.x; i < kBins; i += kThreads) sh.finer[i] = 0;
+      __syncthreads();
+      slice.some(member, [&](float x, u32) {
+        // lanes of one bin (equal logits) add once
+        const u32 b = (hi - key_of<T>(x)) >> shift, same = __match_any_sync(__activemask(), b);
+        if (threadIdx.x % 32 == __ffs(same) - 1) atomicAdd(&sh.finer[b], (u32)__popc(same));
+      });
+      cluster.sync();
+      u32 c[kBinsOf], b0, b1;
+      counts(sh.finer, c);
+      if (by_weight) {
+        // a bin's weights lie between those of its ends, to their own error
+        u64 least[kBinsOf], most[kBinsOf];
+#pragma unroll
+        for (int i = 0; i < kBinsOf; ++i) {
+          const u32 k = hi - ((threadIdx.x * kBinsOf + i) << shift);
+          const u64 w0 = c[i] ? weight(value_of<T>(k)) : 0;
+          const u64 w1 = c[i] ? weight(value_of<T>(max(lo, k - ((1u << shift) - 1)))) : 0;
+          most[i] = c[i] * (w0 + (shift ? (w0 >> 28) + 1 : 0));
+          least[i] = c[i] * (w1 - (shift ? min(w1, (w1 >> 28) + 1) : 0));
+        }
+        window(least, most, f.before_weight, [&](u64, u64, u64& a, u64& b) { a = b = goal; }, b0, b1);
+      } else {
+        u64 all;
+        b0 = b1 = find(c, f.before, goal, all).bin;
+      }
+      b1 = min(b1, (hi - lo) >> shift);
+      const Found in = tokens(c, b0, b1);
+      f.before += in.before;
+      f.count = in.count;
+      const u32 top = hi, span = hi - lo;
+      lo = max(lo, hi - (b1 << shift) - ((1u << shift) - 1));
+      hi -= b0 << shift;
+      if (by_weight) f.before_weight += weight_between(hi, top);
+      if (hi - lo > span / 2) {  // bounds too wide to tell: halve the keys by exact sums
+        const u32 mid = lo + (hi - lo) / 2;
+        const float v0 = value_of<T>(mid), v1 = value_of<T>(hi);
+        u32 here = 0;
+        slice.each([&](float x, u32) { here += x > v0 && x <= v1; });
+        const u64 n = cluster_sum(here);
+        const u64 w = by_weight ? weight_between(mid, hi) : n;
+        if ((by_weight ? f.before_weight : f.before) + w >= goal) {
+          lo = mid + 1;
+          f.count = (u32)n;
+        } else {
+          hi = mid;
+          f.before += (u32)n;
+          f.before_weight += by_weight ? w : 0;
+          f.count -= (u32)n;
+        }
+      }
+      above = value_of<T>(lo);
+      below = value_of<T>(hi);
+      cluster.sync();  // the bins have been read
+    }
+    if (f.count <= kList) {
+      if (threadIdx.x == 0) sh.list.count = 0;
+      __syncthreads();
+      slice.some(member, [&](float x, u32 at) {
+        sh.list.mine[atomicAdd(&sh.list.count, 1u)] = {by_weight ? weight(x) : 1, key_of<T>(x), at};
+      });
+      cluster.sync();
+      // the lists one behind another: entry threadIdx.x of them all
+      const unsigned lane = threadIdx.x % 32;
+      const u32 n = lane < cluster.num_blocks() ? cluster.map_shared_rank(&sh.list, lane)->count : 0;
+      u32 from = 0, i = threadIdx.x;
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) {
+        const u32 k = __shfl_sync(0xffffffffu, n, r);
+        if (from == (u32)r && i >= k) {
+          i -= k;
+          ++from;
+        }
+      }
+      if (threadIdx.x < f.count) sh.list.all[threadIdx.x] = cluster.map_shared_rank(&sh.list, from)->mine[i];
+      __syncthreads();
+      // four threads an entry
+      constexpr int kPer = kThreads / kList;
+      const u32 mine = threadIdx.x / kPer;
+      const Entry me = sh.list.all[min(mine, f.count - 1)];
+      u64 front = 0;
+      for (u32 j = threadIdx.x % kPer; j < f.count; j += kPer) {
+        const Entry o = sh.list.all[j];
+        front += o.key > me.key || (o.key == me.key && o.at < me.at) ? o.weight : 0;
+      }
+#pragma unroll
+      for (int off = 1; off < kPer; off <<= 1) front += __shfl_xor_sync(0xffffffffu, front, off);
+      front += by_weight ? f.before_weight : f.before;
+      if (mine < f.count && threadIdx.x % kPer == 0 && front < goal && goal <= front + me.weight)
+        sh.chosen = me;
+      __syncthreads();
+    } else {  // all equal: the first of them, by place
+      u64 n = goal - f.before;
+      if (by_weight) {
+        const u64 each = weight(value_of<T>(lo));
+        n = (goal - f.before_weight + each - 1) / each;
+      }
+      u32 mine = 0;
+      u64 all;
+      slice.each([&](float x, u32) { mine += x == above; });
+      const u64 inside = scan(mine, all);
+      const u64 front = in_front(exchange(all));
+      select(n - 1, front + inside, mine, [&](float x, u32) { return (u64)(x == above); },
+             [&](u32 at, u64) {
+               for (unsigned r = 0; r < cluster.num_blocks(); ++r)
+                 *cluster.map_shared_rank(&sh.chosen, r) = {0, lo, at};
+             });
+      cluster.sync();
+    }
+    return sh.chosen;
+  }
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs p, int vecs_of_block) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs p, int vecs_of_block) {
   extern __shared__ __align__(16) unsigned char memory[];
   constexpr int N = Vec<T>::N;
   Shared& sh = *reinterpret_cast<Shared*>(memory);
@@ -423,10 +571,9 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs p, int vecs
     }
   }
   asm volatile("cp.async.commit_group;" ::: "memory");
-  if (threadIdx.x < 64) {
-    const double t = exp2(36.0 - threadIdx.x / 64.0);
-    sh.table[threadIdx.x] = (u64)__double2ll_rn(t);
-    sh.factor[threadIdx.x] = (float)t;
+  if (threadIdx.x < 32) {
+    sh.table.whole[threadIdx.x] = kPowers.whole[threadIdx.x];
+    sh.table.factor[threadIdx.x] = kPowers.factor[threadIdx.x];
   }
   const float temp = p.temperature ? p.temperature[r] : 1.f;
   const float top_p = p.top_p ? p.top_p[r] : 1.f, min_p = p.min_p ? p.min_p[r] : 0.f;
@@ -434,30 +581,24 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs p, int vecs
   const float u = p.u[r];
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
-  row.slice = {data, mine, (u32)v0 * N};
+  row.slice = {data, mine, ((mine + kThreads - 1) / kThreads) | 1, (u32)v0 * N};
 
   // the maximum and its first place
-  u64 best = 0;
-  for (int v = threadIdx.x; v < mine; v += kThreads) {
-    float x[N];
-    unpack(data[v], x);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if (x[i] == x[i]) {
-        const u64 k = (u64)key_of(x[i]) << 32 | (u32)~(u32)((v0 + v) * N + i);
-        best = k > best ? k : best;
-      }
+  float most = -INFINITY;
+  u32 most_at = 0xffffffffu;
+  row.slice.each([&](float x, u32 at) {
+    if (x > most) {
+      most = x;
+      most_at = at;
     }
-  }
+  });
+  u64 best = most > -INFINITY ? (u64)key_of<T>(most) << 32 | (u32)~most_at : 0;
   best = row.block_max(best);
-  row.exchange(best, [&](unsigned, u64 o) { best = o > best ? o : best; });
-  const u32 bits = (u32)(best >> 32);
-  const float top = best == 0 ? -INFINITY
-                              : __uint_as_float(bits ^ ((u32)((int32_t)~bits >> 31) | 0x80000000u));
-  const bool bad = !(top > -INFINITY) || !(temp >= 0.f) || top_p != top_p || min_p != min_p || u != u;
-  const bool out = rank == 0 && threadIdx.x == 0;
+  best = Row<T>::warp_max(row.exchange(best));
+  const float top = best == 0 ? -INFINITY : value_of<T>((u32)(best >> 32));
+  const bool bad = best == 0 || !(temp >= 0.f) || top_p != top_p || min_p != min_p || u != u;
   if (bad || temp == 0.f) {
-    if (out) {
+    if (rank == 0 && threadIdx.x == 0) {
       if (bad) raise_status(p.status, GDN_ERR_INVALID_ARGUMENT);
       p.token[r] = bad ? -1 : (int32_t)(~(u32)best) - shift;
       if (p.logprob) p.logprob[r] = bad ? -INFINITY : 0.f;
@@ -465,74 +606,114 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs p, int vecs
     row.cluster.sync();  // no block leaves while another reads its box
     return;
   }
-  const double rate = fmin(1.4426950408889634074 / (double)temp, 1e30);
-  const float hi = (float)rate;
-  row.weight = {top, hi, (float)(rate - (double)hi), top == INFINITY, sh.table, sh.factor};
+  // log2(e) / temperature as two fp32 terms: the quotient and its remainder's
+  constexpr float kLog2e = 1.4426950408889634f, kLog2eRest = (float)(1.4426950408889634074 - kLog2e);
+  float hi = __fdiv_rn(kLog2e, temp);
+  float lo = __fdiv_rn(fmaf(-hi, temp, kLog2e) + kLog2eRest, temp);
+  if (!(hi <= 1e30f)) hi = 1e30f;
+  if (hi == 1e30f || temp > 1e30f) lo = 0.f;
+  row.weight = {top, hi, lo, &sh.table};
+  if (top == INFINITY) {  // such logits share the row: zeros among -inf, all with weight 1
+    for (int v = threadIdx.x; v < mine; v += kThreads) {
+      T* e = reinterpret_cast<T*>(data + v);
+      for (int i = 0; i < N; ++i) e[i] = from_f32<T>(to_f32(e[i]) == INFINITY ? 0.f : -INFINITY);
+    }
+    row.weight = {0.f, 1.f, 0.f, &sh.table};
+    __syncthreads();
+  }
 
   // the last token that top-k and top-p keep; until then every one is
-  u32 last_key = 0, last_at = 0xffffffffu;
+  bool cut = false;
+  float last_value = -INFINITY;
+  u32 last_at = 0xffffffffu;
+  const auto cut_at = [&](const Entry& e) {
+    cut = true;
+    last_value = value_of<T>(e.key);
+    last_at = e.at;
+  };
+  const auto inside_of = [&](float x, u32 at) {
+    return x > last_value || (x == last_value && at <= last_at);
+  };
+  u64 floor_weight = 0;
+  const auto kept = [&](float x, u32 at) -> u64 {
+    const u64 w = row.weight(x);
+    return inside_of(x, at) && w >= floor_weight ? w : 0;
+  };
   const bool by_k = top_k > 0 && top_k < V, by_p = top_p < 1.f;
   if (by_k || by_p) {
-    row.clear(sh.bins);
+    for (int i = threadIdx.x; i < kBins; i += kThreads) sh.count[i] = 0;
+    __syncthreads();
     row.slice.each([&](float x, u32) {
       const float y = row.weight.distance(x);
-      if (y < kRange) {
-        const u32 b = Row<T>::bin_of(y);
-        atomicAdd(&sh.bins.count[b], 1u);
-        atomicAdd(&sh.bins.weight[b], row.weight(x));
-      }
+      if (y < kRange) atomicAdd(&sh.count[Row<T>::bin_of(y)], 1u);
     });
     row.cluster.sync();
-    u32 count;
-    u64 total;
+    u32 c[kBinsOf];
+    u64 all;
+    u32 limit = kBins - 1;  // the last bin with a token kept, where top-k cuts one
+    row.counts(sh.count, c);
     if (by_k) {
-      const Found f = row.find(sh.bins, false, 0, 0, [&](u32, u64) { return (u64)top_k; }, count, total);
-      if (count > (u32)top_k) {
-        const Entry e = row.resolve(f, false, top_k);
-        last_key = e.key;
-        last_at = e.at;
-        total = e.weight;
+      const Found f = row.find(c, 0, (u64)top_k, all);
+      if (all > (u64)top_k) {
+        cut_at(row.resolve(f.bin, f.bin, f, false, (u64)top_k));
+        limit = f.bin;
       }
     }
     if (by_p) {
-      u64 goal = 0, all_weight;
-      const Found f = row.find(
-          sh.bins, true, 0, 0,
-          [&](u32, u64 all) {
-            const u64 of = by_k ? total : all;
-            const double g = ceil((double)top_p * (double)of);
-            goal = g < 1.0 ? 1 : min((u64)g, of);
-            return goal;
-          },
-          count, all_weight);
-      const Entry e = row.resolve(f, true, goal);
-      last_key = e.key;
-      last_at = e.at;
+      // a bin's weights lie between 2^44 times 2^-(its ends), to 2^-16 (a distance is off by 2^-18);
+      // of the last bin some tokens may be left out
+      u64 most[kBinsOf], least[kBinsOf];
+#pragma unroll
+      for (int i = 0; i < kBinsOf; ++i) {
+        const u32 b = threadIdx.x * kBinsOf + i;
+        const float y = (float)b * (kRange / kBins);
+        most[i] = b <= limit ? c[i] * ((u64)(exp2f(44.f - y) * (1.f + 0x1p-16f)) + 1) : 0;
+        least[i] = b < limit || !cut
+                       ? c[i] * (u64)(exp2f(44.f - y - kRange / kBins) * (1.f - 0x1p-16f)) : 0;
+      }
+      const auto share_of = [&](u64 total) {
+        return top_p > 0.f ? max(share(top_p, total, true), (u64)1) : 1;
+      };
+      u32 first, last;
+      row.window(least, most, 0, [&](u64 lo, u64 hi, u64& a, u64& b) {
+        a = share_of(lo);
+        b = share_of(hi);
+      }, first, last);
+      last = min(last, limit);
+      u64 front = 0, total = 0;
+      const auto add = [&](float x, u32) {
+        const u64 w = row.weight(x);
+        total += w;
+        front += Row<T>::bin_of(fminf(row.weight.distance(x), kRange)) < first ? w : 0;
+      };
+      if (cut) row.slice.some(inside_of, add);
+      else row.slice.each(add);
+      Found f = row.tokens(c, first, last);
+      f.before_weight = row.cluster_sum(front);
+      cut_at(row.resolve(first, last, f, true, share_of(row.cluster_sum(total))));
     }
   }
-  const double least = ceil(fmin((double)min_p, 1.0) * 17592186044416.0);  // 2^44
-  const u64 floor_weight = least > 1.0 ? (u64)least : 1;
-  const auto kept = [&](float x, u32 at) -> u64 {
-    const u32 k = key_of(x);
-    if (k < last_key || (k == last_key && at > last_at)) return 0;
+  if (min_p > 0.f) floor_weight = min_p < 1.f ? share(min_p, 1ull << 44, true) : 1ull << 44;
+  u64 sum = 0;
+  const auto add = [&](float x, u32) {
     const u64 w = row.weight(x);
-    return w >= floor_weight ? w : 0;
+    sum += w >= floor_weight ? w : 0;
   };
-  u64 sum = 0, before = 0, total = 0;
-  row.slice.each([&](float x, u32 at) { sum += kept(x, at); });
-  sum = row.block_sum(sum);
-  row.exchange(sum, [&](unsigned i, u64 o) {
-    if (i < rank) before += o;
-    total += o;
-  });
-  const double goal = u > 0.f ? (double)u * (double)total : 0.0;
-  const u64 target = goal >= (double)total ? total - 1 : min((u64)goal, total - 1);
-  u32 at;
-  u64 w;
-  if (before <= target && target < before + sum && row.select(target, before, kept, at, w)) {
+  if (cut) row.slice.some(inside_of, add);
+  else row.slice.each(add);
+  u64 all;
+  const u64 inside = row.scan(sum, all), of_block = row.exchange(all);
+  const u64 front = row.in_front(of_block), total = warp_sum(of_block);
+  const u64 target = u > 0.f ? (u < 1.f ? share(u, total, false) : total - 1) : 0;
+  row.select(target, front + inside, sum, kept, [&](u32 at, u64 w) {
     p.token[r] = (int32_t)at - shift;
-    if (p.logprob) p.logprob[r] = (float)log((double)w / (double)total);
-  }
+    if (p.logprob) {
+      // the quotient's fp32 value, and what that leaves
+      const double q = (double)w / (double)total;
+      const float f = (float)q;
+      p.logprob[r] = logf(f) + (float)(q - (double)f) / f;
+    }
+  });
   row.cluster.sync();  // no block leaves while another reads its box
 }
 
@@ -540,14 +721,21 @@ template <typename T>
 int launch(const SampleArgs& a, cudaStream_t s) {
   constexpr int N = Vec<T>::N;
   const int vecs = (a.vocab + N - 1) / N + 1;  // one more where the row starts off a boundary
-  const int blocks = vecs <= kThreads ? 1 : kMaxCluster;
-  const int of_block = (vecs + blocks - 1) / blocks;
-  const size_t bytes = sizeof(Shared) + (size_t)of_block * 16;
+  const auto share = [&](int blocks) { return (vecs + blocks - 1) / blocks; };
+  const auto memory = [&](int blocks) { return sizeof(Shared) + (size_t)share(blocks) * 16; };
+  // Eight blocks a row, unless fewer still give every SM two (256 rows of 151,936 bf16 logits, top-p:
+  // 423 us with eight, 299 with four; fp32, of which four leave an SM one block: 457 and 478) or the
+  // row is short.
+  int blocks = kMaxCluster;
+  while (blocks > 1 && (vecs <= kThreads || ((int64_t)a.num_rows * blocks / 2 >= 2 * 152 &&
+                                             2 * (memory(blocks / 2) + 1024) <= kMostMemory + 1024)))
+    blocks /= 2;
+  const int of_block = share(blocks);
+  const size_t bytes = memory(blocks);
   static std::atomic<int> done[kMaxDevices];
   const int e = configure_once(done, [] {
-    const size_t most = sizeof(Shared) + ((size_t)(kMaxVocab / N + 1 + kMaxCluster - 1) / kMaxCluster) * 16;
     return (int)cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)most);
+                                     (int)kMostMemory);
   });
   if (e != 0) return e;
   cudaLaunchConfig_t cfg = {};
