@@ -16,6 +16,9 @@
 namespace gdn {
 namespace {
 
+#ifndef NV
+#define NV 2
+#endif
 constexpr float kMinScale = 0x1p-100f, kTop = 448.f;
 
 // 8 elements: 16 bytes of bf16, 32 of fp32
@@ -146,12 +149,16 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(NormArgs p, int team) {
       for (int e = 0; e < 8; ++e) w[e] += p.cfg.weight_offset;
     }
     float g[8];
-    if (p.gate) gate[i].values(g);
+    if (p.gate) {
+      gate[i].values(g);
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) unpair(silu(pair(g[e], g[e + 1])), g[e], g[e + 1]);
+    }
     top[i] = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       float v = s[i][e] * inv * w[e];
-      if (p.gate) v *= silu(g[e]);
+      if (p.gate) v *= g[e];
       s[i][e] = v;
       const float m = fabsf(v);
       if (e < count[i] && m <= 3.4028234e38f) top[i] = fmaxf(top[i], m);
@@ -198,7 +205,7 @@ int launch_rows(const NormArgs& a, int team, cudaStream_t s) {
 template <typename T, bool HEADS>
 int launch(const NormArgs& a, cudaStream_t s) {
   const int vecs = (a.cfg.num_heads * a.cfg.dim + 7) / 8;
-  int vpt = a.num_tokens > 1024 ? (int)(8 / sizeof(T)) : 1;  // 64 bytes of a thread's row
+  int vpt = a.num_tokens > 1024 ? NV : 1;  // 64 bytes of a thread's row
   while (vecs > 1024 * vpt) vpt *= 2;
   int team = 32;
   while (team * vpt < vecs) team *= 2;

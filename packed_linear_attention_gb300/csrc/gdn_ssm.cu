@@ -23,42 +23,6 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr float kLog2e = 1.4426950408889634f;
-
-using f32x2 = unsigned long long;  // two fp32 in a register pair
-__device__ __forceinline__ f32x2 pair(float lo, float hi) {
-  f32x2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void unpair(f32x2 p, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-  f32x2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ f32x2 ex2(f32x2 x) {
-  float lo, hi;
-  unpair(x, lo, hi);
-  return pair(ex2(lo), ex2(hi));
-}
 
 // exp of dt times a rate (held times log2 e). Just below 0 the ex2 instruction errs low by 2e-8 on
 // average, which slow decays would sum up; 3e-8 in its argument leaves 5e-9 (and 2^0 at 1).
@@ -66,18 +30,11 @@ constexpr float kNudge = 3e-8f;
 __device__ __forceinline__ f32x2 decay(f32x2 dt, f32x2 a) {
   return ex2(fma2(dt, a, pair(kNudge, kNudge)));
 }
-__device__ __forceinline__ float rcp(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
 // log(1 + exp(x)) = max(x, 0) + log1p(e), e = exp(-|x|) in (0, 1]. log1p(e) is e times a polynomial
 // fitted to log1p(e) / e (least squares, reweighted towards an even relative error, 3e-8), so that
 // small values keep their relative precision.
 __device__ constexpr float kLog1p[9] = {0.99999994f,  -0.49999493f, 0.33319095f,   -0.24842976f, 0.1910598f,
                              -0.13663195f, 0.07822535f,  -0.029504869f, 0.0052326024f};
-__device__ __forceinline__ f32x2 both(float v) { return pair(v, v); }
 __device__ __forceinline__ f32x2 softplus(f32x2 x) {
   float x0, x1;
   unpair(x, x0, x1);
@@ -92,14 +49,6 @@ __device__ __forceinline__ float softplus(float x) {
   unpair(softplus(pair(x, x)), a, b);
   return a;
 }
-// v / (1 + exp(-v)); past 2^126 the reciprocal is 0, and so is the result to 1e-36
-__device__ __forceinline__ float gate(float v) { return v * rcp(1.f + ex2(-kLog2e * v)); }
-__device__ __forceinline__ f32x2 gate(f32x2 v) {
-  float a, b;
-  unpair(add2(ex2(mul2(v, both(-kLog2e))), both(1.f)), a, b);
-  return mul2(v, pair(rcp(a), rcp(b)));
-}
-
 // The states of one thread: NS of channel c, chunks of four that the SPLIT lanes take in turn
 // (so that the lanes' reads of b and c in shared memory lie side by side).
 template <int NS, int SPLIT>
@@ -381,7 +330,7 @@ struct Scan {
         for (int i = 0; i < kVecs; ++i) h.v[i].raw = sm.z[i][threadIdx.x];
         h.values(f);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sum[i] = mul2(sum[i], gate(pair(f[2 * i], f[2 * i + 1])));
+        for (int i = 0; i < 4; ++i) sum[i] = mul2(sum[i], silu(pair(f[2 * i], f[2 * i + 1])));
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) unpair(sum[i], out[2 * i], out[2 * i + 1]);
@@ -578,7 +527,7 @@ __global__ void __launch_bounds__(kThreads) ssm_step_kernel(SsmArgs p, int chann
   if (part == 0) {
     if (p.cfg.d) sum = fmaf(__ldg(p.cfg.d + ch), x, sum);
     if (p.rows.z)
-      sum *= gate(to_f32(static_cast<const T*>(p.rows.z)[(size_t)row * p.rows.z_stride + ch]));
+      sum *= silu(to_f32(static_cast<const T*>(p.rows.z)[(size_t)row * p.rows.z_stride + ch]));
     static_cast<T*>(p.rows.y)[(size_t)row * p.rows.y_stride + ch] = from_f32<T>(sum);
   }
 }
