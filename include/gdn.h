@@ -737,7 +737,7 @@ typedef enum gdn_activation { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1 } gdn_activatio
  * summed in fp32 and rounded once. Rows in front of a request's first come from its state: the
  * last width - 1 inputs of the request so far, oldest first, [width - 1][channels] io_dtype. */
 typedef struct gdn_conv_config {
-  int32_t channels;     /* C >= 1 */
+  int32_t channels;     /* C, 1 .. 262,144 */
   int32_t width;        /* taps, 2 .. 4 */
   int32_t activation;   /* gdn_activation; silu(v) = v / (1 + exp(-v)) */
   int32_t io_dtype;     /* gdn_dtype of x, y and the states */
@@ -751,7 +751,7 @@ typedef struct gdn_conv_config {
  *  ckpt_states [num_ckpt][width - 1][C] io_dtype, or NULL without checkpoints.
  * Pointers 16-byte aligned, strides multiples of 16 bytes and at least C (so x may be a column
  * range of a projection's output). Results do not depend on the pack around a request.
- * Errors: INVALID_ARGUMENT, UNSUPPORTED (width, more than 4,096 requests), CUDA. */
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED (width, channels, more than 4,096 requests), CUDA. */
 gdn_status gdn_conv_packed(gdn_handle* handle, const gdn_conv_config* cfg,
                            const gdn_requests* req, const void* x, int64_t x_stride, void* y,
                            int64_t y_stride, void* state_pool, void* ckpt_states,
@@ -771,7 +771,7 @@ gdn_status gdn_conv_step(gdn_handle* handle, const gdn_conv_config* cfg, int32_t
  *     y[t][c] = (sum_n c[t][g][n] * h[n] + d[c] * x[t][c]) * silu(z[t][c])
  * in fp32, y rounded once; states fp32 [C][state_dim]. */
 typedef struct gdn_ssm_config {
-  int32_t channels;        /* C >= 1, a multiple of num_groups */
+  int32_t channels;        /* C, 1 .. 262,144, a multiple of num_groups */
   int32_t num_groups;
   int32_t state_dim;       /* N, 1 .. 128 */
   int32_t io_dtype;        /* gdn_dtype of x, delta, b, c, z and y */
@@ -809,7 +809,7 @@ gdn_status gdn_ssm_workspace_size(const gdn_ssm_config* cfg, const gdn_requests*
  * kernel finds each segment's end state from zeros and its decay, a second runs the segments
  * from the joined states; results then differ from the uncut ones by fp32 rounding. The same call
  * gives the same bits. Inputs that are not finite spoil their own channel of their own request.
- * Errors: INVALID_ARGUMENT, UNSUPPORTED (state_dim above 128, more than 4,096 requests),
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED (state_dim above 128, channels, more than 4,096 requests),
  * WORKSPACE_TOO_SMALL, CUDA. */
 gdn_status gdn_ssm_packed(gdn_handle* handle, const gdn_ssm_config* cfg, const gdn_requests* req,
                           const gdn_ssm_rows* rows, float* state_pool, float* ckpt_states,

@@ -16,32 +16,48 @@
 namespace gdn {
 namespace {
 
-#ifndef NV
-#define NV 2
-#endif
 constexpr float kMinScale = 0x1p-100f, kTop = 448.f;
 
-// 8 elements: 16 bytes of bf16, 32 of fp32
+// 8 elements as they lie in memory: 16 bytes of bf16, 32 of fp32. `count` of them are the row's; WHOLE:
+// all 8 or none.
 template <typename T>
 struct Eight {
-  Vec<T> v[8 / Vec<T>::N];
-  __device__ __forceinline__ Eight(const T* p, int count) {
+  static constexpr int kVecs = 8 / Vec<T>::N;
+  Vec<T> v[kVecs];
+  template <bool WHOLE>
+  __device__ __forceinline__ void load(const T* p, int count) {
 #pragma unroll
-    for (int i = 0; i < 8 / Vec<T>::N; ++i)
-      v[i] = load_vec(p + i * Vec<T>::N, count - i * Vec<T>::N, count >= 8);
+    for (int i = 0; i < kVecs; ++i) {
+      if constexpr (WHOLE) {
+        v[i].raw = make_uint4(0, 0, 0, 0);
+        if (count > 0) v[i].raw = reinterpret_cast<const uint4*>(p)[i];
+      } else {
+        v[i] = load_vec(p + i * Vec<T>::N, count - i * Vec<T>::N, count >= 8);
+      }
+    }
   }
-  __device__ __forceinline__ Eight() {}
-  __device__ __forceinline__ void values(float* f) const {
+  __device__ __forceinline__ void values(f32x2* f) const {
+    float x[8];
 #pragma unroll
-    for (int i = 0; i < 8 / Vec<T>::N; ++i) unpack(v[i], f + i * Vec<T>::N);
+    for (int i = 0; i < kVecs; ++i) unpack(v[i], x + i * Vec<T>::N);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = pair(x[2 * i], x[2 * i + 1]);
+  }
+  template <bool WHOLE>
+  __device__ __forceinline__ static void store(T* p, int count, const f32x2* f) {
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) unpair(f[i], x[2 * i], x[2 * i + 1]);
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      if constexpr (WHOLE) {
+        if (count > 0) reinterpret_cast<uint4*>(p)[i] = pack<T>(x + i * Vec<T>::N).raw;
+      } else {
+        store_vec(p + i * Vec<T>::N, pack<T>(x + i * Vec<T>::N), count - i * Vec<T>::N, count >= 8);
+      }
+    }
   }
 };
-template <typename T>
-__device__ __forceinline__ void store8(T* p, int count, const float* f) {
-  constexpr int N = Vec<T>::N;
-#pragma unroll
-  for (int i = 0; i < 8; i += N) store_vec(p + i, pack<T>(f + i), count - i, count >= 8);
-}
 
 // Sum (or maximum) over `width` neighbouring lanes.
 template <bool MAX>
@@ -65,15 +81,19 @@ __device__ __forceinline__ float team_reduce(float v, int team, float* shared) {
   return r;
 }
 
-// The scale of values up to `top`: top / 448, or the least power of two at least that.
-__device__ __forceinline__ float scale_of(float top, bool pow2) {
+// The scale of values up to `top` and its reciprocal: top / 448, or the least power of two at least
+// that.
+__device__ __forceinline__ void scale_of(float top, bool pow2, float& scale, float& inv) {
   if (pow2) {
     // top = m 2^e, m in [1, 2): 448 is 1.75 2^8
     const uint32_t bits = __float_as_uint(top);
-    const int e = (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u);
-    return e <= -100 ? kMinScale : __uint_as_float((uint32_t)(e + 127) << 23);
+    const int e = max(-100, (int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u));
+    scale = __uint_as_float((uint32_t)(127 + e) << 23);
+    inv = __uint_as_float((uint32_t)(127 - e) << 23);
+  } else {
+    scale = fmaxf(top * (1.f / kTop), kMinScale);
+    inv = rcp(scale);
   }
-  return fmaxf(__fdiv_rn(top, kTop), kMinScale);
 }
 
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
@@ -83,8 +103,8 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return lo | (uint32_t)hi << 16;
 }
 
-// HEADS: heads of `dim` elements, each by itself; else the row is one.
-template <typename T, int VPT, bool HEADS, int THREADS>
+// HEADS: heads of `dim` elements, each by itself; else the row is one. WHOLE: rows of a multiple of 8.
+template <typename T, int VPT, bool HEADS, bool WHOLE, int THREADS>
 __global__ void __launch_bounds__(THREADS) norm_kernel(NormArgs p, int team) {
   __shared__ float sums[32], tops[32];
   const int rows = blockDim.x / team;
@@ -93,7 +113,8 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(NormArgs p, int team) {
   const int width = p.cfg.num_heads * p.cfg.dim;
   const bool live = row < p.num_tokens;
   const int64_t r = live ? row : p.num_tokens - 1;
-  float s[VPT][8], sum[VPT];
+  f32x2 s[VPT][4];
+  float sum[VPT];
   int count[VPT];
   Eight<T> gate[VPT];
   {
@@ -102,69 +123,78 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(NormArgs p, int team) {
     for (int i = 0; i < VPT; ++i) {
       const int c = (i * team + me) * 8;
       count[i] = max(0, min(8, width - c));
-      x[i] = Eight<T>(static_cast<const T*>(p.x) + r * p.x_stride + c, count[i]);
+      x[i].template load<WHOLE>(static_cast<const T*>(p.x) + r * p.x_stride + c, count[i]);
       if (p.residual)
-        residual[i] = Eight<T>(static_cast<const T*>(p.residual) + r * p.residual_stride + c, count[i]);
+        residual[i].template load<WHOLE>(static_cast<const T*>(p.residual) + r * p.residual_stride + c, count[i]);
       if (p.gate)
-        gate[i] = Eight<T>(static_cast<const T*>(p.gate) + r * p.gate_stride + c, count[i]);
+        gate[i].template load<WHOLE>(static_cast<const T*>(p.gate) + r * p.gate_stride + c, count[i]);
     }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       x[i].values(s[i]);
       if (p.residual) {
-        float f[8];
+        f32x2 f[4];
         residual[i].values(f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s[i][e] += f[e];
+        for (int e = 0; e < 4; ++e) s[i][e] = add2(s[i][e], f[e]);
       }
     }
   }
   float all = 0.f;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
-    sum[i] = 0.f;
+    f32x2 q = mul2(s[i][0], s[i][0]);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sum[i] = fmaf(s[i][e], s[i][e], sum[i]);
+    for (int e = 1; e < 4; ++e) q = fma2(s[i][e], s[i][e], q);
+    float lo, hi;
+    unpair(q, lo, hi);
+    sum[i] = lo + hi;
     if (HEADS) sum[i] = lanes<false>(sum[i], p.cfg.dim / 8);
     all += sum[i];
+    if (p.sum && live)
+      Eight<T>::template store<WHOLE>(static_cast<T*>(p.sum) + r * p.sum_stride + (i * team + me) * 8, count[i], s[i]);
   }
   if (!HEADS) all = team_reduce<false>(all, team, sums);
   const float inv_dim = 1.f / (float)p.cfg.dim;
-  if (p.sum && live) {
-#pragma unroll
-    for (int i = 0; i < VPT; ++i)
-      store8(static_cast<T*>(p.sum) + r * p.sum_stride + (i * team + me) * 8, count[i], s[i]);
-  }
   float top[VPT], row_top = 0.f;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int c = (i * team + me) * 8;
-    const float inv = rsqrtf(fmaf(HEADS ? sum[i] : all, inv_dim, p.cfg.eps));
-    float w[8];
+    const f32x2 inv = both(rsqrtf(fmaf(HEADS ? sum[i] : all, inv_dim, p.cfg.eps)));
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = 1.f;
-    if (p.cfg.weight && count[i] > 0) {
-      Eight<float>(p.cfg.weight + (HEADS ? c % p.cfg.dim : c), count[i]).values(w);
+    for (int e = 0; e < 4; ++e) s[i][e] = mul2(s[i][e], inv);
+    if (p.cfg.weight) {
+      Eight<float> raw;
+      f32x2 w[4];
+      raw.load<WHOLE>(p.cfg.weight + (HEADS ? c % p.cfg.dim : c), count[i]);
+      raw.values(w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] += p.cfg.weight_offset;
+      for (int e = 0; e < 4; ++e) s[i][e] = mul2(s[i][e], add2(w[e], both(p.cfg.weight_offset)));
     }
-    float g[8];
     if (p.gate) {
+      f32x2 g[4];
       gate[i].values(g);
 #pragma unroll
-      for (int e = 0; e < 8; e += 2) unpair(silu(pair(g[e], g[e + 1])), g[e], g[e + 1]);
+      for (int e = 0; e < 4; ++e) s[i][e] = mul2(s[i][e], silu(g[e]));
     }
+    if (p.y && live)
+      Eight<T>::template store<WHOLE>(static_cast<T*>(p.y) + r * p.y_stride + c, count[i], s[i]);
+    if (!p.codes) continue;
+    // the largest finite value (what lies past the row is 0, or the weights' NaN times it)
+    float v[8];
     top[i] = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float v = s[i][e] * inv * w[e];
-      if (p.gate) v *= g[e];
-      s[i][e] = v;
-      const float m = fabsf(v);
-      if (e < count[i] && m <= 3.4028234e38f) top[i] = fmaxf(top[i], m);
+    for (int e = 0; e < 4; ++e) {
+      unpair(s[i][e], v[2 * e], v[2 * e + 1]);
+      top[i] = fmaxf(top[i], fmaxf(fabsf(v[2 * e]), fabsf(v[2 * e + 1])));
+    }
+    if (top[i] == INFINITY) {
+      top[i] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (fabsf(v[e]) < INFINITY) top[i] = fmaxf(top[i], fabsf(v[e]));
     }
     row_top = fmaxf(row_top, top[i]);
-    if (p.y && live) store8(static_cast<T*>(p.y) + r * p.y_stride + c, count[i], s[i]);
   }
   if (!p.codes) return;
   const int group = p.cfg.scale_group;
@@ -174,18 +204,21 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(NormArgs p, int team) {
   for (int i = 0; i < VPT; ++i) {
     const int c = (i * team + me) * 8;
     const float t = group == 0 ? row_top : lanes<true>(top[i], group / 8);
-    const float scale = scale_of(t, p.cfg.scale_pow2 != 0);
-    const float inv = __fdiv_rn(1.f, scale);
+    float scale, inv;
+    scale_of(t, p.cfg.scale_pow2 != 0, scale, inv);
     if (!live || count[i] == 0) continue;
     if (group == 0) {
       if (c == 0) p.scales[r] = scale;
-    } else if (c % group == 0) {
+    } else if ((c & (group - 1)) == 0) {
       p.scales[r * (width / group) + c / group] = scale;
     }
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) unpair(mul2(s[i][e], both(inv)), v[2 * e], v[2 * e + 1]);
     uint2 q;
-    q.x = e4m3x4(s[i][0] * inv, s[i][1] * inv, s[i][2] * inv, s[i][3] * inv);
-    q.y = e4m3x4(s[i][4] * inv, s[i][5] * inv, s[i][6] * inv, s[i][7] * inv);
-    if (count[i] == 8) {
+    q.x = e4m3x4(v[0], v[1], v[2], v[3]);
+    q.y = e4m3x4(v[4], v[5], v[6], v[7]);
+    if (WHOLE || count[i] == 8) {
       *reinterpret_cast<uint2*>(codes + c) = q;
     } else {
       for (int e = 0; e < count[i]; ++e) codes[c + e] = (uint8_t)((e < 4 ? q.x : q.y) >> (8 * (e & 3)));
@@ -193,28 +226,36 @@ __global__ void __launch_bounds__(THREADS) norm_kernel(NormArgs p, int team) {
   }
 }
 
-template <typename T, int VPT, bool HEADS>
+template <typename T, int VPT, bool HEADS, bool WHOLE>
 int launch_rows(const NormArgs& a, int team, cudaStream_t s) {
   const int threads = std::max(team, 128), rows = threads / team;
   const unsigned grid = (unsigned)((a.num_tokens + (int64_t)rows - 1) / rows);
-  if (threads <= 256) norm_kernel<T, VPT, HEADS, 256><<<grid, threads, 0, s>>>(a, team);
-  else norm_kernel<T, VPT, HEADS, 1024><<<grid, threads, 0, s>>>(a, team);
+  if (threads <= 256) norm_kernel<T, VPT, HEADS, WHOLE, 256><<<grid, threads, 0, s>>>(a, team);
+  else norm_kernel<T, VPT, HEADS, WHOLE, 1024><<<grid, threads, 0, s>>>(a, team);
   return (int)cudaGetLastError();
 }
 
-template <typename T, bool HEADS>
+template <typename T, bool HEADS, bool WHOLE>
 int launch(const NormArgs& a, cudaStream_t s) {
   const int vecs = (a.cfg.num_heads * a.cfg.dim + 7) / 8;
-  int vpt = a.num_tokens > 1024 ? NV : 1;  // 64 bytes of a thread's row
+  // Few rows: as many threads a row as there are vectors. Many: two or four vectors a thread (32,768
+  // rows of 2,048 with residual and codes: 121 us with one, 92 with two, 98 with four; 32 gated heads
+  // of 128: 171, 152 and 146).
+  int vpt = a.num_tokens <= 1024 ? 1 : HEADS && sizeof(T) == 2 ? 4 : 2;
   while (vecs > 1024 * vpt) vpt *= 2;
   int team = 32;
   while (team * vpt < vecs) team *= 2;
   switch (vpt) {
-    case 1: return launch_rows<T, 1, HEADS>(a, team, s);
-    case 2: return launch_rows<T, 2, HEADS>(a, team, s);
-    case 4: return launch_rows<T, 4, HEADS>(a, team, s);
+    case 1: return launch_rows<T, 1, HEADS, WHOLE>(a, team, s);
+    case 2: return launch_rows<T, 2, HEADS, WHOLE>(a, team, s);
+    case 4: return launch_rows<T, 4, HEADS, WHOLE>(a, team, s);
   }
   return (int)cudaErrorInvalidValue;
+}
+template <typename T>
+int launch(const NormArgs& a, cudaStream_t s) {
+  if (a.cfg.num_heads > 1) return launch<T, true, true>(a, s);  // heads are multiples of 8
+  return a.cfg.dim % 8 == 0 ? launch<T, false, true>(a, s) : launch<T, false, false>(a, s);
 }
 
 }  // namespace
@@ -222,9 +263,7 @@ int launch(const NormArgs& a, cudaStream_t s) {
 int launch_rms_norm(const NormArgs& a, void* stream) {
   if (a.num_tokens == 0) return 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (a.cfg.io_dtype == GDN_BF16)
-    return a.cfg.num_heads > 1 ? launch<__nv_bfloat16, true>(a, s) : launch<__nv_bfloat16, false>(a, s);
-  return a.cfg.num_heads > 1 ? launch<float, true>(a, s) : launch<float, false>(a, s);
+  return a.cfg.io_dtype == GDN_BF16 ? launch<__nv_bfloat16>(a, s) : launch<float>(a, s);
 }
 
 }  // namespace gdn

@@ -45,10 +45,13 @@ __device__ __forceinline__ f32x2 softplus(f32x2 x) {
   return fma2(e, p, pair(fmaxf(x0, 0.f), fmaxf(x1, 0.f)));
 }
 __device__ __forceinline__ float softplus(float x) {
-  float a, b;
-  unpair(softplus(pair(x, x)), a, b);
-  return a;
+  const float e = ex2(-kLog2e * fabsf(x));
+  float p = kLog1p[8];
+#pragma unroll
+  for (int i = 7; i >= 0; --i) p = fmaf(e, p, kLog1p[i]);
+  return fmaf(e, p, fmaxf(x, 0.f));
 }
+
 // The states of one thread: NS of channel c, chunks of four that the SPLIT lanes take in turn
 // (so that the lanes' reads of b and c in shared memory lie side by side).
 template <int NS, int SPLIT>
@@ -462,73 +465,79 @@ __global__ void __launch_bounds__(kThreads, kResident<T, SPLIT>) ssm_kernel(SsmA
   else if (pass == 1) scan.s.store(p.ends + scan.state_row(ends + k), scan.part, n);
 }
 
-// One token: LANES lanes a channel, four states each, so that a state goes through as 16-byte
-// accesses side by side. Bound by HBM (the states, in and out).
+// One token: LANES lanes a channel, eight states each (32 bytes, a sector of memory), so that a state
+// goes through as accesses side by side while a channel's own work (softplus, gate, addresses) is
+// repeated by as few lanes as that allows. Bound by HBM (the states, in and out).
 template <typename T>
-__device__ __forceinline__ float4 load_four(const T* p, int count, bool aligned) {
-  float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (aligned && count >= 4) {
-    if (sizeof(T) == 4) return *reinterpret_cast<const float4*>(p);
-    const uint2 w = *reinterpret_cast<const uint2*>(p);
-    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
-                       __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+__device__ __forceinline__ void load_eight(const T* p, int count, bool aligned, f32x2* f) {
+  float x[8];
+  if (aligned && count >= 8) {
+#pragma unroll
+    for (int i = 0; i < 8 / Vec<T>::N; ++i)
+      unpack(Vec<T>{reinterpret_cast<const uint4*>(p)[i]}, x + i * Vec<T>::N);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = i < count ? to_f32(p[i]) : 0.f;
   }
-  if (count > 0) f.x = to_f32(p[0]);
-  if (count > 1) f.y = to_f32(p[1]);
-  if (count > 2) f.z = to_f32(p[2]);
-  if (count > 3) f.w = to_f32(p[3]);
-  return f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = pair(x[2 * i], x[2 * i + 1]);
 }
 
 template <typename T, int LANES>
-__global__ void __launch_bounds__(kThreads) ssm_step_kernel(SsmArgs p, int channel_blocks,
-                                                            bool aligned) {
-  const int row = blockIdx.x / channel_blocks;
-  const int c = blockIdx.x % channel_blocks * (kThreads / LANES) + (int)threadIdx.x / LANES;
-  const int part = threadIdx.x % LANES, n0 = 4 * part, n = p.cfg.state_dim;
+__global__ void __launch_bounds__(kThreads) ssm_step_kernel(SsmArgs p, bool aligned) {
+  const int row = blockIdx.x;
+  const int c = blockIdx.y * (kThreads / LANES) + (int)threadIdx.x / LANES;
+  const int n0 = threadIdx.x % LANES * 8, n = p.cfg.state_dim;
   const int slot = p.req.slot_idx[row];
+  const bool live = c < p.cfg.channels;
+  const int ch = min(c, p.cfg.channels - 1), count = n - n0;
+  const int group = p.cfg.num_groups == 1 ? 0 : ch / (p.cfg.channels / p.cfg.num_groups);
+  const bool whole = n % 8 == 0;
+  const float x = to_f32(static_cast<const T*>(p.rows.x)[row * p.rows.x_stride + ch]);
+  float dt = to_f32(static_cast<const T*>(p.rows.delta)[row * p.rows.delta_stride + ch]);
+  const float z = p.rows.z ? to_f32(static_cast<const T*>(p.rows.z)[row * p.rows.z_stride + ch]) : 0.f;
+  f32x2 a[4], b[4], cc[4], h[4];
+  load_eight(p.cfg.a + (size_t)ch * n + n0, count, whole, a);
+  load_eight(static_cast<const T*>(p.rows.b) + row * p.rows.b_stride + group * n + n0, count, aligned, b);
+  load_eight(static_cast<const T*>(p.rows.c) + row * p.rows.c_stride + group * n + n0, count, aligned, cc);
   if (slot < 0 || slot >= p.req.num_slots) {
-    if (slot >= 0) raise_status(p.status, GDN_ERR_INVALID_ARGUMENT);
+    if (slot >= 0 && blockIdx.y == 0 && threadIdx.x == 0) raise_status(p.status, GDN_ERR_INVALID_ARGUMENT);
     return;
   }
-  const bool live = c < p.cfg.channels;
-  const int ch = min(c, p.cfg.channels - 1);
-  const int count = n - n0;
   float* state = p.pool + ((size_t)slot * p.cfg.channels + ch) * n + n0;
-  const bool whole = n % 4 == 0;
-  float4 h = load_four(state, count, whole);
-  const float4 a = load_four(p.cfg.a + (size_t)ch * n + n0, count, whole);
-  const int group = ch / (p.cfg.channels / p.cfg.num_groups);
-  const float4 b = load_four(
-      static_cast<const T*>(p.rows.b) + (size_t)row * p.rows.b_stride + group * n + n0, count, aligned);
-  const float4 cc = load_four(
-      static_cast<const T*>(p.rows.c) + (size_t)row * p.rows.c_stride + group * n + n0, count, aligned);
-  const float x = to_f32(static_cast<const T*>(p.rows.x)[(size_t)row * p.rows.x_stride + ch]);
-  float dt = to_f32(static_cast<const T*>(p.rows.delta)[(size_t)row * p.rows.delta_stride + ch]);
+  load_eight(state, count, whole, h);
   if (p.cfg.delta_bias) dt += __ldg(p.cfg.delta_bias + ch);
   if (p.cfg.delta_softplus) dt = softplus(dt);
-  const float dtx = dt * x;
-  h.x = fmaf(ex2(fmaf(dt, kLog2e * a.x, kNudge)), h.x, dtx * b.x);
-  h.y = fmaf(ex2(fmaf(dt, kLog2e * a.y, kNudge)), h.y, dtx * b.y);
-  h.z = fmaf(ex2(fmaf(dt, kLog2e * a.z, kNudge)), h.z, dtx * b.z);
-  h.w = fmaf(ex2(fmaf(dt, kLog2e * a.w, kNudge)), h.w, dtx * b.w);
-  float sum = fmaf(cc.x, h.x, cc.y * h.y) + fmaf(cc.z, h.z, cc.w * h.w);
+  const f32x2 t = both(kLog2e * dt), u = both(dt * x);
+  f32x2 acc = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    h[i] = fma2(decay(t, a[i]), h[i], mul2(u, b[i]));
+    acc = i == 0 ? mul2(cc[i], h[i]) : fma2(cc[i], h[i], acc);
+  }
+  float sum, hi;
+  unpair(acc, sum, hi);
+  sum += hi;
 #pragma unroll
   for (int off = LANES / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
   if (!live) return;
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) unpair(h[i], f[2 * i], f[2 * i + 1]);
   if (whole) {
-    if (count >= 4) *reinterpret_cast<float4*>(state) = h;
+    if (count >= 8) {
+      reinterpret_cast<float4*>(state)[0] = make_float4(f[0], f[1], f[2], f[3]);
+      reinterpret_cast<float4*>(state)[1] = make_float4(f[4], f[5], f[6], f[7]);
+    }
   } else {
-    if (count > 0) state[0] = h.x;
-    if (count > 1) state[1] = h.y;
-    if (count > 2) state[2] = h.z;
-    if (count > 3) state[3] = h.w;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < count) state[i] = f[i];
   }
-  if (part == 0) {
+  if (n0 == 0) {
     if (p.cfg.d) sum = fmaf(__ldg(p.cfg.d + ch), x, sum);
-    if (p.rows.z)
-      sum *= silu(to_f32(static_cast<const T*>(p.rows.z)[(size_t)row * p.rows.z_stride + ch]));
-    static_cast<T*>(p.rows.y)[(size_t)row * p.rows.y_stride + ch] = from_f32<T>(sum);
+    if (p.rows.z) sum *= silu(z);
+    static_cast<T*>(p.rows.y)[row * p.rows.y_stride + ch] = from_f32<T>(sum);
   }
 }
 
@@ -589,25 +598,24 @@ int scan_by_shape(const SsmArgs& a, cudaStream_t s) {
 
 template <typename T, int LANES>
 int launch_one(const SsmArgs& a, cudaStream_t s) {
-  const int ch = kThreads / LANES, cb = (a.cfg.channels + ch - 1) / ch;
+  constexpr int ch = kThreads / LANES;
   const auto at = [](const void* p, int64_t stride) {
-    return reinterpret_cast<uintptr_t>(p) % (4 * sizeof(T)) == 0 && stride % 4 == 0;
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % (int64_t)(16 / sizeof(T)) == 0;
   };
   const bool aligned = at(a.rows.b, a.rows.b_stride) && at(a.rows.c, a.rows.c_stride) &&
-                       a.cfg.state_dim % 4 == 0;
-  ssm_step_kernel<T, LANES>
-      <<<(unsigned)((int64_t)a.req.num_tokens * cb), kThreads, 0, s>>>(a, cb, aligned);
+                       a.cfg.state_dim % 8 == 0;
+  const dim3 grid((unsigned)a.req.num_tokens, (unsigned)((a.cfg.channels + ch - 1) / ch));
+  ssm_step_kernel<T, LANES><<<grid, kThreads, 0, s>>>(a, aligned);
   return (int)cudaGetLastError();
 }
 template <typename T>
 int step_by_lanes(const SsmArgs& a, cudaStream_t s) {
   const int n = a.cfg.state_dim;
-  if (n <= 4) return launch_one<T, 1>(a, s);
-  if (n <= 8) return launch_one<T, 2>(a, s);
-  if (n <= 16) return launch_one<T, 4>(a, s);
-  if (n <= 32) return launch_one<T, 8>(a, s);
-  if (n <= 64) return launch_one<T, 16>(a, s);
-  return launch_one<T, 32>(a, s);
+  if (n <= 8) return launch_one<T, 1>(a, s);
+  if (n <= 16) return launch_one<T, 2>(a, s);
+  if (n <= 32) return launch_one<T, 4>(a, s);
+  if (n <= 64) return launch_one<T, 8>(a, s);
+  return launch_one<T, 16>(a, s);
 }
 
 }  // namespace

@@ -48,7 +48,7 @@ gdn_status check_conv(const gdn_conv_config* c) {
       !aligned(c->weight, 4) || !aligned(c->bias, 4) ||
       (c->activation != GDN_ACT_NONE && c->activation != GDN_ACT_SILU))
     return GDN_ERR_INVALID_ARGUMENT;
-  return c->width < 2 || c->width > 4 || c->channels > (1 << 24) ? GDN_ERR_UNSUPPORTED : GDN_OK;
+  return c->width < 2 || c->width > 4 ? GDN_ERR_UNSUPPORTED : GDN_OK;
 }
 
 gdn_status check_ssm(const gdn_ssm_config* c, bool arrays) {
@@ -58,7 +58,7 @@ gdn_status check_ssm(const gdn_ssm_config* c, bool arrays) {
   // a's rows and the states' are read 16 bytes at a time
   if (arrays && (!c->a || !aligned(c->a, 16) || !aligned(c->d, 4) || !aligned(c->delta_bias, 4)))
     return GDN_ERR_INVALID_ARGUMENT;
-  return c->state_dim > 128 || c->channels > (1 << 24) ? GDN_ERR_UNSUPPORTED : GDN_OK;
+  return c->state_dim > 128 ? GDN_ERR_UNSUPPORTED : GDN_OK;
 }
 
 // The rows of a scan: each array by itself, and y against the others.
@@ -91,7 +91,10 @@ gdn_status check_states(const void* pool, int64_t slots, const void* ckpt, int64
   return GDN_OK;
 }
 
-bool grid_ok(double blocks) { return blocks <= (double)INT32_MAX; }
+// What the kernels' grids take: blocks in all, and of a row's channels.
+bool grid_ok(int32_t channels, double blocks) {
+  return channels <= (1 << 18) && blocks <= (double)INT32_MAX;
+}
 
 // The host fields that say how a scan is cut, and its workspace.
 gdn_status plan_scan(const gdn_ssm_config* cfg, const gdn_requests* req, int32_t* segment,
@@ -137,7 +140,7 @@ gdn_status gdn_conv_packed(gdn_handle* h, const gdn_conv_config* cfg, const gdn_
       return GDN_ERR_INVALID_ARGUMENT;
   }
   // one block for every 32 rows and 512 channels at least (16 bytes of 128 threads)
-  if (!grid_ok((tokens / 32.0 + req->num_seqs) * (cfg->channels / 512.0 + 1))) return GDN_ERR_UNSUPPORTED;
+  if (!grid_ok(cfg->channels, (tokens / 32.0 + req->num_seqs) * (cfg->channels / 512.0 + 1))) return GDN_ERR_UNSUPPORTED;
   if (!h) return GDN_ERR_INVALID_ARGUMENT;
   const gdn::ConvArgs a = {*cfg, *req, x, y, x_stride, y_stride, state_pool, ckpt_states, status};
   return on_device(h, [&] { return gdn::launch_conv_packed(a, stream); });
@@ -163,7 +166,7 @@ gdn_status gdn_conv_step(gdn_handle* h, const gdn_conv_config* cfg, int32_t batc
         overlap(pool, span_of(y, batch, y_stride, cfg->channels, e)))
       return GDN_ERR_INVALID_ARGUMENT;
   }
-  if (!grid_ok((double)batch * (cfg->channels / 512.0 + 1))) return GDN_ERR_UNSUPPORTED;
+  if (!grid_ok(cfg->channels, (double)batch * (cfg->channels / 512.0 + 1))) return GDN_ERR_UNSUPPORTED;
   if (!h) return GDN_ERR_INVALID_ARGUMENT;
   gdn::ConvArgs a = {*cfg, {}, x, y, x_stride, y_stride, state_pool, nullptr, status};
   a.req.num_tokens = batch;
@@ -219,7 +222,7 @@ gdn_status gdn_ssm_packed(gdn_handle* h, const gdn_ssm_config* cfg, const gdn_re
   if (workspace_bytes < need) return GDN_ERR_WORKSPACE_TOO_SMALL;
   // blocks: of a group's channels 16 at least
   const double units = req->num_seqs + (segment ? (double)tokens / segment : 0.0);
-  if (!grid_ok(units * (cfg->channels / 16.0 + cfg->num_groups))) return GDN_ERR_UNSUPPORTED;
+  if (!grid_ok(cfg->channels, units * (cfg->channels / 16.0 + cfg->num_groups))) return GDN_ERR_UNSUPPORTED;
   if (!h) return GDN_ERR_INVALID_ARGUMENT;
   gdn::SsmArgs a = {*cfg, *req, *rows, state_pool, ckpt_states, static_cast<float*>(workspace),
                     reinterpret_cast<float*>(static_cast<char*>(workspace) + ends), segment, status};
@@ -249,7 +252,7 @@ gdn_status gdn_ssm_step(gdn_handle* h, const gdn_ssm_config* cfg, int32_t batch,
         (rows->z && overlap(pool, span_of(rows->z, batch, rows->z_stride, cfg->channels, e))))
       return GDN_ERR_INVALID_ARGUMENT;
   }
-  if (!grid_ok((double)batch * (cfg->channels / 4.0 + 1))) return GDN_ERR_UNSUPPORTED;
+  if (!grid_ok(cfg->channels, batch)) return GDN_ERR_UNSUPPORTED;
   if (!h) return GDN_ERR_INVALID_ARGUMENT;
   gdn::SsmArgs a = {*cfg, {}, *rows, state_pool, nullptr, nullptr, nullptr, 0, status};
   a.req.num_tokens = batch;
