@@ -144,9 +144,10 @@ template <typename T, int NS, int SPLIT>
 struct Scan {
   static constexpr int kPadded = NS * SPLIT;
   static constexpr int kCh = kThreads / SPLIT;
-  // a tile of 8 elements a thread, while b and c stay within 16 KB
-  static constexpr int kTile = SPLIT == 8 ? 16 : 8 * SPLIT;
-  static constexpr int kTasks = kTile * kCh / 8;
+  // 8 or 16 elements of a tile a thread, while b and c stay within 16 KB
+  static constexpr int kTile = SPLIT == 4 ? 32 : 16;
+  static constexpr int kAcross = kCh / 8, kStep = kThreads / kAcross;  // shares of a row; rows between a thread's
+  static constexpr int kShares = (kTile + kStep - 1) / kStep;          // of a thread
   static constexpr int kVecs = 8 / Vec<T>::N;
   static constexpr int kShare = (kTile * kPadded + kThreads - 1) / kThreads;  // of b and of c
   static constexpr bool kAhead = kShare <= 4;
@@ -155,7 +156,7 @@ struct Scan {
     float4 y[kTile][kCh / 4];  // at quad_at
     float b[kTile][kPadded], c[kTile][kPadded];
     float4 bias[kCh / 4], skip[kCh / 4];  // at quad_at
-    uint4 x[kVecs][kTasks], z[kVecs][kTasks];  // of the rows being scanned
+    uint4 x[kShares][kVecs][kThreads], z[kShares][kVecs][kThreads];  // of the rows being scanned
   };
   // Where 16 bytes of a row lie, so that neither the 8 channels of a thread's share nor the channels
   // of a warp's lanes meet in a bank: chunk q of pairs, chunk q of fours.
@@ -196,10 +197,10 @@ struct Scan {
     part = threadIdx.x % SPLIT;
     live = first + local < per;
     channel = group * per + min(first + local, per - 1);
-    task_row = threadIdx.x / (kCh / 8);
-    task_col = threadIdx.x % (kCh / 8) * 8;
+    task_row = threadIdx.x / kAcross;
+    task_col = threadIdx.x % kAcross * 8;
     task_channel = group * per + first + task_col;
-    count = threadIdx.x < kTasks ? max(0, min(8, per - first - task_col)) : 0;
+    count = max(0, min(8, per - first - task_col));
     whole = count == 8 && (p.cfg.num_groups == 1 || per % Vec<T>::N == 0);
     s.rates(p.cfg.a + (size_t)channel * p.cfg.state_dim, part, p.cfg.state_dim);
     my_f = 2 * pair_at(local / 2) + local % 2;
@@ -270,17 +271,24 @@ struct Scan {
     }
 
     // Addresses are worked out anew for each tile: registers are what is short while it is scanned.
-    auto row_of = [&](const void* base, int64_t stride, int t0) {
+    auto row_of = [&](const void* base, int64_t stride, int t) {
       int row = task_row;
       asm volatile("" : "+r"(row));
-      return static_cast<const T*>(base) + (int64_t)(span.lo + t0 + row) * stride + task_channel;
+      return static_cast<const T*>(base) + (int64_t)(span.lo + t + row) * stride + task_channel;
     };
-    Eight xn, dn, zn;  // the next tile's rows
+    // whether this thread has share i of the tile at t0
+    auto mine = [&](int i, int t0) {
+      return count > 0 && task_row + i * kStep < kTile && t0 + task_row + i * kStep < len;
+    };
+    Eight xn[kShares], dn[kShares], zn[kShares];  // the next tile's rows
     auto fetch = [&](int t0) {
-      if (t0 + task_row < len && count > 0) {
-        xn.load(row_of(p.rows.x, p.rows.x_stride, t0), count, whole);
-        dn.load(row_of(p.rows.delta, p.rows.delta_stride, t0), count, whole);
-        if (gated) zn.load(row_of(p.rows.z, p.rows.z_stride, t0), count, whole);
+#pragma unroll
+      for (int i = 0; i < kShares; ++i) {
+        if (mine(i, t0)) {
+          xn[i].load(row_of(p.rows.x, p.rows.x_stride, t0 + i * kStep), count, whole);
+          dn[i].load(row_of(p.rows.delta, p.rows.delta_stride, t0 + i * kStep), count, whole);
+          if (gated) zn[i].load(row_of(p.rows.z, p.rows.z_stride, t0 + i * kStep), count, whole);
+        }
       }
     };
     // this thread's 8 channels in a row of fours, as pairs
@@ -293,11 +301,11 @@ struct Scan {
       }
     };
     // dt and dt x of this thread's share
-    auto prepare = [&] {
+    auto prepare = [&](int s) {
       float xf[8], df[8];
       f32x2 bias[4];
-      xn.values(xf);
-      dn.values(df);
+      xn[s].values(xf);
+      dn[s].values(df);
       quads(sm.bias, bias);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -306,38 +314,38 @@ struct Scan {
         float4 f;
         unpair(dt, f.x, f.z);
         unpair(mul2(dt, pair(xf[2 * i], xf[2 * i + 1])), f.y, f.w);
-        sm.f[task_row][pair_at(task_col / 2 + i)] = f;
+        sm.f[task_row + s * kStep][pair_at(task_col / 2 + i)] = f;
       }
       if (OUT) {
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
-          sm.x[i][threadIdx.x] = xn.v[i].raw;
-          if (gated) sm.z[i][threadIdx.x] = zn.v[i].raw;
+          sm.x[s][i][threadIdx.x] = xn[s].v[i].raw;
+          if (gated) sm.z[s][i][threadIdx.x] = zn[s].v[i].raw;
         }
       }
     };
-    auto finish = [&](int t0) {
-      if (t0 + task_row >= len || count <= 0) return;
+    auto finish = [&](int t0, int s) {
+      if (!mine(s, t0)) return;
       float f[8], out[8];
       f32x2 skip[4], sum[4];
       Eight h;
 #pragma unroll
-      for (int i = 0; i < kVecs; ++i) h.v[i].raw = sm.x[i][threadIdx.x];
+      for (int i = 0; i < kVecs; ++i) h.v[i].raw = sm.x[s][i][threadIdx.x];
       h.values(f);
       quads(sm.skip, skip);
-      quads(sm.y[task_row], sum);
+      quads(sm.y[task_row + s * kStep], sum);
 #pragma unroll
       for (int i = 0; i < 4; ++i) sum[i] = fma2(skip[i], pair(f[2 * i], f[2 * i + 1]), sum[i]);
       if (gated) {
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) h.v[i].raw = sm.z[i][threadIdx.x];
+        for (int i = 0; i < kVecs; ++i) h.v[i].raw = sm.z[s][i][threadIdx.x];
         h.values(f);
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum[i] = mul2(sum[i], silu(pair(f[2 * i], f[2 * i + 1])));
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) unpair(sum[i], out[2 * i], out[2 * i + 1]);
-      T* y = const_cast<T*>(row_of(p.rows.y, p.rows.y_stride, t0));
+      T* y = const_cast<T*>(row_of(p.rows.y, p.rows.y_stride, t0 + s * kStep));
 #pragma unroll
       for (int i = 0; i < kVecs; ++i)
         store_vec(y + i * Vec<T>::N, pack<T>(out + i * Vec<T>::N), count - i * Vec<T>::N, whole);
@@ -361,8 +369,11 @@ struct Scan {
     for (int t0 = 0; t0 < len; t0 += kTile) {
       const bool more = t0 + kTile < len;
       if (!kAhead) load_bc(w, span.lo + t0, min(len - t0, kTile));
-      if (OUT && t0 > 0) finish(t0 - kTile);
-      if (t0 + task_row < len && count > 0) prepare();
+#pragma unroll
+      for (int i = 0; i < kShares; ++i) {
+        if (OUT && t0 > 0) finish(t0 - kTile, i);
+        if (mine(i, t0)) prepare(i);
+      }
       store_bc(w);
       if (more) {
         fetch(t0 + kTile);
@@ -385,7 +396,10 @@ struct Scan {
       }
       __syncthreads();
     }
-    if (OUT && len > 0) finish((len - 1) / kTile * kTile);
+    if (OUT && len > 0) {
+#pragma unroll
+      for (int i = 0; i < kShares; ++i) finish((len - 1) / kTile * kTile, i);
+    }
   }
 };
 
