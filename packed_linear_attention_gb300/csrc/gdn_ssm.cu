@@ -144,13 +144,11 @@ template <typename T, int NS, int SPLIT>
 struct Scan {
   static constexpr int kPadded = NS * SPLIT;
   static constexpr int kCh = kThreads / SPLIT;
-  // 8 or 16 elements of a tile a thread, while b and c stay within 16 KB
-  static constexpr int kTile = SPLIT == 4 ? 32 : 16;
+  static constexpr int kTile = 16;
   static constexpr int kAcross = kCh / 8, kStep = kThreads / kAcross;  // shares of a row; rows between a thread's
   static constexpr int kShares = (kTile + kStep - 1) / kStep;          // of a thread
   static constexpr int kVecs = 8 / Vec<T>::N;
   static constexpr int kShare = (kTile * kPadded + kThreads - 1) / kThreads;  // of b and of c
-  static constexpr bool kAhead = kShare <= 4;
   struct Shared {
     float4 f[kTile][kCh / 2];  // dt and dt x of two channels, at pair_at
     float4 y[kTile][kCh / 4];  // at quad_at
@@ -362,13 +360,12 @@ struct Scan {
       }
     };
 
-    Shares w;  // the next tile's b and c, where a thread's share of them is small
-    if (kAhead) load_bc(w, span.lo, min(len, kTile));
+    Shares w;  // the next tile's b and c
+    load_bc(w, span.lo, min(len, kTile));
     fetch(0);
     __syncthreads();  // bias and skip
     for (int t0 = 0; t0 < len; t0 += kTile) {
       const bool more = t0 + kTile < len;
-      if (!kAhead) load_bc(w, span.lo + t0, min(len - t0, kTile));
 #pragma unroll
       for (int i = 0; i < kShares; ++i) {
         if (OUT && t0 > 0) finish(t0 - kTile, i);
@@ -377,7 +374,7 @@ struct Scan {
       store_bc(w);
       if (more) {
         fetch(t0 + kTile);
-        if (kAhead) load_bc(w, span.lo + t0 + kTile, min(len - t0 - kTile, kTile));
+        load_bc(w, span.lo + t0 + kTile, min(len - t0 - kTile, kTile));
       }
       __syncthreads();
       const int rows = min(len - t0, kTile);
