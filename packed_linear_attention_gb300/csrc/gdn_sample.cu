@@ -152,6 +152,32 @@ struct Weights {
                   (u32)__float2int_rn(__uint_as_float(table->factor[n & 31]) * (r * q));
     return y < kRange ? (u64)w << 13 >> (n >> 5) : 0;
   }
+  // The same for two logits, the same roundings: half the instructions. y: the distances, negated.
+  __device__ __forceinline__ void two(float l0, float l1, u64 (&w)[2], float (&ny)[2]) const {
+    const f32x2 l = pair(l0, l1), t = both(top), minus = both(-1.f);
+    const f32x2 d = fma2(l, minus, t), b = add2(d, both(-top));
+    const f32x2 err = fma2(add2(l, b), minus, fma2(fma2(b, minus, d), minus, t));
+    const f32x2 y = mul2(d, both(-hi));
+    const f32x2 rest = fma2(err, both(hi), fma2(d, both(lo), fma2(d, both(hi), y)));
+    unpair(y, ny[0], ny[1]);
+    const f32x2 held = pair(fmaxf(ny[0], -kRange), fmaxf(ny[1], -kRange));
+    constexpr float kMagic = 0x1.8p23f;
+    const f32x2 shifted = fma2(held, both(-32.f), both(kMagic));
+    float s0, s1;
+    unpair(shifted, s0, s1);
+    const u32 n0 = __float_as_uint(s0) & 0x7ffu, n1 = __float_as_uint(s1) & 0x7ffu;
+    const f32x2 r = fma2(fma2(add2(shifted, both(-kMagic)), both(1.f / 32.f), held), minus, rest);
+    f32x2 q = fma2(r, both(0.0096181291f), both(-0.0555041087f));
+    q = fma2(r, q, both(0.2402265070f));
+    q = fma2(r, q, both(-0.6931471806f));
+    const f32x2 f = pair(__uint_as_float(table->factor[n0 & 31]), __uint_as_float(table->factor[n1 & 31]));
+    float e0, e1;
+    unpair(mul2(f, mul2(r, q)), e0, e1);
+    const u32 w0 = table->whole[n0 & 31] + (u32)__float2int_rn(e0);
+    const u32 w1 = table->whole[n1 & 31] + (u32)__float2int_rn(e1);
+    w[0] = ny[0] > -kRange ? (u64)w0 << 13 >> (n0 >> 5) : 0;
+    w[1] = ny[1] > -kRange ? (u64)w1 << 13 >> (n1 >> 5) : 0;
+  }
 };
 
 // A block's part of a row. A thread owns `each` neighbouring vectors (an odd number of them, so that
@@ -171,6 +197,17 @@ struct Slice {
       unpack(data[v], x);
 #pragma unroll
       for (int i = 0; i < N; ++i) f(x[i], first + v * N + i);
+    }
+  }
+  // f(two values, place of the first) for every two elements
+  template <class F>
+  __device__ __forceinline__ void twos(F f) const {
+    const int v1 = min(vecs, ((int)threadIdx.x + 1) * per_thread);
+    for (int v = threadIdx.x * per_thread; v < v1; ++v) {
+      float x[N];
+      unpack(data[v], x);
+#pragma unroll
+      for (int i = 0; i < N; i += 2) f(x[i], x[i + 1], first + v * N + i);
     }
   }
   // f(value, place) for the elements that are wanted, where they are few: looked for side by side,
@@ -272,8 +309,9 @@ struct Row {
     return warp_max(threadIdx.x % 32 < kWarps ? sh.warp_weight[threadIdx.x % 32] : 0);
   }
 
+  __device__ __forceinline__ static float bins_of(float y) { return y * (kBins / kRange); }
   __device__ __forceinline__ static u32 bin_of(float y) {
-    return min((u32)(y * (kBins / kRange)), (u32)kBins - 1);
+    return min((u32)bins_of(y), (u32)kBins - 1);
   }
 
   // The cluster's counts of this thread's bins.
@@ -379,12 +417,38 @@ struct Row {
     }
   }
 
-  // The weight of the keys above `low`, up to `high`.
-  __device__ __forceinline__ u64 weight_between(u32 low, u32 high) {
+  // f(weight, distance) for all tokens, or for those that are wanted, about `count` of the cluster's. A weight of its
+  // own takes a lane some 60 instructions with the others waiting, one of two 22: where every eighth
+  // token is wanted, all are worked out.
+  template <class F>
+  __device__ __forceinline__ void weigh_all(F f) const {
+    slice.twos([&](float x0, float x1, u32) {
+      u64 w[2];
+      float ny[2];
+      weight.two(x0, x1, w, ny);
+      f(w[0], -ny[0]);
+      f(w[1], -ny[1]);
+    });
+  }
+  template <class Want, class F>
+  __device__ __forceinline__ void weigh(u32 count, Want want, F f) const {
+    if (count / 4 < (u32)(slice.vecs * Slice<T>::N / 32) * cluster.num_blocks()) {
+      slice.some(want, [&](float x, u32) { f(weight(x), weight.distance(x)); });
+      return;
+    }
+    slice.twos([&](float x0, float x1, u32 at) {
+      u64 w[2];
+      float ny[2];
+      weight.two(x0, x1, w, ny);
+      if (want(x0, at)) f(w[0], -ny[0]);
+      if (want(x1, at + 1)) f(w[1], -ny[1]);
+    });
+  }
+  // The weight of the keys above `low`, up to `high`, about `count` tokens.
+  __device__ __forceinline__ u64 weight_between(u32 count, u32 low, u32 high) {
     u64 sum = 0;
     const float v0 = value_of<T>(low), v1 = value_of<T>(high);
-    slice.some([&](float x, u32) { return x > v0 && x <= v1; },
-               [&](float x, u32) { sum += weight(x); });
+    weigh(count, [&](float x, u32) { return x > v0 && x <= v1; }, [&](u64 w, float) { sum += w; });
     return cluster_sum(sum);
   }
 
@@ -395,11 +459,12 @@ struct Row {
     bool by_key = false;
     u32 hi = 0, lo = 0;            // by_key: the keys lo .. hi
     float above = 0.f, below = 0.f;  // and their values
+    // bin_of in first .. last, without the rounding to whole bins (kRange cuts the last one)
+    const float from_bin = (float)first, to_bin = last < kBins - 1 ? (float)(last + 1) : INFINITY;
     const auto member = [&](float x, u32) {
       if (by_key) return x >= above && x <= below;
-      const float y = weight.distance(x);
-      const u32 b = bin_of(fminf(y, kRange));
-      return y < kRange && b >= first && b <= last;
+      const float y = weight.distance(x), b = bins_of(y);
+      return y < kRange && b >= from_bin && b < to_bin;
     };
     if (f.count > kList) {
       above = INFINITY;
@@ -431,13 +496,12 @@ struct Row {
       const int shift = max(0, 21 - __clz(hi - lo));  // (hi - lo) >> shift is below 2,048
       for (int i = threadIdx.x; i < kBins; i += kThreads) sh.finer[i] = 0;
       __syncthreads();
-      slice.some(member, [&](float x, u32) {
-        // lanes of one bin (equal logits) add once
-        const u32 b = (hi - key_of<T>(x)) >> shift, same = __match_any_sync(__activemask(), b);
-        if (threadIdx.x % 32 == __ffs(same) - 1) atomicAdd(&sh.finer[b], (u32)__popc(same));
+      slice.each([&](float x, u32) {
+        if (x >= above && x <= below) atomicAdd(&sh.finer[(hi - key_of<T>(x)) >> shift], 1u);
       });
       cluster.sync();
       u32 c[kBinsOf], b0, b1;
+      u64 front = 0;  // this thread's part of the weight in front of bin b0
       counts(sh.finer, c);
       if (by_weight) {
         // a bin's weights lie between those of its ends, to their own error
@@ -451,6 +515,8 @@ struct Row {
           least[i] = c[i] * (w1 - (shift ? min(w1, (w1 >> 28) + 1) : 0));
         }
         window(least, most, f.before_weight, [&](u64, u64, u64& a, u64& b) { a = b = goal; }, b0, b1);
+#pragma unroll
+        for (int i = 0; i < kBinsOf; ++i) front += threadIdx.x * kBinsOf + i < b0 ? most[i] : 0;
       } else {
         u64 all;
         b0 = b1 = find(c, f.before, goal, all).bin;
@@ -462,14 +528,15 @@ struct Row {
       const u32 top = hi, span = hi - lo;
       lo = max(lo, hi - (b1 << shift) - ((1u << shift) - 1));
       hi -= b0 << shift;
-      if (by_weight) f.before_weight += weight_between(hi, top);
+      // a bin of one key has its weight times its count
+      if (by_weight) f.before_weight += shift ? weight_between(in.before, hi, top) : block_sum(front);
       if (hi - lo > span / 2) {  // bounds too wide to tell: halve the keys by exact sums
         const u32 mid = lo + (hi - lo) / 2;
         const float v0 = value_of<T>(mid), v1 = value_of<T>(hi);
         u32 here = 0;
         slice.each([&](float x, u32) { here += x > v0 && x <= v1; });
         const u64 n = cluster_sum(here);
-        const u64 w = by_weight ? weight_between(mid, hi) : n;
+        const u64 w = by_weight ? weight_between((u32)n, mid, hi) : n;
         if ((by_weight ? f.before_weight : f.before) + w >= goal) {
           lo = mid + 1;
           f.count = (u32)n;
@@ -624,6 +691,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs p, int v
 
   // the last token that top-k and top-p keep; until then every one is
   bool cut = false;
+  u32 num_kept = (u32)V;  // about as many, or more
   float last_value = -INFINITY;
   u32 last_at = 0xffffffffu;
   const auto cut_at = [&](const Entry& e) {
@@ -657,6 +725,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs p, int v
       if (all > (u64)top_k) {
         cut_at(row.resolve(f.bin, f.bin, f, false, (u64)top_k));
         limit = f.bin;
+        num_kept = (u32)top_k;
       }
     }
     if (by_p) {
@@ -681,26 +750,23 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs p, int v
       }, first, last);
       last = min(last, limit);
       u64 front = 0, total = 0;
-      const auto add = [&](float x, u32) {
-        const u64 w = row.weight(x);
+      const auto add = [&](u64 w, float y) {
         total += w;
-        front += Row<T>::bin_of(fminf(row.weight.distance(x), kRange)) < first ? w : 0;
+        front += Row<T>::bins_of(y) < (float)first ? w : 0;
       };
-      if (cut) row.slice.some(inside_of, add);
-      else row.slice.each(add);
+      if (cut) row.weigh(num_kept, inside_of, add);
+      else row.weigh_all(add);
       Found f = row.tokens(c, first, last);
+      num_kept = min(num_kept, f.before + f.count);
       f.before_weight = row.cluster_sum(front);
       cut_at(row.resolve(first, last, f, true, share_of(row.cluster_sum(total))));
     }
   }
   if (min_p > 0.f) floor_weight = min_p < 1.f ? share(min_p, 1ull << 44, true) : 1ull << 44;
   u64 sum = 0;
-  const auto add = [&](float x, u32) {
-    const u64 w = row.weight(x);
-    sum += w >= floor_weight ? w : 0;
-  };
-  if (cut) row.slice.some(inside_of, add);
-  else row.slice.each(add);
+  const auto add = [&](u64 w, float) { sum += w >= floor_weight ? w : 0; };
+  if (cut) row.weigh(num_kept, inside_of, add);
+  else row.weigh_all(add);
   u64 all;
   const u64 inside = row.scan(sum, all), of_block = row.exchange(all);
   const u64 front = row.in_front(of_block), total = warp_sum(of_block);
