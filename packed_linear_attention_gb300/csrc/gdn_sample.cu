@@ -16,6 +16,7 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <cfloat>
 
 #include "gdn_internal.h"
 #include "gdn_step_internal.h"
@@ -152,15 +153,16 @@ struct Weights {
                   (u32)__float2int_rn(__uint_as_float(table->factor[n & 31]) * (r * q));
     return y < kRange ? (u64)w << 13 >> (n >> 5) : 0;
   }
-  // The same for two logits, the same roundings: half the instructions. y: the distances, negated.
-  __device__ __forceinline__ void two(float l0, float l1, u64 (&w)[2], float (&ny)[2]) const {
+  // The same for two logits with the same roundings, half of the instructions in pairs.
+  __device__ __forceinline__ void two(float l0, float l1, u64 (&w)[2]) const {
     const f32x2 l = pair(l0, l1), t = both(top), minus = both(-1.f);
     const f32x2 d = fma2(l, minus, t), b = add2(d, both(-top));
     const f32x2 err = fma2(add2(l, b), minus, fma2(fma2(b, minus, d), minus, t));
     const f32x2 y = mul2(d, both(-hi));
     const f32x2 rest = fma2(err, both(hi), fma2(d, both(lo), fma2(d, both(hi), y)));
-    unpair(y, ny[0], ny[1]);
-    const f32x2 held = pair(fmaxf(ny[0], -kRange), fmaxf(ny[1], -kRange));
+    float y0, y1;  // the distances, negated
+    unpair(y, y0, y1);
+    const f32x2 held = pair(fmaxf(y0, -kRange), fmaxf(y1, -kRange));
     constexpr float kMagic = 0x1.8p23f;
     const f32x2 shifted = fma2(held, both(-32.f), both(kMagic));
     float s0, s1;
@@ -175,8 +177,8 @@ struct Weights {
     unpair(mul2(f, mul2(r, q)), e0, e1);
     const u32 w0 = table->whole[n0 & 31] + (u32)__float2int_rn(e0);
     const u32 w1 = table->whole[n1 & 31] + (u32)__float2int_rn(e1);
-    w[0] = ny[0] > -kRange ? (u64)w0 << 13 >> (n0 >> 5) : 0;
-    w[1] = ny[1] > -kRange ? (u64)w1 << 13 >> (n1 >> 5) : 0;
+    w[0] = y0 > -kRange ? (u64)w0 << 13 >> (n0 >> 5) : 0;
+    w[1] = y1 > -kRange ? (u64)w1 << 13 >> (n1 >> 5) : 0;
   }
 };
 
@@ -417,31 +419,29 @@ struct Row {
     }
   }
 
-  // f(weight, distance) for all tokens, or for those that are wanted, about `count` of the cluster's. A weight of its
+  // f(weight, value) for all tokens, or for those that are wanted, about `count` of the cluster's. A weight of its
   // own takes a lane some 60 instructions with the others waiting, one of two 22: where every eighth
   // token is wanted, all are worked out.
   template <class F>
   __device__ __forceinline__ void weigh_all(F f) const {
     slice.twos([&](float x0, float x1, u32) {
       u64 w[2];
-      float ny[2];
-      weight.two(x0, x1, w, ny);
-      f(w[0], -ny[0]);
-      f(w[1], -ny[1]);
+      weight.two(x0, x1, w);
+      f(w[0], x0);
+      f(w[1], x1);
     });
   }
   template <class Want, class F>
   __device__ __forceinline__ void weigh(u32 count, Want want, F f) const {
     if (count / 4 < (u32)(slice.vecs * Slice<T>::N / 32) * cluster.num_blocks()) {
-      slice.some(want, [&](float x, u32) { f(weight(x), weight.distance(x)); });
+      slice.some(want, [&](float x, u32) { f(weight(x), x); });
       return;
     }
     slice.twos([&](float x0, float x1, u32 at) {
       u64 w[2];
-      float ny[2];
-      weight.two(x0, x1, w, ny);
-      if (want(x0, at)) f(w[0], -ny[0]);
-      if (want(x1, at + 1)) f(w[1], -ny[1]);
+      weight.two(x0, x1, w);
+      if (want(x0, at)) f(w[0], x0);
+      if (want(x1, at + 1)) f(w[1], x1);
     });
   }
   // The weight of the keys above `low`, up to `high`, about `count` tokens.
@@ -452,53 +452,62 @@ struct Row {
     return cluster_sum(sum);
   }
 
-  // The last token kept, which one of the bins first .. last of the distances holds: the one at which
-  // the count (or weight) of the order reaches goal. f: what lies in front of those bins, and the
-  // tokens in them.
-  __device__ __forceinline__ Entry resolve(u32 first, u32 last, Found f, bool by_weight, u64 goal) {
-    bool by_key = false;
-    u32 hi = 0, lo = 0;            // by_key: the keys lo .. hi
-    float above = 0.f, below = 0.f;  // and their values
-    // bin_of in first .. last, without the rounding to whole bins (kRange cuts the last one)
-    const float from_bin = (float)first, to_bin = last < kBins - 1 ? (float)(last + 1) : INFINITY;
-    const auto member = [&](float x, u32) {
-      if (by_key) return x >= above && x <= below;
-      const float y = weight.distance(x), b = bins_of(y);
-      return y < kRange && b >= from_bin && b < to_bin;
+  // The keys lo .. hi whose distances lie in the bins first .. last: distances fall as keys rise. One
+  // warp looks for either end, in 32 places at a time.
+  __device__ __forceinline__ void keys_of(u32 first, u32 last, u32& hi, u32& lo) {
+    const u32 top = key_of<T>(weight.top);
+    const float to = last < kBins - 1 ? (float)(last + 1) : INFINITY;
+    // at the least key for which it holds, at `top` if for none below
+    const auto least = [&](auto holds) {
+      u32 a = key_of<T>(-FLT_MAX), b = top;
+      while (a < b) {
+        const u32 step = (b - a) / 32 + 1, k = (u32)min((u64)b, a + (u64)(threadIdx.x % 32) * step);
+        const u32 yes = __ballot_sync(0xffffffffu, k == b || holds(weight.distance(value_of<T>(k))));
+        const u32 n = yes ? __ffs(yes) - 1 : 32;
+        const u32 end = (u32)min((u64)b, a + (u64)n * step);
+        if (n > 0) a = (u32)min((u64)b, a + (u64)(n - 1) * step + 1);
+        if (n < 32) b = end;
+      }
+      return a;
     };
-    if (f.count > kList) {
-      above = INFINITY;
-      below = -INFINITY;
-      slice.each([&](float x, u32 at) {
-        const bool in = member(x, at);
-        below = in ? fmaxf(below, x) : below;
-        above = in ? fminf(above, x) : above;
-      });
-      u32 inv = ~key_of<T>(above);
-      hi = key_of<T>(below);
-      hi = __reduce_max_sync(0xffffffffu, hi);
-      inv = __reduce_max_sync(0xffffffffu, inv);
-      __syncthreads();
-      if (threadIdx.x % 32 == 0) sh.warp_weight[threadIdx.x / 32] = (u64)hi << 32 | inv;
-      __syncthreads();
-      const u64 of = sh.warp_weight[threadIdx.x % kWarps];
-      hi = __reduce_max_sync(0xffffffffu, (u32)(of >> 32));
-      inv = __reduce_max_sync(0xffffffffu, (u32)of);
-      const u64 both = exchange((u64)hi << 32 | inv);
-      hi = __reduce_max_sync(0xffffffffu, (u32)(both >> 32));
-      inv = __reduce_max_sync(0xffffffffu, (u32)both);
-      lo = ~inv;
-      by_key = true;
-      above = value_of<T>(lo);
-      below = value_of<T>(hi);
+    if (threadIdx.x < 64) {
+      u32 k;
+      if (threadIdx.x < 32) {
+        k = least([&](float y) { return y < kRange && bins_of(y) < to; });
+      } else {
+        k = first == 0 ? top : least([&](float y) { return bins_of(y) < (float)first; }) - 1;
+      }
+      if (threadIdx.x % 32 == 0) sh.window[threadIdx.x / 32] = k;
     }
+    __syncthreads();
+    lo = sh.window[0];
+    hi = sh.window[1];
+  }
+  // The finer bins of the keys lo .. hi.
+  __device__ __forceinline__ static int shift_of(u32 lo, u32 hi) {
+    return max(0, 21 - __clz(hi - lo));  // (hi - lo) >> shift is below 2,048
+  }
+  __device__ __forceinline__ void clear_finer() {
+    for (int i = threadIdx.x; i < kBins; i += kThreads) sh.finer[i] = 0;
+    __syncthreads();
+  }
+
+  // The last token kept, whose key lies in lo .. hi: the one at which the count (or weight) of the order
+  // reaches goal. f: what lies in front of those keys, and the tokens in them. `counted`: the finer bins
+  // hold their counts.
+  __device__ __forceinline__ Entry resolve(u32 lo, u32 hi, Found f, bool by_weight, u64 goal,
+                                           bool counted) {
+    float above = value_of<T>(lo), below = value_of<T>(hi);
+    const auto member = [&](float x, u32) { return x >= above && x <= below; };
     while (f.count > kList && lo < hi) {  // the keys left are halved at least
-      const int shift = max(0, 21 - __clz(hi - lo));  // (hi - lo) >> shift is below 2,048
-      for (int i = threadIdx.x; i < kBins; i += kThreads) sh.finer[i] = 0;
-      __syncthreads();
-      slice.each([&](float x, u32) {
-        if (x >= above && x <= below) atomicAdd(&sh.finer[(hi - key_of<T>(x)) >> shift], 1u);
-      });
+      const int shift = shift_of(lo, hi);
+      if (!counted) {
+        clear_finer();
+        slice.each([&](float x, u32 at) {
+          if (member(x, at)) atomicAdd(&sh.finer[(hi - key_of<T>(x)) >> shift], 1u);
+        });
+      }
+      counted = false;
       cluster.sync();
       u32 c[kBinsOf], b0, b1;
       u64 front = 0;  // this thread's part of the weight in front of bin b0
@@ -723,7 +732,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs p, int v
     if (by_k) {
       const Found f = row.find(c, 0, (u64)top_k, all);
       if (all > (u64)top_k) {
-        cut_at(row.resolve(f.bin, f.bin, f, false, (u64)top_k));
+        u32 lo, hi;
+        row.keys_of(f.bin, f.bin, hi, lo);
+        cut_at(row.resolve(lo, hi, f, false, (u64)top_k, false));
         limit = f.bin;
         num_kept = (u32)top_k;
       }
@@ -749,17 +760,29 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs p, int v
         b = share_of(hi);
       }, first, last);
       last = min(last, limit);
-      u64 front = 0, total = 0;
-      const auto add = [&](u64 w, float y) {
-        total += w;
-        front += Row<T>::bins_of(y) < (float)first ? w : 0;
-      };
-      if (cut) row.weigh(num_kept, inside_of, add);
-      else row.weigh_all(add);
       Found f = row.tokens(c, first, last);
-      num_kept = min(num_kept, f.before + f.count);
+      u32 key_lo, key_hi;
+      row.keys_of(first, last, key_hi, key_lo);
+      const float above = value_of<T>(key_lo), below = value_of<T>(key_hi);
+      u64 front = 0, total = 0;
+      const auto add = [&](u64 w, float x) {
+        total += w;
+        front += x > below ? w : 0;
+      };
+      if (cut) {
+        row.weigh(num_kept, inside_of, add);
+      } else {
+        row.clear_finer();
+        const int shift = Row<T>::shift_of(key_lo, key_hi);
+        row.weigh_all([&](u64 w, float x) {
+          add(w, x);
+          if (x >= above && x <= below) atomicAdd(&sh.finer[(key_hi - key_of<T>(x)) >> shift], 1u);
+        });
+      }
       f.before_weight = row.cluster_sum(front);
-      cut_at(row.resolve(first, last, f, true, share_of(row.cluster_sum(total))));
+      num_kept = min(num_kept, f.before + f.count);
+      const u64 goal = share_of(row.cluster_sum(total));
+      cut_at(row.resolve(key_lo, key_hi, f, true, goal, !cut));
     }
   }
   if (min_p > 0.f) floor_weight = min_p < 1.f ? share(min_p, 1ull << 44, true) : 1ull << 44;
