@@ -75,7 +75,7 @@ struct Found {
   u64 before_weight;
   u32 bin, before, count;
 };
-struct Shared {
+struct alignas(16) Shared {  // the slice lies behind it, read 16 bytes at a time
   u32 count[kBins];  // tokens at each distance from the maximum
   union {
     u32 finer[kBins];
@@ -87,8 +87,10 @@ struct Shared {
   u32 warp_count[kWarps];
   Found found;
   u32 window[2];
+  int row;
   Entry chosen;       // the last token kept
 };
+static_assert(sizeof(Shared) % 16 == 0, "the slice's vectors are aligned");
 
 // x times `total` for x in [0, 1), rounded down or up: exact, in whole numbers (fp64 arithmetic is
 // two lanes a clock here).
@@ -258,6 +260,28 @@ struct Row {
   int turn = 0;
 
   __device__ __forceinline__ Row(Shared& s) : cluster(cg::this_cluster()), sh(s) {}
+
+  // The row of cluster j: rows with top-p, which take the longest, come first.
+  __device__ __forceinline__ int place_of(const SampleArgs& p, int j) {
+    const int per = (p.num_rows + kThreads - 1) / kThreads;
+    const int first = min(p.num_rows, (int)threadIdx.x * per), last = min(p.num_rows, first + per);
+    const auto is_long = [&](int n) {
+      return p.top_p[n] < 1.f && !(p.temperature && p.temperature[n] == 0.f);
+    };
+    int mine = 0;
+    for (int n = first; n < last; ++n) mine += is_long(n);
+    u64 all;
+    const int front = (int)scan((u64)mine, all), others = first - front;
+    const bool want = j < (int)all;
+    const int from = want ? front : (int)all + others, have = want ? mine : last - first - mine;
+    if (from <= j && j < from + have) {
+      int at = from;
+      for (int n = first; n < last; ++n)
+        if (is_long(n) == want && at++ == j) sh.row = n;
+    }
+    __syncthreads();
+    return sh.row;
+  }
 
   // Every block's value (thread 0's): lane r of every warp has block r's, others 0. Read side by side:
   // a read from another block takes about 300 ns.
@@ -619,14 +643,14 @@ struct Row {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs p, int vecs_of_block) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs p, int vecs_of_block, bool ordered) {
   extern __shared__ __align__(16) unsigned char memory[];
   constexpr int N = Vec<T>::N;
   Shared& sh = *reinterpret_cast<Shared*>(memory);
   Vec<T>* data = reinterpret_cast<Vec<T>*>(memory + sizeof(Shared));
   Row<T> row(sh);
   const unsigned rank = row.cluster.block_rank(), blocks = row.cluster.num_blocks();
-  const int r = blockIdx.x / blocks;
+  const int r = ordered ? row.place_of(p, blockIdx.x / blocks) : blockIdx.x / blocks;
   const int V = p.vocab;
   const T* logits = static_cast<const T*>(p.logits) + (int64_t)r * p.stride;
   // places count from the 16-byte boundary at or in front of the row
@@ -820,6 +844,8 @@ int launch(const SampleArgs& a, cudaStream_t s) {
                                              2 * (memory(blocks / 2) + 1024) <= kMostMemory + 1024)))
     blocks /= 2;
   const int of_block = share(blocks);
+  // Rows are put in order where not all run at once, and a thread looks at few of them.
+  const bool ordered = a.top_p && (int64_t)a.num_rows * blocks > 2 * 152 && a.num_rows <= 8 * kThreads;
   const size_t bytes = memory(blocks);
   static std::atomic<int> done[kMaxDevices];
   const int e = configure_once(done, [] {
@@ -837,7 +863,7 @@ int launch(const SampleArgs& a, cudaStream_t s) {
   attr[0].val.clusterDim = {(unsigned)blocks, 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return (int)cudaLaunchKernelEx(&cfg, sample_kernel<T>, a, of_block);
+  return (int)cudaLaunchKernelEx(&cfg, sample_kernel<T>, a, of_block, ordered);
 }
 
 }  // namespace

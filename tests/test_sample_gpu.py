@@ -69,6 +69,42 @@ def test_rows(kind, io, rows, vocab, spread):
     compare(logits, io, vocab, *settings(rng, rows, kind), rng.random(rows))
 
 
+@pytest.mark.parametrize("kind", ["top_k", "top_p", "all"])
+@pytest.mark.parametrize("io,vocab,spread", [
+    ("f32", 20000, 1e-3), ("bf16", 20000, 1e-3), ("f32", 60000, 0.05), ("bf16", 60000, 0.3),
+    ("f32", 60000, 30.0), ("bf16", 60000, 30.0)])
+def test_logits_around_zero(kind, io, vocab, spread):
+    """The last token kept among many whose keys span the exponents."""
+    rng = np.random.default_rng(int(spread * 1000))
+    logits = up(spread * rng.standard_normal((16, vocab)), io)
+    t, k, p, m = settings(rng, 16, kind)
+    k = None if k is None else rng.integers(1, vocab, 16)
+    compare(logits, io, vocab, t, k, p, m, rng.random(16))
+
+
+@pytest.mark.parametrize("io,rows,vocab", [("f32", 700, 1000), ("bf16", 1023, 300), ("f32", 4100, 40)])
+def test_many_rows_as_few(io, rows, vocab):
+    """Rows in any order of their settings: each as in a call of a few rows, refused ones too."""
+    torch = torch_cuda()
+    rng = np.random.default_rng(rows)
+    logits = up(2.0 * rng.standard_normal((rows, vocab)), io)
+    t, k, p, m = settings(rng, rows, "mixed")
+    p[rng.random(rows) < 0.02] = np.nan
+    u = rng.random(rows)
+    for setting in ((t, k, p, m), (t, None, p, None), (None, None, p, None), (t, k, np.ones(rows), m),
+                    (t, k, np.full(rows, 0.5), m)):
+        token, lp, status = draw(logits, io, vocab, *setting, u)
+        cut = lambda x, a: None if x is None else x[a:a + 32]  # noqa: E731
+        refused = 0
+        for a in range(0, rows, 32):
+            few, few_lp, bad = draw(logits[a:a + 32].contiguous(), io, vocab,
+                                    *(cut(x, a) for x in setting), u[a:a + 32])
+            assert token[a:a + 32] == few and lp[a:a + 32] == few_lp
+            refused = max(refused, bad)
+        assert status == refused
+    torch.cuda.synchronize()
+
+
 def test_rows_off_16_byte_boundaries():
     torch = torch_cuda()
     rng = np.random.default_rng(1)
