@@ -837,14 +837,15 @@ int launch(const SampleArgs& a, cudaStream_t s) {
   const auto share = [&](int blocks) { return (vecs + blocks - 1) / blocks; };
   const auto memory = [&](int blocks) { return sizeof(Shared) + (size_t)share(blocks) * 16; };
   // Eight blocks a row, unless fewer still give every SM two (256 rows of 151,936 bf16 logits, top-p:
-  // 423 us with eight, 299 with four; fp32, of which four leave an SM one block: 457 and 478) or the
-  // row is short.
+  // 372 us with eight, 237 with four; fp32, of which four leave an SM one block: 427 and 419, without
+  // a filter 119 and 132) or the row is short.
   int blocks = kMaxCluster;
   while (blocks > 1 && (vecs <= kThreads || ((int64_t)a.num_rows * blocks / 2 >= 2 * 152 &&
                                              2 * (memory(blocks / 2) + 1024) <= kMostMemory + 1024)))
     blocks /= 2;
   const int of_block = share(blocks);
-  // Rows are put in order where not all run at once, and a thread looks at few of them.
+  // Rows are put in order where not all run at once, and a thread looks at few of them (256 bf16 rows, a
+  // quarter of them with top-p: 158 us as they stand, 139 in order; all with top-p: 233 and 236).
   const bool ordered = a.top_p && (int64_t)a.num_rows * blocks > 2 * 152 && a.num_rows <= 8 * kThreads;
   const size_t bytes = memory(blocks);
   static std::atomic<int> done[kMaxDevices];
