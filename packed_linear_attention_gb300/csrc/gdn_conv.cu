@@ -5,10 +5,10 @@
 //
 // Every output needs W inputs of its own channel and nothing else, so a thread takes four channels,
 // keeps their last W - 1 rows in registers and walks down its rows: x is read once (and W - 1 rows
-// more for every kTile rows), y written once, 8 or 16 bytes a thread. Bound by HBM: four channels
+// more for every block's rows), y written once, 8 or 16 bytes a thread. Bound by HBM: four channels
 // are few enough registers for the loads in flight that it takes.
 //
-// A block takes kTile rows of one request and 128 threads' channels. The block of a request's
+// A block takes `tile` rows of one request and 128 threads' channels. The block of a request's
 // first rows is the only one that touches its state: it reads the rows in front from the slot,
 // then writes the slot and the request's checkpoints, copies of rows of x (or of the old state
 // where the request is shorter than W - 1).
@@ -18,8 +18,14 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kTile = 128;  // rows of a block (32: 246 us for 32 x 1,024 rows of 8,192 channels, 64: 225, 128: 221)
-constexpr int kAhead = 4;   // rows loaded at once
+// Rows loaded at once and blocks of an SM: loads on their way are what the wave waits for. bf16, 32 x
+// 1,024 rows of 8,192 channels, blocks of 128 rows: four rows and as many blocks as fit (six) 210 us, six
+// and seven 181, six and six 189, seven and seven 194 (registers spill), four and eight 196, eight and
+// five 195. fp32: four and five 328, three and six 333.
+template <typename T>
+constexpr int kAhead = sizeof(T) == 2 ? 6 : 4;
+template <typename T>
+constexpr int kResident = sizeof(T) == 2 ? 7 : 5;
 
 // Four channels of a row as they lie in memory.
 template <typename T>
@@ -137,10 +143,11 @@ struct Taps {
 template <typename T, int W, bool WHOLE>
 __device__ __forceinline__ void walk(const Taps<W>& taps, f32x2 (&rows)[W - 1][2], const T* x, T* y,
                                      const ConvArgs& p, int left, int count, bool act) {
-  Four<T> next[kAhead];  // on their way while the rows in front of them are worked on
+  constexpr int N = kAhead<T>;
+  Four<T> next[N];  // on their way while the rows in front of them are worked on
   const auto fetch = [&](int n) {
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
+    for (int i = 0; i < N; ++i) {
       if (i < n) next[i].load(x, count, WHOLE);
       x += p.x_stride;
     }
@@ -159,37 +166,37 @@ __device__ __forceinline__ void walk(const Taps<W>& taps, f32x2 (&rows)[W - 1][2
     y += p.y_stride;
   };
   fetch(left);
-  for (; left >= 2 * kAhead; left -= kAhead) {
-    Four<T> in[kAhead];
+  for (; left >= 2 * N; left -= N) {
+    Four<T> in[N];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) in[i] = next[i];
-    fetch(kAhead);
+    for (int i = 0; i < N; ++i) in[i] = next[i];
+    fetch(N);
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) one(in[i]);
+    for (int i = 0; i < N; ++i) one(in[i]);
   }
   while (left > 0) {  // the last rows, fewer than two groups
-    Four<T> in[kAhead];
+    Four<T> in[N];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) in[i] = next[i];
-    fetch(left - kAhead);
+    for (int i = 0; i < N; ++i) in[i] = next[i];
+    fetch(left - N);
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i)
+    for (int i = 0; i < N; ++i)
       if (i < left) one(in[i]);
-    left -= kAhead;
+    left -= N;
   }
 }
 
 template <typename T, int W>
-__global__ void __launch_bounds__(kThreads) conv_kernel(ConvArgs p, int channel_blocks) {
+__global__ void __launch_bounds__(kThreads, kResident<T>) conv_kernel(ConvArgs p, int channel_blocks, int tile) {
   const int unit = blockIdx.x / channel_blocks, block = blockIdx.x % channel_blocks;
   int32_t* status = blockIdx.x == 0 ? p.status : nullptr;
   const gdn_requests& req = p.req;
-  // a request has a unit for every kTile rows, one at least: that of its state
+  // a request has a unit for every `tile` rows, one at least: that of its state
   const Unit u = find_unit<kThreads>(
       req.num_seqs, unit,
       [&](int n) {
         const Request q = load_request(req, n, status);
-        return q.len < 0 ? 0 : max(1, (q.len + kTile - 1) / kTile);
+        return q.len < 0 ? 0 : max(1, (q.len + tile - 1) / tile);
       },
       [](int) { return 0; });
   if (u.seq < 0) return;
@@ -200,7 +207,7 @@ __global__ void __launch_bounds__(kThreads) conv_kernel(ConvArgs p, int channel_
   const T* x = static_cast<const T*>(p.x) + (size_t)q.lo * p.x_stride + k.c0;
   T* y = static_cast<T*>(p.y) + (size_t)q.lo * p.y_stride + k.c0;
   T* state = static_cast<T*>(p.pool) + (size_t)q.slot * (W - 1) * channels + k.c0;
-  const int t0 = u.place * kTile, t1 = min(q.len, t0 + kTile);
+  const int t0 = u.place * tile, t1 = min(q.len, t0 + tile);
 
   f32x2 rows[W - 1][2];
   if (t0 == 0) {
@@ -287,11 +294,31 @@ __global__ void __launch_bounds__(kThreads) conv_step_kernel(ConvArgs p, int cha
 
 int channel_blocks(int channels) { return (channels + kThreads * 4 - 1) / (kThreads * 4); }
 
+// Rows of a block: a start costs about as much as eight rows, and the last blocks run as long as all
+// others. 32 x 1,024 rows of 8,192 channels, bf16: 212 us with blocks of 32 rows, 177 with 512 (all
+// run at once); 4 x 1,024 rows of 2,048: 19 and 72.
+template <typename T>
+int tile_of(int64_t tokens, int cb) {
+  constexpr int64_t kPlaces = 152 * kResident<T>;
+  int best = 0;
+  int64_t least = 0;
+  for (int tile = 32; tile <= 512; tile *= 2) {
+    const int64_t blocks = (tokens + tile - 1) / tile * cb;
+    const int64_t cost = (blocks + kPlaces - 1) / kPlaces * (tile + 8);
+    if (best == 0 || cost <= least) {
+      best = tile;
+      least = cost;
+    }
+  }
+  return best;
+}
+
 template <typename T, int W>
 int launch_packed(const ConvArgs& a, cudaStream_t s) {
   const int cb = channel_blocks(a.cfg.channels);
-  const int64_t units = (int64_t)a.req.num_tokens / kTile + a.req.num_seqs;
-  conv_kernel<T, W><<<(unsigned)(units * cb), kThreads, 0, s>>>(a, cb);
+  const int tile = tile_of<T>(a.req.num_tokens, cb);
+  const int64_t units = (int64_t)a.req.num_tokens / tile + a.req.num_seqs;
+  conv_kernel<T, W><<<(unsigned)(units * cb), kThreads, 0, s>>>(a, cb, tile);
   return (int)cudaGetLastError();
 }
 template <typename T, int W>
