@@ -103,9 +103,14 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return lo | (uint32_t)hi << 16;
 }
 
+// Blocks of 256 threads on an SM; 0: as many as the registers give. 32 gated heads of 128, 32,768 rows, four
+// vectors a thread: 139 us at 64 registers, 147 at the 78 that it would take.
+template <typename T, int VPT, bool HEADS, int THREADS>
+constexpr int kResident = sizeof(T) == 2 && VPT == 4 && HEADS && THREADS == 256 ? 4 : 0;
+
 // HEADS: heads of `dim` elements, each by itself; else the row is one. WHOLE: rows of a multiple of 8.
 template <typename T, int VPT, bool HEADS, bool WHOLE, int THREADS>
-__global__ void __launch_bounds__(THREADS) norm_kernel(NormArgs p, int team) {
+__global__ void __launch_bounds__(THREADS, kResident<T, VPT, HEADS, THREADS>) norm_kernel(NormArgs p, int team) {
   __shared__ float sums[32], tops[32];
   const int rows = blockDim.x / team;
   const int64_t row = (int64_t)blockIdx.x * rows + threadIdx.x / team;
@@ -240,7 +245,7 @@ int launch(const NormArgs& a, cudaStream_t s) {
   const int vecs = (a.cfg.num_heads * a.cfg.dim + 7) / 8;
   // Few rows: as many threads a row as there are vectors. Many: two or four vectors a thread (32,768
   // rows of 2,048 with residual and codes: 121 us with one, 92 with two, 98 with four; 32 gated heads
-  // of 128: 171, 152 and 146).
+  // of 128: 171, 152 and 139).
   int vpt = a.num_tokens <= 1024 ? 1 : HEADS && sizeof(T) == 2 ? 4 : 2;
   while (vecs > 1024 * vpt) vpt *= 2;
   int team = 32;
