@@ -61,6 +61,18 @@ def test_packed(lens, ch, width, io, bias, act):
     assert (got[p.cu[-1]:] == 7).all()  # rows behind the last request
 
 
+@pytest.mark.parametrize("io,tokens", [("bf16", 60_000), ("bf16", 130_000), ("bf16", 260_000),
+                                       ("bf16", 500_000), ("f32", 45_000), ("f32", 190_000)])
+def test_packed_in_blocks_of_more_rows(io, tokens):
+    """Calls large enough for blocks of 64 to 512 rows, requests that end beside their borders."""
+    rng = np.random.default_rng(tokens)
+    lens = [63, 64, 65, 127, 128, 129, 255, 256, 257, 511, 512, 513, 1, 0, 3, 1024, 7000]
+    lens += list(rng.integers(0, 4000, 2000))
+    total = np.cumsum(lens)
+    cut = int(np.searchsorted(total, tokens))
+    test_packed([int(n) for n in lens[:cut]], 8, 4, io, True, 1)
+
+
 @pytest.mark.parametrize("ch,width,io", [(8192, 4, "bf16"), (13, 3, "bf16"), (260, 4, "f32"),
                                          (5, 2, "f32")])
 @pytest.mark.parametrize("in_place", [False, True])
