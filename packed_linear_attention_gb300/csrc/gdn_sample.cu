@@ -16,7 +16,6 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
-#include <cfloat>
 
 #include "gdn_internal.h"
 #include "gdn_step_internal.h"
@@ -111,16 +110,18 @@ __device__ __forceinline__ u64 share(float x, u64 total, bool up) {
   return q + (up && rest ? 1 : 0);
 }
 
-// Orders logits as unsigned numbers (-0 as 0): 32 bits of an fp32 value, 16 of a bf16 one.
+// Orders logits as unsigned numbers: 32 bits of an fp32 value, 16 of a bf16 one. A value is as far
+// from 2^31 as its magnitude's bits say, so the two zeros share a key and neighbouring keys are
+// neighbouring values: a bound may be any key, and comparing values is the same as comparing keys.
 template <typename T>
 __device__ __forceinline__ u32 key_of(float x) {
-  const u32 b = __float_as_uint(x + 0.f), k = b ^ ((u32)((int32_t)b >> 31) | 0x80000000u);
+  const u32 b = __float_as_uint(x), k = b >> 31 ? 0u - b : b + 0x80000000u;
   return sizeof(T) == 2 ? k >> 16 : k;
 }
 template <typename T>
 __device__ __forceinline__ float value_of(u32 key) {
-  const u32 k = sizeof(T) == 4 ? key : key << 16 | (key & 0x8000u ? 0 : 0xffffu);
-  return __uint_as_float(k ^ ((u32)((int32_t)~k >> 31) | 0x80000000u));
+  const u32 k = sizeof(T) == 4 ? key : key << 16;
+  return __uint_as_float(k >> 31 ? k - 0x80000000u : 0u - k);
 }
 
 // Weights of one row.
@@ -483,7 +484,7 @@ struct Row {
     const float to = last < kBins - 1 ? (float)(last + 1) : INFINITY;
     // at the least key for which it holds, at `top` if for none below
     const auto least = [&](auto holds) {
-      u32 a = key_of<T>(-FLT_MAX), b = top;
+      u32 a = key_of<T>(-INFINITY) + 1, b = top;
       while (a < b) {
         const u32 step = (b - a) / 32 + 1, k = (u32)min((u64)b, a + (u64)(threadIdx.x % 32) * step);
         const u32 yes = __ballot_sync(0xffffffffu, k == b || holds(weight.distance(value_of<T>(k))));
