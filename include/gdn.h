@@ -717,7 +717,8 @@ gdn_status gdn_attn_paged(gdn_handle* handle, const gdn_attn_config* cfg,
  * slot or rows (cu out of order, status raised) race for them, and some of them may be left out. */
 typedef struct gdn_requests {
   int32_t num_seqs;          /* 1 .. 4,096 requests                                          */
-  int32_t num_tokens;        /* rows of the call's arrays, cu[num_seqs] or more              */
+  int32_t num_tokens;        /* rows of the call's arrays, cu[num_seqs] or more, below
+                                2^31 - 4,096                                                 */
   int32_t max_len;           /* host bound of the requests' lengths                          */
   int32_t num_slots;         /* slots of the state pool                                      */
   const int32_t* cu;         /* [num_seqs + 1] first rows; a request of no rows is allowed   */
@@ -751,7 +752,7 @@ typedef struct gdn_conv_config {
  *  ckpt_states [num_ckpt][width - 1][C] io_dtype, or NULL without checkpoints.
  * Pointers 16-byte aligned, strides multiples of 16 bytes and at least C (so x may be a column
  * range of a projection's output). Results do not depend on the pack around a request.
- * Errors: INVALID_ARGUMENT, UNSUPPORTED (width, channels, more than 4,096 requests), CUDA. */
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED (width, channels, more requests or rows), CUDA. */
 gdn_status gdn_conv_packed(gdn_handle* handle, const gdn_conv_config* cfg,
                            const gdn_requests* req, const void* x, int64_t x_stride, void* y,
                            int64_t y_stride, void* state_pool, void* ckpt_states,
@@ -809,7 +810,7 @@ gdn_status gdn_ssm_workspace_size(const gdn_ssm_config* cfg, const gdn_requests*
  * kernel finds each segment's end state from zeros and its decay, a second runs the segments
  * from the joined states; results then differ from the uncut ones by fp32 rounding. The same call
  * gives the same bits. Inputs that are not finite spoil their own channel of their own request.
- * Errors: INVALID_ARGUMENT, UNSUPPORTED (state_dim above 128, channels, more than 4,096 requests),
+ * Errors: INVALID_ARGUMENT, UNSUPPORTED (state_dim above 128, channels, more requests or rows),
  * WORKSPACE_TOO_SMALL, CUDA. */
 gdn_status gdn_ssm_packed(gdn_handle* handle, const gdn_ssm_config* cfg, const gdn_requests* req,
                           const gdn_ssm_rows* rows, float* state_pool, float* ckpt_states,

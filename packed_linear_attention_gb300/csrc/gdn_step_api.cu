@@ -28,7 +28,7 @@ gdn_status check_requests(const gdn_requests* r, bool arrays) {
         (r->ckpt_cu && r->num_ckpt > 0 && !r->ckpt_pos) || (!r->slot_idx && r->num_seqs > r->num_slots))
       return GDN_ERR_INVALID_ARGUMENT;
   }
-  return r->num_seqs > gdn::kMaxRequests ? GDN_ERR_UNSUPPORTED : GDN_OK;
+  return r->num_seqs > gdn::kMaxRequests || r->num_tokens > gdn::kMaxRows ? GDN_ERR_UNSUPPORTED : GDN_OK;
 }
 
 bool row_ok(const void* p, int64_t stride, int32_t n, int32_t dtype) {

@@ -11,6 +11,8 @@
 namespace gdn {
 
 constexpr int kMaxRequests = 4096;  // of one packed call
+// Its rows: the kernels step past a request's last row by a block of 512 at most.
+constexpr int32_t kMaxRows = INT32_MAX - 4096;
 
 struct ConvArgs {
   gdn_conv_config cfg;
