@@ -844,6 +844,7 @@ typedef struct gdn_norm_config {
 
 /* The norm of num_tokens rows of num_heads * dim elements (at most 32,768), one kernel.
  *  residual, sum, gate  NULL where not wanted (sum needs residual). y NULL where codes are given.
+ *          A call of no rows checks none of the arrays.
  *  codes   [num_tokens] rows of e4m3 at codes + t * codes_stride (bytes), with
  *  scales  [num_tokens][num_heads * dim / scale_group, or 1] fp32; or both NULL.
  * Pointers 16-byte aligned (scales 4), strides multiples of 16 bytes. sum and y may each be x,

@@ -273,7 +273,8 @@ gdn_status gdn_rms_norm(gdn_handle* h, const gdn_norm_config* cfg, int32_t num_t
   const int32_t group = cfg->scale_group, d = cfg->dim, heads = cfg->num_heads;
   const int64_t row = (int64_t)heads * d;
   if (group > 0 && d % group != 0) return GDN_ERR_INVALID_ARGUMENT;
-  if ((codes == nullptr) != (scales == nullptr) || (!y && !codes) || (sum && !residual))
+  // a call of no rows may come with no arrays
+  if (num_tokens > 0 && ((codes == nullptr) != (scales == nullptr) || (!y && !codes) || (sum && !residual)))
     return GDN_ERR_INVALID_ARGUMENT;
   if (row > INT32_MAX) return GDN_ERR_UNSUPPORTED;
   if (num_tokens > 0) {
