@@ -873,8 +873,8 @@ gdn_status gdn_rms_norm(gdn_handle* handle, const gdn_norm_config* cfg, int32_t 
  * A logit of -inf or NaN is never drawn; where a row has +inf, those alone are drawn from. A row
  * without any other logit, or with a temperature below 0 or a NaN among its settings, gives token
  * -1 and logprob -inf and raises status (may be NULL) to GDN_ERR_INVALID_ARGUMENT.
- * Weights are fixed-point numbers of 2^-44 of the maximum's, right to 2^-30 of their own value
- * (or half a unit), and their sums are exact: results depend on no order of additions, and the same
+ * Weights are fixed-point numbers of 2^-44 of the maximum's, right to 2^-28 of their own value
+ * (or a unit), and their sums are exact: results depend on no order of additions, and the same
  * call gives the same bits. Supported: vocab 1 .. 262,144.
  * Errors: INVALID_ARGUMENT, UNSUPPORTED, CUDA. */
 gdn_status gdn_sample(gdn_handle* handle, int32_t io_dtype, int32_t num_rows, int32_t vocab,
