@@ -796,8 +796,8 @@ typedef struct gdn_ssm_rows {
   int64_t x_stride, delta_stride, b_stride, c_stride, z_stride, y_stride;
 } gdn_ssm_rows;
 
-/* Device workspace of gdn_ssm_packed for such requests (multiple of 256; the host fields of req
- * alone are read). */
+/* Device workspace of gdn_ssm_packed for calls of at most these num_seqs, num_tokens and max_len
+ * (multiple of 256; the host fields of req alone are read). */
 gdn_status gdn_ssm_workspace_size(const gdn_ssm_config* cfg, const gdn_requests* req,
                                   size_t* bytes);
 

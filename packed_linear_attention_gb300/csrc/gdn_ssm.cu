@@ -417,7 +417,6 @@ __global__ void __launch_bounds__(kThreads, kResident<T, SPLIT>) ssm_kernel(SsmA
   const int unit = blockIdx.x / channel_blocks;
   int32_t* status = blockIdx.x == 0 && pass < 2 ? p.status : nullptr;
   const int seg = p.segment;
-  const int cap = seg ? p.req.num_tokens / seg : 0;  // end states the workspace holds
   Unit u = {unit, 0, 0};
   if (pass > 0) {
     const auto behind = [&](int n) {  // segments behind the first
@@ -441,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, kResident<T, SPLIT>) ssm_kernel(SsmA
   if (q.len < 0) return;
   const int later = seg && q.len > 0 ? (q.len - 1) / seg : 0;
   const int k = pass == 2 ? u.place + 1 : u.place;  // this block's segment
-  if (later > 0 && u.extra + later > cap) {  // only where requests overlap
+  if (later > 0 && u.extra + later > p.units) {  // only where requests overlap
     if (threadIdx.x == 0) raise_status(p.status, GDN_ERR_INVALID_ARGUMENT);
     return;
   }
@@ -570,11 +569,18 @@ Shape shape_of(int n) {
   while (16 * split < n) split *= 2;
   return {16, split};
 }
+// Warps of a request's channels.
+int64_t channel_warps(const gdn_ssm_config& cfg) {
+  return ((int64_t)cfg.channels * shape_of(cfg.state_dim).split + 31) / 32;
+}
+// Rows that the requests may have in all.
+int64_t rows_of(const gdn_requests& req) {
+  return std::min<int64_t>(req.num_tokens, (int64_t)req.num_seqs * req.max_len);
+}
 // Warps that run side by side: those of a request's channels, times the requests that the rows
 // make up at their longest.
 int64_t warps_of(const gdn_ssm_config& cfg, const gdn_requests& req) {
-  const int64_t warps = ((int64_t)cfg.channels * shape_of(cfg.state_dim).split + 31) / 32;
-  return warps * std::max<int64_t>(1, std::min<int64_t>(req.num_seqs, req.num_tokens / std::max(1, req.max_len)));
+  return channel_warps(cfg) * std::max<int64_t>(1, rows_of(req) / std::max(1, req.max_len));
 }
 
 template <typename T, int NS, int SPLIT>
@@ -586,11 +592,10 @@ int launch_scan(const SsmArgs& a, cudaStream_t s) {
     return (int)cudaGetLastError();
   }
   // disjoint requests: at most a segment more than their whole ones each
-  const int64_t behind = a.req.num_tokens / a.segment;
   ssm_kernel<T, NS, SPLIT>
-      <<<(unsigned)((behind + a.req.num_seqs) * cb), kThreads, 0, s>>>(a, cb, 1);
-  if (behind > 0)
-    ssm_kernel<T, NS, SPLIT><<<(unsigned)(behind * cb), kThreads, 0, s>>>(a, cb, 2);
+      <<<(unsigned)(((int64_t)a.units + a.req.num_seqs) * cb), kThreads, 0, s>>>(a, cb, 1);
+  if (a.units > 0)
+    ssm_kernel<T, NS, SPLIT><<<(unsigned)((int64_t)a.units * cb), kThreads, 0, s>>>(a, cb, 2);
   return (int)cudaGetLastError();
 }
 
@@ -639,13 +644,25 @@ int step_by_lanes(const SsmArgs& a, cudaStream_t s) {
 // three quarters of a warp each: 32,768 rows of 2,048 channels take 3,620 us whole and 540 in 57
 // pieces, four requests of 4,096 rows and 4,096 channels 542 and 550. Shorter pieces than 64 rows
 // spend more on their starts than they win (a prompt of 100 rows: 17 us whole, 21 in four).
+constexpr int64_t kFew = kSchedulers * 3 / 4, kWanted = 6 * kSchedulers, kLeast = 64, kMost = 64;
 int32_t ssm_segment(const gdn_ssm_config& cfg, const gdn_requests& req) {
-  constexpr int64_t kFew = kSchedulers * 3 / 4, kWanted = 6 * kSchedulers, kLeast = 64, kMost = 64;
   const int64_t warps = warps_of(cfg, req);
   if (req.max_len < 1 || warps > kFew) return 0;
   const int64_t pieces = std::min<int64_t>(kMost, kWanted / warps);
   const int64_t seg = std::max<int64_t>(kLeast, ((int64_t)req.max_len + pieces - 1) / pieces + 31) / 32 * 32;
   return req.max_len >= 2 * seg ? (int32_t)seg : 0;
+}
+
+int64_t ssm_units(const gdn_requests& req, int32_t segment) { return segment ? rows_of(req) / segment : 0; }
+
+// Fewer requests or shorter ones may be cut where the largest call is not. A segment has kLeast rows at
+// least, and max_len / pieces. With R = rows / max_len requests side by side pieces are kWanted /
+// (channel warps * R rounded down, 1 at least), so that rows / segment is below twice kWanted over the
+// channel warps.
+int64_t ssm_most_units(const gdn_ssm_config& cfg, const gdn_requests& req) {
+  const int64_t warps = channel_warps(cfg);
+  if (warps > kFew || req.max_len < 2 * kLeast) return 0;
+  return std::min<int64_t>(rows_of(req) / kLeast, 2 * kWanted / warps);
 }
 
 int launch_ssm_packed(const SsmArgs& a, void* stream) {

@@ -3,6 +3,7 @@
 // enqueued; the handle comes last, so that a call without one shows what else is wrong with it.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -96,19 +97,10 @@ bool grid_ok(int32_t channels, double blocks) {
   return channels <= (1 << 18) && blocks <= (double)INT32_MAX;
 }
 
-// The host fields that say how a scan is cut, and its workspace.
-gdn_status plan_scan(const gdn_ssm_config* cfg, const gdn_requests* req, int32_t* segment,
-                     size_t* ends, size_t* bytes) {
-  gdn_status s = check_ssm(cfg, false);
-  if (s == GDN_OK) s = check_requests(req, false);
-  if (s != GDN_OK) return s;
-  *segment = gdn::ssm_segment(*cfg, *req);
-  const size_t units = *segment ? (size_t)(req->num_tokens / *segment) : 0;
-  const size_t state = (size_t)cfg->channels * cfg->state_dim * 4;
-  *ends = (units * state + 255) / 256 * 256;
-  *bytes = *ends + (units * cfg->channels * 4 + 255) / 256 * 256;
-  if (*bytes == 0) *bytes = 256;
-  return GDN_OK;
+// Bytes of `units` end states, and of them with their sums of dt: the workspace.
+void scan_bytes(const gdn_ssm_config& cfg, int64_t units, size_t* ends, size_t* bytes) {
+  *ends = ((size_t)units * cfg.channels * cfg.state_dim * 4 + 255) / 256 * 256;
+  *bytes = std::max<size_t>(256, *ends + ((size_t)units * cfg.channels * 4 + 255) / 256 * 256);
 }
 
 }  // namespace
@@ -177,12 +169,12 @@ gdn_status gdn_conv_step(gdn_handle* h, const gdn_conv_config* cfg, int32_t batc
 
 gdn_status gdn_ssm_workspace_size(const gdn_ssm_config* cfg, const gdn_requests* req,
                                   size_t* bytes) {
-  int32_t segment;
-  size_t ends, n;
-  const gdn_status s = plan_scan(cfg, req, &segment, &ends, &n);
+  gdn_status s = check_ssm(cfg, false);
+  if (s == GDN_OK) s = check_requests(req, false);
   if (s != GDN_OK) return s;
   if (!bytes) return GDN_ERR_INVALID_ARGUMENT;
-  *bytes = n;
+  size_t ends;
+  scan_bytes(*cfg, gdn::ssm_most_units(*cfg, *req), &ends, bytes);
   return GDN_OK;
 }
 
@@ -198,10 +190,10 @@ gdn_status gdn_ssm_packed(gdn_handle* h, const gdn_ssm_config* cfg, const gdn_re
   s = check_states(state_pool, req->num_slots, ckpt_states, num_ckpt, state, 4);
   if (s != GDN_OK) return s;
   if (!aligned(status, 4) || !ssm_rows_ok(*cfg, rows, tokens)) return GDN_ERR_INVALID_ARGUMENT;
-  int32_t segment;
+  const int32_t segment = gdn::ssm_segment(*cfg, *req);
+  const int64_t units = gdn::ssm_units(*req, segment);
   size_t ends, need;
-  s = plan_scan(cfg, req, &segment, &ends, &need);
-  if (s != GDN_OK) return s;
+  scan_bytes(*cfg, units, &ends, &need);
   if (!workspace || !aligned(workspace, 256)) return GDN_ERR_INVALID_ARGUMENT;
   const Span pool = whole(state_pool, req->num_slots * state, 4);
   const Span ckpt = whole(ckpt_states, num_ckpt * state, 4);
@@ -221,11 +213,12 @@ gdn_status gdn_ssm_packed(gdn_handle* h, const gdn_ssm_config* cfg, const gdn_re
   }
   if (workspace_bytes < need) return GDN_ERR_WORKSPACE_TOO_SMALL;
   // blocks: of a group's channels 16 at least
-  const double units = req->num_seqs + (segment ? (double)tokens / segment : 0.0);
-  if (!grid_ok(cfg->channels, units * (cfg->channels / 16.0 + cfg->num_groups))) return GDN_ERR_UNSUPPORTED;
+  if (!grid_ok(cfg->channels, (double)(req->num_seqs + units) * (cfg->channels / 16.0 + cfg->num_groups)))
+    return GDN_ERR_UNSUPPORTED;
   if (!h) return GDN_ERR_INVALID_ARGUMENT;
   gdn::SsmArgs a = {*cfg, *req, *rows, state_pool, ckpt_states, static_cast<float*>(workspace),
-                    reinterpret_cast<float*>(static_cast<char*>(workspace) + ends), segment, status};
+                    reinterpret_cast<float*>(static_cast<char*>(workspace) + ends), segment,
+                    (int32_t)units, status};
   return on_device(h, [&] { return gdn::launch_ssm_packed(a, stream); });
 }
 
@@ -254,7 +247,7 @@ gdn_status gdn_ssm_step(gdn_handle* h, const gdn_ssm_config* cfg, int32_t batch,
   }
   if (!grid_ok(cfg->channels, batch)) return GDN_ERR_UNSUPPORTED;
   if (!h) return GDN_ERR_INVALID_ARGUMENT;
-  gdn::SsmArgs a = {*cfg, {}, *rows, state_pool, nullptr, nullptr, nullptr, 0, status};
+  gdn::SsmArgs a = {*cfg, {}, *rows, state_pool, nullptr, nullptr, nullptr, 0, 0, status};
   a.req.num_tokens = batch;
   a.req.num_slots = num_slots;
   a.req.slot_idx = slot_idx;

@@ -37,10 +37,15 @@ struct SsmArgs {
   float* ends;    // [units][C][N] end states of the segments of cut requests (workspace)
   float* steps;   // [units][C] their sums of dt
   int32_t segment;  // tokens of a segment; 0: requests run whole
+  int32_t units;    // end states that the workspace holds
   int32_t* status;
 };
 // Tokens of a segment for calls of this shape, or 0 when requests run whole.
 int32_t ssm_segment(const gdn_ssm_config& cfg, const gdn_requests& req);
+// Segments behind their requests' first that the workspace has room for: those of disjoint requests.
+int64_t ssm_units(const gdn_requests& req, int32_t segment);
+// The most units of any call with at most as many requests and tokens, no longer ones.
+int64_t ssm_most_units(const gdn_ssm_config& cfg, const gdn_requests& req);
 int launch_ssm_packed(const SsmArgs& a, void* stream);
 int launch_ssm_step(const SsmArgs& a, void* stream);
 

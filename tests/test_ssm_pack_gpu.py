@@ -1,0 +1,34 @@
+"""The selective scan: what a request's results and a call's workspace owe to the calls around them."""
+import numpy as np
+import pytest
+
+from packed_linear_attention_gb300 import gdn
+
+from gpu_util import handle, torch_cuda
+from step_util import empty_rows, i32, up
+from test_ssm_gpu import Layer, run
+
+pytestmark = pytest.mark.gpu
+
+
+def test_one_workspace_for_every_step():
+    """Sized for the largest call, used by smaller ones, which are cut where that one is not."""
+    torch = torch_cuda()
+    rng = np.random.default_rng(31)
+    layer = Layer(rng, 2048, 16, 1, "bf16")
+    most = 12 * 600
+    t = layer.inputs(rng, most)
+    size = gdn.gdn_ssm_workspace_size(layer.cfg, gdn.make_requests(i32([0] * 13), most, 600, 12))
+    work = torch.zeros(size + 512, dtype=torch.uint8, device="cuda")
+    start = up(rng.standard_normal((12, 2048, 16)))
+    for lens, rows, max_len in (([600] * 12, most, 600), ([600], 600, 600), ([600, 1, 500], most, 600),
+                                ([130], most, 130), ([1] * 12, 12, 600), ([300] * 3, 900, 300)):
+        req = gdn.make_requests(i32(np.concatenate([[0], np.cumsum(lens)])), rows, max_len, 12)
+        part = {k: v[:rows] for k, v in t.items()}
+        ys, pools = [empty_rows(rows, 2048, "bf16") for _ in range(2)], [start.clone() for _ in range(2)]
+        work.fill_(255)  # NaN, and a mark behind the end
+        gdn.gdn_ssm_packed(handle(), layer.cfg, req, gdn.make_ssm_rows(y=ys[0], **part), pools[0], None,
+                           work, size)
+        run(layer, req, part, ys[1], pools[1])
+        assert torch.equal(*ys) and torch.equal(*pools) and (work[size:] == 255).all()
+        assert torch.isfinite(pools[0]).all()

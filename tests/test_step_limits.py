@@ -1,10 +1,12 @@
 """The calls around the recurrent layers at the ends of what they take, on the host: no call gets as
 far as a kernel (validation comes before any CUDA call, and a NULL handle is the last thing checked)."""
+import random
+
 import pytest
 
 from packed_linear_attention_gb300 import build, gdn
 
-from test_step_abi import (INVALID, P, UNSUPPORTED, conv_config, norm_config, requests, ssm_config,
+from test_step_abi import (INVALID, P, SMALL, UNSUPPORTED, conv_config, norm_config, requests, ssm_config,
                            ssm_rows)
 
 TOP = (1 << 31) - 4096
@@ -55,3 +57,44 @@ def test_norm_of_empty_tensors():
     gdn.gdn_rms_norm(handle(), cfg, 0, x, 256, codes=empty(torch.uint8), codes_stride=256,
                      scales=torch.empty(0, 1, device="cuda"))
     torch.cuda.synchronize()
+
+
+def scan_takes(cfg, seqs, tokens, max_len, size):
+    ch, gn = cfg.channels, cfg.num_groups * cfg.state_dim
+    rows = ssm_rows(x=FAR[0], delta=FAR[1], b=FAR[2], c=FAR[3], z=FAR[4], y=FAR[5], x_stride=ch,
+                    delta_stride=ch, z_stride=ch, y_stride=ch, b_stride=gn, c_stride=gn)
+    req = requests(num_seqs=seqs, num_tokens=tokens, max_len=max_len, num_slots=seqs, ckpt_cu=None)
+    st = gdn.gdn_ssm_packed(None, cfg, req, rows, FAR[6], None, FAR[7], size, None, raise_on_error=False)
+    assert st in (INVALID, SMALL)  # the NULL handle, or the workspace
+    return st == INVALID
+
+
+def test_a_workspace_for_the_largest_scan_serves_every_smaller_one():
+    """Fewer and shorter requests may be cut where many are not."""
+    rng = random.Random(3)
+    far = lambda top: int(2.0 ** rng.uniform(0, top))  # noqa: E731
+    for _ in range(300):
+        cfg = ssm_config(channels=8 * far(11), num_groups=1, state_dim=rng.choice([3, 8, 16, 64, 128]))
+        seqs, max_len = far(7), far(16)
+        tokens = min((1 << 31) - 5000, int(seqs * max_len * rng.uniform(0.3, 1.2)) + 1)
+        size = gdn.gdn_ssm_workspace_size(cfg, requests(num_seqs=seqs, num_tokens=tokens, max_len=max_len,
+                                                        num_slots=seqs))
+        assert size % 256 == 0
+        for _ in range(20):
+            n, m = rng.randint(1, seqs), rng.randint(1, max_len)
+            t = rng.randint(1, tokens)
+            assert scan_takes(cfg, n, t, m, size), (cfg.channels, cfg.state_dim, n, t, m)
+        for n in (1, 2, 3, seqs):  # as many rows as such requests have
+            n = min(n, seqs)
+            assert scan_takes(cfg, n, min(tokens, n * max_len), max_len, size)
+            assert scan_takes(cfg, n, tokens, max_len, size)
+
+
+def test_one_prompt_beside_a_wave():
+    cfg = ssm_config(channels=4096, num_groups=1)
+    wave = dict(num_seqs=32, num_slots=32, num_tokens=32768, max_len=1024)
+    size = gdn.gdn_ssm_workspace_size(cfg, requests(**wave))
+    for n in (1, 2, 3, 8, 32):
+        assert scan_takes(cfg, n, n * 1024, 1024, size) and scan_takes(cfg, n, 32768, 1024, size)
+    assert not scan_takes(cfg, 1, 1024, 1024, 256)  # cut: it needs room
+    assert size < 1 << 24
