@@ -31,21 +31,35 @@ __device__ __forceinline__ f32x2 decay(f32x2 dt, f32x2 a) {
   return ex2(fma2(dt, a, pair(kNudge, kNudge)));
 }
 // log(1 + exp(x)) = max(x, 0) + log1p(e), e = exp(-|x|) in (0, 1]. log1p(e) is e times a polynomial
-// fitted to log1p(e) / e (least squares, reweighted towards an even relative error, 3e-8), so that
-// small values keep their relative precision.
+// fitted to log1p(e) / e (least squares, reweighted towards an even relative error, 3e-8).
 __device__ constexpr float kLog1p[9] = {0.99999994f,  -0.49999493f, 0.33319095f,   -0.24842976f, 0.1910598f,
                              -0.13663195f, 0.07822535f,  -0.029504869f, 0.0052326024f};
+// exp(-|x|) = 2^y exp(r): y = -|x| log2 e as rounded (at |x| = 30 that is off by 2^-19, and so would be
+// the result) and r = -|x| - y ln 2, what the rounding left, where exp(r) is 1 + r. So small results keep
+// their relative precision, 2^-20, down to 2^-126. |x| is held at 127, past which 2^y is 0 anyway, for
+// infinities to leave no NaN; a NaN stays.
+constexpr float kLn2 = 0.6931471805599453f;
+// -|x|, held at -127
+__device__ __forceinline__ float minus_abs(float x) {
+  float a;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(a) : "f"(fabsf(x)), "f"(127.f));
+  return -a;
+}
 __device__ __forceinline__ f32x2 softplus(f32x2 x) {
   float x0, x1;
   unpair(x, x0, x1);
-  const f32x2 e = pair(ex2(-kLog2e * fabsf(x0)), ex2(-kLog2e * fabsf(x1)));
+  const f32x2 a = pair(minus_abs(x0), minus_abs(x1)), y = mul2(a, both(kLog2e));
+  f32x2 e = ex2(y);
+  e = fma2(e, fma2(y, both(-kLn2), a), e);
   f32x2 p = both(kLog1p[8]);
 #pragma unroll
   for (int i = 7; i >= 0; --i) p = fma2(e, p, both(kLog1p[i]));
   return fma2(e, p, pair(fmaxf(x0, 0.f), fmaxf(x1, 0.f)));
 }
 __device__ __forceinline__ float softplus(float x) {
-  const float e = ex2(-kLog2e * fabsf(x));
+  const float a = minus_abs(x), y = a * kLog2e;
+  float e = ex2(y);
+  e = fmaf(e, fmaf(y, -kLn2, a), e);
   float p = kLog1p[8];
 #pragma unroll
   for (int i = 7; i >= 0; --i) p = fmaf(e, p, kLog1p[i]);
@@ -494,9 +508,10 @@ __device__ __forceinline__ void load_eight(const T* p, int count, bool aligned, 
 }
 
 // Everything but the state is read before the slot is looked at. (Two rows a thread, their loads on the
-// way together: 20.5 us for 128 rows of 4,096 channels and 16 states against 18.5.)
+// way together: 20.5 us for 128 rows of 4,096 channels and 16 states against 18.4; nine blocks an SM,
+// at the 54 registers that it would take: 19.9.)
 template <typename T, int LANES>
-__global__ void __launch_bounds__(kThreads) ssm_step_kernel(SsmArgs p, bool aligned) {
+__global__ void __launch_bounds__(kThreads, 10) ssm_step_kernel(SsmArgs p, bool aligned) {
   const int64_t row = blockIdx.x;
   const int c = blockIdx.y * (kThreads / LANES) + (int)threadIdx.x / LANES;
   const int n0 = threadIdx.x % LANES * 8, n = p.cfg.state_dim;
