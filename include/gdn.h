@@ -808,8 +808,8 @@ gdn_status gdn_ssm_workspace_size(const gdn_ssm_config* cfg, const gdn_requests*
  * Where the call has too few channels and requests to fill the GPU, requests longer than a
  * segment (chosen from num_tokens, max_len, C and N, never from device values) are cut: a first
  * kernel finds each segment's end state from zeros and its decay, a second runs the segments
- * from the joined states; results then differ from the uncut ones by fp32 rounding. The same call
- * gives the same bits. Inputs that are not finite spoil their own channel of their own request.
+ * from the joined states; results then differ from the uncut ones by fp32 rounding. Those of calls that
+ * are not cut do not depend on the pack around a request. The same call gives the same bits. Inputs that are not finite spoil their own channel of their own request.
  * Errors: INVALID_ARGUMENT, UNSUPPORTED (state_dim above 128, channels, more requests or rows),
  * WORKSPACE_TOO_SMALL, CUDA. */
 gdn_status gdn_ssm_packed(gdn_handle* handle, const gdn_ssm_config* cfg, const gdn_requests* req,

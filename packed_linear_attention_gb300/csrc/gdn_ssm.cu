@@ -126,12 +126,15 @@ struct States {
       }
     }
   }
-  // one row; b and c: the padded row in shared memory. Returns this thread's part of c . h.
+  // one row; b and c: the padded row in shared memory. Returns this thread's part of c . h. Even and odd
+  // chunks are added up apart: a thread with 16 states has two sums that are those of two lanes with 8
+  // each. Which of the two shapes a call takes goes by the requests around a request, whose bits shall not.
   template <bool OUT>
   __device__ __forceinline__ float step(float dt, float dtx, const float* b, const float* c,
                                         int part) {
+    constexpr int kSums = NS == 4 || (NS == 8 && SPLIT == 2) ? 1 : 2;
     const f32x2 t = pair(dt, dt), u = pair(dtx, dtx);
-    f32x2 acc[2] = {0, 0};
+    f32x2 acc[kSums] = {};
 #pragma unroll
     for (int i = 0; i < NS / 4; ++i) {
       const ulonglong2 bv = *reinterpret_cast<const ulonglong2*>(b + chunk(i, part));
@@ -139,13 +142,19 @@ struct States {
       h[2 * i + 1] = fma2(decay(t, a[2 * i + 1]), h[2 * i + 1], mul2(u, bv.y));
       if (OUT) {
         const ulonglong2 cv = *reinterpret_cast<const ulonglong2*>(c + chunk(i, part));
-        acc[0] = i == 0 ? mul2(cv.x, h[0]) : fma2(cv.x, h[2 * i], acc[0]);
-        acc[1] = i == 0 ? mul2(cv.y, h[1]) : fma2(cv.y, h[2 * i + 1], acc[1]);
+        f32x2& s = acc[i % kSums];
+        s = i < kSums ? mul2(cv.x, h[2 * i]) : fma2(cv.x, h[2 * i], s);
+        s = fma2(cv.y, h[2 * i + 1], s);
       }
     }
-    float lo, hi;
-    unpair(add2(acc[0], acc[1]), lo, hi);
-    return lo + hi;
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < kSums; ++k) {
+      float lo, hi;
+      unpair(acc[k], lo, hi);
+      sum = k == 0 ? lo + hi : sum + (lo + hi);
+    }
+    return sum;
   }
 };
 
