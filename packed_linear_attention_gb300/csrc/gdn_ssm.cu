@@ -628,7 +628,7 @@ int scan_by_shape(const SsmArgs& a, cudaStream_t s) {
   const Shape k = shape_of(a.cfg.state_dim);
   if (k.ns == 4) return launch_scan<T, 4, 1>(a, s);
   if (k.ns == 8) return launch_scan<T, 8, 1>(a, s);
-  const int64_t pieces = a.segment ? (a.req.max_len + a.segment - 1) / a.segment : 1;
+  const int64_t pieces = a.segment ? ((int64_t)a.req.max_len + a.segment - 1) / a.segment : 1;
   if (k.split == 1 && warps_of(a.cfg, a.req) * pieces < 4 * kSchedulers)
     return launch_scan<T, 8, 2>(a, s);
   switch (k.split) {

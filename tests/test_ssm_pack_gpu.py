@@ -157,3 +157,17 @@ def test_a_long_prompt_of_many_channels(io):
     again, pool2 = empty_rows(n, ch, io), start.clone()
     run(layer, req, t, again, pool2, torch.zeros_like(ckpt))
     assert torch.equal(again, y) and torch.equal(pool, pool2)
+
+
+@pytest.mark.parametrize("ch", [64, 2048])
+def test_a_bound_of_the_lengths_that_says_nothing(ch):
+    """max_len at its largest: the segments it leads to are longer than the requests, which run whole."""
+    torch = torch_cuda()
+    rng = np.random.default_rng(35)
+    layer = Layer(rng, ch, 16, 1, "bf16")
+    cu, rows = i32([0, 50, 51, 110]), 110
+    t, start = layer.inputs(rng, rows), up(rng.standard_normal((3, ch, 16)))
+    pools, ys = [start.clone() for _ in range(2)], [empty_rows(rows, ch, "bf16") for _ in range(2)]
+    for max_len, y, pool in zip((59, 2 ** 31 - 1), ys, pools):
+        run(layer, gdn.make_requests(cu, rows, max_len, 3), t, y, pool)
+    assert torch.equal(*pools) and torch.equal(*ys)
