@@ -20,8 +20,8 @@ namespace {
 constexpr int kThreads = 128;
 // Rows loaded at once and blocks of an SM: loads on their way are what the wave waits for. bf16, 32 x
 // 1,024 rows of 8,192 channels, blocks of 128 rows: four rows and as many blocks as fit (six) 210 us, six
-// and seven 181, six and six 189, seven and seven 194 (registers spill), four and eight 196, eight and
-// five 195. fp32: four and five 328, three and six 333.
+// and seven 181 (124 bytes of a thread's registers spill), six and six 189, seven and seven 194 (472
+// bytes), four and eight 196, eight and five 195. fp32: four and five 328, three and six 333.
 template <typename T>
 constexpr int kAhead = sizeof(T) == 2 ? 6 : 4;
 template <typename T>

@@ -104,7 +104,7 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 }
 
 // Blocks of 256 threads on an SM; 0: as many as the registers give. 32 gated heads of 128, 32,768 rows, four
-// vectors a thread: 139 us at 64 registers, 147 at the 78 that it would take.
+// vectors a thread: 139 us at 64 registers (76 bytes a thread spill), 147 at the 78 that it would take.
 template <typename T, int VPT, bool HEADS, int THREADS>
 constexpr int kResident = sizeof(T) == 2 && VPT == 4 && HEADS && THREADS == 256 ? 4 : 0;
 
@@ -245,7 +245,8 @@ int launch(const NormArgs& a, cudaStream_t s) {
   const int vecs = (a.cfg.num_heads * a.cfg.dim + 7) / 8;
   // Few rows: as many threads a row as there are vectors. Many: two or four vectors a thread (32,768
   // rows of 2,048 with residual and codes: 121 us with one, 92 with two, 98 with four; 32 gated heads
-  // of 128: 171, 152 and 139).
+  // of 128: 171, 152 and 139). Measured at these widths: rows of fewer vectors than a warp's leave some
+  // empty (4 gated heads of 64: 33 us, 7.4 of them bytes).
   int vpt = a.num_tokens <= 1024 ? 1 : HEADS && sizeof(T) == 2 ? 4 : 2;
   while (vecs > 1024 * vpt) vpt *= 2;
   int team = 32;

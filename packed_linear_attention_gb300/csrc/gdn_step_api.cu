@@ -131,7 +131,7 @@ gdn_status gdn_conv_packed(gdn_handle* h, const gdn_conv_config* cfg, const gdn_
     if (overlap(in, pool) || overlap(out, pool) || overlap(in, ckpt) || overlap(out, ckpt))
       return GDN_ERR_INVALID_ARGUMENT;
   }
-  // one block for every 32 rows and 512 channels at least (16 bytes of 128 threads)
+  // one block for every 32 rows and 512 channels at least (four channels of 128 threads)
   if (!grid_ok(cfg->channels, (tokens / 32.0 + req->num_seqs) * (cfg->channels / 512.0 + 1))) return GDN_ERR_UNSUPPORTED;
   if (!h) return GDN_ERR_INVALID_ARGUMENT;
   const gdn::ConvArgs a = {*cfg, *req, x, y, x_stride, y_stride, state_pool, ckpt_states, status};
