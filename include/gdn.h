@@ -710,8 +710,9 @@ gdn_status gdn_attn_paged(gdn_handle* handle, const gdn_attn_config* cfg,
  * be captured in a CUDA graph: request n is rows [cu[n], cu[n+1]) and its state lives in slot
  * slot_idx[n] of the caller's pool, where it is updated in place. Any mix of prompts and single
  * tokens is served. A request whose rows or slot are out of range, or that is longer than max_len,
- * is refused whole (nothing of it is read or written); a slot below 0 skips its request. Rows
- * outside every request served are not written. Where `status` is a non-NULL device int32 the
+ * is refused whole (nothing of it is read or written); a slot below 0 skips its request. A request
+ * that gdn_kv_plan refused (kv_len 0) may have rows in cu all the same: give it such a slot for its
+ * state to stay as it was. Rows outside every request served are not written. Where `status` is a non-NULL device int32 the
  * kernels raise it (atomic maximum) to GDN_ERR_INVALID_ARGUMENT when they refused something; they
  * never clear it. Distinct slots and disjoint rows are the caller's duty: requests that share a
  * slot or rows (cu out of order, status raised) race for them, and some of them may be left out. */
@@ -809,7 +810,8 @@ gdn_status gdn_ssm_workspace_size(const gdn_ssm_config* cfg, const gdn_requests*
  * segment (chosen from num_tokens, max_len, C and N, never from device values) are cut: a first
  * kernel finds each segment's end state from zeros and its decay, a second runs the segments
  * from the joined states; results then differ from the uncut ones by fp32 rounding. Those of calls that
- * are not cut do not depend on the pack around a request. The same call gives the same bits. Inputs that are not finite spoil their own channel of their own request.
+ * are not cut do not depend on the pack around a request. The same call gives the same bits. Inputs
+ * that are not finite spoil their own channel of their own request.
  * Errors: INVALID_ARGUMENT, UNSUPPORTED (state_dim above 128, channels, more requests or rows),
  * WORKSPACE_TOO_SMALL, CUDA. */
 gdn_status gdn_ssm_packed(gdn_handle* handle, const gdn_ssm_config* cfg, const gdn_requests* req,
